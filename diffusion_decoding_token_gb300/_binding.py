@@ -17,8 +17,10 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdlm.so")
 
 DLM_F32, DLM_BF16, DLM_F16 = 0, 1, 2
-DEV_NONFINITE, DEV_POOL_CLIPPED, DEV_TIMEOUT, DEV_BAD_INDEX = 1, 2, 4, 8
+DEV_NONFINITE, DEV_POOL_CLIPPED, DEV_TIMEOUT, DEV_BAD_INDEX, DEV_BAD_PARAM = 1, 2, 4, 8, 16
 MAX_BLK = 256
+MAX_TOPK = 1024              # DLM_MAX_TOPK
+MAX_SEARCH_VOCAB = 1048575   # DLM_MAX_SEARCH_VOCAB
 
 _DT = {torch.float32: DLM_F32, torch.bfloat16: DLM_BF16, torch.float16: DLM_F16}
 
@@ -44,6 +46,12 @@ class DapdParams(ctypes.Structure):
 class StepRules(ctypes.Structure):
     _fields_ = [("rules", ctypes.c_uint32), ("tau", ctypes.c_float), ("depcap", DepcapParams),
                 ("cold_start", ctypes.c_void_p), ("cap", CapParams), ("cap_scope_from_boundary", ctypes.c_int32)]
+
+
+class SampleParams(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("temperature_rows", ctypes.c_void_p), ("top_k_rows", ctypes.c_void_p),
+                ("top_p_rows", ctypes.c_void_p), ("min_p_rows", ctypes.c_void_p)]
 
 
 RULE_THRESHOLD, RULE_BOUNDARY, RULE_CAP = 1, 2, 4
@@ -108,7 +116,14 @@ def lib():
         L.dlm_row_stats_attention.argtypes = [P, P, ctypes.c_int, I32, I32, I64, I64, P, P, P, P, P, P, P,
                                               ctypes.c_int, I32, I32, I64, I64, I64, I64, I32, P,
                                               ctypes.POINTER(DapdParams), P, Z, P, P]
-        for f in ("dlm_row_stats", "dlm_select_threshold", "dlm_depcap_boundary", "dlm_cap_select",
+        E, U = ctypes.c_int, ctypes.c_uint32
+        L.dlm_row_topk.argtypes = [P, E, I64, I64, I64, P, I64, I32, F, P, P, P, P, U, P]
+        L.dlm_row_sample.argtypes = [P, E, I64, I64, I64, P, I64, P, ctypes.POINTER(SampleParams), P, P, P, P, P, U, P]
+        L.dlm_distill_loss.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, F, P, P, P, P, P]
+        L.dlm_distill_grad.argtypes = [P, E, I64, I64, I64, P, P, E, I32, F, P, P, P, P, I64, P, P]
+        L.dlm_distill_step.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, F, P, P, P, I64, P, P]
+        for f in ("dlm_row_topk", "dlm_row_sample", "dlm_distill_loss", "dlm_distill_grad", "dlm_distill_step",
+                  "dlm_row_stats", "dlm_select_threshold", "dlm_depcap_boundary", "dlm_cap_select",
                   "dlm_dapd_graph_mis", "dlm_dapd_graph", "dlm_dapd_select", "dlm_select_topk",
                   "dlm_select_factor", "dlm_parallel_certificate", "dlm_depcap_boundary_ragged",
                   "dlm_revocable_step", "dlm_attention_influence", "dlm_row_stats_rules",
@@ -202,6 +217,213 @@ def row_stats(cur: torch.Tensor, prev: torch.Tensor | None = None, *, row_index:
                                   _p(out.lse_prev) if prev is not None else None, _p(status),
                                   flags, _stream(cur.device)))
     return out
+
+
+def _on(device, call, *args) -> None:
+    """Run a C call on the current stream of the tensors' device."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        _check(call(*args, _stream(device)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, _stream(device)))
+
+
+def _rows_arg(t: torch.Tensor, name: str) -> None:
+    if not t.is_cuda:
+        raise ValueError("libdlm takes CUDA tensors only")
+    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be [rows, V] with contiguous rows")
+
+
+def _stride(t: torch.Tensor) -> int:
+    # a single row's stride is never used; torch reports any value for it
+    epv = 16 // t.element_size()
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + epv - 1) // epv * epv
+
+
+def _same(t: torch.Tensor | None, shape, dtype, device, name: str, dtypes=None) -> None:
+    """An argument that is used in place: its shape, type, device and layout."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous() or \
+            (t.dtype not in dtypes if dtypes else t.dtype != dtype):
+        want = "/".join(str(d) for d in dtypes) if dtypes else str(dtype)
+        raise ValueError(f"{name} must be a contiguous {want} tensor of shape {tuple(shape)} on {device}")
+
+
+class RowTopk(NamedTuple):
+    values: torch.Tensor
+    ids: torch.Tensor
+    lse: torch.Tensor
+
+
+class RowSample(NamedTuple):
+    token: torch.Tensor
+    prob: torch.Tensor
+    conf: torch.Tensor | None
+
+
+class DistillLoss(NamedTuple):
+    loss: torch.Tensor
+    state: torch.Tensor
+
+
+DISTILL_STATE = 8  # DLM_DISTILL_STATE
+
+
+def _gathered(logits, row_index, gather):
+    """(row index, rows processed, rows of the per-row arrays)."""
+    rows = logits.shape[0]
+    if row_index is None:
+        if gather:
+            raise ValueError("gather needs a row_index")
+        return None, rows, rows
+    if row_index.device != logits.device:
+        raise ValueError("row_index must be on the logits' device")
+    row_index = row_index.to(torch.int32).contiguous()
+    n = row_index.numel()
+    return row_index, n, n if gather else rows
+
+
+def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0, row_index: torch.Tensor | None = None,
+             gather: bool = False, out: RowTopk | None = None, status: torch.Tensor | None = None) -> RowTopk:
+    """dlm_row_topk: the ``k`` largest logits of each row of ``logits``
+    ([rows, V], unit column stride) in descending order (ties to the lower
+    position) with their positions, and the row's log-sum-exp of
+    logits / temperature.  ``row_index`` and ``gather`` as in :func:`row_stats`."""
+    _rows_arg(logits, "logits")
+    row_index, n, m = _gathered(logits, row_index, gather)
+    dev = logits.device
+    if out is None:
+        out = RowTopk(torch.empty((m, k), dtype=torch.float32, device=dev),
+                      torch.empty((m, k), dtype=torch.int32, device=dev),
+                      torch.empty(m, dtype=torch.float32, device=dev))
+    else:
+        _same(out.values, (m, k), torch.float32, dev, "out.values")
+        _same(out.ids, (m, k), torch.int32, dev, "out.ids")
+        _same(out.lse, (m,), torch.float32, dev, "out.lse")
+    _on(dev, lib().dlm_row_topk, _p(logits), _dt(logits), n, logits.shape[1], _stride(logits), _p(row_index),
+        logits.shape[0], int(k), float(temperature), _p(out.values), _p(out.ids), _p(out.lse), _p(status),
+        ROWS_GATHER if gather else 0)
+    return out
+
+
+def row_sample(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+               lse: torch.Tensor | None = None, row_index: torch.Tensor | None = None, gather: bool = False,
+               out: RowSample | None = None, status: torch.Tensor | None = None) -> RowSample:
+    """dlm_row_sample: one token per row of ``logits`` ([rows, V], unit column
+    stride) from the caller's ``uniform`` numbers in [0, 1).  Each setting is a
+    number or a tensor with one value per row (float32; top_k int32).  With
+    ``lse`` (:func:`row_stats`' at the same rows) ``conf`` is the token's
+    unfiltered probability at temperature 1, which the selection rules take.
+    ``row_index`` and ``gather`` as in :func:`row_stats`."""
+    _rows_arg(logits, "logits")
+    row_index, n, m = _gathered(logits, row_index, gather)
+    dev = logits.device
+    _same(uniform, (m,), torch.float32, dev, "uniform")
+    _same(lse, (m,), torch.float32, dev, "lse")
+    prm = SampleParams(1.0, 0, 1.0, 0.0, None, None, None, None)
+    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(v, torch.Tensor):
+            _same(v, (m,), dtype, dev, name)
+            setattr(prm, name + "_rows", v.data_ptr())
+        else:
+            setattr(prm, name, v)
+    if out is None:
+        f = dict(dtype=torch.float32, device=dev)
+        out = RowSample(torch.empty(m, dtype=torch.int32, device=dev), torch.empty(m, **f),
+                        None if lse is None else torch.empty(m, **f))
+    else:
+        _same(out.token, (m,), torch.int32, dev, "out.token")
+        _same(out.prob, (m,), torch.float32, dev, "out.prob")
+        _same(out.conf, (m,), torch.float32, dev, "out.conf")
+    _on(dev, lib().dlm_row_sample, _p(logits), _dt(logits), n, logits.shape[1], _stride(logits), _p(row_index),
+        logits.shape[0], _p(uniform), ctypes.byref(prm), _p(lse), _p(out.token), _p(out.prob), _p(out.conf),
+        _p(status), ROWS_GATHER if gather else 0)
+    return out
+
+
+def _distill_args(student, ids, teacher, weights, teacher_lse=None):
+    _rows_arg(student, "student")
+    rows, dev = student.shape[0], student.device
+    if ids.dim() != 2 or ids.shape[0] != rows:
+        raise ValueError("ids must be [rows, k]")
+    _same(ids, ids.shape, torch.int32, dev, "ids")
+    _same(teacher, ids.shape, None, dev, "teacher", tuple(_DT))
+    _same(weights, (rows,), torch.float32, dev, "weights")
+    _same(teacher_lse, (rows,), torch.float32, dev, "teacher_lse")
+    return (_p(student), _dt(student), rows, student.shape[1], _stride(student), _p(ids), _p(teacher), _dt(teacher),
+            ids.shape[1])
+
+
+def _grad_out(student, out):
+    if out is None:
+        # rows at the student's stride, which is a multiple of 16 bytes
+        rows, V = student.shape
+        return torch.empty((rows, _stride(student)), dtype=student.dtype, device=student.device)[:, :V]
+    _rows_arg(out, "the gradient")
+    if out.shape != student.shape or out.dtype != student.dtype or out.device != student.device:
+        raise ValueError("the gradient must match the student in shape, dtype and device")
+    return out
+
+
+def distill_loss(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *,
+                 teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
+                 weights: torch.Tensor | None = None, out: DistillLoss | None = None,
+                 status: torch.Tensor | None = None) -> DistillLoss:
+    """dlm_distill_loss: the loss of each row of ``student`` ([rows, V], unit
+    column stride) against the teacher's top logits ``teacher`` at ``ids`` (both
+    [rows, k]; a negative id is an empty entry), and the state that
+    :func:`distill_grad` takes.  With ``teacher_lse`` the teacher's mass outside
+    the list is one more class, without it the list is renormalised."""
+    args = _distill_args(student, ids, teacher, weights, teacher_lse)
+    rows, dev = student.shape[0], student.device
+    if out is None:
+        out = DistillLoss(torch.empty(rows, dtype=torch.float32, device=dev),
+                          torch.empty((rows, DISTILL_STATE), dtype=torch.float32, device=dev))
+    else:
+        _same(out.loss, (rows,), torch.float32, dev, "out.loss")
+        _same(out.state, (rows, DISTILL_STATE), torch.float32, dev, "out.state")
+    _on(dev, lib().dlm_distill_loss, *args, _p(teacher_lse), float(temperature), _p(weights), _p(out.loss),
+        _p(out.state), _p(status))
+    return out
+
+
+def distill_grad(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, state: torch.Tensor,
+                 grad_loss: torch.Tensor | None = None, *, temperature: float = 1.0,
+                 weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None) -> torch.Tensor:
+    """dlm_distill_grad: the gradient of sum_r grad_loss[r] * loss[r] with
+    respect to ``student``, from the state of the :func:`distill_loss` call with
+    the same arguments.  ``out`` may be ``student`` itself."""
+    args = _distill_args(student, ids, teacher, weights)
+    rows, dev = student.shape[0], student.device
+    _same(state, (rows, DISTILL_STATE), torch.float32, dev, "state")
+    _same(grad_loss, (rows,), torch.float32, dev, "grad_loss")
+    out = _grad_out(student, out)
+    _on(dev, lib().dlm_distill_grad, *args, float(temperature), _p(weights), _p(state), _p(grad_loss), _p(out),
+        _stride(out), _p(status))
+    return out
+
+
+def distill_step(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *,
+                 teacher_lse: torch.Tensor | None = None, temperature: float = 1.0,
+                 weights: torch.Tensor | None = None, loss: torch.Tensor | None = None,
+                 grad: torch.Tensor | None = None, status: torch.Tensor | None = None):
+    """dlm_distill_step: (loss [rows], gradient of their sum [rows, V]) in one
+    launch; ``grad`` may be ``student`` itself.  Feed a model's own graph with
+    ``logits.backward(grad)``."""
+    args = _distill_args(student, ids, teacher, weights, teacher_lse)
+    rows, dev = student.shape[0], student.device
+    if loss is None:
+        loss = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _same(loss, (rows,), torch.float32, dev, "loss")
+    grad = _grad_out(student, grad)
+    _on(dev, lib().dlm_distill_step, *args, _p(teacher_lse), float(temperature), _p(weights), _p(loss), _p(grad),
+        _stride(grad), _p(status))
+    return loss, grad
 
 
 PARTIAL_FLOATS = 8  # dlm_row_partial: 8 four-byte fields

@@ -609,4 +609,176 @@ dlm_status dlm_row_stats_attention(const void* cur, const void* prev, dlm_dtype 
     return from_cuda(dlm::launch_dapd_graph(d, sm_count(), s, false));
 }
 
+// Checks shared by the row search calls; fills everything but the outputs.
+static dlm_status row_search_prepare(dlm::RowSearchArgs& a, const void* logits, dlm_dtype dtype, int64_t n_rows,
+                                     int64_t vocab, int64_t row_stride, const int32_t* row_index, int64_t n_src_rows,
+                                     uint32_t* dev_status, uint32_t flags) {
+    if (!dtype_ok(dtype)) return DLM_ERR_UNSUPPORTED;
+    if ((flags & ~DLM_ROWS_GATHER) || n_rows < 0 || vocab < 1 || vocab > DLM_MAX_SEARCH_VOCAB ||
+        row_stride < vocab || n_src_rows < 0)
+        return DLM_ERR_INVALID_ARG;
+    if (!row_index && n_src_rows > 0 && n_rows > n_src_rows) return DLM_ERR_INVALID_ARG;
+    if (n_rows == 0) return DLM_OK;
+    if (!logits) return DLM_ERR_INVALID_ARG;
+    if (!aligned16(logits) || (row_stride * dtype_size(dtype)) % 16 != 0) return DLM_ERR_ALIGNMENT;
+    a = dlm::RowSearchArgs{};
+    a.logits = logits;
+    a.n_rows = n_rows;
+    a.vocab = vocab;
+    a.row_stride = row_stride;
+    a.row_index = row_index;
+    a.n_src = n_src_rows;
+    a.gather = (flags & DLM_ROWS_GATHER) ? 1 : 0;
+    a.dev_status = dev_status;
+    a.split = dlm::row_search_split(dtype, n_rows, vocab, sm_count());
+    if (n_rows > 0x7fffffffLL / a.split) return DLM_ERR_INVALID_ARG;
+    return DLM_OK;
+}
+
+static bool temperature_ok(float t) { return t >= DLM_MIN_TEMPERATURE && isfinite(t); }
+
+dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                        const int32_t* row_index, int64_t n_src_rows, int32_t k, float temperature, float* values,
+                        int32_t* ids, float* lse, uint32_t* dev_status, uint32_t flags, dlm_stream_t stream) {
+    if (k < 1 || k > DLM_MAX_TOPK || !temperature_ok(temperature)) return DLM_ERR_INVALID_ARG;
+    dlm::RowSearchArgs a{};
+    const dlm_status st = row_search_prepare(a, logits, dtype, n_rows, vocab, row_stride, row_index, n_src_rows,
+                                             dev_status, flags);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!values || !ids) return DLM_ERR_INVALID_ARG;
+    a.k = k;
+    a.temperature = temperature;
+    a.top_p = 1.f;
+    a.values = values;
+    a.ids = ids;
+    a.lse = lse;
+    return from_cuda(dlm::launch_row_topk(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                          const int32_t* row_index, int64_t n_src_rows, const float* uniform,
+                          const dlm_sample_params* params, const float* lse, int32_t* token, float* prob, float* conf,
+                          uint32_t* dev_status, uint32_t flags, dlm_stream_t stream) {
+    if (!params) return DLM_ERR_INVALID_ARG;
+    // a setting that comes per row is checked on the device instead
+    if (!params->temperature_rows && params->temperature != 0.f && !temperature_ok(params->temperature))
+        return DLM_ERR_INVALID_ARG;
+    if (!params->top_k_rows && params->top_k < 0) return DLM_ERR_INVALID_ARG;
+    if (!params->top_p_rows && !(params->top_p > 0.f && params->top_p <= 1.f)) return DLM_ERR_INVALID_ARG;
+    if (!params->min_p_rows && !(params->min_p >= 0.f && params->min_p <= 1.f)) return DLM_ERR_INVALID_ARG;
+    if ((lse == nullptr) != (conf == nullptr)) return DLM_ERR_INVALID_ARG;
+    dlm::RowSearchArgs a{};
+    const dlm_status st = row_search_prepare(a, logits, dtype, n_rows, vocab, row_stride, row_index, n_src_rows,
+                                             dev_status, flags);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!uniform || !token || !prob) return DLM_ERR_INVALID_ARG;
+    a.uniform = uniform;
+    a.temperature = params->temperature;
+    a.k = params->top_k;
+    a.top_p = params->top_p;
+    a.min_p = params->min_p;
+    a.temperature_rows = params->temperature_rows;
+    a.top_k_rows = params->top_k_rows;
+    a.top_p_rows = params->top_p_rows;
+    a.min_p_rows = params->min_p_rows;
+    a.lse_in = lse;
+    a.token = token;
+    a.prob = prob;
+    a.conf = conf;
+    return from_cuda(dlm::launch_row_sample(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Checks shared by the distillation calls.
+static dlm_status distill_prepare(dlm::DistillArgs& a, const void* student, dlm_dtype dtype, int64_t n_rows,
+                                  int64_t vocab, int64_t row_stride, const int32_t* ids, const void* teacher,
+                                  dlm_dtype teacher_dtype, int32_t k, float temperature, const float* weights,
+                                  uint32_t* dev_status) {
+    if (!dtype_ok(dtype) || !dtype_ok(teacher_dtype)) return DLM_ERR_UNSUPPORTED;
+    if (n_rows < 0 || vocab < 1 || vocab > DLM_MAX_SEARCH_VOCAB || row_stride < vocab || k < 1 || k > DLM_MAX_TOPK ||
+        !temperature_ok(temperature))
+        return DLM_ERR_INVALID_ARG;
+    if (n_rows == 0) return DLM_OK;
+    if (!student || !ids || !teacher) return DLM_ERR_INVALID_ARG;
+    if (!aligned16(student) || (row_stride * dtype_size(dtype)) % 16 != 0) return DLM_ERR_ALIGNMENT;
+    a = dlm::DistillArgs{};
+    a.student = student;
+    a.n_rows = n_rows;
+    a.vocab = vocab;
+    a.row_stride = row_stride;
+    a.ids = ids;
+    a.teacher = teacher;
+    a.teacher_dtype = teacher_dtype;
+    a.k = k;
+    a.temperature = temperature;
+    a.weights = weights;
+    a.dev_status = dev_status;
+    a.split = dlm::distill_split(dtype, n_rows, vocab, sm_count());
+    if (n_rows > 0x7fffffffLL / a.split) return DLM_ERR_INVALID_ARG;
+    return DLM_OK;
+}
+
+// The gradient's memory: aligned like the student's, and the same rows or none of them.
+static dlm_status distill_grad_ok(const dlm::DistillArgs& a, dlm_dtype dtype, const void* grad, int64_t grad_stride) {
+    if (!grad || grad_stride < a.vocab) return DLM_ERR_INVALID_ARG;
+    const int64_t esz = dtype_size(dtype);
+    if (!aligned16(grad) || (grad_stride * esz) % 16 != 0) return DLM_ERR_ALIGNMENT;
+    const char* s0 = static_cast<const char*>(a.student);
+    const char* g0 = static_cast<const char*>(grad);
+    if (s0 == g0 && grad_stride == a.row_stride) return DLM_OK;
+    const char* s1 = s0 + ((a.n_rows - 1) * a.row_stride + a.vocab) * esz;
+    const char* g1 = g0 + ((a.n_rows - 1) * grad_stride + a.vocab) * esz;
+    return g0 < s1 && s0 < g1 ? DLM_ERR_INVALID_ARG : DLM_OK;
+}
+
+dlm_status dlm_distill_loss(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
+                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            float* state, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::DistillArgs a{};
+    const dlm_status st = distill_prepare(a, student, dtype, n_rows, vocab, row_stride, ids, teacher, teacher_dtype,
+                                          k, temperature, weights, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!loss) return DLM_ERR_INVALID_ARG;
+    a.teacher_lse = teacher_lse;
+    a.loss = loss;
+    a.state = state;
+    return from_cuda(dlm::launch_distill_loss(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dlm_status dlm_distill_grad(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
+                            float temperature, const float* weights, const float* state, const float* grad_loss,
+                            void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::DistillArgs a{};
+    dlm_status st = distill_prepare(a, student, dtype, n_rows, vocab, row_stride, ids, teacher, teacher_dtype, k,
+                                    temperature, weights, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!state) return DLM_ERR_INVALID_ARG;
+    st = distill_grad_ok(a, dtype, grad, grad_stride);
+    if (st != DLM_OK) return st;
+    a.state = const_cast<float*>(state);
+    a.grad_loss = grad_loss;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return from_cuda(dlm::launch_distill_grad(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
+                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::DistillArgs a{};
+    dlm_status st = distill_prepare(a, student, dtype, n_rows, vocab, row_stride, ids, teacher, teacher_dtype, k,
+                                    temperature, weights, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!loss) return DLM_ERR_INVALID_ARG;
+    st = distill_grad_ok(a, dtype, grad, grad_stride);
+    if (st != DLM_OK) return st;
+    a.teacher_lse = teacher_lse;
+    a.loss = loss;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return from_cuda(dlm::launch_distill_loss(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -214,6 +214,59 @@ struct RowRules {
     CapArgs c;
 };
 cudaError_t launch_row_stats_rules(const RowStatsArgs& a, const RowRules& r, int dtype, cudaStream_t s);
+// The row search (dlm_row_topk, dlm_row_sample).
+struct RowSearchArgs {
+    const void* logits;
+    int64_t n_rows, vocab, row_stride;
+    const int32_t* row_index;
+    int64_t n_src;            // rows the logits hold (0 = unchecked)
+    int gather;               // per-row arrays at r instead of q
+    int split;                // CTAs per row (thread-block cluster size)
+    uint32_t* dev_status;
+    int k;                    // topk: entries per row; sample: top_k
+    float temperature, top_p, min_p;
+    const float* temperature_rows;  // nullable: per-row settings
+    const int32_t* top_k_rows;
+    const float* top_p_rows;
+    const float* min_p_rows;
+    // topk outputs
+    float* values;
+    int32_t* ids;
+    float* lse;
+    // sample
+    const float* uniform;
+    const float* lse_in;
+    int32_t* token;
+    float* prob;
+    float* conf;
+};
+int row_search_split(int dtype, int64_t n_rows, int64_t vocab, int num_sms);
+cudaError_t launch_row_topk(const RowSearchArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_row_sample(const RowSearchArgs& a, int dtype, cudaStream_t s);
+
+// Distillation from a teacher's top logits.
+struct DistillArgs {
+    const void* student;
+    int64_t n_rows, vocab, row_stride;
+    int split;                // CTAs per row (thread-block cluster size)
+    const int32_t* ids;       // [n_rows][k]
+    const void* teacher;      // [n_rows][k]
+    int teacher_dtype;
+    int k;
+    const float* teacher_lse; // [n_rows], nullable: renormalised over the list
+    float temperature;
+    const float* weights;     // [n_rows], nullable: 1
+    const float* grad_loss;   // [n_rows], nullable: 1 (gradient call)
+    float* loss;
+    float* state;             // [n_rows][DLM_DISTILL_STATE]
+    void* grad;               // non-null in the loss launch: the gradient too
+    int64_t grad_stride;
+    uint32_t* dev_status;
+};
+int distill_split(int dtype, int64_t n_rows, int64_t vocab, int num_sms);
+cudaError_t launch_distill_loss(const DistillArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
+
 // attention -> sums (every sequence) -> infl[b][j] = column sums over masked rows / (L H)
 cudaError_t launch_attention_influence(DapdArgs& a, int num_sms, float* infl, cudaStream_t s);
 

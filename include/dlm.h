@@ -64,6 +64,9 @@ typedef enum dlm_dtype { DLM_F32 = 0, DLM_BF16 = 1, DLM_F16 = 2 } dlm_dtype;
                                    row was neither read nor written (row pass), or
                                    its pairs scored NaN (CAP) */
 
+#define DLM_DEV_BAD_PARAM 16u   /* a per-row setting of dlm_row_sample was out of range:
+                                   that row's token is -1                           */
+
 /* Maximum block size accepted by the selection calls. */
 #define DLM_MAX_BLK 256
 #define DLM_MAX_BATCH 1048575 /* 2^20 - 1: CAP / DAPD launch grids stay below 2^31 CTAs */
@@ -662,6 +665,148 @@ dlm_status dlm_revocable_step(const int32_t* argmax, const float* conf, const fl
                               int32_t* tok, uint8_t* masked, uint8_t* seed, int32_t* last_seed, int32_t* remasks,
                               int32_t* last_tok, uint8_t* outcome, int32_t* n_drafted, int32_t* n_revoked,
                               int32_t* flipflops, dlm_stream_t stream);
+
+/*
+ * dlm_row_topk -- the k largest logits of each row, and the row's
+ * log-sum-exp.
+ *
+ * Row q's entries are the first k of the order (logit descending, position
+ * ascending): values[o][j] the logit (exact) and ids[o][j] its position,
+ * lse[o] = log sum_v exp(z_v / temperature).  -inf logits carry no probability
+ * and are not listed: entries past the finite logits are (-inf, -1).  What a
+ * teacher's row needs stored for dlm_distill_loss.
+ *
+ * logits, dtype, n_rows, vocab, row_stride, row_index, n_src_rows : as in
+ *               dlm_row_stats_ex; vocab <= DLM_MAX_SEARCH_VOCAB.
+ * k           : 1 <= k <= DLM_MAX_TOPK (may exceed vocab).
+ * temperature : >= DLM_MIN_TEMPERATURE, finite; enters lse only.
+ * values, ids : float / int32 [.][k] outputs; lse: nullable float output.
+ *               Row r processed is stored at o = q, or at o = r with
+ *               DLM_ROWS_GATHER (the only flag).
+ * dev_status  : DLM_DEV_NONFINITE for a row that holds NaN or +inf, or -inf
+ *               only: its entries are (-inf, -1) and its lse NaN, +inf or -inf.
+ *               DLM_DEV_BAD_INDEX as in dlm_row_stats_ex.
+ */
+#define DLM_MAX_TOPK 1024
+#define DLM_MAX_SEARCH_VOCAB 1048575 /* 2^20 - 1: a row's mass in units of 2^-44 fits 64 bits */
+#define DLM_MIN_TEMPERATURE 1e-4f
+
+dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                        const int32_t* row_index, int64_t n_src_rows, int32_t k, float temperature, float* values,
+                        int32_t* ids, float* lse, uint32_t* dev_status, uint32_t flags, dlm_stream_t stream);
+
+/*
+ * dlm_row_sample -- one token per row, sampled with temperature, top-k, top-p
+ * and min-p from a uniform number that the caller gives.
+ *
+ * With w_v = exp((z_v - max z) / T) and the order (logit descending, position
+ * ascending), the tokens that stay are those that pass, in turn:
+ *   top_k : the first top_k of the order (0 or >= vocab: all);
+ *   top_p : of these, the shortest prefix whose mass reaches top_p of theirs
+ *           (the tokens whose predecessors' mass is below top_p; 1: all);
+ *   min_p : w_v >= min_p (0: all).
+ * -inf logits never stay.  The token is the smallest kept position v with
+ *   sum of w over the kept positions <= v  >  u * (sum over all kept),
+ * prob = w_token / (sum over all kept).  temperature 0 takes the first maximum
+ * (prob 1) whatever the filters.  The sums that decide are exact integers
+ * (64-bit fixed point, weights to 2^-37): the token is that of the real-number
+ * definition unless u * sum lies within about 1e-11 of a border, and equal
+ * inputs give equal tokens on every launch.
+ *
+ * logits .. n_src_rows, flags : as in dlm_row_topk (row r's uniform, settings,
+ *               lse and outputs at o = q, or o = r with DLM_ROWS_GATHER).
+ * uniform     : float [.], 0 <= u < 1.
+ * params      : the call's settings; a non-null *_rows array gives row o's own.
+ *               temperature 0 or in [DLM_MIN_TEMPERATURE, FLT_MAX], top_k >= 0,
+ *               0 < top_p <= 1, 0 <= min_p <= 1.  Scalars are checked on the
+ *               host; a row whose own settings or u are out of range gets
+ *               token -1, prob 0 and sets DLM_DEV_BAD_PARAM.
+ * lse         : nullable float [.] (dlm_row_stats' lse); with conf, conf[o] =
+ *               exp(z_token - lse[o]): the token's unfiltered probability at
+ *               temperature 1, which the selection rules take.  Both or none.
+ * token, prob : int32 / float outputs.  A row that holds NaN or +inf, or -inf
+ *               only, gets token -1, prob 0 (conf 0) and sets DLM_DEV_NONFINITE.
+ */
+typedef struct dlm_sample_params {
+    float temperature;
+    int32_t top_k;
+    float top_p;
+    float min_p;
+    const float* temperature_rows; /* nullable device arrays */
+    const int32_t* top_k_rows;
+    const float* top_p_rows;
+    const float* min_p_rows;
+} dlm_sample_params;
+
+dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                          const int32_t* row_index, int64_t n_src_rows, const float* uniform,
+                          const dlm_sample_params* params, const float* lse, int32_t* token, float* prob, float* conf,
+                          uint32_t* dev_status, uint32_t flags, dlm_stream_t stream);
+
+/*
+ * dlm_distill_loss / dlm_distill_grad / dlm_distill_step -- distillation of a
+ * student's logit rows from the teacher's top logits.
+ *
+ * Row r: q = softmax(student row / T); p_j the teacher's probability of
+ * ids[r][j]: softmax(teacher[r] / T) over the row's entries, or with
+ * teacher_lse  p_j = exp(teacher[r][j] / T - teacher_lse[r]) and the rest of
+ * the mass p_rest = max(0, 1 - sum_j p_j) as one more class, q_rest being the
+ * student's mass outside the list (a weight below 2^-126 of the row's largest
+ * counts as 0):
+ *   loss[r] = weights[r] * ( sum_j p_j (ln p_j - ln q_{ids_j})
+ *                            [ + p_rest (ln p_rest - ln q_rest) ] )
+ *   d loss[r] / d s_v = weights[r] / T * ( q_v - p_v )                  v listed
+ *                     = weights[r] / T * q_v (1 - p_rest / q_rest)      otherwise
+ * (p_rest = 0 without teacher_lse).  Multiply by T^2 through weights where a
+ * mix with another loss asks for it.
+ *
+ * dlm_distill_loss writes loss and, if given, the state that dlm_distill_grad
+ * takes to write grad[r] = grad_loss[r] * d loss[r] / d s.  dlm_distill_step
+ * writes both in one launch, the gradient being that of sum_r loss[r].
+ *
+ * student     : [n_rows][row_stride] logits; alignment and dtypes as in
+ *               dlm_row_stats, vocab <= DLM_MAX_SEARCH_VOCAB.  -inf logits
+ *               carry no probability (a listed one with p > 0: loss +inf).
+ * ids         : int32 [n_rows][k], 1 <= k <= DLM_MAX_TOPK.  A negative id is an
+ *               empty entry (shorter lists); an id >= vocab is treated as one
+ *               and sets DLM_DEV_BAD_INDEX.  The entries of an id that is
+ *               listed more than once add up.  A row without entries (or with
+ *               -inf teacher logits only) and without teacher_lse has loss 0
+ *               and gradient 0.
+ * teacher     : [n_rows][k] logits of teacher_dtype (values of empty entries
+ *               are not used); teacher_lse: nullable float [n_rows],
+ *               ln sum_v exp(t_v / T) of the whole teacher row (dlm_row_topk).
+ * temperature : T >= DLM_MIN_TEMPERATURE, finite.
+ * weights     : nullable float [n_rows] (1).  A row of weight 0 is not read:
+ *               loss 0, gradient 0.
+ * loss        : float [n_rows] output.
+ * state       : float [n_rows][DLM_DISTILL_STATE], opaque; nullable in
+ *               dlm_distill_loss.  dlm_distill_grad must get the ids, teacher,
+ *               temperature, weights and student of the call that wrote it.
+ * grad_loss   : nullable float [n_rows] (1); 0 writes a zero row unread.
+ * grad        : [n_rows][grad_stride] in the student's dtype, aligned like it;
+ *               may be the student's memory itself (same base and stride), else
+ *               it must not overlap it.  Elements past vocab are left alone.
+ * dev_status  : DLM_DEV_NONFINITE for a row whose student logits hold NaN or
+ *               +inf, or -inf only, or whose listed teacher logits (or
+ *               teacher_lse) are NaN or +inf: loss and gradient are NaN there.
+ */
+#define DLM_DISTILL_STATE 8
+
+dlm_status dlm_distill_loss(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
+                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            float* state, uint32_t* dev_status, dlm_stream_t stream);
+
+dlm_status dlm_distill_grad(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
+                            float temperature, const float* weights, const float* state, const float* grad_loss,
+                            void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
+
+dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                            const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
+                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
 
 #ifdef __cplusplus
 }
