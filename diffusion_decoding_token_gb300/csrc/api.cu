@@ -630,7 +630,8 @@ static dlm_status row_search_prepare(dlm::RowSearchArgs& a, const void* logits, 
     a.n_src = n_src_rows;
     a.gather = (flags & DLM_ROWS_GATHER) ? 1 : 0;
     a.dev_status = dev_status;
-    a.split = dlm::row_search_split(dtype, n_rows, vocab, sm_count());
+    a.num_sms = sm_count();
+    a.split = dlm::row_search_split(dtype, n_rows, vocab, a.num_sms);
     if (n_rows > 0x7fffffffLL / a.split) return DLM_ERR_INVALID_ARG;
     return DLM_OK;
 }

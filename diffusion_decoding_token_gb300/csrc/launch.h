@@ -222,6 +222,7 @@ struct RowSearchArgs {
     int64_t n_src;            // rows the logits hold (0 = unchecked)
     int gather;               // per-row arrays at r instead of q
     int split;                // CTAs per row (thread-block cluster size)
+    int num_sms;
     uint32_t* dev_status;
     int k;                    // topk: entries per row; sample: top_k
     float temperature, top_p, min_p;

@@ -13,12 +13,25 @@
 // weights relative to the batch's own maximum.  The k-th largest run maximum
 // c is at most the k-th largest logit, so all of the top k lie in runs whose
 // maximum is >= c: only those few runs are read again (from L2).  The
-// candidates are sorted and decided with 64-bit integer weights (weight.cuh).
-// A row whose filters keep more than the candidate list holds is searched
-// over the whole row: radix passes over the ordered keys with counts (top-k)
-// or 64-bit masses (top-p), then one pass for the kept mass of each batch.
+// candidates are decided with 64-bit integer weights (weight.cuh).
 //
-// A row is worked by one CTA, or by a cluster of CTAs when rows are few.
+// Tokens that no short list can decide (a nucleus of thousands of tokens on a
+// flat row, or no filter at all) are decided from sums over the row, in tiers.
+// A tier knows how far its sums may be off; a token whose borders lie further
+// than that from the target is the answer, otherwise the next tier looks:
+//   0  the first pass's batch sums (off by 2^-18; no filter only);
+//   1  one more pass with the exponent split into integer and fraction (2^-20.8);
+//   2  the same pass with integer weights (2^-36).
+// The passes of tiers 1 and 2 find the nucleus' end by a bracket: a sample of
+// the row says between which two logits it must lie, the pass sums what is
+// above, lists what is inside, and the list is sorted.  What the bracket
+// misses (ties by the thousand, a top-k beyond the list) goes to a search by
+// radix passes over the ordered keys, with counts (top-k) or integer masses.
+//
+// A row is worked by one CTA, or by a cluster of CTAs when rows are few.  With
+// one CTA per row the rows that need another pass are left to a second launch
+// that works each with a cluster: alone, a CTA would be at such a row long after
+// all the others have ended.
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
@@ -33,8 +46,17 @@ constexpr int kWarps = kRowWarps;
 constexpr int kRuns = 4;               // runs (of 32 vectors) per batch
 constexpr int kBatchVecs = 32 * kRuns;
 constexpr int kCap = 2048;             // candidates held in shared memory
+constexpr int kBracketCap = 2 * kCap;  // tokens of a bracket (the weights' space too)
+constexpr int kFine = 1024;            // bins that a bracket's tokens are sorted into
+constexpr int kListRuns = 128;         // run maxima that open a nucleus' candidate list
+constexpr int kBracketSide = 1200;     // tokens on either side of its middle
+constexpr int kSampleTokens = 16384;   // the sample that places a bracket
+constexpr int kOpenSplit = 4;          // CTAs per row that the first launch left open
+constexpr int kTries = 4;              // brackets that a row gets
+constexpr uint64_t kOne = 1ull << kWeightBits;
 constexpr int kBins = 2048;            // radix bins of a pass over the whole row
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // ordered key of -inf
+static_assert(kFine % kThreads == 0 && kFine >= kThreads, "whole bins per thread");
 static_assert(kCap >= 2 * DLM_MAX_TOPK, "a candidate list holds the largest top-k and ties");
 
 // Keys whose unsigned order is the order of the floats; -0 counts as +0.
@@ -47,44 +69,71 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // What one row's CTA (the first of its cluster) and the others share.
+enum Verdict : int { kRadix = 0, kDone = 1, kTier1 = 2, kTier2 = 3 };
+
 struct Ctrl {
     WeightScale ws;
-    float temperature, top_p, u;
-    float z_least;        // min-p: the smallest logit that stays
+    float top_p, min_p, u;
     int top_k;            // 0: off
     int bad;              // a parameter of this row is out of range
-    int done;             // the row's outputs are written
-    uint32_t count;       // candidates found (may exceed kCap)
+    int verdict;          // what the cluster does next
+    uint32_t count;       // candidates found (may exceed the list)
+    uint32_t runs;        // runs to read again
     int n;                // tokens kept, or -1
+    uint64_t least;       // min-p: the smallest weight that stays
+    uint64_t total;       // the row's mass, within margin
+    uint64_t margin;
+    uint64_t whole;       // a slice's mass
+    float z_lo, z_hi;     // the bracket: z_lo <= z < z_hi
+    int bin_lo, bin_hi;   // the same in 1/32 of an exponent below the maximum
+    int tries;
     // the search over the whole row
     uint32_t prefix;      // key bits found so far
     uint64_t above;       // count or mass of the keys above the prefix
-    uint64_t total;
-    uint32_t cut_key;     // kept: keys above cut_key, and the first cut_ties positions at it
-    uint32_t cut_ties;
-    uint64_t scan[kWarps];
-    float fscan[kWarps];
+    uint32_t cut_key;     // kept: keys above cut_key, and of the positions at it
+    uint32_t cut_ties;    // the first cut_ties that are <= cut_last
+    uint32_t cut_last;
     uint64_t mass;        // kept mass
     uint64_t left;        // target inside the chosen batch
+    uint64_t sure;        // bracket: the last candidate that surely stays, the mass
+    uint64_t sure_mass;   // up to it, and up to the last one that may stay
+    uint64_t slack;
     int batch;
     uint32_t ties_before;
-    uint64_t margin;
+    int first_bin, last_bin;
+    int token;            // found by walk_batch
+    float z;
+    uint64_t lo_side, hi_side;
+    int hits[2][kWarps];
+    uint32_t first[kWarps];
+    float wmax[kWarps];   // the first pass's maximum of each warp
+    float fscan[kWarps];
+    uint64_t scan[kWarps];
 };
 
-// Shared memory of a CTA: sub[4 nb] run maxima, bsum[nb] batch sums, bmass[nb]
-// and bties[nb] of the whole-row search, buf[kCap] candidates (or radix bins)
-// and wbuf[kCap] their weights.
+// Shared memory of a CTA.  buf[kCap] holds candidates or radix bins; wbuf[kCap]
+// their weights, and behind buf the rest of a bracket's tokens.  sub[4 nb] and
+// bsum[nb], the first pass's run maxima and batch sums, and bties[nb] of the
+// radix search are used when wbuf is not and share its space.  fine[kFine]: the
+// bins of a bracket, then the few tokens around its end.  bmass[nb] is the
+// batches' mass; while runs are read again the list of them lies there.
 struct Smem {
     Ctrl* c;
     uint64_t* buf;
     uint64_t* wbuf;
+    uint64_t* fine;
     uint64_t* bmass;
+    uint16_t* runs;
     uint32_t* bties;
     float* sub;
     float* bsum;
 };
 
 __host__ __device__ inline size_t ctrl_bytes() { return (sizeof(Ctrl) + 15) & ~(size_t)15; }
+__host__ __device__ inline size_t shared_space(int nb) {
+    const size_t first = sizeof(float) * (size_t)nb * (kRuns + 2), list = sizeof(uint64_t) * kCap;
+    return ((first > list ? first : list) + 15) & ~(size_t)15;
+}
 
 __device__ __forceinline__ Smem carve(unsigned char* p, int nb) {
     Smem s;
@@ -93,25 +142,34 @@ __device__ __forceinline__ Smem carve(unsigned char* p, int nb) {
     s.buf = reinterpret_cast<uint64_t*>(p);
     p += sizeof(uint64_t) * kCap;
     s.wbuf = reinterpret_cast<uint64_t*>(p);
-    p += sizeof(uint64_t) * kCap;
     s.sub = reinterpret_cast<float*>(p);  // 16-byte aligned: a batch's four maxima are stored at once
-    p += sizeof(float) * nb * kRuns;
+    s.bsum = s.sub + nb * kRuns;
+    s.bties = reinterpret_cast<uint32_t*>(s.bsum + nb);
+    p += shared_space(nb);
+    s.fine = reinterpret_cast<uint64_t*>(p);
+    p += sizeof(uint64_t) * kFine;
     s.bmass = reinterpret_cast<uint64_t*>(p);
-    p += sizeof(uint64_t) * nb;
-    s.bsum = reinterpret_cast<float*>(p);
-    p += sizeof(float) * nb;
-    s.bties = reinterpret_cast<uint32_t*>(p);
+    s.runs = reinterpret_cast<uint16_t*>(p);
     return s;
 }
 
 size_t smem_bytes(int nb) {
-    return ctrl_bytes() + sizeof(uint64_t) * (2 * kCap + nb) + sizeof(float) * (size_t)nb * (kRuns + 2);
+    return ctrl_bytes() + sizeof(uint64_t) * (kCap + kFine + (size_t)nb) + shared_space(nb);
 }
 
-// Sort buf[0, n) ascending (n <= kCap).  Short lists by rank (every thread
+// 64-bit sum in shared memory by two native 32-bit atomics: the carry of the
+// lower half goes into the upper one.
+__device__ __forceinline__ void shared_add(uint64_t* p, uint64_t v) {
+    uint32_t* half = reinterpret_cast<uint32_t*>(p);
+    const uint32_t lo = (uint32_t)v, old = atomicAdd(half, lo);
+    const uint32_t hi = (uint32_t)(v >> 32) + (old + lo < old ? 1u : 0u);
+    if (hi) atomicAdd(half + 1, hi);
+}
+
+// Sort buf[0, n) ascending (n <= kBracketCap).  Short lists by rank (every thread
 // counts the smaller ones, broadcast reads, two barriers), longer ones by a
 // bitonic network padded to a power of two.
-__device__ void sort_u64(uint64_t* buf, int n) {
+__device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
     if (n <= kThreads) {
         const int i = threadIdx.x;
         const uint64_t v = i < n ? buf[i] : 0;
@@ -146,71 +204,131 @@ __device__ void sort_u64(uint64_t* buf, int n) {
 __device__ __forceinline__ uint64_t candidate(float z, uint32_t i) { return ((uint64_t)(~key_of(z)) << 32) | i; }
 __device__ __forceinline__ float candidate_value(uint64_t c) { return key_value(~(uint32_t)(c >> 32)); }
 
-// The k-th largest of the n floats of `sub` (-inf when n < k), by 8-bit radix
-// passes over their keys; bins is kThreads words of scratch.
-__device__ float kth_largest(const float* sub, int n, int k, uint32_t* bins, Ctrl* c) {
+// A threshold that at least k of the n floats of `sub` reach and few more
+// (-inf when fewer than k are finite).  Each step cuts the interval into nine:
+// warp w counts what reaches the w-th inner border, so a step is one look at
+// `sub` and one barrier, and three or four steps bring the count within a
+// quarter of k.
+__device__ float threshold_for(const float* sub, int n, int k, float m, Ctrl* c) {
     if (n < k) return -INFINITY;
-    uint32_t prefix = 0, left = (uint32_t)k;
-    const int t = threadIdx.x;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        bins[t] = 0;
-        __syncthreads();
-        for (int i = t; i < n; i += kThreads) {
-            const uint32_t key = key_of(sub[i]);
-            if (shift == 24 || (key >> (shift + 8)) == prefix) atomicAdd(&bins[(key >> shift) & 255u], 1u);
-        }
-        __syncthreads();
-        // thread t looks at bin 255 - t: the counts above it come from the scan
-        uint64_t total;
-        const uint32_t mine = bins[255 - t];
-        const uint64_t before = block_scan(mine, c->scan, total);
-        if (before < left && before + mine >= left) {
-            c->prefix = (prefix << 8) | (uint32_t)(255 - t);
-            c->above = before;
-        }
-        __syncthreads();
-        prefix = c->prefix;
-        left -= (uint32_t)c->above;
-        __syncthreads();
+    if (k == 1) return m;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float lo = m;
+    int at = 0;  // how many reach lo
+    for (int i = lane; i < n; i += 32) {  // every warp for itself
+        const float x = sub[i];
+        at += x > -INFINITY;
+        if (x > -INFINITY) lo = fminf(lo, x);
     }
-    return key_value(prefix);
+    lo = -warp_max_nan(-lo);
+    at = __reduce_add_sync(DLM_FULL_MASK, at);
+    if (at < k) return -INFINITY;
+    float hi = m;
+    const int most = k + max(8, k / 4);
+    for (int step = 0; step < 12 && at > most; ++step) {
+        const float width = (hi - lo) * (1.f / (kWarps + 1));
+        const float mid = lo + width * (float)(warp + 1);
+        int h = 0;
+        for (int i = lane; i < n; i += 32) h += sub[i] >= mid;
+        h = __reduce_add_sync(DLM_FULL_MASK, h);
+        if (lane == 0) c->hits[step & 1][warp] = h;
+        __syncthreads();
+        const float base = lo;
+        int top = -1;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const int hw = c->hits[step & 1][w];
+            if (hw >= k) top = w, at = hw;
+        }
+        if (top >= 0) lo = base + width * (float)(top + 1);
+        if (top < kWarps - 1) hi = base + width * (float)(top + 2);
+        if (!(width > 0.f)) break;
+    }
+    __syncthreads();
+    return lo;
 }
 
-// Push the elements z >= least of batches [b0, b1) into the list dst, its
-// length in *count (both may be another CTA's of the cluster).  With `sub`,
-// runs whose maximum is below `least` are skipped unread.
+// Push the elements z >= least of one loaded vector of each lane (positions
+// from pos0 on) into the list dst of `cap` entries, its length in *count.
 template <int DT>
-__device__ void gather(const char* row, int64_t V, int b0, int b1, const float* sub, float least, uint64_t* dst,
-                       uint32_t* count) {
+__device__ __forceinline__ void push(uint4 w, uint32_t pos0, float least, float below, uint64_t* dst, uint32_t cap,
+                                     uint32_t* count) {
     constexpr int EPV = Row<DT>::EPV;
+    const int lane = threadIdx.x & 31;
+    float z[EPV];
+    Row<DT>::unpack(w, z);
+    uint32_t mine = 0;
+#pragma unroll
+    for (int e = 0; e < EPV; ++e) mine |= (uint32_t)(z[e] >= least && z[e] < below && z[e] > -INFINITY) << e;
+    if (!__any_sync(DLM_FULL_MASK, mine != 0)) return;
+    const int n = __popc(mine);
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(DLM_FULL_MASK, inc, o);
+        if (lane >= o) inc += x;
+    }
+    uint32_t base = 0;
+    if (lane == 31) base = atomicAdd(count, (uint32_t)inc);
+    base = __shfl_sync(DLM_FULL_MASK, base, 31) + (uint32_t)(inc - n);
+    if (mine) {
+#pragma unroll
+        for (int e = 0; e < EPV; ++e)
+            if ((mine >> e) & 1u) {
+                if (base < cap) dst[base] = candidate(z[e], pos0 + (uint32_t)e);
+                ++base;
+            }
+    }
+}
+
+// The elements z >= least of the whole row into buf (c->count of them, which
+// may exceed kCap): the runs whose maximum reaches it are listed first, then
+// each warp reads four of them at a time.
+template <int DT>
+__device__ void gather_runs(const char* row, int64_t V, int nsub, const Smem& s, float least) {
+    constexpr int EPV = Row<DT>::EPV;
+    constexpr int kAhead = 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Ctrl* c = s.c;
+    if (threadIdx.x == 0) c->runs = c->count = 0;
+    __syncthreads();
+    for (int i0 = warp * 32; i0 < nsub; i0 += kThreads) {
+        const int i = i0 + lane;
+        const bool hit = i < nsub && s.sub[i] >= least;
+        const uint32_t who = __ballot_sync(DLM_FULL_MASK, hit);
+        if (!who) continue;
+        uint32_t base = 0;
+        if (lane == 0) base = atomicAdd(&c->runs, (uint32_t)__popc(who));
+        base = __shfl_sync(DLM_FULL_MASK, base, 0);
+        if (hit) s.runs[base + __popc(who & ((1u << lane) - 1u))] = (uint16_t)i;
+    }
+    __syncthreads();
+    const int n = (int)c->runs;
+    for (int i = warp; i < n; i += kWarps * kAhead) {
+        uint4 w[kAhead];
+        int v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int at = i + j * kWarps;
+            v[j] = at < n ? (int)s.runs[at] * 32 + lane : -1;
+            if (at < n) w[j] = load_vec<DT>(row, V, v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (v[j] >= 0) push<DT>(w[j], (uint32_t)(v[j] * EPV), least, INFINITY, s.buf, kCap, &c->count);
+    }
+    __syncthreads();
+}
+
+// The same over every run of batches [b0, b1), into a list that may be
+// another CTA's of the cluster.
+template <int DT>
+__device__ __noinline__ void gather_slice(const char* row, int64_t V, int b0, int b1, float least, uint64_t* dst,
+                                          uint32_t* count) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int s = b0 * kRuns + warp; s < b1 * kRuns; s += kWarps) {
-        if (sub && !(sub[s] >= least)) continue;
         const int v = s * 32 + lane;
-        float z[EPV];
-        Row<DT>::unpack(load_vec<DT>(row, V, v), z);
-        int mine = 0;
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) mine += z[e] >= least && z[e] > -INFINITY;
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(DLM_FULL_MASK, inc, o);
-            if (lane >= o) inc += x;
-        }
-        uint32_t base = 0;
-        const int all = __shfl_sync(DLM_FULL_MASK, inc, 31);
-        if (all == 0) continue;
-        if (lane == 0) base = atomicAdd(count, (uint32_t)all);
-        base = __shfl_sync(DLM_FULL_MASK, base, 0) + (uint32_t)(inc - mine);
-        if (mine) {
-#pragma unroll
-            for (int e = 0; e < EPV; ++e)
-                if (z[e] >= least && z[e] > -INFINITY) {
-                    if (base < (uint32_t)kCap) dst[base] = candidate(z[e], (uint32_t)(v * EPV + e));
-                    ++base;
-                }
-        }
+        push<DT>(load_vec<DT>(row, V, v), (uint32_t)(v * Row<DT>::EPV), least, INFINITY, dst, kCap, count);
     }
 }
 
@@ -218,13 +336,13 @@ __device__ void gather(const char* row, int64_t V, int b0, int b1, const float* 
 
 // Run maxima of batches [b0, b1), and with `sums` each batch's sum of
 // 2^((z - ref) c), ref the batch's maximum (a batch of -inf only sums to 0).
+// The next batch is loaded while one is summed.  Returns the warp's maximum.
 template <int DT>
-__device__ __forceinline__ void scan_rows(const char* row, int64_t V, int b0, int b1, bool sums, float c, float* sub,
-                                          float* bsum) {
+__device__ __forceinline__ float scan_rows(const char* row, int64_t V, int b0, int b1, bool sums, float c, float* sub,
+                                           float* bsum) {
     constexpr int EPV = Row<DT>::EPV;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int b = b0 + warp; b < b1; b += kWarps) {
-        uint4 w[kRuns];
+    auto fetch = [&](int b, uint4 (&w)[kRuns]) {
         const int v0 = b * kBatchVecs + lane;
         if ((int64_t)(b + 1) * kBatchVecs * EPV <= V) {
 #pragma unroll
@@ -233,12 +351,22 @@ __device__ __forceinline__ void scan_rows(const char* row, int64_t V, int b0, in
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) w[i] = load_vec<DT>(row, V, v0 + i * 32);
         }
+    };
+    float most = -INFINITY;
+    uint4 next[kRuns];
+    if (b0 + warp < b1) fetch(b0 + warp, next);
+    for (int b = b0 + warp; b < b1; b += kWarps) {
+        uint4 w[kRuns];
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) w[i] = next[i];
+        if (b + kWarps < b1) fetch(b + kWarps, next);
         float m[kRuns];
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) m[i] = warp_max_nan(Row<DT>::vmax(w[i]));
         if (lane == 0) *reinterpret_cast<float4*>(sub + b * kRuns) = make_float4(m[0], m[1], m[2], m[3]);
-        if (!sums) continue;
         const float ref = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+        most = max_nan(most, ref);
+        if (!sums) continue;
         const float r = ref > -INFINITY ? ref : 0.f;  // -inf - 0 stays -inf: weight 0
         const f2 r2 = pack2(r, r), c2 = pack2(c, c);
         f2 acc[kRuns];
@@ -260,6 +388,7 @@ __device__ __forceinline__ void scan_rows(const char* row, int64_t V, int b0, in
         for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(DLM_FULL_MASK, s, o);
         if (lane == 0) bsum[b] = s;
     }
+    return most;
 }
 
 // A batch's sum relative to the row's maximum, in units of 2^-44.
@@ -272,27 +401,111 @@ __device__ __forceinline__ uint64_t batch_mass(const float* sub, const float* bs
 // ---- candidates ------------------------------------------------------------
 
 // Writes the row's token (thread-wise: the one thread that found it).
-template <int DT>
-__device__ __forceinline__ void write_token(const RowSearchArgs& a, const Ctrl* c, const char* row, int64_t o,
-                                            int token, uint64_t mass) {
-    const float z = Row<DT>::scalar(row, token);
+__device__ __forceinline__ void write_token(const RowSearchArgs& a, const Ctrl* c, int64_t o,
+                                            int token, float z, uint64_t mass) {
     float lo;
     const float y = weight_exponent(z, c->ws, lo);
     // 2^-(y + lo) over the kept mass
     const float w = exp2f(-y) * fmaf(lo, -kLn2, 1.0f);
-    a.token[o] = token;
-    a.prob[o] = y < INFINITY ? fminf(1.0f, w / ((float)mass * 5.684341886080802e-14f)) : 0.f;
+    *(volatile int32_t*)(a.token + o) = token;
+    __threadfence();  // the token first: open_rows_kernel takes prob only while the mark stands
+    a.prob[o] = y < INFINITY ? fminf(1.0f, w / ((float)mass * 0x1p-44f)) : 0.f;
     if (a.conf) a.conf[o] = expf(z - a.lse_in[o]);
 }
 
-// How many of the N sorted candidates stay, and their mass.  K: candidates
-// under the top-k (N when it is off).  `complete`: the list holds every token
-// that any filter could keep; otherwise the row's mass is known only as
-// total +- margin, the list holds its N largest tokens, and the result is -1
-// when that does not decide.
-__device__ void keep_candidates(const Smem& s, int K, bool complete) {
+// A list's contract with the filters.
+struct ListRule {
+    int k;            // top-k (the list's length when it is off)
+    bool complete;    // every token that top-k and min-p could keep is listed, and
+                      // the mass that top_p is a share of is the k largest's; else
+                      // it is c->total +- c->margin
+    bool all_least;   // every token with a weight >= c->least is listed
+};
+
+// The nucleus' target mass, as the two ends of what it may be.
+__device__ __forceinline__ void nucleus_target(const Ctrl* c, const ListRule& rule, uint64_t listed, uint64_t& lo,
+                                               uint64_t& hi) {
+    const uint64_t e = rule.complete ? 0 : c->margin, s = rule.complete ? listed : c->total;
+    const float p = c->top_p;
+    lo = p < 1.f ? scale_ceil(s - e, p) : ~0ull;
+    hi = p < 1.f ? scale_ceil(s + e, p) : ~0ull;
+}
+
+// The row's token from a list of at most kThreads candidates, one thread each
+// and no sort: a candidate's rank and the mass before it are sums over the
+// list.  False when the list does not decide.
+__device__ bool decide_small(const RowSearchArgs& a, const Smem& s, int n, ListRule rule, int64_t o) {
     Ctrl* c = s.c;
-    const int t = threadIdx.x;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const uint64_t mine = t < n ? s.buf[t] : ~0ull;
+    const uint64_t w = t < n ? weight44(candidate_value(mine), c->ws) : 0ull;
+    if (t < n) s.wbuf[t] = w;
+    __syncthreads();
+    uint64_t before = 0;
+    int rank = 0;
+    if (t < n) {
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const bool less = s.buf[j] < mine;
+            rank += less;
+            before += less ? s.wbuf[j] : 0ull;
+        }
+    }
+    const bool in_k = t < n && rank < rule.k;
+    uint64_t listed;
+    block_scan(in_k ? w : 0ull, c->scan, listed);
+    uint64_t lo, hi;
+    nucleus_target(c, rule, listed, lo, hi);
+    const bool pass = in_k && w >= c->least;
+    const bool stays = pass && before < hi;
+    // bit 0: the nucleus ends inside the list, for every target it may have;
+    // bit 1: a min-p token may lie past the nucleus' end; bit 2: min-p ends
+    // inside the list
+    int flags = (in_k && before < lo && before + w >= hi ? 1 : 0) | (pass && before >= lo ? 2 : 0) |
+                (in_k && w < c->least ? 4 : 0);
+    flags = __reduce_or_sync(DLM_FULL_MASK, flags);
+    const int kept_here = __popc(__ballot_sync(DLM_FULL_MASK, stays));
+    uint32_t first = __reduce_min_sync(DLM_FULL_MASK, stays ? (uint32_t)mine : 0xffffffffu);
+    if (lane == 0) {
+        c->hits[0][warp] = flags;
+        c->hits[1][warp] = kept_here;
+        c->first[warp] = first;
+    }
+    if (t < n) s.wbuf[t] = stays ? w : 0ull;
+    uint64_t mass;
+    block_scan(stays ? w : 0ull, c->scan, mass);
+    flags = 0;
+    int kept = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        flags |= c->hits[0][i];
+        kept += c->hits[1][i];
+        first = min(first, c->first[i]);
+    }
+    if (!rule.complete && !(flags & 1) && ((flags & 2) || !(rule.all_least || (flags & 4)))) return false;
+    if (kept == 1) {
+        if (stays) write_token(a, c, o, (int)(uint32_t)mine, candidate_value(mine), mass);
+        return true;
+    }
+    if (stays) {
+        bool cut;
+        const uint64_t target = scale_floor(mass, c->u, cut);
+        const uint32_t i = (uint32_t)mine;
+        uint64_t run = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) run += (uint32_t)s.buf[j] < i ? s.wbuf[j] : 0ull;
+        // u = 0: the first kept position, however small its weight
+        if (c->u == 0.f ? i == first : (run <= target && target < run + w))
+            write_token(a, c, o, (int)i, candidate_value(s.buf[t]), mass);
+    }
+    return true;
+}
+
+// How many of the n sorted candidates of a longer list stay (c->n, or -1 when
+// the list does not decide), and their mass.
+__device__ __noinline__ void keep_candidates(const Smem& s, int n, ListRule rule) {
+    Ctrl* c = s.c;
+    const int t = threadIdx.x, K = min(n, rule.k);
     const int per = (K + kThreads - 1) / kThreads, i0 = min(K, t * per), i1 = min(K, i0 + per);
     uint64_t sum = 0;
     for (int i = i0; i < i1; ++i) {
@@ -300,77 +513,57 @@ __device__ void keep_candidates(const Smem& s, int K, bool complete) {
         s.wbuf[i] = w;
         sum += w;
     }
-    if (t == 0) c->n = K;
-    uint64_t total;
-    const uint64_t before = block_scan(sum, c->scan, total);  // (its barriers order c->n too)
-    const float p = c->top_p;
-    // the nucleus: the shortest prefix whose mass reaches p of the total
-    if (p < 1.0f) {
-        const uint64_t lo = complete ? total : c->total - c->margin, hi = complete ? total : c->total + c->margin;
-        const uint64_t x_lo = scale_ceil(lo, p), x_hi = scale_ceil(hi, p);
-        if (!complete && total < x_hi) {
-            if (t == 0) c->n = -1;
-        } else {
-            uint64_t m = before;
-            for (int i = i0; i < i1; ++i) {
-                const uint64_t next = m + s.wbuf[i];
-                // x_hi is reached first here; x_lo must be too
-                if (m < x_hi && next >= x_hi) c->n = m < x_lo ? i + 1 : -1;
-                m = next;
-            }
-        }
-    } else if (!complete && t == 0) {
-        c->n = -1;
+    if (t == 0) {
+        c->n = c->top_p < 1.f ? -1 : K;
+        c->batch = 0;
     }
-    __syncthreads();
-    // min-p: a prefix too; the last candidate that passes ends it
-    const float least = c->z_least;
+    uint64_t listed;
+    const uint64_t before = block_scan(sum, c->scan, listed);  // (its barriers order c->n too)
+    uint64_t lo, hi;
+    nucleus_target(c, rule, listed, lo, hi);
+    // the nucleus: the shortest prefix whose mass reaches the target
+    uint64_t m = before;
     int last = -1;
-    for (int i = i0; i < i1; ++i)
-        if (candidate_value(s.buf[i]) >= least) last = i;
-    if (last >= 0 && (last + 1 == K || candidate_value(s.buf[last + 1]) < least)) c->batch = last + 1;
+    for (int i = i0; i < i1; ++i) {
+        const uint64_t w = s.wbuf[i];
+        if (c->top_p < 1.f && m < lo && m + w >= hi) c->n = i + 1;
+        // min-p keeps a prefix too, and the last token that passes ends it
+        if (w >= c->least) last = i;
+        m += w;
+    }
+    if (last >= 0) atomicMax(&c->batch, last + 1);
     __syncthreads();
     const int n_min = c->batch;
-    if (t == 0) {
-        if (c->n < 0) {
-            // the nucleus is not known, but min-p may cut inside the list and
-            // well before the nucleus ends
-            if (!complete && n_min < K) c->left = 1; else c->left = 0;
-        } else if (n_min < c->n) {
-            c->n = n_min;
-        }
+    // min-p ends the row when its last token surely belongs to the nucleus
+    const bool inside = rule.complete || rule.all_least || n_min < K;
+    bool by_min = false;
+    m = before;
+    for (int i = i0; i < i1; ++i) {
+        by_min |= i == n_min - 1 && inside && m < lo;
+        m += s.wbuf[i];
     }
+    by_min = __syncthreads_or(by_min);
+    if (t == 0 && by_min && (c->n < 0 || n_min < c->n)) c->n = n_min;
     __syncthreads();
-    if (c->n < 0 && c->left) {
-        const uint64_t x_lo = p < 1.0f ? scale_ceil(c->total - c->margin, p) : ~0ull;
-        uint64_t m = before;
-        for (int i = i0; i < i1; ++i) {
-            if (i == n_min - 1 && m < x_lo) c->n = n_min;  // the last kept token belongs to the nucleus
-            m += s.wbuf[i];
-        }
-    }
-    __syncthreads();
-    const int n = c->n;
-    if (n > 0) {
-        uint64_t m = before;
-        for (int i = i0; i < i1; ++i) {
-            m += s.wbuf[i];
-            if (i == n - 1) c->mass = m;
-        }
+    const int kept = c->n;
+    m = before;
+    for (int i = i0; i < i1; ++i) {
+        m += s.wbuf[i];
+        if (i == kept - 1) c->mass = m;
     }
     __syncthreads();
 }
 
 // The token among the first n candidates, in vocabulary order.
 template <int DT>
-__device__ void pick_candidate(const RowSearchArgs& a, const Smem& s, int n, const char* row, int64_t o) {
+__device__ __noinline__ void pick_candidate(const RowSearchArgs& a, const Smem& s, int n, const char* row, int64_t o) {
     Ctrl* c = s.c;
     const int t = threadIdx.x;
     const uint64_t mass = c->mass;
     bool cut;
     const uint64_t target = scale_floor(mass, c->u, cut);
     if (n == 1) {
-        if (t == 0) write_token<DT>(a, c, row, o, (int)(uint32_t)s.buf[0], mass);
+        if (t == 0) write_token(a, c, o, (int)(uint32_t)s.buf[0], candidate_value(s.buf[0]), mass);
         return;
     }
     const bool first = c->u == 0.0f;  // the first kept position, however small its weight
@@ -385,7 +578,7 @@ __device__ void pick_candidate(const RowSearchArgs& a, const Smem& s, int n, con
                 less += b;
             }
             if (first ? less == 0 : (before <= target && target < before + s.wbuf[t]))
-                write_token<DT>(a, c, row, o, (int)i, mass);
+                write_token(a, c, o, (int)i, candidate_value(s.buf[t]), mass);
         }
         return;
     }
@@ -398,7 +591,7 @@ __device__ void pick_candidate(const RowSearchArgs& a, const Smem& s, int n, con
     uint64_t m = block_scan(sum, c->scan, total);
     for (int i = i0; i < i1; ++i) {
         const uint64_t next = m + s.wbuf[(uint32_t)s.buf[i]];
-        if (first ? i == 0 : (m <= target && target < next)) write_token<DT>(a, c, row, o, (int)(s.buf[i] >> 32), mass);
+        if (first ? i == 0 : (m <= target && target < next)) write_token(a, c, o, (int)(s.buf[i] >> 32), Row<DT>::scalar(row, (int64_t)(s.buf[i] >> 32)), mass);
         m = next;
     }
 }
@@ -410,7 +603,7 @@ __device__ void pick_candidate(const RowSearchArgs& a, const Smem& s, int n, con
 // (MASS false) or the mass (true) of the elements whose key has the bits
 // `prefix` above shift + 11 and b below.  lo / hi: the two 32-bit halves.
 template <int DT, bool MASS>
-__device__ void radix_pass(const char* row, int64_t V, int b0, int b1, uint32_t prefix, int shift, int bits,
+__device__ __noinline__ void radix_pass(const char* row, int64_t V, int b0, int b1, uint32_t prefix, int shift, int bits,
                            uint32_t floor_key, const WeightScale& ws, uint32_t* lo, uint32_t* hi) {
     constexpr int EPV = Row<DT>::EPV;
     for (int i = threadIdx.x; i < kBins; i += kThreads) lo[i] = hi[i] = 0;
@@ -443,7 +636,7 @@ __device__ void radix_pass(const char* row, int64_t V, int b0, int b1, uint32_t 
 // CTA's ctrl: prefix (with the bin appended), above (before the bin), and
 // total (the sum of all bins) -- left unchanged but for total when no bin
 // reaches it.  kThreads threads, kBins / kThreads bins each.
-__device__ void radix_pick(const Cluster& cl, const Smem& s, uint32_t prefix, int bits, uint64_t above,
+__device__ __noinline__ void radix_pick(const Cluster& cl, const Smem& s, uint32_t prefix, int bits, uint64_t above,
                            uint64_t target) {
     cl.sync();
     if (cl.rank == 0) {
@@ -486,7 +679,7 @@ __device__ __forceinline__ int radix_bits(int l) { return l == 2 ? 10 : 11; }
 // When the keys at or above a bin fit the candidate list the search stops
 // there: *list is set and the result is that bin's lower edge.
 template <int DT>
-__device__ void count_cut(const Cluster& cl, const Smem& s, const char* row, int64_t V, int b0, int b1, int k,
+__device__ __noinline__ void count_cut(const Cluster& cl, const Smem& s, const char* row, int64_t V, int b0, int b1, int k,
                           const WeightScale& ws, uint32_t& key, uint32_t& ties, bool& list) {
     uint32_t* lo = reinterpret_cast<uint32_t*>(s.buf);
     const Ctrl* c0 = cl.at(s.c, 0);
@@ -521,7 +714,7 @@ __device__ void count_cut(const Cluster& cl, const Smem& s, const char* row, int
 // Top-p over the keys above floor_key plus floor_ties positions at it: the
 // key at which the mass reaches p of the total, and how many positions there.
 template <int DT>
-__device__ void mass_cut(const Cluster& cl, const Smem& s, const char* row, int64_t V, int b0, int b1, float p,
+__device__ __noinline__ void mass_cut(const Cluster& cl, const Smem& s, const char* row, int64_t V, int b0, int b1, float p,
                          uint32_t floor_key, uint32_t floor_ties, const WeightScale& ws, uint32_t& key,
                          uint32_t& ties) {
     uint32_t* lo = reinterpret_cast<uint32_t*>(s.buf);
@@ -554,10 +747,11 @@ __device__ void mass_cut(const Cluster& cl, const Smem& s, const char* row, int6
     ties = (uint32_t)((target - above + w - 1) / w);
 }
 
-// Mass of the keys above cut_key and the number of positions at it, per batch.
+// Mass of the keys above cut_key with a weight of at least `least`, and the
+// number of positions at cut_key, per batch.
 template <int DT>
-__device__ void batch_masses(const char* row, int64_t V, int b0, int b1, uint32_t cut_key, const WeightScale& ws,
-                             uint64_t* bmass, uint32_t* bties) {
+__device__ __noinline__ void batch_masses(const char* row, int64_t V, int b0, int b1, uint32_t cut_key, uint64_t least,
+                                          const WeightScale& ws, uint64_t* bmass, uint32_t* bties) {
     constexpr int EPV = Row<DT>::EPV;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int b = b0 + warp; b < b1; b += kWarps) {
@@ -569,7 +763,10 @@ __device__ void batch_masses(const char* row, int64_t V, int b0, int b1, uint32_
 #pragma unroll
             for (int e = 0; e < EPV; ++e) {
                 const uint32_t key = key_of(z[e]);
-                if (key > cut_key) m += weight44(z[e], ws);
+                if (key > cut_key) {
+                    const uint64_t w = weight44(z[e], ws);
+                    m += w >= least ? w : 0ull;
+                }
                 ties += key == cut_key;
             }
         }
@@ -589,104 +786,95 @@ __device__ void find_batch(const Smem& s, int nb, uint64_t w_tie, uint32_t cut_t
     Ctrl* c = s.c;
     const int t = threadIdx.x;
     const int per = (nb + kThreads - 1) / kThreads, b0 = min(nb, t * per), b1 = min(nb, b0 + per);
-    uint64_t n = 0, total;
-    for (int b = b0; b < b1; ++b) n += s.bties[b];
-    const uint64_t ties0 = block_scan(n, c->scan, total);
-    uint64_t ties = ties0, m = 0;
-    for (int b = b0; b < b1; ++b) {
-        const uint64_t room = ties < cut_ties ? cut_ties - ties : 0;
-        m += s.bmass[b] + min((uint64_t)s.bties[b], room) * w_tie;
-        ties += s.bties[b];
+    uint64_t ties0 = 0;
+    if (w_tie) {
+        uint64_t n = 0, total;
+        for (int b = b0; b < b1; ++b) n += s.bties[b];
+        ties0 = block_scan(n, c->scan, total);
     }
+    auto tie_mass = [&](int b, uint64_t& ties) {
+        if (!w_tie) return (uint64_t)0;
+        const uint64_t room = ties < cut_ties ? cut_ties - ties : 0;
+        ties += s.bties[b];
+        return min((uint64_t)s.bties[b], room) * w_tie;
+    };
+    uint64_t ties = ties0, m = 0;
+    for (int b = b0; b < b1; ++b) m += s.bmass[b] + tie_mass(b, ties);
     uint64_t mass;
     uint64_t before = block_scan(m, c->scan, mass);
     bool cut;
     const uint64_t target = scale_floor(mass, c->u, cut);
     ties = ties0;
     for (int b = b0; b < b1; ++b) {
-        const uint64_t room = ties < cut_ties ? cut_ties - ties : 0;
-        const uint64_t here = s.bmass[b] + min((uint64_t)s.bties[b], room) * w_tie;
+        const uint32_t ties_here = (uint32_t)ties;
+        const uint64_t here = s.bmass[b] + tie_mass(b, ties);
         if (before <= target && target < before + here) {
             c->batch = b;
             c->left = target - before;
-            c->ties_before = (uint32_t)ties;
+            c->ties_before = ties_here;
         }
         before += here;
-        ties += s.bties[b];
     }
     if (t == 0) c->mass = mass;
     __syncthreads();
 }
 
-// One warp walks a batch in order to the element whose running kept mass
-// passes `left`; returns its position and the sums on both sides of it, or -1.
+// The whole CTA walks the chosen batch (ctrl: batch, left, cut_key, cut_ties,
+// cut_last, ties_before, least) to the element whose running kept mass passes
+// `left`: in ctrl, its position (token, -1 if there is none) and the sums on
+// both sides of it (lo_side, hi_side).  A thread takes 8 bytes of the batch.
 template <int DT>
-__device__ int walk_batch(const char* row, int64_t V, int b, uint64_t left, uint32_t cut_key, uint32_t cut_ties,
-                          uint32_t ties_before, const WeightScale& ws, uint64_t& lo_side, uint64_t& hi_side) {
-    constexpr int EPV = Row<DT>::EPV;
-    const int lane = threadIdx.x & 31;
-    uint64_t before = 0;
-    uint32_t ties = ties_before;
-    for (int i = 0; i < kRuns; ++i) {
-        const int v = b * kBatchVecs + i * 32 + lane;
-        float z[EPV];
-        Row<DT>::unpack(load_vec<DT>(row, V, v), z);
-        uint32_t mine = 0;
+__device__ __noinline__ void walk_batch(const char* row, int64_t V, Ctrl* c) {
+    constexpr int N = 8 / Row<DT>::ESZ;
+    static_assert(N * kThreads == kBatchVecs * Row<DT>::EPV, "a batch is 8 bytes per thread");
+    const int t = threadIdx.x;
+    const int64_t at = (int64_t)c->batch * (N * kThreads) + t * N;
+    const uint32_t cut_key = c->cut_key, cut_ties = c->cut_ties;
+    const WeightScale ws = c->ws;
+    float z[N];
 #pragma unroll
-        for (int e = 0; e < EPV; ++e) mine += key_of(z[e]) == cut_key;
-        uint32_t inc = mine;
+    for (int e = 0; e < N; ++e) z[e] = at + e < V ? Row<DT>::scalar(row, at + e) : -INFINITY;
+    if (t == 0) c->token = -1;
+    uint64_t rank = 0, sum = 0, all;
+    if (cut_ties != 0 && cut_ties != 0xffffffffu) {  // a tie's rank over the row decides
+        uint64_t mine = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(DLM_FULL_MASK, inc, o);
-            if (lane >= o) inc += x;
-        }
-        uint32_t rank = ties + inc - mine;
-        ties += __shfl_sync(DLM_FULL_MASK, inc, 31);
-        uint64_t w[EPV], sum = 0;
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            const uint32_t key = key_of(z[e]);
-            const bool tie = key == cut_key;
-            w[e] = key > cut_key || (tie && rank < cut_ties) ? weight44(z[e], ws) : 0ull;
-            rank += tie;
-            sum += w[e];
-        }
-        uint64_t run = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t x = __shfl_up_sync(DLM_FULL_MASK, run, o);
-            if (lane >= o) run += x;
-        }
-        uint64_t m = before + run - sum;
-        int found = -1;
-        uint64_t fl = 0, fh = 0;
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) {
-            if (m <= left && left < m + w[e]) {
-                found = v * EPV + e;
-                fl = m;
-                fh = m + w[e];
-            }
-            m += w[e];
-        }
-        before += __shfl_sync(DLM_FULL_MASK, run, 31);
-        const uint32_t who = __ballot_sync(DLM_FULL_MASK, found >= 0);
-        if (who) {
-            const int src = __ffs(who) - 1;
-            lo_side = __shfl_sync(DLM_FULL_MASK, fl, src);
-            hi_side = __shfl_sync(DLM_FULL_MASK, fh, src);
-            return __shfl_sync(DLM_FULL_MASK, found, src);
-        }
+        for (int e = 0; e < N; ++e) mine += key_of(z[e]) == cut_key;
+        rank = c->ties_before + block_scan(mine, c->scan, all);
     }
-    return -1;
+    uint64_t w[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const uint32_t key = key_of(z[e]);
+        const bool tie = key == cut_key;
+        const bool stays = key > cut_key || (tie && rank < cut_ties && (uint32_t)(at + e) <= c->cut_last);
+        w[e] = stays ? weight44(z[e], ws) : 0ull;
+        if (w[e] < c->least) w[e] = 0;
+        rank += tie;
+        sum += w[e];
+    }
+    uint64_t m = block_scan(sum, c->scan, all);
+    const uint64_t left = c->left;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (m <= left && left < m + w[e]) {
+            c->token = (int)(at + e);
+            c->z = z[e];
+            c->lo_side = m;
+            c->hi_side = m + w[e];
+        }
+        m += w[e];
+    }
+    __syncthreads();
 }
 
 // u = 0: the first kept position of the row, whatever its weight (one warp of
 // the first CTA; reads the row until it meets one).
 template <int DT>
-__device__ int first_kept(const char* row, int64_t V, int nb, uint32_t cut_key, uint32_t cut_ties) {
+__device__ __noinline__ int first_kept(const char* row, int64_t V, int nb, const Ctrl* c) {
     constexpr int EPV = Row<DT>::EPV;
     const int lane = threadIdx.x & 31;
+    const WeightScale ws = c->ws;
     for (int v0 = 0; v0 < nb * kBatchVecs; v0 += 32) {
         float z[EPV];
         Row<DT>::unpack(load_vec<DT>(row, V, v0 + lane), z);
@@ -694,7 +882,9 @@ __device__ int first_kept(const char* row, int64_t V, int nb, uint32_t cut_key, 
 #pragma unroll
         for (int e = EPV - 1; e >= 0; --e) {
             const uint32_t key = key_of(z[e]);
-            if (key > cut_key || (key == cut_key && cut_ties > 0)) e0 = e;
+            const bool in = key > c->cut_key || (key == c->cut_key && c->cut_ties > 0 &&
+                                                 (uint32_t)((v0 + lane) * EPV + e) <= c->cut_last);
+            if (in && (c->least == 0 || weight44(z[e], ws) >= c->least)) e0 = e;
         }
         const uint32_t who = __ballot_sync(DLM_FULL_MASK, e0 < EPV);
         if (who) {
@@ -705,9 +895,413 @@ __device__ int first_kept(const char* row, int64_t V, int nb, uint32_t cut_key, 
     return -1;
 }
 
+// ---- the nucleus by a bracket ------------------------------------------------
+
+// Two weights in 32 bits with a relative error below 6 * 2^-24: the exponent's
+// integer part goes into the float's exponent field exactly, ex2 sees the
+// fraction.  The logits must be within 100 powers of 2 of the maximum.
+struct SplitScale {
+    f2 m, nc_hi, nc_lo;  // the maximum, and minus log2(e) / T in two floats
+};
+__device__ __forceinline__ f2 weight_split(f2 z, const SplitScale& s) {
+    const f2 magic = pack2(12582912.0f, 12582912.0f);  // 1.5 * 2^23: rounds to an integer
+    const f2 d = sub2(s.m, z);
+    const f2 b = sub2(d, s.m);
+    const f2 err = sub2(sub2(s.m, sub2(d, b)), add2(z, b));
+    const f2 t = fma2(d, s.nc_hi, magic);
+    f2 f = fma2(d, s.nc_hi, sub2(magic, t));
+    f = fma2(d, s.nc_lo, f);
+    f = fma2(err, s.nc_hi, f);
+    float x, y, tx, ty;
+    unpack2(ex2x2(f), x, y);
+    unpack2(t, tx, ty);
+    return pack2(__int_as_float(__float_as_int(x) + (__float_as_int(tx) << 23)),
+                 __int_as_float(__float_as_int(y) + (__float_as_int(ty) << 23)));
+}
+
+// Two logits that the nucleus' end should lie between, from a sample of the
+// row: the mass below it is (1 - top_p) of the total, the sample's masses per
+// 1/32 of an exponent tell where the row's lower end adds up to that, and the
+// bracket takes the kBracketSide tokens on either side.  On a flat row of 152064
+// tokens that is three to four standard deviations of the sample; where few
+// tokens hold the mass it reaches up to the largest.  One CTA; sets c->bin_lo,
+// c->bin_hi.
+template <int DT>
+__device__ __noinline__ void place_bracket(const char* row, int64_t V, int nb, const Smem& s) {
+    constexpr int EPV = Row<DT>::EPV;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    Ctrl* c = s.c;
+    uint32_t* bins = reinterpret_cast<uint32_t*>(s.buf);
+    for (int i = t; i < kBins; i += kThreads) bins[i] = 0;
+    __syncthreads();
+    const int nsub = (int)((V + 32 * EPV - 1) / (32 * EPV));
+    const int n = min(nsub, kSampleTokens / (32 * EPV));
+    const float c32 = c->ws.c_hi * 32.f, m = c->ws.m;
+#pragma unroll 4
+    for (int i = warp; i < n; i += kWarps) {
+        const int run = (int)((int64_t)i * nsub / n);
+        float z[EPV];
+        Row<DT>::unpack(load_vec<DT>(row, V, run * 32 + lane), z);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+            if (!(z[e] > -INFINITY)) continue;
+            // a bin adds up its tokens' weights relative to its own upper end,
+            // in 2^-16 (between 0.97 and 1 each, so the sample's fit 32 bits)
+            const float x = (m - z[e]) * c32;
+            const int bin = min(kBins - 1, (int)x);
+            atomicAdd(&bins[bin], (uint32_t)(65536.f * ex2(fmaxf(((float)bin - x) * 0.03125f, -1.f))));
+        }
+    }
+    __syncthreads();
+    // thread t takes bins from the lowest weights up
+    constexpr int PER = kBins / kThreads;
+    const float scale = (float)nsub / (float)n;
+    float mass = 0.f;
+    uint64_t tokens = 0;  // in 2^-16, a little short
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int bin = kBins - 1 - (t * PER + j);
+        mass += (float)bins[bin] * 0x1p-16f * ex2(-(float)bin * 0.03125f);
+        tokens += bins[bin];
+    }
+    // exclusive sums over the threads in integers (a sample's mass is at most 2^14)
+    uint64_t all;
+    float run = (float)block_scan((uint64_t)__float2ull_rn(mass * 0x1p44f), c->scan, all) * 0x1p-44f;
+    uint64_t seen = block_scan(tokens, c->scan, all);
+    // the sample's share of the mass below the nucleus' end
+    const float want = (1.f - c->top_p) * ((float)c->total * 0x1p-44f) / scale;
+    if (t == 0) {  // for a sample that does not reach it
+        c->left = 0;
+        c->bin_lo = kBins;
+        c->bin_hi = 0;
+    }
+    __syncthreads();
+    const uint64_t seen0 = seen;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int bin = kBins - 1 - (t * PER + j);
+        const float next = run + (float)bins[bin] * 0x1p-16f * ex2(-(float)bin * 0.03125f);
+        if (run <= want && next > want) c->left = seen + bins[bin] / 2;
+        run = next;
+        seen += bins[bin];
+    }
+    __syncthreads();
+    const uint64_t mid = c->left, side = (uint64_t)((float)kBracketSide * 65536.f / scale);
+    seen = seen0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int bin = kBins - 1 - (t * PER + j);
+        const uint64_t next = seen + bins[bin];
+        if (mid > side && seen <= mid - side && next > mid - side) c->bin_lo = bin + 1;
+        if (seen < mid + side && next >= mid + side) c->bin_hi = bin;
+        seen = next;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void set_bracket(Ctrl* c) {
+    const float c32 = c->ws.c_hi * 32.f;
+    c->z_lo = c->ws.m - (float)c->bin_lo / c32;
+    c->z_hi = c->ws.m - (float)c->bin_hi / c32;
+    if (c->top_p >= 1.f) c->z_lo = c->z_hi = -INFINITY;  // everything is above: sums only
+    c->tries = 0;
+    c->count = 0;
+}
+
+// One pass over a slice: bmass[b] the mass of batch b at z >= z_hi, c->whole
+// the slice's whole mass, and the tokens of [z_lo, z_hi) into dst, c->count of
+// them (which may exceed kBracketCap).  EXACT: integer weights, else weight_split summed over a vector in 32 bits.
+template <int DT, bool EXACT>
+__device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, int b1, float z_lo, float z_hi,
+                                          const WeightScale ws, uint64_t* bmass, Ctrl* c, uint64_t* dst) {
+    constexpr int EPV = Row<DT>::EPV;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float z_min = fmaxf(ws.m - 99.f / ws.c_hi, -FLT_MAX);  // a weight of 2^-99 counts as 0
+    const SplitScale sp{pack2(ws.m, ws.m), pack2(-ws.c_hi, -ws.c_hi), pack2(-ws.c_lo, -ws.c_lo)};
+    uint64_t whole = 0, sum = 0;
+    for (int b = b0 + warp; b < b1; b += kWarps) {
+        uint64_t above = 0;
+        uint4 w4[kRuns];
+        const int v0 = b * kBatchVecs + lane;
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) w4[i] = load_vec<DT>(row, V, v0 + i * 32);
+        uint32_t mask = 0;  // tokens inside, a bit each
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            float z[EPV];
+            Row<DT>::unpack(w4[i], z);
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    const uint64_t w = weight44(z[e], ws);
+                    const bool up = z[e] >= z_hi;
+                    above += up ? w : 0ull;
+                    whole += w;
+                    mask |= (uint32_t)(!up && z[e] >= z_lo) << (i * EPV + e);
+                }
+            } else {
+                f2 up[EPV / 2], all[EPV / 2];
+#pragma unroll
+                for (int p = 0; p < EPV / 2; ++p) {
+                    const float x = fmaxf(z[2 * p], z_min), y = fmaxf(z[2 * p + 1], z_min);
+                    all[p] = weight_split(pack2(x, y), sp);
+                    float wx, wy;
+                    unpack2(all[p], wx, wy);
+                    const bool ux = x >= z_hi, uy = y >= z_hi;
+                    up[p] = pack2(ux ? wx : 0.f, uy ? wy : 0.f);
+                    mask |= (uint32_t)(!ux && x >= z_lo) << (i * EPV + 2 * p);
+                    mask |= (uint32_t)(!uy && y >= z_lo) << (i * EPV + 2 * p + 1);
+                }
+#pragma unroll
+                for (int h = EPV / 4; h; h >>= 1)
+#pragma unroll
+                    for (int p = 0; p < h; ++p) {
+                        up[p] = add2(up[p], up[p + h]);
+                        all[p] = add2(all[p], all[p + h]);
+                    }
+                above += __float2ull_rn(hsum2(up[0]) * 0x1p44f);
+                whole += __float2ull_rn(hsum2(all[0]) * 0x1p44f);
+            }
+        }
+        above = (uint64_t)warp_sum_ll((long long)above);
+        if (lane == 0) bmass[b] = above;
+        if (!__any_sync(DLM_FULL_MASK, mask != 0)) continue;
+        const int mine = __popc(mask);
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(DLM_FULL_MASK, inc, o);
+            if (lane >= o) inc += x;
+        }
+        uint32_t at = 0;
+        if (lane == 31) at = atomicAdd(&c->count, (uint32_t)inc);
+        at = __shfl_sync(DLM_FULL_MASK, at, 31) + (uint32_t)(inc - mine);
+        while (mask) {
+            const int bit = __ffs(mask) - 1;
+            mask &= mask - 1;
+            const int64_t pos = (int64_t)(v0 + (bit / EPV) * 32) * EPV + bit % EPV;
+            if (at < (uint32_t)kBracketCap) dst[at] = candidate(Row<DT>::scalar(row, pos), (uint32_t)pos);
+            ++at;
+        }
+    }
+    block_scan(whole, c->scan, sum);
+    if (threadIdx.x == 0) c->whole = sum;
+    __syncthreads();
+}
+
+// After a pass, in the first CTA: the kept set and the token.  Returns the
+// next verdict.  err: how far the pass's sums may be off, every weight by the
+// same share at most.  A sum over part of the mass and that part's share of
+// the whole then differ by 2 share (1 - share) err at most from what they
+// should.  The last tier's token stands whatever its distance from a border.
+template <int DT>
+__device__ __noinline__ int resolve_bracket(const RowSearchArgs& a, const Smem& s, const char* row, int64_t V, int nb,
+                                            int64_t o, uint64_t total, bool last_tier) {
+    constexpr int BEL = kBatchVecs * Row<DT>::EPV;
+    Ctrl* c = s.c;
+    const int t = threadIdx.x;
+    uint64_t v = 0, above;
+    for (int b = t; b < nb; b += kThreads) v += s.bmass[b];
+    block_scan(v, c->scan, above);
+    // integer weights 2^-37; else, in 2^-24, ex2 4, the fraction's roundings and
+    // the conversion 2, three levels of additions 3
+    const uint64_t err = last_tier ? (total >> 36) + (uint64_t)nb : (total >> 24) * 9 + (uint64_t)nb;
+    uint64_t slack = 0, sure = ~0ull;
+    // another bracket: above or below this one (with a quarter of it), or the
+    // middle of one that holds too many tokens
+    auto miss = [&](bool up, bool down) {
+        __syncthreads();
+        if (t == 0) {
+            const float lo = c->z_lo, hi = c->z_hi, width = fmaxf(hi - lo, 1e-6f * fabsf(hi));
+            if (up) {
+                c->z_lo = hi - 0.25f * width;
+                c->z_hi = hi + 2.f * width;
+            } else if (down) {
+                c->z_lo = lo - 2.f * width;
+                c->z_hi = lo + 0.25f * width;
+            } else {
+                c->z_lo = lo + 0.4f * width;
+                c->z_hi = hi - 0.4f * width;
+            }
+            c->tries += 1;
+        }
+        __syncthreads();
+        return c->tries < kTries ? (last_tier ? kTier2 : kTier1) : kRadix;
+    };
+    if (c->top_p < 1.f) {
+        const uint32_t n = c->count;
+        const uint64_t x = scale_ceil(total, c->top_p);
+        // 2 p (1 - p) err, rounded up
+        const uint64_t off = (uint64_t)((float)err * 2.0001f * c->top_p * (1.f - c->top_p)) + 2;
+        // the bracket holds the nucleus' end: what is above is short of the
+        // target, what is above and inside reaches it, and all of it is listed
+        if (above + off >= x) return miss(true, false);
+        if (n > (uint32_t)kBracketCap) return miss(false, false);
+        const uint64_t t_mid = x - above, t_lo = t_mid - off, t_hi = t_mid + off;
+        // the tokens into bins from z_hi down, with their mass
+        const float z_hi = c->z_hi, per_bin = (float)kFine / (c->z_hi - c->z_lo);
+        auto bin_of = [&](uint64_t e) { return max(0, min(kFine - 1, (int)((z_hi - candidate_value(e)) * per_bin))); };
+        for (int i = t; i < kFine; i += kThreads) s.fine[i] = 0;
+        if (t == 0) c->runs = 0;
+        __syncthreads();
+        for (int i0 = 0; i0 < (int)n; i0 += kThreads) {
+            // 16-bit logits repeat: equal ones of a warp are added once
+            const int i = i0 + t;
+            const uint64_t e = i < (int)n ? s.buf[i] : 0;
+            const uint32_t like = __match_any_sync(DLM_FULL_MASK, i < (int)n ? (uint32_t)(e >> 32) : 0xffffffffu);
+            if (i < (int)n && __ffs(like) - 1 == (t & 31))
+                shared_add(&s.fine[bin_of(e)], weight44(candidate_value(e), c->ws) * __popc(like));
+        }
+        __syncthreads();
+        constexpr int PER = kFine / kThreads;
+        uint64_t sum = 0, inside;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) sum += s.fine[t * PER + j];
+        uint64_t m = block_scan(sum, c->scan, inside);
+        if (inside < t_hi) return miss(false, true);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const uint64_t next = m + s.fine[t * PER + j];
+            if (m < t_lo && next >= t_lo) {
+                c->first_bin = t * PER + j;
+                c->left = m;
+            }
+            if (m < t_hi && next >= t_hi) c->last_bin = t * PER + j;
+            m = next;
+        }
+        __syncthreads();
+        // tokens before the first of the end's bins stay; those in the end's
+        // bins are put in order
+        const int f0 = c->first_bin, f1 = c->last_bin;
+        const uint64_t before_bin = c->left;
+        auto keep = [&](uint64_t e, uint64_t w) { shared_add(&s.bmass[(uint32_t)e / BEL], w); };
+        for (int i = t; i < (int)n; i += kThreads) {
+            const uint64_t e = s.buf[i];
+            const int bin = bin_of(e);
+            if (bin < f0) {
+                keep(e, weight44(candidate_value(e), c->ws));
+            } else if (bin <= f1) {
+                const uint32_t at = atomicAdd(&c->runs, 1u);
+                if (at < (uint32_t)kFine) s.fine[at] = e;
+            }
+        }
+        __syncthreads();
+        const int n2 = (int)c->runs;
+        if (n2 > kFine) return kRadix;
+        auto crossing = [&](uint64_t e, uint64_t m0, uint64_t w) {
+            const uint64_t next = m0 + w;
+            if (m0 < t_lo && next >= t_lo) {
+                c->sure = e;
+                c->sure_mass = next;
+            }
+            if (m0 < t_mid && next >= t_mid) {
+                c->cut_key = ~(uint32_t)(e >> 32);
+                c->cut_last = (uint32_t)e;
+                c->left = next;
+            }
+            if (m0 < t_hi && next >= t_hi) c->slack = next;
+            if (m0 < t_mid) keep(e, w);
+        };
+        if (n2 <= kThreads) {
+            const uint64_t mine = t < n2 ? s.fine[t] : ~0ull;
+            const uint64_t w = t < n2 ? weight44(candidate_value(mine), c->ws) : 0ull;
+            if (t < n2) s.buf[t] = w;
+            __syncthreads();
+            if (t < n2) {
+                uint64_t m0 = before_bin;
+#pragma unroll 4
+                for (int j = 0; j < n2; ++j) m0 += s.fine[j] < mine ? s.buf[j] : 0ull;
+                crossing(mine, m0, w);
+            }
+        } else {
+            sort_u64(s.fine, n2);
+            const int per = (n2 + kThreads - 1) / kThreads, i0 = min(n2, t * per), i1 = min(n2, i0 + per);
+            uint64_t mine = 0, all;
+            for (int i = i0; i < i1; ++i) mine += weight44(candidate_value(s.fine[i]), c->ws);
+            uint64_t m0 = before_bin + block_scan(mine, c->scan, all);
+            for (int i = i0; i < i1; ++i) {
+                const uint64_t w = weight44(candidate_value(s.fine[i]), c->ws);
+                crossing(s.fine[i], m0, w);
+                m0 += w;
+            }
+        }
+        if (t == 0) {
+            c->cut_ties = 0xffffffffu;
+            c->ties_before = 0;
+        }
+        __syncthreads();
+        sure = c->sure;
+        slack = max(c->slack - c->left, c->left - c->sure_mass);
+    } else if (t == 0) {
+        c->cut_key = kKeyNegInf;
+        c->cut_ties = 0;
+        c->cut_last = 0;
+        c->ties_before = 0;
+    }
+    __syncthreads();
+    find_batch(s, nb, 0, 0);
+    const bool first = c->u == 0.f;
+    if (!first) {
+        walk_batch<DT>(row, V, c);
+    } else {
+        if (t < 32) {
+            const int token = first_kept<DT>(row, V, nb, c);
+            if (t == 0) {
+                c->token = token;
+                c->z = token >= 0 ? Row<DT>::scalar(row, token) : 0.f;
+            }
+        }
+        __syncthreads();
+    }
+    // the token has to be further from its borders than the sums' error and
+    // the slack of the kept mass, to stay whichever token ends the nucleus, and
+    // prob to be within 2^-17
+    const uint64_t off = slack + err / 2 + 1;
+    bool done = c->token >= 0;
+    if (done && !last_tier)
+        done = slack <= (c->mass >> 17) && (first || (c->lo_side + off <= c->left && c->left + off < c->hi_side)) &&
+               candidate(c->z, (uint32_t)c->token) <= sure;
+    if (t == 0 && done) write_token(a, c, o, c->token, c->z, c->mass);
+    return done ? kDone : last_tier ? kRadix : kTier2;
+}
+
+// The first cut_ties positions at cut_key, after the c->count candidates that
+// buf holds (one warp).
+template <int DT>
+__device__ __noinline__ void first_ties(const char* row, int64_t V, int nb, uint32_t cut_key, uint32_t cut_ties,
+                                        uint64_t* buf, Ctrl* c) {
+    constexpr int EPV = Row<DT>::EPV;
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = c->count;
+    uint32_t found = 0;
+    for (int v0 = 0; v0 < nb * kBatchVecs && found < cut_ties; v0 += 32) {
+        float z[EPV];
+        Row<DT>::unpack(load_vec<DT>(row, V, v0 + lane), z);
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) mine += key_of(z[e]) == cut_key;
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(DLM_FULL_MASK, inc, o);
+            if (lane >= o) inc += x;
+        }
+        uint32_t rank = found + inc - mine;
+#pragma unroll
+        for (int e = 0; e < EPV; ++e)
+            if (key_of(z[e]) == cut_key) {
+                if (rank < cut_ties && base + rank < (uint32_t)kCap)
+                    buf[base + rank] = candidate(z[e], (uint32_t)((v0 + lane) * EPV + e));
+                ++rank;
+            }
+        found += __shfl_sync(DLM_FULL_MASK, inc, 31);
+    }
+    __syncwarp();
+    if (lane == 0) c->count = base + min(found, cut_ties);
+}
+
 // ---- the kernels -----------------------------------------------------------
 
-template <int DT>
 __device__ void write_topk(const RowSearchArgs& a, const Smem& s, int n, int64_t o) {
     for (int i = threadIdx.x; i < a.k; i += kThreads) {
         a.values[o * a.k + i] = i < n ? candidate_value(s.buf[i]) : -INFINITY;
@@ -715,281 +1309,225 @@ __device__ void write_topk(const RowSearchArgs& a, const Smem& s, int n, int64_t
     }
 }
 
-template <int DT, bool SAMPLE>
-__global__ void __launch_bounds__(kThreads) row_search_kernel(const RowSearchArgs a) {
-    extern __shared__ __align__(16) unsigned char s_raw[];
-    const int t = threadIdx.x;
-    Cluster cl;
-    cl.split = a.split;
-    const int64_t r = blockIdx.x / a.split;
-    cl.rank = (int)(blockIdx.x - r * a.split);
-    const int64_t q = a.row_index ? (int64_t)a.row_index[r] : r;
-    if (q < 0 || (a.n_src > 0 && q >= a.n_src)) {  // the same for every CTA of the cluster
-        if (cl.rank == 0 && t == 0) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
-        return;
-    }
-    const int64_t o = a.gather ? r : q;
-    const int64_t V = a.vocab;
-    const char* row = static_cast<const char*>(a.logits) + q * a.row_stride * Row<DT>::ESZ;
-    constexpr int BEL = kBatchVecs * Row<DT>::EPV;  // elements of a batch
-    const int nb = (int)((V + BEL - 1) / BEL);
-    const int per = (nb + a.split - 1) / a.split;
-    const int b0 = min(nb, cl.rank * per), b1 = min(nb, b0 + per);
-    const Smem s = carve(s_raw, nb);
+// The first CTA's decision after the first pass, from few candidates or from
+// the batch sums.  Returns the verdict.
+template <int DT>
+__device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem& s, const char* row, int64_t V, int nb,
+                                             int64_t o, bool whole) {
     Ctrl* c = s.c;
-
-    if (t == 0) {
-        float T = a.temperature, p = a.top_p, least = a.min_p;
-        int k = a.k;
-        bool bad = false;
-        if constexpr (SAMPLE) {
-            if (a.temperature_rows) T = a.temperature_rows[o];
-            if (a.top_k_rows) k = a.top_k_rows[o];
-            if (a.top_p_rows) p = a.top_p_rows[o];
-            if (a.min_p_rows) least = a.min_p_rows[o];
-            const float u = a.uniform[o];
-            bad = !(T == 0.f || (T >= DLM_MIN_TEMPERATURE && T <= FLT_MAX)) || k < 0 || !(p > 0.f && p <= 1.f) ||
-                  !(least >= 0.f && least <= 1.f) || !(u >= 0.f && u < 1.f);
-            c->u = u;
-            if (T == 0.f) k = 1, T = 1.f, p = 1.f, least = 0.f;  // the argmax
-            if (k >= V) k = 0;
+    const int t = threadIdx.x, nsub = nb * kRuns;
+    const int k = c->top_k;
+    const float p = c->top_p, m = c->ws.m;
+    const bool by_p = p < 1.f, by_least = c->least > 0;
+    // the smallest logit that min-p can keep (a little lower: the weights decide)
+    const float z_least = by_least ? m + (1.0001f * __logf(c->min_p) - 1e-5f) / (c->ws.c_hi * kLn2) - 1e-6f * fabsf(m)
+                                   : -INFINITY;
+    ListRule rule{k > 0 ? k : 0x7fffffff, true, true};
+    float least;
+    if (whole) {
+        least = -INFINITY;
+    } else if (k > 0) {
+        if (k > DLM_MAX_TOPK) return kRadix;
+        least = threshold_for(s.sub, nsub, k, m, c);
+        if (!(least > -INFINITY)) return kRadix;
+    } else if (by_least) {
+        least = z_least;
+        rule.complete = !by_p;
+    } else if (by_p) {
+        rule.complete = rule.all_least = false;
+        uint64_t lo, hi;
+        nucleus_target(c, rule, 0, lo, hi);
+        least = m;
+        if (hi > kOne) {  // more than the largest logit alone
+            least = threshold_for(s.sub, nsub, min(kListRuns, nb), m, c);
+            // what the runs' maxima hold of the nucleus: a list of the runs
+            // that is far short of it is not made
+            float v = 0.f;
+            if (least > -INFINITY)
+                for (int i = t; i < nsub; i += kThreads)
+                    if (s.sub[i] >= least) v += ex2((s.sub[i] - m) * c->ws.c_hi);
+            uint64_t held;
+            block_scan((uint64_t)__float2ull_rn(v * 17592186044416.0f), c->scan, held);
+            if (held + held / 2 < hi) return kTier1;
         }
-        c->bad = bad;
-        c->temperature = T;
-        c->top_k = k;
-        c->top_p = p;
-        c->z_least = least;  // min-p until the maximum is known
-        c->ws = weight_scale(0.f, bad ? 1.f : T);
-        c->done = 0;
-        c->count = 0;
-        c->batch = 0;
-    }
-    __syncthreads();
-    if (SAMPLE && c->bad) {
-        if (cl.rank == 0 && t == 0) {
-            a.token[o] = -1;
-            a.prob[o] = 0.f;
-            if (a.conf) a.conf[o] = 0.f;
-            raise_status(a.dev_status, DLM_DEV_BAD_PARAM);
-        }
-        return;
-    }
-    // a top-k within the candidate list needs no sums; min-p alone neither
-    const bool few = SAMPLE && c->top_k > 0 && c->top_k <= DLM_MAX_TOPK;
-    const bool whole = V <= kCap;  // every logit fits the list
-    const bool sums = !SAMPLE || (!few && !whole && (c->top_p < 1.f || c->z_least == 0.f));
-    scan_rows<DT>(row, V, b0, b1, sums, c->ws.c_hi, s.sub, s.bsum);
-    cl.sync();
-
-    if (cl.rank == 0) {
-        for (int rk = 1; rk < cl.split; ++rk) {  // the other slices' maxima and sums
-            const int x0 = min(nb, rk * per), x1 = min(nb, x0 + per);
-            const float* rs = cl.at(s.sub, rk);
-            const float* rb = cl.at(s.bsum, rk);
-            for (int i = x0 * kRuns + t; i < x1 * kRuns; i += kThreads) s.sub[i] = rs[i];
-            if (sums)
-                for (int i = x0 + t; i < x1; i += kThreads) s.bsum[i] = rb[i];
-        }
-        __syncthreads();
-        float m = -INFINITY;
-        for (int i = t; i < nb * kRuns; i += kThreads) m = max_nan(m, s.sub[i]);
-        m = block_max_nan(m, c->fscan);
+    } else {
+        // no filter: the batch sums lead to the token, if it is further than
+        // their error from a border
+        if (c->u == 0.f) return kTier1;
         if (t == 0) {
-            c->ws.m = m;
-            if (SAMPLE) {
-                const float mp = c->z_least;
-                c->z_least = mp > 0.f ? __double2float_ru((double)m + (double)c->temperature * log((double)mp)) : -INFINITY;
-            }
+            c->cut_key = kKeyNegInf;
+            c->cut_ties = c->cut_last = c->ties_before = 0;
         }
-        __syncthreads();
-        const WeightScale ws = c->ws;
-        if (!(m > -INFINITY && m < INFINITY)) {  // NaN, +inf, or nothing but -inf
-            if constexpr (SAMPLE) {
-                if (t == 0) {
-                    a.token[o] = -1;
-                    a.prob[o] = 0.f;
-                    if (a.conf) a.conf[o] = 0.f;
-                }
-            } else {
-                write_topk<DT>(a, s, 0, o);
-                if (t == 0 && a.lse) a.lse[o] = m;  // -inf, +inf or NaN
-            }
-            if (t == 0) {
-                raise_status(a.dev_status, DLM_DEV_NONFINITE);
-                c->done = 1;
-            }
-        } else {
-            uint64_t total = 0;
-            if (sums) {
-                uint64_t v = 0;
-                for (int b = t; b < nb; b += kThreads) {
-                    const uint64_t x = batch_mass(s.sub, s.bsum, b, ws);
-                    s.bmass[b] = x;
-                    v += x;
-                }
-                block_scan(v, c->scan, total);
-            }
-            if constexpr (!SAMPLE) {
-                if (t == 0 && a.lse)
-                    a.lse[o] = m / c->temperature + logf((float)total * 5.684341886080802e-14f);
-                const float least = kth_largest(s.sub, nb * kRuns, a.k, reinterpret_cast<uint32_t*>(s.buf), c);
-                if (least > -INFINITY || whole) {
-                    gather<DT>(row, V, 0, nb, s.sub, least, s.buf, &c->count);
-                    __syncthreads();
-                    const int n = (int)min(c->count, (uint32_t)0x7fffffff);
-                    if (n <= kCap) {
-                        sort_u64(s.buf, n);
-                        write_topk<DT>(a, s, min(n, a.k), o);
-                        if (t == 0) c->done = 1;
-                    }
-                }
-            } else {
-                // the sums' error, in 2^-24: 4 for each ex2 (the weight's and
-                // its batch's), 2.1 per unit of exponent (three roundings),
-                // whose mean over the mass is at most log2 V <= 20, 12 for
-                // ten levels of additions and the products: 2^-18 in all.
-                // The target and the running sum carry it each
-                if (t == 0) {
-                    c->total = total;
-                    c->margin = (total >> 17) + nb;
-                }
-                const bool p_off = c->top_p >= 1.f;
-                float least = -INFINITY;
-                bool list = true, complete = true;
-                if (few) {
-                    least = kth_largest(s.sub, nb * kRuns, c->top_k, reinterpret_cast<uint32_t*>(s.buf), c);
-                    list = least > -INFINITY || whole;
-                } else if (whole) {
-                } else if (c->top_k > 0) {
-                    list = false;
-                } else if (c->z_least > -INFINITY && p_off) {
-                    least = c->z_least;
-                } else if (!p_off) {
-                    complete = false;
-                    const int k0 = max(1, min(128, nb));
-                    least = kth_largest(s.sub, nb * kRuns, k0, reinterpret_cast<uint32_t*>(s.buf), c);
-                } else {
-                    list = false;
+        find_batch(s, nb, 0, 0);
+        walk_batch<DT>(row, V, c);
+        // every weight off by a share e at most, a running sum of the share u
+        // of the mass and u times the whole differ by at most 2 u (1 - u) e of
+        // the mass from what they should: e / 2
+        const uint64_t off = c->margin / 2 + 1;
+        const bool sure = c->token >= 0 && c->lo_side + off <= c->left && c->left + off < c->hi_side;
+        if (t == 0 && sure) write_token(a, c, o, c->token, c->z, c->mass);
+        return sure ? kDone : kTier1;
+    }
+    gather_runs<DT>(row, V, nsub, s, least);
+    const uint32_t n = c->count;
+    // a min-p list that overflows, or a top-k's ties, go over the whole row
+    const int other = by_p && k == 0 && !by_least ? kTier1 : kRadix;
+    if (n > (uint32_t)kCap) return other;
+    if (n <= (uint32_t)kThreads) return decide_small(a, s, (int)n, rule, o) ? kDone : other;
+    sort_u64(s.buf, (int)n);
+    keep_candidates(s, (int)n, rule);
+    const int kept = c->n;
+    if (kept <= 0) return other;
+    pick_candidate<DT>(a, s, kept, row, o);
+    return kDone;
+}
+
+// A row's settings into ctrl (one thread of each CTA of its cluster).
+template <bool SAMPLE>
+__device__ __forceinline__ void load_settings(const RowSearchArgs& a, int64_t o, Ctrl* c) {
+    float T = a.temperature, p = a.top_p, least = a.min_p;
+    int k = a.k;
+    bool bad = false;
+    if constexpr (SAMPLE) {
+        if (a.temperature_rows) T = a.temperature_rows[o];
+        if (a.top_k_rows) k = a.top_k_rows[o];
+        if (a.top_p_rows) p = a.top_p_rows[o];
+        if (a.min_p_rows) least = a.min_p_rows[o];
+        const float u = a.uniform[o];
+        bad = !(T == 0.f || (T >= DLM_MIN_TEMPERATURE && T <= FLT_MAX)) || k < 0 || !(p > 0.f && p <= 1.f) ||
+              !(least >= 0.f && least <= 1.f) || !(u >= 0.f && u < 1.f);
+        c->u = u;
+        if (T == 0.f) k = 1, T = 1.f, p = 1.f, least = 0.f;  // the argmax
+        if (k >= a.vocab) k = 0;
+    }
+    c->bad = bad;
+    c->top_k = k;
+    c->top_p = p;
+    c->min_p = least;
+    c->least = bad ? 0 : least < 1.f ? scale_ceil(kOne, least) : kOne;
+    c->ws = weight_scale(0.f, bad ? 1.f : T);
+}
+
+__device__ __forceinline__ void write_none(const RowSearchArgs& a, int64_t o) {
+    a.token[o] = -1;
+    a.prob[o] = 0.f;
+    if (a.conf) a.conf[o] = 0.f;
+}
+
+// A CTA's share of a row.
+struct Work {
+    const char* row;
+    int64_t o;    // where the row's results go
+    int nb, per, b0, b1;
+    __device__ Work(const RowSearchArgs& a, const Cluster& cl, int64_t q, int64_t out, int esz, int bel) {
+        row = static_cast<const char*>(a.logits) + q * a.row_stride * esz;
+        o = out;
+        nb = (int)((a.vocab + bel - 1) / bel);
+        per = (nb + cl.split - 1) / cl.split;
+        b0 = min(nb, cl.rank * per);
+        b1 = min(nb, b0 + per);
+    }
+};
+
+// What the first pass left open, by every CTA of the row's cluster: the tiers
+// from `verdict` on, then the radix search.  Ctrl holds the row's settings in
+// every CTA, and in the first one the maximum and the bracket.
+template <int DT, bool SAMPLE>
+__device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster& cl, const Smem& s, const Work& w,
+                                           int verdict) {
+    const int t = threadIdx.x, nb = w.nb;
+    const int64_t V = a.vocab, o = w.o;
+    const char* row = w.row;
+    Ctrl* c = s.c;
+    const Ctrl* c0 = cl.at(c, 0);
+    const WeightScale ws = c0->ws;
+    uint64_t* dst = cl.at(s.buf, 0);
+    uint32_t* count = &cl.at(c, 0)->count;
+    if constexpr (SAMPLE) {
+        while (verdict >= kTier1) {
+            const float z_lo = c0->z_lo, z_hi = c0->z_hi;
+            if (t == 0) c->count = 0;
+            __syncthreads();
+            if (verdict == kTier1)
+                bracket_pass<DT, false>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf);
+            else
+                bracket_pass<DT, true>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf);
+            cl.sync();
+            if (cl.rank == 0) {
+                // the other slices' sums, and their tokens behind the first one's
+                uint64_t total = c->whole, tokens = c->count;
+                for (int rk = 1; rk < cl.split; ++rk) {
+                    const Ctrl* rc = cl.at(c, rk);
+                    total += rc->whole;
+                    const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
+                    const uint64_t* rm = cl.at(s.bmass, rk);
+                    for (int i = x0 + t; i < x1; i += kThreads) s.bmass[i] = rm[i];
+                    const uint64_t* rb = cl.at(s.buf, rk);
+                    const uint64_t n = rc->count;
+                    for (uint64_t i = t; i < n && tokens + i < (uint64_t)kBracketCap; i += kThreads)
+                        s.buf[tokens + i] = rb[i];
+                    tokens += n;
                 }
                 __syncthreads();
-                if (list) {
-                    gather<DT>(row, V, 0, nb, s.sub, least, s.buf, &c->count);
-                    __syncthreads();
-                    const int n = (int)min(c->count, (uint32_t)0x7fffffff);
-                    if (n <= kCap) {
-                        sort_u64(s.buf, n);
-                        const int k = c->top_k;
-                        keep_candidates(s, k > 0 ? min(k, n) : n, complete);
-                        const int kept = c->n;
-                        if (kept > 0) {
-                            pick_candidate<DT>(a, s, kept, row, o);
-                            if (t == 0) c->done = 1;
-                        }
-                    }
-                } else if (c->top_k == 0) {
-                    // nothing is filtered: the batch sums lead to the token,
-                    // if it is further than their error from a border
-                    for (int b = t; b < nb; b += kThreads) s.bties[b] = 0;
-                    __syncthreads();
-                    find_batch(s, nb, 0, 0);
-                    if (t < 32 && c->u > 0.f) {
-                        uint64_t lo, hi;
-                        const int tok = walk_batch<DT>(row, V, c->batch, c->left, kKeyNegInf, 0, 0, ws, lo, hi);
-                        if (tok >= 0 && lo + c->margin <= c->left && c->left + c->margin < hi && t == 0) {
-                            write_token<DT>(a, c, row, o, tok, c->mass);
-                            c->done = 1;
-                        }
-                    }
-                }
+                if (t == 0) c->count = (uint32_t)min(tokens, (uint64_t)0xffffffffu);
+                __syncthreads();
+                const int next = resolve_bracket<DT>(a, s, row, V, nb, o, total, verdict == kTier2);
+                __syncthreads();
+                if (t == 0) c->verdict = next;
             }
+            cl.sync();
+            verdict = c0->verdict;
+        }
+        if (verdict == kDone) {
+            cl.sync();  // (the first CTA's ctrl has been read)
+            return;
         }
     }
     cl.sync();
-    const Ctrl* c0 = cl.at(c, 0);
-    const bool done = c0->done != 0;
-    const WeightScale ws = c0->ws;
-    const float z_least = SAMPLE ? c0->z_least : 0.f;
-    cl.sync();
-    if (done) return;
 
     // the search over the whole row
     const int k = c->top_k;
     uint32_t cut_key = kKeyNegInf, cut_ties = 0;
     if (k > 0) {
         bool list;
-        count_cut<DT>(cl, s, row, V, b0, b1, k, ws, cut_key, cut_ties, list);
+        count_cut<DT>(cl, s, row, V, w.b0, w.b1, k, ws, cut_key, cut_ties, list);
         if (!SAMPLE || list) {
             // the list, once more: every key from the cut on (or, when the
             // last key's ties overflow it, the keys above and the first ties)
             if (cl.rank == 0 && t == 0) c->count = 0;
             cl.sync();
-            Ctrl* lead = cl.at(c, 0);
-            uint64_t* dst = cl.at(s.buf, 0);
-            if (list) {
-                gather<DT>(row, V, b0, b1, nullptr, key_value(cut_key), dst, &lead->count);
-                cl.sync();
-            } else {
-                gather<DT>(row, V, b0, b1, nullptr, key_value(cut_key + 1), dst, &lead->count);
-                cl.sync();
-                if (cl.rank == 0 && t < 32) {  // the ties in order, by one warp
-                    constexpr int EPV = Row<DT>::EPV;
-                    uint32_t found = 0, base = c->count;
-                    for (int v0 = 0; v0 < nb * kBatchVecs && found < cut_ties; v0 += 32) {
-                        float z[EPV];
-                        Row<DT>::unpack(load_vec<DT>(row, V, v0 + t), z);
-                        uint32_t mine = 0;
-#pragma unroll
-                        for (int e = 0; e < EPV; ++e) mine += key_of(z[e]) == cut_key;
-                        uint32_t inc = mine;
-#pragma unroll
-                        for (int of = 1; of < 32; of <<= 1) {
-                            const uint32_t x = __shfl_up_sync(DLM_FULL_MASK, inc, of);
-                            if (t >= of) inc += x;
-                        }
-                        uint32_t rank = found + inc - mine;
-#pragma unroll
-                        for (int e = 0; e < EPV; ++e)
-                            if (key_of(z[e]) == cut_key) {
-                                if (rank < cut_ties) s.buf[base + rank] = candidate(z[e], (uint32_t)((v0 + t) * EPV + e));
-                                ++rank;
-                            }
-                        found += __shfl_sync(DLM_FULL_MASK, inc, 31);
-                    }
-                    if (t == 0) c->count = base + min(found, cut_ties);
+            gather_slice<DT>(row, V, w.b0, w.b1, key_value(list ? cut_key : cut_key + 1), dst, count);
+            cl.sync();
+            if (cl.rank == 0) {
+                if (!list) {
+                    if (t < 32) first_ties<DT>(row, V, nb, cut_key, cut_ties, s.buf, c);
+                    __syncthreads();
+                }
+                const int n = (int)c->count;
+                sort_u64(s.buf, n);
+                if constexpr (!SAMPLE) {
+                    write_topk(a, s, min(n, k), o);
+                } else {
+                    keep_candidates(s, n, ListRule{k, true, true});
+                    pick_candidate<DT>(a, s, c->n, row, o);
                 }
             }
-            if (cl.rank != 0) return;
-            __syncthreads();
-            const int n = (int)c->count;
-            sort_u64(s.buf, n);
-            if constexpr (!SAMPLE) {
-                write_topk<DT>(a, s, min(n, k), o);
-            } else {
-                keep_candidates(s, min(n, k), true);
-                pick_candidate<DT>(a, s, c->n, row, o);
-            }
+            cl.sync();
             return;
         }
     }
     if constexpr (SAMPLE) {
         if (c->top_p < 1.f) {
             uint32_t key, ties;
-            mass_cut<DT>(cl, s, row, V, b0, b1, c->top_p, cut_key, cut_ties, ws, key, ties);
+            mass_cut<DT>(cl, s, row, V, w.b0, w.b1, c->top_p, cut_key, cut_ties, ws, key, ties);
             cut_key = key;
             cut_ties = ties;
         }
-        if (z_least > -INFINITY) {
-            const uint32_t key = key_of(z_least);
-            if (key > cut_key) {
-                cut_key = key;
-                cut_ties = 0xffffffffu;
-            }
-        }
-        batch_masses<DT>(row, V, b0, b1, cut_key, ws, s.bmass, s.bties);
+        batch_masses<DT>(row, V, w.b0, w.b1, cut_key, c->least, ws, s.bmass, s.bties);
         cl.sync();
         if (cl.rank == 0) {
             for (int rk = 1; rk < cl.split; ++rk) {
-                const int x0 = min(nb, rk * per), x1 = min(nb, x0 + per);
+                const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
                 const uint64_t* rm = cl.at(s.bmass, rk);
                 const uint32_t* rt = cl.at(s.bties, rk);
                 for (int i = x0 + t; i < x1; i += kThreads) {
@@ -997,53 +1535,276 @@ __global__ void __launch_bounds__(kThreads) row_search_kernel(const RowSearchArg
                     s.bties[i] = rt[i];
                 }
             }
+            if (t == 0) {
+                c->cut_key = cut_key;
+                c->cut_ties = cut_ties;
+                c->cut_last = 0xffffffffu;
+                c->ties_before = 0;
+            }
             __syncthreads();
-            const uint64_t w_tie = cut_key > kKeyNegInf ? weight44(key_value(cut_key), ws) : 0;
+            uint64_t w_tie = cut_key > kKeyNegInf && cut_ties > 0 ? weight44(key_value(cut_key), ws) : 0;
+            if (w_tie < c->least) w_tie = 0;
             find_batch(s, nb, w_tie, cut_ties);
-            if (t < 32) {
-                uint64_t lo, hi;
-                const int tok = c->u > 0.f ? walk_batch<DT>(row, V, c->batch, c->left, cut_key, cut_ties, c->ties_before,
-                                                            ws, lo, hi)
-                                           : first_kept<DT>(row, V, nb, cut_key, cut_ties);
-                if (t == 0) write_token<DT>(a, c, row, o, max(tok, 0), c->mass);
+            if (c->u > 0.f) {
+                walk_batch<DT>(row, V, c);
+                if (t == 0) write_token(a, c, o, max(c->token, 0), c->z, c->mass);
+            } else if (t < 32) {
+                const int token = max(first_kept<DT>(row, V, nb, c), 0);
+                if (t == 0) write_token(a, c, o, token, Row<DT>::scalar(row, token), c->mass);
             }
         }
         cl.sync();
     }
 }
 
-template <int DT, bool SAMPLE>
-cudaError_t launch_typed(const RowSearchArgs& a, cudaStream_t st) {
+// A row that the first launch leaves to the second: bits 24..26 of its token
+// hold the verdict, below them the bracket's bins; the sign marks it (a token
+// of -1, a row without one, has the bits above 26 set).  Its maximum is in prob.
+constexpr uint32_t kOpenMask = 0xf8000000u, kOpenMark = 0x80000000u;
+
+// DEFER: rows that the first pass leaves open go to open_rows_kernel.
+template <int DT, bool SAMPLE, bool DEFER>
+__global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearchArgs a) {
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    const int t = threadIdx.x;
+    if (DEFER) asm volatile("griddepcontrol.launch_dependents;");
+    Cluster cl;
+    cl.split = DEFER ? 1 : a.split;
+    const int64_t r = blockIdx.x / cl.split;
+    cl.rank = (int)(blockIdx.x - r * cl.split);
+    const int64_t q = a.row_index ? (int64_t)a.row_index[r] : r;
+    if (q < 0 || (a.n_src > 0 && q >= a.n_src)) {  // the same for every CTA of the cluster
+        if (cl.rank == 0 && t == 0) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
+        return;
+    }
+    const int64_t V = a.vocab;
+    const Work w(a, cl, q, a.gather ? r : q, Row<DT>::ESZ, kBatchVecs * Row<DT>::EPV);
+    const int nb = w.nb;
+    const int64_t o = w.o;
+    const Smem s = carve(s_raw, nb);
+    Ctrl* c = s.c;
+
+    if (t == 0) load_settings<SAMPLE>(a, o, c);
+    __syncthreads();
+    if (SAMPLE && c->bad) {
+        if (cl.rank == 0 && t == 0) {
+            write_none(a, o);
+            raise_status(a.dev_status, DLM_DEV_BAD_PARAM);
+        }
+        return;
+    }
+    // Every logit of a short row fits the list, if a filter makes one.  A
+    // top-k within the list needs no sums, and min-p without top-p neither.
+    const int k = c->top_k;
+    const bool filtered = k > 0 || c->top_p < 1.f || c->least > 0;
+    const bool whole = V <= kCap && filtered;
+    const bool sums = !SAMPLE || (k == 0 && !whole && (c->top_p < 1.f || c->least == 0));
+    const float most = scan_rows<DT>(w.row, V, w.b0, w.b1, sums, c->ws.c_hi, s.sub, s.bsum);
+    if ((t & 31) == 0) c->wmax[t >> 5] = most;
+    cl.sync();
+
+    if (cl.rank == 0) {
+        float m = -INFINITY;
+        for (int rk = 0; rk < cl.split; ++rk) {
+            const float* wm = cl.at(c->wmax, rk);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) m = max_nan(m, wm[i]);
+        }
+        for (int rk = 1; rk < cl.split; ++rk) {  // the other slices' maxima and sums
+            const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
+            const float* rs = cl.at(s.sub, rk);
+            const float* rb = cl.at(s.bsum, rk);
+            for (int i = x0 * kRuns + t; i < x1 * kRuns; i += kThreads) s.sub[i] = rs[i];
+            if (sums)
+                for (int i = x0 + t; i < x1; i += kThreads) s.bsum[i] = rb[i];
+        }
+        if (t == 0) c->ws.m = m;
+        __syncthreads();
+        int verdict = kDone;
+        if (!(m > -INFINITY && m < INFINITY)) {  // NaN, +inf, or nothing but -inf
+            if constexpr (SAMPLE) {
+                if (t == 0) write_none(a, o);
+            } else {
+                write_topk(a, s, 0, o);
+                if (t == 0 && a.lse) a.lse[o] = m;  // -inf, +inf or NaN
+            }
+            if (t == 0) raise_status(a.dev_status, DLM_DEV_NONFINITE);
+        } else {
+            if (sums) {
+                const WeightScale ws = c->ws;
+                uint64_t v = 0, total;
+                for (int b = t; b < nb; b += kThreads) {
+                    const uint64_t x = batch_mass(s.sub, s.bsum, b, ws);
+                    s.bmass[b] = x;
+                    v += x;
+                }
+                block_scan(v, c->scan, total);
+                // the sums' error, in 2^-24: 4 for each ex2 (the weight's and
+                // its batch's), 2.1 per unit of exponent (three roundings),
+                // whose mean over the mass is at most log2 V <= 20, 12 for
+                // ten levels of additions and the products: 2^-18 in all
+                if (t == 0) {
+                    c->total = total;
+                    c->margin = (total >> 18) + nb;
+                    if (!SAMPLE && a.lse) a.lse[o] = m / a.temperature + logf((float)total * 0x1p-44f);
+                }
+                __syncthreads();
+            }
+            if constexpr (SAMPLE) {
+                verdict = sample_leader<DT>(a, s, w.row, V, nb, o, whole);
+                if (verdict == kTier1 && c->top_p < 1.f) place_bracket<DT>(w.row, V, nb, s);
+            } else {
+                const float least = whole ? -INFINITY : threshold_for(s.sub, nb * kRuns, k, m, c);
+                verdict = kRadix;
+                if (whole || least > -INFINITY) {
+                    gather_runs<DT>(w.row, V, nb * kRuns, s, least);
+                    const uint32_t n = c->count;
+                    if (n <= (uint32_t)kCap) {
+                        sort_u64(s.buf, (int)n);
+                        write_topk(a, s, min((int)n, k), o);
+                        verdict = kDone;
+                    }
+                }
+            }
+        }
+        if (DEFER) {
+            if (t == 0 && verdict != kDone) {
+                const uint32_t bins = c->top_p < 1.f && verdict == kTier1 ? (uint32_t)c->bin_lo << 12 | c->bin_hi : 0u;
+                a.token[o] = (int32_t)(kOpenMark | (uint32_t)verdict << 24 | bins);
+                a.prob[o] = m;
+            }
+            return;
+        }
+        if (t == 0) {
+            c->verdict = verdict;
+            set_bracket(c);
+        }
+    }
+    if (DEFER) return;
+    cl.sync();
+    const int verdict = cl.at(c, 0)->verdict;
+    if (verdict == kDone)
+        cl.sync();  // (the first CTA's ctrl has been read)
+    else
+        finish_row<DT, SAMPLE>(a, cl, s, w, verdict);
+}
+
+// The rows that row_search_kernel left open: cluster i of the grid looks at
+// rows i, i + clusters, ...  A row that is listed twice (a repeated row index)
+// may be finished by another cluster between two looks: its maximum is taken
+// only if the mark still stands after it was read (write_token writes the token
+// first), and finishing it again writes the same values.
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 4) open_rows_kernel(const RowSearchArgs a) {
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    __shared__ int s_row[kThreads], s_mark[kThreads];
+    __shared__ float s_max[kThreads];
+    __shared__ int s_n;
+    const int t = threadIdx.x;
+    Cluster cl;
+    cl.split = a.split;
+    cl.rank = (int)(blockIdx.x % a.split);
+    const int64_t first = blockIdx.x / a.split, step = gridDim.x / a.split;
     constexpr int BEL = kBatchVecs * Row<DT>::EPV;
-    const size_t smem = smem_bytes((int)((a.vocab + BEL - 1) / BEL));
-    if (smem > 48 * 1024) {  // the same limit whatever the call's size: calls may run side by side
-        const int most = (int)smem_bytes((DLM_MAX_SEARCH_VOCAB + BEL - 1) / BEL);
-        const cudaError_t e = cudaFuncSetAttribute(row_search_kernel<DT, SAMPLE>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const Smem s = carve(s_raw, (int)((a.vocab + BEL - 1) / BEL));
+    Ctrl* c = s.c;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the first launch's marks
+    for (int64_t base = first; base < a.n_rows; base += step * kThreads) {
+        if (t == 0) s_n = 0;
+        __syncthreads();
+        if (cl.rank == 0) {
+            const int64_t r = base + t * step;
+            const int64_t q = r >= a.n_rows ? -1 : a.row_index ? (int64_t)a.row_index[r] : r;
+            if (q >= 0 && !(a.n_src > 0 && q >= a.n_src)) {
+                const int64_t o = a.gather ? r : q;
+                const volatile int32_t* token = a.token + o;
+                const int32_t mark = *token;
+                if (((uint32_t)mark & kOpenMask) == kOpenMark) {
+                    const float m = *(const volatile float*)(a.prob + o);
+                    __threadfence();
+                    if (*token == mark) {
+                        const int i = atomicAdd(&s_n, 1);
+                        s_row[i] = t;
+                        s_mark[i] = mark;
+                        s_max[i] = m;
+                    }
+                }
+            }
+        }
+        cl.sync();
+        const int n = *cl.at(&s_n, 0);
+        for (int i = 0; i < n; ++i) {
+            const int64_t r = base + *cl.at(&s_row[i], 0) * step;
+            const uint32_t mark = (uint32_t)*cl.at(&s_mark[i], 0);
+            const float m = *cl.at(&s_max[i], 0);
+            const int64_t q = a.row_index ? (int64_t)a.row_index[r] : r;
+            const Work w(a, cl, q, a.gather ? r : q, Row<DT>::ESZ, BEL);
+            if (t == 0) {
+                load_settings<true>(a, w.o, c);
+                c->ws.m = m;
+                c->bin_lo = (int)(mark >> 12) & 0xfff;
+                c->bin_hi = (int)mark & 0xfff;
+                set_bracket(c);
+            }
+            cl.sync();
+            finish_row<DT, true>(a, cl, s, w, (int)(mark >> 24) & 7);
+        }
+        cl.sync();
+    }
+}
+
+template <int DT>
+size_t smem_for(int64_t V) {
+    constexpr int BEL = kBatchVecs * Row<DT>::EPV;
+    return smem_bytes((int)((V + BEL - 1) / BEL));
+}
+
+template <int DT, typename F>
+cudaError_t launch_rows(F kernel, const RowSearchArgs& a, int64_t grid, bool programmatic, cudaStream_t st) {
+    const size_t smem = smem_for<DT>(a.vocab);
+    if (smem > 40 * 1024) {  // the same limit whatever the call's size: calls may run side by side
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)smem_for<DT>(DLM_MAX_SEARCH_VOCAB));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.n_rows * a.split));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, row_search_kernel<DT, SAMPLE>, a);
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (a.split > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = a.split;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (programmatic) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = n ? attr : nullptr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <bool SAMPLE>
-cudaError_t launch(const RowSearchArgs& a, int dtype, cudaStream_t st) {
-    switch (dtype) {
-    case DLM_BF16: return launch_typed<DLM_BF16, SAMPLE>(a, st);
-    case DLM_F16: return launch_typed<DLM_F16, SAMPLE>(a, st);
-    default: return launch_typed<DLM_F32, SAMPLE>(a, st);
-    }
+template <int DT>
+cudaError_t launch_sample(const RowSearchArgs& a, cudaStream_t st) {
+    if (a.split > 1) return launch_rows<DT>(row_search_kernel<DT, true, false>, a, a.n_rows * a.split, false, st);
+    const cudaError_t e = launch_rows<DT>(row_search_kernel<DT, true, true>, a, a.n_rows, false, st);
+    if (e != cudaSuccess) return e;
+    RowSearchArgs open = a;
+    open.split = kOpenSplit;
+    const int64_t clusters = a.n_rows < a.num_sms ? a.n_rows : a.num_sms;
+    return launch_rows<DT>(open_rows_kernel<DT>, open, clusters * kOpenSplit, true, st);
+}
+
+template <int DT>
+cudaError_t launch_topk(const RowSearchArgs& a, cudaStream_t st) {
+    return launch_rows<DT>(row_search_kernel<DT, false, false>, a, a.n_rows * a.split, false, st);
 }
 
 }  // namespace
@@ -1057,7 +1818,20 @@ int row_search_split(int dtype, int64_t n_rows, int64_t vocab, int num_sms) {
     return split;
 }
 
-cudaError_t launch_row_topk(const RowSearchArgs& a, int dtype, cudaStream_t st) { return launch<false>(a, dtype, st); }
-cudaError_t launch_row_sample(const RowSearchArgs& a, int dtype, cudaStream_t st) { return launch<true>(a, dtype, st); }
+cudaError_t launch_row_topk(const RowSearchArgs& a, int dtype, cudaStream_t st) {
+    switch (dtype) {
+    case DLM_BF16: return launch_topk<DLM_BF16>(a, st);
+    case DLM_F16: return launch_topk<DLM_F16>(a, st);
+    default: return launch_topk<DLM_F32>(a, st);
+    }
+}
+
+cudaError_t launch_row_sample(const RowSearchArgs& a, int dtype, cudaStream_t st) {
+    switch (dtype) {
+    case DLM_BF16: return launch_sample<DLM_BF16>(a, st);
+    case DLM_F16: return launch_sample<DLM_F16>(a, st);
+    default: return launch_sample<DLM_F32>(a, st);
+    }
+}
 
 }  // namespace dlm

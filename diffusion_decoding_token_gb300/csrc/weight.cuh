@@ -109,12 +109,13 @@ struct WeightScale {
     float m, c_hi, c_lo;
 };
 
+// log2(e) / T to 2^-47: a float quotient and its remainder's.
 DLM_HD WeightScale weight_scale(float m, float temperature) {
-    const double c = 1.4426950408889634 / (double)temperature;
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2(e)
     WeightScale s;
     s.m = m;
-    s.c_hi = (float)c;
-    s.c_lo = (float)(c - (double)s.c_hi);
+    s.c_hi = kHi / temperature;
+    s.c_lo = (fmaf(-s.c_hi, temperature, kHi) + kLo) / temperature;
     return s;
 }
 

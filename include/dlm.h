@@ -708,10 +708,12 @@ dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int
  * -inf logits never stay.  The token is the smallest kept position v with
  *   sum of w over the kept positions <= v  >  u * (sum over all kept),
  * prob = w_token / (sum over all kept).  temperature 0 takes the first maximum
- * (prob 1) whatever the filters.  The sums that decide are exact integers
- * (64-bit fixed point, weights to 2^-37): the token is that of the real-number
+ * (prob 1) whatever the filters.  The sums that decide are integers (64-bit
+ * fixed point, weights to 2^-37; 32-bit sums decide only where their error can
+ * not): the token is that of the real-number
  * definition unless u * sum lies within about 1e-11 of a border, and equal
- * inputs give equal tokens on every launch.
+ * inputs give equal tokens on every launch.  prob is within 2^-20 (relative),
+ * and within 2^-17 where top_p keeps hundreds of tokens or more.
  *
  * logits .. n_src_rows, flags : as in dlm_row_topk (row r's uniform, settings,
  *               lse and outputs at o = q, or o = r with DLM_ROWS_GATHER).

@@ -3,7 +3,9 @@ masks where they can go wrong.
 
 Tolerances.  Tokens and ids are compared exactly.  prob is one weight over the
 kept mass: exp2f (2 ulp), a product, a 64-bit sum rounded to float and a
-division, 2^-20 in all.  lse: the 32-bit sum of exponentials is within 2^-18
+division, 2^-20 in all; where a nucleus is too long for a list, which token ends
+it may stay open while the mass of the open ones is at most 2^-17 of the kept
+mass, so there prob is within 2^-17 more.  lse: the 32-bit sum of exponentials is within 2^-18
 (ex2 2^-22, an exponent of up to ~20 rounded three times at 2^-24, ten levels
 of additions), and the float result and m / T round at 2^-23 of their value.
 """
@@ -16,6 +18,7 @@ import row_ref as ref
 pytestmark = pytest.mark.gpu
 
 PROB_RTOL = 2.0 ** -20
+LIST = 64  # shorter nuclei always fit a candidate list
 
 
 @pytest.fixture(scope="module")
@@ -63,7 +66,9 @@ def check_sample(dlm, z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, mixe
     for i, row in enumerate(ref.host(z)):
         want, p = ref.sample(row, u[i], at(temperature, i), at(top_k, i), at(top_p, i), at(min_p, i))
         assert token[i] == want, (i, token[i], want)
-        assert abs(prob[i] - p) <= PROB_RTOL * p, (i, prob[i], p)
+        kept = len(ref.kept(row, *(at(v, i) for v in (temperature, top_k, top_p, min_p)))[0])
+        open_end = 2.0 ** -17 if kept > LIST and at(top_p, i) < 1 else 0.0
+        assert abs(prob[i] - p) <= (PROB_RTOL + open_end) * p, (i, prob[i], p)
     return r
 
 
