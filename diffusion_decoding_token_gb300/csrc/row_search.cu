@@ -53,6 +53,7 @@ constexpr int kBracketSide = 1200;     // tokens on either side of its middle
 constexpr int kSampleTokens = 16384;   // the sample that places a bracket
 constexpr int kOpenSplit = 4;          // CTAs per row that the first launch left open
 constexpr int kTries = 4;              // brackets that a row gets
+constexpr int kListTopk = 1700;        // largest top-k whose list a sample's threshold can be trusted with
 constexpr uint64_t kOne = 1ull << kWeightBits;
 constexpr int kBins = 2048;            // radix bins of a pass over the whole row
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // ordered key of -inf
@@ -69,7 +70,10 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // What one row's CTA (the first of its cluster) and the others share.
-enum Verdict : int { kRadix = 0, kDone = 1, kTier1 = 2, kTier2 = 3 };
+// What is to be done for a row: nothing more, a pass of tier 1 or 2, a list of
+// everything above a threshold, a pass of tier 1 around min-p's cut, or the
+// radix search.
+enum Verdict : int { kRadix = 0, kDone = 1, kTier1 = 2, kTier2 = 3, kList = 4, kMinP = 5 };
 
 struct Ctrl {
     WeightScale ws;
@@ -83,7 +87,11 @@ struct Ctrl {
     uint64_t least;       // min-p: the smallest weight that stays
     uint64_t total;       // the row's mass, within margin
     uint64_t margin;
-    uint64_t whole;       // a slice's mass
+    uint64_t whole;       // a slice's mass, and the part of it above the bracket
+    uint64_t top;
+    uint64_t t_lo, t_mid, t_hi;  // what the bracket's tokens have to add: least, likely, most
+    uint64_t err;
+    int by_min;           // min-p's cut ends the row, not the nucleus
     float z_lo, z_hi;     // the bracket: z_lo <= z < z_hi
     int bin_lo, bin_hi;   // the same in 1/32 of an exponent below the maximum
     int tries;
@@ -919,18 +927,21 @@ __device__ __forceinline__ f2 weight_split(f2 z, const SplitScale& s) {
                  __int_as_float(__float_as_int(y) + (__float_as_int(ty) << 23)));
 }
 
-// Two logits that the nucleus' end should lie between, from a sample of the
-// row: the mass below it is (1 - top_p) of the total, the sample's masses per
-// 1/32 of an exponent tell where the row's lower end adds up to that, and the
-// bracket takes the kBracketSide tokens on either side.  On a flat row of 152064
-// tokens that is three to four standard deviations of the sample; where few
-// tokens hold the mass it reaches up to the largest.  One CTA; sets c->bin_lo,
-// c->bin_hi.
+// The smallest logit that min-p can keep (or one a little lower: the weights
+// decide).
+__device__ __forceinline__ float min_p_logit(const Ctrl* c) {
+    return c->ws.m + (1.0001f * __logf(c->min_p) - 1e-5f) / (c->ws.c_hi * kLn2) - 1e-6f * fabsf(c->ws.m);
+}
+
+// A sample of the row in buf's kBins words: per 1/32 of an exponent below the
+// maximum the weights relative to the bin's upper end, in 2^-16 (between 0.97
+// and 1 each, so the bin counts its tokens too).  Returns how many of the row's
+// tokens one of the sample stands for.
 template <int DT>
-__device__ __noinline__ void place_bracket(const char* row, int64_t V, int nb, const Smem& s) {
+__device__ __noinline__ float sample_row(const char* row, int64_t V, const Smem& s) {
     constexpr int EPV = Row<DT>::EPV;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    Ctrl* c = s.c;
+    const Ctrl* c = s.c;
     uint32_t* bins = reinterpret_cast<uint32_t*>(s.buf);
     for (int i = t; i < kBins; i += kThreads) bins[i] = 0;
     __syncthreads();
@@ -945,67 +956,123 @@ __device__ __noinline__ void place_bracket(const char* row, int64_t V, int nb, c
 #pragma unroll
         for (int e = 0; e < EPV; ++e) {
             if (!(z[e] > -INFINITY)) continue;
-            // a bin adds up its tokens' weights relative to its own upper end,
-            // in 2^-16 (between 0.97 and 1 each, so the sample's fit 32 bits)
             const float x = (m - z[e]) * c32;
             const int bin = min(kBins - 1, (int)x);
             atomicAdd(&bins[bin], (uint32_t)(65536.f * ex2(fmaxf(((float)bin - x) * 0.03125f, -1.f))));
         }
     }
     __syncthreads();
-    // thread t takes bins from the lowest weights up
+    return (float)nsub / (float)n;
+}
+
+// Two logits that the nucleus' end should lie between: the mass below it is
+// (1 - top_p) of the total, the sample tells where the row's lower end adds up
+// to that, and the bracket takes the kBracketSide tokens on either side.  On a
+// flat row of 152064 tokens that is three to four standard deviations of the
+// sample; where few tokens hold the mass it reaches up to the largest.  When
+// min-p's cut is higher the bracket is put around it.  One CTA; sets c->bin_lo,
+// c->bin_hi and returns kTier1 or kMinP.
+template <int DT>
+__device__ __noinline__ int place_bracket(const char* row, int64_t V, const Smem& s) {
     constexpr int PER = kBins / kThreads;
-    const float scale = (float)nsub / (float)n;
-    float mass = 0.f;
-    uint64_t tokens = 0;  // in 2^-16, a little short
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int bin = kBins - 1 - (t * PER + j);
-        mass += (float)bins[bin] * 0x1p-16f * ex2(-(float)bin * 0.03125f);
-        tokens += bins[bin];
-    }
-    // exclusive sums over the threads in integers (a sample's mass is at most 2^14)
-    uint64_t all;
-    float run = (float)block_scan((uint64_t)__float2ull_rn(mass * 0x1p44f), c->scan, all) * 0x1p-44f;
-    uint64_t seen = block_scan(tokens, c->scan, all);
-    // the sample's share of the mass below the nucleus' end
-    const float want = (1.f - c->top_p) * ((float)c->total * 0x1p-44f) / scale;
+    const int t = threadIdx.x;
+    Ctrl* c = s.c;
+    const uint32_t* bins = reinterpret_cast<const uint32_t*>(s.buf);
+    const bool by_least = c->least > 0;
+    const int cut = by_least ? (int)fminf((c->ws.m - min_p_logit(c)) * c->ws.c_hi * 32.f, (float)(kBins - 2)) : kBins;
+    float want = 0.f, scale = 1.f;
     if (t == 0) {  // for a sample that does not reach it
         c->left = 0;
         c->bin_lo = kBins;
         c->bin_hi = 0;
+        c->batch = kBins;
+    }
+    if (c->top_p < 1.f) {
+        scale = sample_row<DT>(row, V, s);
+        // thread t takes bins from the lowest weights up
+        float mass = 0.f;
+        uint64_t tokens = 0;  // in 2^-16, a little short
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int bin = kBins - 1 - (t * PER + j);
+            mass += (float)bins[bin] * 0x1p-16f * ex2(-(float)bin * 0.03125f);
+            tokens += bins[bin];
+        }
+        // exclusive sums over the threads in integers (a sample's mass is at most 2^14)
+        uint64_t all;
+        float run = (float)block_scan((uint64_t)__float2ull_rn(mass * 0x1p44f), c->scan, all) * 0x1p-44f;
+        const uint64_t seen0 = block_scan(tokens, c->scan, all);
+        uint64_t seen = seen0;
+        // the sample's share of the mass below the nucleus' end
+        want = (1.f - c->top_p) * ((float)c->total * 0x1p-44f) / scale;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int bin = kBins - 1 - (t * PER + j);
+            const float next = run + (float)bins[bin] * 0x1p-16f * ex2(-(float)bin * 0.03125f);
+            if (run <= want && next > want) {
+                c->left = seen + bins[bin] / 2;
+                c->batch = bin;
+            }
+            run = next;
+            seen += bins[bin];
+        }
+        __syncthreads();
+        const uint64_t mid = c->left, side = (uint64_t)((float)kBracketSide * 65536.f / scale);
+        seen = seen0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int bin = kBins - 1 - (t * PER + j);
+            const uint64_t next = seen + bins[bin];
+            if (mid > side && seen <= mid - side && next > mid - side) c->bin_lo = bin + 1;
+            if (seen < mid + side && next >= mid + side) c->bin_hi = bin;
+            seen = next;
+        }
     }
     __syncthreads();
-    const uint64_t seen0 = seen;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int bin = kBins - 1 - (t * PER + j);
-        const float next = run + (float)bins[bin] * 0x1p-16f * ex2(-(float)bin * 0.03125f);
-        if (run <= want && next > want) c->left = seen + bins[bin] / 2;
-        run = next;
-        seen += bins[bin];
+    const bool by_min = by_least && cut <= c->batch;
+    __syncthreads();
+    if (t == 0 && by_min) {
+        c->bin_lo = cut + 2;
+        c->bin_hi = max(cut - 1, 0);
     }
     __syncthreads();
-    const uint64_t mid = c->left, side = (uint64_t)((float)kBracketSide * 65536.f / scale);
-    seen = seen0;
+    return by_min ? kMinP : kTier1;
+}
+
+// A threshold that about sqrt(k kCap) of the row's logits reach, between k and
+// the list's length by three standard deviations of the sample.  One CTA; sets
+// c->bin_lo and returns kList, or kRadix when no bin is near.
+template <int DT>
+__device__ __noinline__ int place_list(const char* row, int64_t V, int k, const Smem& s) {
+    constexpr int PER = kBins / kThreads;
+    const int t = threadIdx.x;
+    Ctrl* c = s.c;
+    const uint32_t* bins = reinterpret_cast<const uint32_t*>(s.buf);
+    const float scale = sample_row<DT>(row, V, s);
+    if (t == 0) c->bin_lo = 0;
+    uint64_t tokens = 0, all;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) tokens += bins[t * PER + j];
+    uint64_t seen = block_scan(tokens, c->scan, all);  // from the largest down
+    const float want = sqrtf((float)k * (float)kCap) * 64700.f / scale;  // a token counts 0.987 * 2^16 on average
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int bin = kBins - 1 - (t * PER + j);
-        const uint64_t next = seen + bins[bin];
-        if (mid > side && seen <= mid - side && next > mid - side) c->bin_lo = bin + 1;
-        if (seen < mid + side && next >= mid + side) c->bin_hi = bin;
+        const uint64_t next = seen + bins[t * PER + j];
+        if ((float)seen < want && (float)next >= want) c->bin_lo = t * PER + j + 1;
         seen = next;
     }
     __syncthreads();
+    return c->bin_lo > 0 && c->bin_lo < kBins ? kList : kRadix;
 }
 
-__device__ __forceinline__ void set_bracket(Ctrl* c) {
+// The bracket in logits from its bins (one thread).
+__device__ __forceinline__ void set_bracket(Ctrl* c, int verdict) {
     const float c32 = c->ws.c_hi * 32.f;
     c->z_lo = c->ws.m - (float)c->bin_lo / c32;
     c->z_hi = c->ws.m - (float)c->bin_hi / c32;
-    if (c->top_p >= 1.f) c->z_lo = c->z_hi = -INFINITY;  // everything is above: sums only
+    c->by_min = verdict == kMinP;
+    if (verdict == kTier1 && c->top_p >= 1.f) c->z_lo = c->z_hi = -INFINITY;  // everything is above: sums only
     c->tries = 0;
-    c->count = 0;
 }
 
 // One pass over a slice: bmass[b] the mass of batch b at z >= z_hi, c->whole
@@ -1018,7 +1085,7 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float z_min = fmaxf(ws.m - 99.f / ws.c_hi, -FLT_MAX);  // a weight of 2^-99 counts as 0
     const SplitScale sp{pack2(ws.m, ws.m), pack2(-ws.c_hi, -ws.c_hi), pack2(-ws.c_lo, -ws.c_lo)};
-    uint64_t whole = 0, sum = 0;
+    uint64_t whole = 0, top = 0, sum = 0;
     for (int b = b0 + warp; b < b1; b += kWarps) {
         uint64_t above = 0;
         uint4 w4[kRuns];
@@ -1063,6 +1130,7 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
                 whole += __float2ull_rn(hsum2(all[0]) * 0x1p44f);
             }
         }
+        top += above;
         above = (uint64_t)warp_sum_ll((long long)above);
         if (lane == 0) bmass[b] = above;
         if (!__any_sync(DLM_FULL_MASK, mask != 0)) continue;
@@ -1086,108 +1154,180 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
     }
     block_scan(whole, c->scan, sum);
     if (threadIdx.x == 0) c->whole = sum;
+    block_scan(top, c->scan, sum);
+    if (threadIdx.x == 0) c->top = sum;
     __syncthreads();
 }
 
-// After a pass, in the first CTA: the kept set and the token.  Returns the
-// next verdict.  err: how far the pass's sums may be off, every weight by the
-// same share at most.  A sum over part of the mass and that part's share of
-// the whole then differ by 2 share (1 - share) err at most from what they
-// should.  The last tier's token stands whatever its distance from a border.
-template <int DT>
-__device__ __noinline__ int resolve_bracket(const RowSearchArgs& a, const Smem& s, const char* row, int64_t V, int nb,
-                                            int64_t o, uint64_t total, bool last_tier) {
-    constexpr int BEL = kBatchVecs * Row<DT>::EPV;
+// The bin of a bracket's token, from z_hi down.
+__device__ __forceinline__ int fine_bin(uint64_t e, float z_hi, float per_bin) {
+    return max(0, min(kFine - 1, (int)((z_hi - candidate_value(e)) * per_bin)));
+}
+
+// A slice's tokens of the bracket into its CTA's bins, with their mass.  16-bit
+// logits repeat: equal ones of a warp are added once.
+__device__ __noinline__ void bin_tokens(const Smem& s, float z_hi, float per_bin, const WeightScale ws) {
+    const int t = threadIdx.x, n = (int)min(s.c->count, (uint32_t)kBracketCap);
+    for (int i = t; i < kFine; i += kThreads) s.fine[i] = 0;
+    __syncthreads();
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + t;
+        const uint64_t e = i < n ? s.buf[i] : 0;
+        const uint32_t like = __match_any_sync(DLM_FULL_MASK, i < n ? (uint32_t)(e >> 32) : 0xffffffffu);
+        if (i < n && __ffs(like) - 1 == (t & 31))
+            shared_add(&s.fine[fine_bin(e, z_hi, per_bin)], weight44(candidate_value(e), ws) * __popc(like));
+    }
+    __syncthreads();
+}
+
+// After a pass, in the first CTA: where the row ends.  Every weight of the
+// pass is off by the share err / total at most, so a sum over part of the mass
+// and that part's share of the whole differ by 2 share (1 - share) err at most
+// from what they should.  Returns kDone when the end is inside the bracket:
+// ctrl then has the bins that may hold it (first_bin, last_bin), the mass before
+// them (left) and the targets; else another bracket is set and it is a tier's,
+// or kRadix.
+__device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, bool last_tier) {
     Ctrl* c = s.c;
     const int t = threadIdx.x;
-    uint64_t v = 0, above;
-    for (int b = t; b < nb; b += kThreads) v += s.bmass[b];
-    block_scan(v, c->scan, above);
+    uint64_t total = 0, above = 0, n = 0;
+    for (int rk = 0; rk < cl.split; ++rk) {
+        const Ctrl* rc = cl.at(c, rk);
+        total += rc->whole;
+        above += rc->top;
+        n = max(n, (uint64_t)rc->count);
+    }
     // integer weights 2^-37; else, in 2^-24, ex2 4, the fraction's roundings and
     // the conversion 2, three levels of additions 3
     const uint64_t err = last_tier ? (total >> 36) + (uint64_t)nb : (total >> 24) * 9 + (uint64_t)nb;
-    uint64_t slack = 0, sure = ~0ull;
-    // another bracket: above or below this one (with a quarter of it), or the
-    // middle of one that holds too many tokens
-    auto miss = [&](bool up, bool down) {
+    const float p = c->top_p;
+    const uint64_t x = p < 1.f ? scale_ceil(total, p) : ~0ull;
+    const uint64_t off = p < 1.f ? (uint64_t)((float)err * 2.0001f * p * (1.f - p)) + 2 : 0;  // rounded up
+    // another bracket: above this one or below (with a quarter of it), the
+    // middle of one that holds too many tokens, or the other filter's
+    enum { kUp, kDown, kMiddle, kToMin, kToNucleus };
+    auto miss = [&](int how) {
         __syncthreads();
         if (t == 0) {
             const float lo = c->z_lo, hi = c->z_hi, width = fmaxf(hi - lo, 1e-6f * fabsf(hi));
-            if (up) {
+            if (how == kUp || how == kToNucleus) {
                 c->z_lo = hi - 0.25f * width;
                 c->z_hi = hi + 2.f * width;
-            } else if (down) {
+                c->by_min = 0;
+            } else if (how == kDown) {
                 c->z_lo = lo - 2.f * width;
                 c->z_hi = lo + 0.25f * width;
-            } else {
+            } else if (how == kMiddle) {
                 c->z_lo = lo + 0.4f * width;
                 c->z_hi = hi - 0.4f * width;
+            } else {
+                const float z = min_p_logit(c), step = 0.03125f / c->ws.c_hi;
+                c->z_lo = z - step;
+                c->z_hi = z + step;
+                c->by_min = 1;
             }
             c->tries += 1;
         }
         __syncthreads();
         return c->tries < kTries ? (last_tier ? kTier2 : kTier1) : kRadix;
     };
-    if (c->top_p < 1.f) {
-        const uint32_t n = c->count;
-        const uint64_t x = scale_ceil(total, c->top_p);
-        // 2 p (1 - p) err, rounded up
-        const uint64_t off = (uint64_t)((float)err * 2.0001f * c->top_p * (1.f - c->top_p)) + 2;
-        // the bracket holds the nucleus' end: what is above is short of the
-        // target, what is above and inside reaches it, and all of it is listed
-        if (above + off >= x) return miss(true, false);
-        if (n > (uint32_t)kBracketCap) return miss(false, false);
-        const uint64_t t_mid = x - above, t_lo = t_mid - off, t_hi = t_mid + off;
-        // the tokens into bins from z_hi down, with their mass
-        const float z_hi = c->z_hi, per_bin = (float)kFine / (c->z_hi - c->z_lo);
-        auto bin_of = [&](uint64_t e) { return max(0, min(kFine - 1, (int)((z_hi - candidate_value(e)) * per_bin))); };
-        for (int i = t; i < kFine; i += kThreads) s.fine[i] = 0;
-        if (t == 0) c->runs = 0;
+    if (t == 0) {
+        c->total = total;
+        c->err = err;
+        c->runs = 0;
+        c->above = above;
+    }
+    if (c->by_min) {
+        if (n > (uint64_t)kBracketCap) return kRadix;
+        // the cut has to be inside the bracket (the logits' estimate was near)
+        if (weight44(fminf(c->z_hi, c->ws.m), c->ws) < c->least || weight44(c->z_lo, c->ws) >= c->least) return kRadix;
         __syncthreads();
-        for (int i0 = 0; i0 < (int)n; i0 += kThreads) {
-            // 16-bit logits repeat: equal ones of a warp are added once
-            const int i = i0 + t;
-            const uint64_t e = i < (int)n ? s.buf[i] : 0;
-            const uint32_t like = __match_any_sync(DLM_FULL_MASK, i < (int)n ? (uint32_t)(e >> 32) : 0xffffffffu);
-            if (i < (int)n && __ffs(like) - 1 == (t & 31))
-                shared_add(&s.fine[bin_of(e)], weight44(candidate_value(e), c->ws) * __popc(like));
-        }
+        return kDone;
+    }
+    if (p >= 1.f) {
         __syncthreads();
-        constexpr int PER = kFine / kThreads;
-        uint64_t sum = 0, inside;
+        return kDone;
+    }
+    // what is above is short of the target, what is above and inside reaches
+    // it, and all of it is listed
+    if (above + off >= x) return miss(kUp);
+    if (n > (uint64_t)kBracketCap) return miss(kMiddle);
+    const uint64_t t_lo = x - above - off, t_hi = x - above + off;
+    constexpr int PER = kFine / kThreads;
+    uint64_t v[PER], sum = 0, inside;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) sum += s.fine[t * PER + j];
-        uint64_t m = block_scan(sum, c->scan, inside);
-        if (inside < t_hi) return miss(false, true);
+    for (int j = 0; j < PER; ++j) {
+        v[j] = 0;
+        for (int rk = 0; rk < cl.split; ++rk) v[j] += cl.at(s.fine, rk)[t * PER + j];
+        sum += v[j];
+    }
+    uint64_t m = block_scan(sum, c->scan, inside);
+    if (inside < t_hi) return miss(kDown);
+    if (t == 0) {
+        c->t_lo = t_lo;
+        c->t_mid = x - above;
+        c->t_hi = t_hi;
+    }
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const uint64_t next = m + s.fine[t * PER + j];
-            if (m < t_lo && next >= t_lo) {
-                c->first_bin = t * PER + j;
-                c->left = m;
-            }
-            if (m < t_hi && next >= t_hi) c->last_bin = t * PER + j;
-            m = next;
+    for (int j = 0; j < PER; ++j) {
+        const uint64_t next = m + v[j];
+        if (m < t_lo && next >= t_lo) {
+            c->first_bin = t * PER + j;
+            c->left = m;
         }
-        __syncthreads();
-        // tokens before the first of the end's bins stay; those in the end's
-        // bins are put in order
-        const int f0 = c->first_bin, f1 = c->last_bin;
-        const uint64_t before_bin = c->left;
-        auto keep = [&](uint64_t e, uint64_t w) { shared_add(&s.bmass[(uint32_t)e / BEL], w); };
-        for (int i = t; i < (int)n; i += kThreads) {
-            const uint64_t e = s.buf[i];
-            const int bin = bin_of(e);
-            if (bin < f0) {
-                keep(e, weight44(candidate_value(e), c->ws));
-            } else if (bin <= f1) {
-                const uint32_t at = atomicAdd(&c->runs, 1u);
-                if (at < (uint32_t)kFine) s.fine[at] = e;
-            }
+        if (m < t_hi && next >= t_hi) c->last_bin = t * PER + j;
+        m = next;
+    }
+    __syncthreads();
+    // (a bin's lowest logit, and what else is in it, decides min-p)
+    if (c->least > 0) {
+        const float z = c->z_hi - (float)(c->last_bin + 1) / (float)kFine * (c->z_hi - c->z_lo) * 1.0001f;
+        if (weight44(z, c->ws) < c->least) return miss(kToMin);
+    }
+    return kDone;
+}
+
+// A slice's tokens that surely stay go into its batches' mass, those of the
+// bins that may hold the end into the first CTA's `fine`.
+template <int DT>
+__device__ __noinline__ void keep_tokens(const Cluster& cl, const Smem& s, const Ctrl* c0, float z_hi, float per_bin,
+                                         const WeightScale ws) {
+    constexpr int BEL = kBatchVecs * Row<DT>::EPV;
+    const int n = (int)min(s.c->count, (uint32_t)kBracketCap);
+    const bool by_min = c0->by_min;
+    const int f0 = c0->first_bin, f1 = c0->last_bin;
+    const uint64_t least = s.c->least;
+    uint64_t* end = cl.at(s.fine, 0);
+    uint32_t* count = &cl.at(s.c, 0)->runs;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t e = s.buf[i];
+        const int bin = by_min ? 0 : fine_bin(e, z_hi, per_bin);
+        if (by_min || bin < f0) {
+            const uint64_t w = weight44(candidate_value(e), ws);
+            if (w >= least) shared_add(&s.bmass[(uint32_t)e / BEL], w);
+        } else if (bin <= f1) {
+            const uint32_t at = atomicAdd(count, 1u);
+            if (at < (uint32_t)kFine) end[at] = e;
         }
+    }
+}
+
+// The last step of a pass, in the first CTA: the tokens around the nucleus' end
+// in order, the kept mass, and the token.  The last tier's token stands
+// whatever its distance from a border.  Returns the next verdict.
+template <int DT>
+__device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const char* row, int64_t V, int nb,
+                                    int64_t o, bool last_tier) {
+    constexpr int BEL = kBatchVecs * Row<DT>::EPV;
+    Ctrl* c = s.c;
+    const int t = threadIdx.x;
+    uint64_t slack = 0, sure = ~0ull;
+    const uint64_t err = c->err;
+    if (c->top_p < 1.f && !c->by_min) {
+        const uint64_t before_bin = c->left, t_lo = c->t_lo, t_mid = c->t_mid, t_hi = c->t_hi;
+        const int n = (int)c->runs;
+        if (n > kFine) return kRadix;
         __syncthreads();
-        const int n2 = (int)c->runs;
-        if (n2 > kFine) return kRadix;
         auto crossing = [&](uint64_t e, uint64_t m0, uint64_t w) {
             const uint64_t next = m0 + w;
             if (m0 < t_lo && next >= t_lo) {
@@ -1200,22 +1340,22 @@ __device__ __noinline__ int resolve_bracket(const RowSearchArgs& a, const Smem& 
                 c->left = next;
             }
             if (m0 < t_hi && next >= t_hi) c->slack = next;
-            if (m0 < t_mid) keep(e, w);
+            if (m0 < t_mid) shared_add(&s.bmass[(uint32_t)e / BEL], w);
         };
-        if (n2 <= kThreads) {
-            const uint64_t mine = t < n2 ? s.fine[t] : ~0ull;
-            const uint64_t w = t < n2 ? weight44(candidate_value(mine), c->ws) : 0ull;
-            if (t < n2) s.buf[t] = w;
+        if (n <= kThreads) {
+            const uint64_t mine = t < n ? s.fine[t] : ~0ull;
+            const uint64_t w = t < n ? weight44(candidate_value(mine), c->ws) : 0ull;
+            if (t < n) s.buf[t] = w;
             __syncthreads();
-            if (t < n2) {
+            if (t < n) {
                 uint64_t m0 = before_bin;
 #pragma unroll 4
-                for (int j = 0; j < n2; ++j) m0 += s.fine[j] < mine ? s.buf[j] : 0ull;
+                for (int j = 0; j < n; ++j) m0 += s.fine[j] < mine ? s.buf[j] : 0ull;
                 crossing(mine, m0, w);
             }
         } else {
-            sort_u64(s.fine, n2);
-            const int per = (n2 + kThreads - 1) / kThreads, i0 = min(n2, t * per), i1 = min(n2, i0 + per);
+            sort_u64(s.fine, n);
+            const int per = (n + kThreads - 1) / kThreads, i0 = min(n, t * per), i1 = min(n, i0 + per);
             uint64_t mine = 0, all;
             for (int i = i0; i < i1; ++i) mine += weight44(candidate_value(s.fine[i]), c->ws);
             uint64_t m0 = before_bin + block_scan(mine, c->scan, all);
@@ -1232,7 +1372,7 @@ __device__ __noinline__ int resolve_bracket(const RowSearchArgs& a, const Smem& 
         __syncthreads();
         sure = c->sure;
         slack = max(c->slack - c->left, c->left - c->sure_mass);
-    } else if (t == 0) {
+    } else if (t == 0) {  // everything, or (the walk looks at the weights) what min-p keeps
         c->cut_key = kKeyNegInf;
         c->cut_ties = 0;
         c->cut_last = 0;
@@ -1240,6 +1380,19 @@ __device__ __noinline__ int resolve_bracket(const RowSearchArgs& a, const Smem& 
     }
     __syncthreads();
     find_batch(s, nb, 0, 0);
+    // min-p ends the row only if its tokens are all inside the nucleus
+    if (c->by_min && c->top_p < 1.f && c->mass + 2 * err >= scale_ceil(c->total, c->top_p)) {
+        __syncthreads();
+        if (t == 0) {
+            const float hi = c->z_hi, width = hi - c->z_lo;
+            c->z_lo = hi - 1.1f * width;
+            c->z_hi = hi + 4.f * width;
+            c->by_min = 0;
+            c->tries += 1;
+        }
+        __syncthreads();
+        return c->tries < kTries ? (last_tier ? kTier2 : kTier1) : kRadix;
+    }
     const bool first = c->u == 0.f;
     if (!first) {
         walk_batch<DT>(row, V, c);
@@ -1263,6 +1416,30 @@ __device__ __noinline__ int resolve_bracket(const RowSearchArgs& a, const Smem& 
                candidate(c->z, (uint32_t)c->token) <= sure;
     if (t == 0 && done) write_token(a, c, o, c->token, c->z, c->mass);
     return done ? kDone : last_tier ? kRadix : kTier2;
+}
+
+// The other slices' lists behind the first CTA's own (`count` of them may
+// exceed `cap`, then the list is cut off).
+__device__ __forceinline__ void join_lists(const Cluster& cl, const Smem& s, uint32_t cap) {
+    uint32_t n = s.c->count;
+    for (int rk = 1; rk < cl.split; ++rk) {
+        const uint64_t* rb = cl.at(s.buf, rk);
+        const uint32_t m = cl.at(s.c, rk)->count;
+        for (uint32_t i = threadIdx.x; i < m && n + i < cap; i += kThreads) s.buf[n + i] = rb[i];
+        n += m;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.c->count = n;
+    __syncthreads();
+}
+
+__device__ __forceinline__ void join_masses(const Cluster& cl, const Smem& s, int nb, int per) {
+    for (int rk = 1; rk < cl.split; ++rk) {
+        const int x0 = min(nb, rk * per), x1 = min(nb, x0 + per);
+        const uint64_t* rm = cl.at(s.bmass, rk);
+        for (int i = x0 + (int)threadIdx.x; i < x1; i += kThreads) s.bmass[i] = rm[i];
+    }
+    __syncthreads();
 }
 
 // The first cut_ties positions at cut_key, after the c->count candidates that
@@ -1319,17 +1496,15 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
     const int k = c->top_k;
     const float p = c->top_p, m = c->ws.m;
     const bool by_p = p < 1.f, by_least = c->least > 0;
-    // the smallest logit that min-p can keep (a little lower: the weights decide)
-    const float z_least = by_least ? m + (1.0001f * __logf(c->min_p) - 1e-5f) / (c->ws.c_hi * kLn2) - 1e-6f * fabsf(m)
-                                   : -INFINITY;
+    const float z_least = by_least ? min_p_logit(c) : -INFINITY;
     ListRule rule{k > 0 ? k : 0x7fffffff, true, true};
     float least;
     if (whole) {
         least = -INFINITY;
     } else if (k > 0) {
-        if (k > DLM_MAX_TOPK) return kRadix;
-        least = threshold_for(s.sub, nsub, k, m, c);
-        if (!(least > -INFINITY)) return kRadix;
+        // (more than the runs: a list from a threshold that a sample gives)
+        least = k <= DLM_MAX_TOPK ? threshold_for(s.sub, nsub, k, m, c) : -INFINITY;
+        if (!(least > -INFINITY)) return k <= kListTopk ? kList : kRadix;
     } else if (by_least) {
         least = z_least;
         rule.complete = !by_p;
@@ -1370,8 +1545,8 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
     }
     gather_runs<DT>(row, V, nsub, s, least);
     const uint32_t n = c->count;
-    // a min-p list that overflows, or a top-k's ties, go over the whole row
-    const int other = by_p && k == 0 && !by_least ? kTier1 : kRadix;
+    // a top-k's ties go over the whole row
+    const int other = k == 0 ? kTier1 : kRadix;
     if (n > (uint32_t)kCap) return other;
     if (n <= (uint32_t)kThreads) return decide_small(a, s, (int)n, rule, o) ? kDone : other;
     sort_u64(s.buf, (int)n);
@@ -1441,47 +1616,63 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
     Ctrl* c = s.c;
     const Ctrl* c0 = cl.at(c, 0);
     const WeightScale ws = c0->ws;
-    uint64_t* dst = cl.at(s.buf, 0);
-    uint32_t* count = &cl.at(c, 0)->count;
     if constexpr (SAMPLE) {
-        while (verdict >= kTier1) {
-            const float z_lo = c0->z_lo, z_hi = c0->z_hi;
+        while (verdict == kTier1 || verdict == kTier2) {
+            const float z_lo = c0->z_lo, z_hi = c0->z_hi, per_bin = (float)kFine / (z_hi - z_lo);
+            const bool bins = c->top_p < 1.f && !c0->by_min;
             if (t == 0) c->count = 0;
             __syncthreads();
             if (verdict == kTier1)
                 bracket_pass<DT, false>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf);
             else
                 bracket_pass<DT, true>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf);
+            if (bins) bin_tokens(s, z_hi, per_bin, ws);
             cl.sync();
             if (cl.rank == 0) {
-                // the other slices' sums, and their tokens behind the first one's
-                uint64_t total = c->whole, tokens = c->count;
-                for (int rk = 1; rk < cl.split; ++rk) {
-                    const Ctrl* rc = cl.at(c, rk);
-                    total += rc->whole;
-                    const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
-                    const uint64_t* rm = cl.at(s.bmass, rk);
-                    for (int i = x0 + t; i < x1; i += kThreads) s.bmass[i] = rm[i];
-                    const uint64_t* rb = cl.at(s.buf, rk);
-                    const uint64_t n = rc->count;
-                    for (uint64_t i = t; i < n && tokens + i < (uint64_t)kBracketCap; i += kThreads)
-                        s.buf[tokens + i] = rb[i];
-                    tokens += n;
-                }
-                __syncthreads();
-                if (t == 0) c->count = (uint32_t)min(tokens, (uint64_t)0xffffffffu);
-                __syncthreads();
-                const int next = resolve_bracket<DT>(a, s, row, V, nb, o, total, verdict == kTier2);
-                __syncthreads();
+                const int next = find_end(cl, s, nb, verdict == kTier2);
                 if (t == 0) c->verdict = next;
             }
             cl.sync();
+            if (c0->verdict == kDone) {  // the end is inside the bracket
+                keep_tokens<DT>(cl, s, c0, z_hi, per_bin, ws);
+                cl.sync();
+                if (cl.rank == 0) {
+                    join_masses(cl, s, nb, w.per);
+                    const int next = end_row<DT>(a, s, row, V, nb, o, verdict == kTier2);
+                    __syncthreads();
+                    if (t == 0) c->verdict = next;
+                }
+                cl.sync();
+            }
             verdict = c0->verdict;
+            cl.sync();  // (read before the first CTA sets it again)
         }
-        if (verdict == kDone) {
-            cl.sync();  // (the first CTA's ctrl has been read)
-            return;
+        if (verdict == kDone) return;
+    }
+    if (verdict == kList) {
+        if (t == 0) c->count = 0;
+        __syncthreads();
+        gather_slice<DT>(row, V, w.b0, w.b1, c0->z_lo, s.buf, &c->count);
+        cl.sync();
+        if (cl.rank == 0) {
+            join_lists(cl, s, kCap);
+            const int n = (int)c->count, k = c->top_k;
+            const bool fits = n >= k && n <= kCap;
+            if (fits) {
+                sort_u64(s.buf, n);
+                if constexpr (!SAMPLE) {
+                    write_topk(a, s, k, o);
+                } else {
+                    keep_candidates(s, n, ListRule{k, true, true});
+                    pick_candidate<DT>(a, s, c->n, row, o);
+                }
+            }
+            if (t == 0) c->verdict = fits ? kDone : kRadix;
         }
+        cl.sync();
+        verdict = c0->verdict;
+        cl.sync();
+        if (verdict == kDone) return;
     }
     cl.sync();
 
@@ -1494,11 +1685,12 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
         if (!SAMPLE || list) {
             // the list, once more: every key from the cut on (or, when the
             // last key's ties overflow it, the keys above and the first ties)
-            if (cl.rank == 0 && t == 0) c->count = 0;
-            cl.sync();
-            gather_slice<DT>(row, V, w.b0, w.b1, key_value(list ? cut_key : cut_key + 1), dst, count);
+            if (t == 0) c->count = 0;
+            __syncthreads();
+            gather_slice<DT>(row, V, w.b0, w.b1, key_value(list ? cut_key : cut_key + 1), s.buf, &c->count);
             cl.sync();
             if (cl.rank == 0) {
+                join_lists(cl, s, kCap);
                 if (!list) {
                     if (t < 32) first_ties<DT>(row, V, nb, cut_key, cut_ties, s.buf, c);
                     __syncthreads();
@@ -1526,14 +1718,11 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
         batch_masses<DT>(row, V, w.b0, w.b1, cut_key, c->least, ws, s.bmass, s.bties);
         cl.sync();
         if (cl.rank == 0) {
+            join_masses(cl, s, nb, w.per);
             for (int rk = 1; rk < cl.split; ++rk) {
                 const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
-                const uint64_t* rm = cl.at(s.bmass, rk);
                 const uint32_t* rt = cl.at(s.bties, rk);
-                for (int i = x0 + t; i < x1; i += kThreads) {
-                    s.bmass[i] = rm[i];
-                    s.bties[i] = rt[i];
-                }
+                for (int i = x0 + t; i < x1; i += kThreads) s.bties[i] = rt[i];
             }
             if (t == 0) {
                 c->cut_key = cut_key;
@@ -1640,23 +1829,27 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
                 }
                 block_scan(v, c->scan, total);
                 // the sums' error, in 2^-24: 4 for each ex2 (the weight's and
-                // its batch's), 2.1 per unit of exponent (three roundings),
-                // whose mean over the mass is at most log2 V <= 20, 12 for
-                // ten levels of additions and the products: 2^-18 in all
+                // its batch's), 12 for eleven levels of additions and the
+                // products, 2.1 per unit of exponent (three roundings), whose
+                // mean over the mass is at most log2 V less log2 of the mass
                 if (t == 0) {
                     c->total = total;
-                    c->margin = (total >> 18) + nb;
+                    const float mean = fmaxf(0.f, __log2f((float)V) + 0.01f - __log2f((float)total * 0x1p-44f));
+                    c->margin = (total >> 24) * (uint64_t)(21.f + 2.1f * mean) + nb;
                     if (!SAMPLE && a.lse) a.lse[o] = m / a.temperature + logf((float)total * 0x1p-44f);
                 }
                 __syncthreads();
             }
             if constexpr (SAMPLE) {
                 verdict = sample_leader<DT>(a, s, w.row, V, nb, o, whole);
-                if (verdict == kTier1 && c->top_p < 1.f) place_bracket<DT>(w.row, V, nb, s);
+                if (verdict == kTier1 && filtered) verdict = place_bracket<DT>(w.row, V, s);
+                if (verdict == kList) verdict = place_list<DT>(w.row, V, k, s);
             } else {
                 const float least = whole ? -INFINITY : threshold_for(s.sub, nb * kRuns, k, m, c);
                 verdict = kRadix;
-                if (whole || least > -INFINITY) {
+                if (!whole && !(least > -INFINITY)) {
+                    verdict = place_list<DT>(w.row, V, k, s);
+                } else {
                     gather_runs<DT>(w.row, V, nb * kRuns, s, least);
                     const uint32_t n = c->count;
                     if (n <= (uint32_t)kCap) {
@@ -1669,15 +1862,16 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
         }
         if (DEFER) {
             if (t == 0 && verdict != kDone) {
-                const uint32_t bins = c->top_p < 1.f && verdict == kTier1 ? (uint32_t)c->bin_lo << 12 | c->bin_hi : 0u;
+                const bool placed = verdict == kMinP || verdict == kList || (verdict == kTier1 && filtered);
+                const uint32_t bins = placed ? (uint32_t)c->bin_lo << 12 | (uint32_t)(verdict == kList ? 0 : c->bin_hi) : 0u;
                 a.token[o] = (int32_t)(kOpenMark | (uint32_t)verdict << 24 | bins);
                 a.prob[o] = m;
             }
             return;
         }
         if (t == 0) {
-            c->verdict = verdict;
-            set_bracket(c);
+            set_bracket(c, verdict);
+            c->verdict = verdict == kMinP ? kTier1 : verdict;
         }
     }
     if (DEFER) return;
@@ -1739,15 +1933,16 @@ __global__ void __launch_bounds__(kThreads, 4) open_rows_kernel(const RowSearchA
             const float m = *cl.at(&s_max[i], 0);
             const int64_t q = a.row_index ? (int64_t)a.row_index[r] : r;
             const Work w(a, cl, q, a.gather ? r : q, Row<DT>::ESZ, BEL);
-            if (t == 0) {
+            if (t == 0) {  // every CTA of the cluster keeps the row's settings
                 load_settings<true>(a, w.o, c);
                 c->ws.m = m;
                 c->bin_lo = (int)(mark >> 12) & 0xfff;
                 c->bin_hi = (int)mark & 0xfff;
-                set_bracket(c);
+                set_bracket(c, (int)(mark >> 24) & 7);
             }
             cl.sync();
-            finish_row<DT, true>(a, cl, s, w, (int)(mark >> 24) & 7);
+            const int verdict = (int)(mark >> 24) & 7;
+            finish_row<DT, true>(a, cl, s, w, verdict == kMinP ? kTier1 : verdict);
         }
         cl.sync();
     }
