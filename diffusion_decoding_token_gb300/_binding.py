@@ -221,11 +221,17 @@ def row_stats(cur: torch.Tensor, prev: torch.Tensor | None = None, *, row_index:
 
 def _on(device, call, *args) -> None:
     """Run a C call on the current stream of the tensors' device."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        _check(call(*args, _stream(device)))
+    if device.index == torch.cuda.current_device():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with torch.cuda.device(device):
-            _check(call(*args, _stream(device)))
+            status = call(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if status != 0:
+        _check(status)
+
+
+def _ptr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _rows_arg(t: torch.Tensor, name: str) -> None:
@@ -245,7 +251,7 @@ def _same(t: torch.Tensor | None, shape, dtype, device, name: str, dtypes=None) 
     """An argument that is used in place: its shape, type, device and layout."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous() or \
+    if t.shape != shape or t.device != device or not t.is_contiguous() or \
             (t.dtype not in dtypes if dtypes else t.dtype != dtype):
         want = "/".join(str(d) for d in dtypes) if dtypes else str(dtype)
         raise ValueError(f"{name} must be a contiguous {want} tensor of shape {tuple(shape)} on {device}")
@@ -302,8 +308,8 @@ def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0, row_inde
         _same(out.values, (m, k), torch.float32, dev, "out.values")
         _same(out.ids, (m, k), torch.int32, dev, "out.ids")
         _same(out.lse, (m,), torch.float32, dev, "out.lse")
-    _on(dev, lib().dlm_row_topk, _p(logits), _dt(logits), n, logits.shape[1], _stride(logits), _p(row_index),
-        logits.shape[0], int(k), float(temperature), _p(out.values), _p(out.ids), _p(out.lse), _p(status),
+    _on(dev, lib().dlm_row_topk, _ptr(logits), _dt(logits), n, logits.shape[1], _stride(logits), _ptr(row_index),
+        logits.shape[0], int(k), float(temperature), _ptr(out.values), _ptr(out.ids), _ptr(out.lse), _ptr(status),
         ROWS_GATHER if gather else 0)
     return out
 
@@ -338,9 +344,9 @@ def row_sample(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.0, 
         _same(out.token, (m,), torch.int32, dev, "out.token")
         _same(out.prob, (m,), torch.float32, dev, "out.prob")
         _same(out.conf, (m,), torch.float32, dev, "out.conf")
-    _on(dev, lib().dlm_row_sample, _p(logits), _dt(logits), n, logits.shape[1], _stride(logits), _p(row_index),
-        logits.shape[0], _p(uniform), ctypes.byref(prm), _p(lse), _p(out.token), _p(out.prob), _p(out.conf),
-        _p(status), ROWS_GATHER if gather else 0)
+    _on(dev, lib().dlm_row_sample, _ptr(logits), _dt(logits), n, logits.shape[1], _stride(logits), _ptr(row_index),
+        logits.shape[0], _ptr(uniform), ctypes.byref(prm), _ptr(lse), _ptr(out.token), _ptr(out.prob), _ptr(out.conf),
+        _ptr(status), ROWS_GATHER if gather else 0)
     return out
 
 
@@ -353,7 +359,7 @@ def _distill_args(student, ids, teacher, weights, teacher_lse=None):
     _same(teacher, ids.shape, None, dev, "teacher", tuple(_DT))
     _same(weights, (rows,), torch.float32, dev, "weights")
     _same(teacher_lse, (rows,), torch.float32, dev, "teacher_lse")
-    return (_p(student), _dt(student), rows, student.shape[1], _stride(student), _p(ids), _p(teacher), _dt(teacher),
+    return (_ptr(student), _dt(student), rows, student.shape[1], _stride(student), _ptr(ids), _ptr(teacher), _dt(teacher),
             ids.shape[1])
 
 
@@ -385,8 +391,8 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
     else:
         _same(out.loss, (rows,), torch.float32, dev, "out.loss")
         _same(out.state, (rows, DISTILL_STATE), torch.float32, dev, "out.state")
-    _on(dev, lib().dlm_distill_loss, *args, _p(teacher_lse), float(temperature), _p(weights), _p(out.loss),
-        _p(out.state), _p(status))
+    _on(dev, lib().dlm_distill_loss, *args, _ptr(teacher_lse), float(temperature), _ptr(weights), _ptr(out.loss),
+        _ptr(out.state), _ptr(status))
     return out
 
 
@@ -402,8 +408,8 @@ def distill_grad(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
     _same(state, (rows, DISTILL_STATE), torch.float32, dev, "state")
     _same(grad_loss, (rows,), torch.float32, dev, "grad_loss")
     out = _grad_out(student, out)
-    _on(dev, lib().dlm_distill_grad, *args, float(temperature), _p(weights), _p(state), _p(grad_loss), _p(out),
-        _stride(out), _p(status))
+    _on(dev, lib().dlm_distill_grad, *args, float(temperature), _ptr(weights), _ptr(state), _ptr(grad_loss), _ptr(out),
+        _stride(out), _ptr(status))
     return out
 
 
@@ -421,8 +427,8 @@ def distill_step(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
     else:
         _same(loss, (rows,), torch.float32, dev, "loss")
     grad = _grad_out(student, grad)
-    _on(dev, lib().dlm_distill_step, *args, _p(teacher_lse), float(temperature), _p(weights), _p(loss), _p(grad),
-        _stride(grad), _p(status))
+    _on(dev, lib().dlm_distill_step, *args, _ptr(teacher_lse), float(temperature), _ptr(weights), _ptr(loss), _ptr(grad),
+        _stride(grad), _ptr(status))
     return loss, grad
 
 

@@ -51,7 +51,7 @@ constexpr int kFine = 1024;            // bins that a bracket's tokens are sorte
 constexpr int kListRuns = 128;         // run maxima that open a nucleus' candidate list
 constexpr int kBracketSide = 1200;     // tokens on either side of its middle
 constexpr int kSampleTokens = 16384;   // the sample that places a bracket
-constexpr int kOpenSplit = 4;          // CTAs per row that the first launch left open
+constexpr int kOpenSplit = 2;          // CTAs per row that the first launch left open
 constexpr int kTries = 4;              // brackets that a row gets
 constexpr int kListTopk = 1700;        // largest top-k whose list a sample's threshold can be trusted with
 constexpr uint64_t kOne = 1ull << kWeightBits;
@@ -176,7 +176,9 @@ __device__ __forceinline__ void shared_add(uint64_t* p, uint64_t v) {
 
 // Sort buf[0, n) ascending (n <= kBracketCap).  Short lists by rank (every thread
 // counts the smaller ones, broadcast reads, two barriers), longer ones by a
-// bitonic network padded to a power of two.
+// bitonic network padded to a power of two: each warp has an eighth of it, and
+// only the steps that reach past an eighth (6 of 66 for 2048) need the block's
+// barrier.
 __device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
     if (n <= kThreads) {
         const int i = threadIdx.x;
@@ -193,19 +195,28 @@ __device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
     while (m < n) m <<= 1;
     for (int i = n + threadIdx.x; i < m; i += kThreads) buf[i] = ~0ull;
     __syncthreads();
+    const int lane = threadIdx.x & 31, seg = m / kWarps, first = (threadIdx.x >> 5) * seg;
+    auto step = [&](int i, int k, int j) {
+        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+        const uint64_t a = buf[lo], b = buf[hi];
+        if ((a > b) == ((lo & k) == 0)) {
+            buf[lo] = b;
+            buf[hi] = a;
+        }
+    };
     for (int k = 2; k <= m; k <<= 1) {
         for (int j = k >> 1; j > 0; j >>= 1) {
-            for (int i = threadIdx.x; i < m / 2; i += kThreads) {
-                const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-                const uint64_t a = buf[lo], b = buf[hi];
-                if ((a > b) == ((lo & k) == 0)) {
-                    buf[lo] = b;
-                    buf[hi] = a;
-                }
+            if (2 * j <= seg) {
+                for (int i = first / 2 + lane; i < (first + seg) / 2; i += 32) step(i, k, j);
+                __syncwarp();
+            } else {
+                if (2 * j == k) __syncthreads();  // (the steps before it were the warps' own)
+                for (int i = threadIdx.x; i < m / 2; i += kThreads) step(i, k, j);
+                __syncthreads();
             }
-            __syncthreads();
         }
     }
+    __syncthreads();
 }
 
 // A candidate: sorts by logit descending, then position ascending.
@@ -254,6 +265,33 @@ __device__ float threshold_for(const float* sub, int n, int k, float m, Ctrl* c)
     }
     __syncthreads();
     return lo;
+}
+
+// Keeps of the n > kThreads candidates in buf the first k of the order and few
+// more, where that makes the list short enough to need no sort: the threshold
+// search over the candidates' values, then the rest is copied out and back.
+// Returns how many are left.
+__device__ int top_candidates(const Smem& s, int n, int k) {
+    if (n <= kThreads || k > kThreads * 3 / 4) return n;
+    const int t = threadIdx.x;
+    Ctrl* c = s.c;
+    float* values = reinterpret_cast<float*>(s.wbuf);
+    uint64_t* out = s.wbuf + kCap / 2;
+    for (int i = t; i < n; i += kThreads) values[i] = candidate_value(s.buf[i]);
+    if (t == 0) c->runs = 0;
+    __syncthreads();
+    const float least = threshold_for(values, n, k, c->ws.m, c);
+    for (int i = t; i < n; i += kThreads)
+        if (values[i] >= least) {
+            const uint32_t at = atomicAdd(&c->runs, 1u);
+            if (at < (uint32_t)kThreads) out[at] = s.buf[i];
+        }
+    __syncthreads();
+    const int left = (int)c->runs;
+    if (left > kThreads) return n;  // ties
+    if (t < left) s.buf[t] = out[t];
+    __syncthreads();
+    return left;
 }
 
 // Push the elements z >= least of one loaded vector of each lane (positions
@@ -344,9 +382,10 @@ __device__ __noinline__ void gather_slice(const char* row, int64_t V, int b0, in
 
 // Run maxima of batches [b0, b1), and with `sums` each batch's sum of
 // 2^((z - ref) c), ref the batch's maximum (a batch of -inf only sums to 0).
-// The next batch is loaded while one is summed.  Returns the warp's maximum.
-template <int DT>
-__device__ __forceinline__ float scan_rows(const char* row, int64_t V, int b0, int b1, bool sums, float c, float* sub,
+// The next batch is loaded while one is summed, and the first while `begin` finds
+// out the scale (0: no sums; negative: leave).  Returns the warp's maximum.
+template <int DT, typename F>
+__device__ __forceinline__ float scan_rows(const char* row, int64_t V, int b0, int b1, F begin, float* sub,
                                            float* bsum) {
     constexpr int EPV = Row<DT>::EPV;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -363,6 +402,9 @@ __device__ __forceinline__ float scan_rows(const char* row, int64_t V, int b0, i
     float most = -INFINITY;
     uint4 next[kRuns];
     if (b0 + warp < b1) fetch(b0 + warp, next);
+    const float c = begin();
+    const bool sums = c > 0.f;
+    if (c < 0.f) return 0.f;
     for (int b = b0 + warp; b < b1; b += kWarps) {
         uint4 w[kRuns];
 #pragma unroll
@@ -415,8 +457,7 @@ __device__ __forceinline__ void write_token(const RowSearchArgs& a, const Ctrl* 
     const float y = weight_exponent(z, c->ws, lo);
     // 2^-(y + lo) over the kept mass
     const float w = exp2f(-y) * fmaf(lo, -kLn2, 1.0f);
-    *(volatile int32_t*)(a.token + o) = token;
-    __threadfence();  // the token first: open_rows_kernel takes prob only while the mark stands
+    a.token[o] = token;
     a.prob[o] = y < INFINITY ? fminf(1.0f, w / ((float)mass * 0x1p-44f)) : 0.f;
     if (a.conf) a.conf[o] = expf(z - a.lse_in[o]);
 }
@@ -1086,12 +1127,21 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
     const float z_min = fmaxf(ws.m - 99.f / ws.c_hi, -FLT_MAX);  // a weight of 2^-99 counts as 0
     const SplitScale sp{pack2(ws.m, ws.m), pack2(-ws.c_hi, -ws.c_hi), pack2(-ws.c_lo, -ws.c_lo)};
     uint64_t whole = 0, top = 0, sum = 0;
+    uint4 next[kRuns];  // the next batch is loaded while one is summed
+    if (b0 + warp < b1) {
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) next[i] = load_vec<DT>(row, V, (b0 + warp) * kBatchVecs + i * 32 + lane);
+    }
     for (int b = b0 + warp; b < b1; b += kWarps) {
         uint64_t above = 0;
         uint4 w4[kRuns];
         const int v0 = b * kBatchVecs + lane;
 #pragma unroll
-        for (int i = 0; i < kRuns; ++i) w4[i] = load_vec<DT>(row, V, v0 + i * 32);
+        for (int i = 0; i < kRuns; ++i) w4[i] = next[i];
+        if (b + kWarps < b1) {
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) next[i] = load_vec<DT>(row, V, v0 + kWarps * kBatchVecs + i * 32);
+        }
         uint32_t mask = 0;  // tokens inside, a bit each
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
@@ -1544,10 +1594,10 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
         return sure ? kDone : kTier1;
     }
     gather_runs<DT>(row, V, nsub, s, least);
-    const uint32_t n = c->count;
     // a top-k's ties go over the whole row
     const int other = k == 0 ? kTier1 : kRadix;
-    if (n > (uint32_t)kCap) return other;
+    if (c->count > (uint32_t)kCap) return other;
+    const uint32_t n = k > 0 ? (uint32_t)top_candidates(s, (int)c->count, k) : c->count;
     if (n <= (uint32_t)kThreads) return decide_small(a, s, (int)n, rule, o) ? kDone : other;
     sort_u64(s.buf, (int)n);
     keep_candidates(s, (int)n, rule);
@@ -1749,7 +1799,7 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
 // A row that the first launch leaves to the second: bits 24..26 of its token
 // hold the verdict, below them the bracket's bins; the sign marks it (a token
 // of -1, a row without one, has the bits above 26 set).  Its maximum is in prob.
-constexpr uint32_t kOpenMask = 0xf8000000u, kOpenMark = 0x80000000u;
+constexpr uint32_t kOpenMask = 0xf8000000u, kOpenMark = 0x80000000u, kClaimed = 0x08000000u;
 
 // DEFER: rows that the first pass leaves open go to open_rows_kernel.
 template <int DT, bool SAMPLE, bool DEFER>
@@ -1773,8 +1823,18 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
     const Smem s = carve(s_raw, nb);
     Ctrl* c = s.c;
 
-    if (t == 0) load_settings<SAMPLE>(a, o, c);
-    __syncthreads();
+    // Every logit of a short row fits the list, if a filter makes one.  A
+    // top-k within the list needs no sums, and min-p without top-p neither.
+    bool filtered = true, whole = false, sums = true;
+    const float most = scan_rows<DT>(w.row, V, w.b0, w.b1, [&]() {
+        if (t == 0) load_settings<SAMPLE>(a, o, c);
+        __syncthreads();
+        if (SAMPLE && c->bad) return -1.f;
+        filtered = c->top_k > 0 || c->top_p < 1.f || c->least > 0;
+        whole = V <= kCap && filtered;
+        sums = !SAMPLE || (c->top_k == 0 && !whole && (c->top_p < 1.f || c->least == 0));
+        return sums ? c->ws.c_hi : 0.f;
+    }, s.sub, s.bsum);
     if (SAMPLE && c->bad) {
         if (cl.rank == 0 && t == 0) {
             write_none(a, o);
@@ -1782,13 +1842,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
         }
         return;
     }
-    // Every logit of a short row fits the list, if a filter makes one.  A
-    // top-k within the list needs no sums, and min-p without top-p neither.
     const int k = c->top_k;
-    const bool filtered = k > 0 || c->top_p < 1.f || c->least > 0;
-    const bool whole = V <= kCap && filtered;
-    const bool sums = !SAMPLE || (k == 0 && !whole && (c->top_p < 1.f || c->least == 0));
-    const float most = scan_rows<DT>(w.row, V, w.b0, w.b1, sums, c->ws.c_hi, s.sub, s.bsum);
     if ((t & 31) == 0) c->wmax[t >> 5] = most;
     cl.sync();
 
@@ -1851,10 +1905,10 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
                     verdict = place_list<DT>(w.row, V, k, s);
                 } else {
                     gather_runs<DT>(w.row, V, nb * kRuns, s, least);
-                    const uint32_t n = c->count;
-                    if (n <= (uint32_t)kCap) {
-                        sort_u64(s.buf, (int)n);
-                        write_topk(a, s, min((int)n, k), o);
+                    if (c->count <= (uint32_t)kCap) {
+                        const int n = top_candidates(s, (int)c->count, k);
+                        sort_u64(s.buf, n);
+                        write_topk(a, s, min(n, k), o);
                         verdict = kDone;
                     }
                 }
@@ -1883,69 +1937,84 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
         finish_row<DT, SAMPLE>(a, cl, s, w, verdict);
 }
 
-// The rows that row_search_kernel left open: cluster i of the grid looks at
-// rows i, i + clusters, ...  A row that is listed twice (a repeated row index)
-// may be finished by another cluster between two looks: its maximum is taken
-// only if the mark still stands after it was read (write_token writes the token
-// first), and finishing it again writes the same values.
+// The rows that row_search_kernel left open.  Which rows they are is not known
+// at the launch, and a cluster takes tens of microseconds for one, so clusters
+// claim them: the first CTA looks for a marked token, each cluster from its own
+// place in the batch on, and changes the mark to a claimed one.  (Rows i,
+// i + clusters, ... for cluster i, without claims: the cluster with the most
+// open rows had twice the average and set the time, 440 us for 839 rows.)
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 4) open_rows_kernel(const RowSearchArgs a) {
     extern __shared__ __align__(16) unsigned char s_raw[];
-    __shared__ int s_row[kThreads], s_mark[kThreads];
-    __shared__ float s_max[kThreads];
-    __shared__ int s_n;
+    __shared__ unsigned long long s_pick;
+    __shared__ int64_t s_row;
+    __shared__ uint32_t s_mark;
     const int t = threadIdx.x;
     Cluster cl;
     cl.split = a.split;
     cl.rank = (int)(blockIdx.x % a.split);
-    const int64_t first = blockIdx.x / a.split, step = gridDim.x / a.split;
+    const int64_t place = (int64_t)(blockIdx.x / a.split) * a.n_rows / (gridDim.x / a.split);
     constexpr int BEL = kBatchVecs * Row<DT>::EPV;
     const Smem s = carve(s_raw, (int)((a.vocab + BEL - 1) / BEL));
     Ctrl* c = s.c;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the first launch's marks
-    for (int64_t base = first; base < a.n_rows; base += step * kThreads) {
-        if (t == 0) s_n = 0;
-        __syncthreads();
+    int64_t from = 0;  // rows looked at, from `place` on, that are not open any more
+    while (true) {
         if (cl.rank == 0) {
-            const int64_t r = base + t * step;
-            const int64_t q = r >= a.n_rows ? -1 : a.row_index ? (int64_t)a.row_index[r] : r;
-            if (q >= 0 && !(a.n_src > 0 && q >= a.n_src)) {
-                const int64_t o = a.gather ? r : q;
-                const volatile int32_t* token = a.token + o;
-                const int32_t mark = *token;
-                if (((uint32_t)mark & kOpenMask) == kOpenMark) {
-                    const float m = *(const volatile float*)(a.prob + o);
-                    __threadfence();
-                    if (*token == mark) {
-                        const int i = atomicAdd(&s_n, 1);
-                        s_row[i] = t;
-                        s_mark[i] = mark;
-                        s_max[i] = m;
+            if (t == 0) s_row = -1;
+            while (from < a.n_rows) {
+                // the first marked row of the next kThreads
+                if (t == 0) s_pick = ~0ull;
+                __syncthreads();
+                const int64_t i = from + t;
+                int64_t r = place + i;
+                if (r >= a.n_rows) r -= a.n_rows;
+                const int64_t q = i >= a.n_rows ? -1 : a.row_index ? (int64_t)a.row_index[r] : r;
+                if (q >= 0 && !(a.n_src > 0 && q >= a.n_src)) {
+                    const int32_t mark = *(const volatile int32_t*)(a.token + (a.gather ? r : q));
+                    if (((uint32_t)mark & kOpenMask) == kOpenMark) atomicMin(&s_pick, (unsigned long long)i);
+                }
+                __syncthreads();
+                const unsigned long long pick = s_pick;
+                __syncthreads();
+                if (pick == ~0ull) {
+                    from += kThreads;
+                    continue;
+                }
+                if (t == 0) {
+                    int64_t row = place + (int64_t)pick;
+                    if (row >= a.n_rows) row -= a.n_rows;
+                    const int64_t o = a.gather || !a.row_index ? row : (int64_t)a.row_index[row];
+                    const int32_t mark = *(const volatile int32_t*)(a.token + o);
+                    if (((uint32_t)mark & kOpenMask) == kOpenMark &&
+                        atomicCAS(a.token + o, mark, (int32_t)((uint32_t)mark | kClaimed)) == mark) {
+                        s_row = row;
+                        s_mark = (uint32_t)mark;
                     }
                 }
+                __syncthreads();
+                from = (int64_t)pick + 1;
+                if (s_row >= 0) break;
             }
         }
         cl.sync();
-        const int n = *cl.at(&s_n, 0);
-        for (int i = 0; i < n; ++i) {
-            const int64_t r = base + *cl.at(&s_row[i], 0) * step;
-            const uint32_t mark = (uint32_t)*cl.at(&s_mark[i], 0);
-            const float m = *cl.at(&s_max[i], 0);
-            const int64_t q = a.row_index ? (int64_t)a.row_index[r] : r;
-            const Work w(a, cl, q, a.gather ? r : q, Row<DT>::ESZ, BEL);
-            if (t == 0) {  // every CTA of the cluster keeps the row's settings
-                load_settings<true>(a, w.o, c);
-                c->ws.m = m;
-                c->bin_lo = (int)(mark >> 12) & 0xfff;
-                c->bin_hi = (int)mark & 0xfff;
-                set_bracket(c, (int)(mark >> 24) & 7);
-            }
-            cl.sync();
-            const int verdict = (int)(mark >> 24) & 7;
-            finish_row<DT, true>(a, cl, s, w, verdict == kMinP ? kTier1 : verdict);
+        const int64_t r = *cl.at(&s_row, 0);
+        const uint32_t mark = *cl.at(&s_mark, 0);
+        if (r < 0) break;
+        const int64_t q = a.row_index ? (int64_t)a.row_index[r] : r;
+        const Work w(a, cl, q, a.gather ? r : q, Row<DT>::ESZ, BEL);
+        const int verdict = (int)(mark >> 24) & 7;
+        if (t == 0) {  // every CTA of the cluster keeps the row's settings
+            load_settings<true>(a, w.o, c);
+            c->ws.m = *(const volatile float*)(a.prob + w.o);
+            c->bin_lo = (int)(mark >> 12) & 0xfff;
+            c->bin_hi = (int)mark & 0xfff;
+            set_bracket(c, verdict);
         }
         cl.sync();
+        finish_row<DT, true>(a, cl, s, w, verdict == kMinP ? kTier1 : verdict);
     }
+    cl.sync();  // (the first CTA's choice has been read)
 }
 
 template <int DT>
@@ -1957,7 +2026,7 @@ size_t smem_for(int64_t V) {
 template <int DT, typename F>
 cudaError_t launch_rows(F kernel, const RowSearchArgs& a, int64_t grid, bool programmatic, cudaStream_t st) {
     const size_t smem = smem_for<DT>(a.vocab);
-    if (smem > 40 * 1024) {  // the same limit whatever the call's size: calls may run side by side
+    if (smem > 47 * 1024) {  // (static shared memory on top) the same limit whatever the call's size: calls may run side by side
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)smem_for<DT>(DLM_MAX_SEARCH_VOCAB));
         if (e != cudaSuccess) return e;
@@ -1988,12 +2057,15 @@ cudaError_t launch_rows(F kernel, const RowSearchArgs& a, int64_t grid, bool pro
 
 template <int DT>
 cudaError_t launch_sample(const RowSearchArgs& a, cudaStream_t st) {
-    if (a.split > 1) return launch_rows<DT>(row_search_kernel<DT, true, false>, a, a.n_rows * a.split, false, st);
+    // rows of fewer batches than two per warp are finished where they are: a
+    // pass over one takes its CTA less than a launch does
+    if (a.split > 1 || a.vocab <= 2 * kWarps * kBatchVecs * Row<DT>::EPV)
+        return launch_rows<DT>(row_search_kernel<DT, true, false>, a, a.n_rows * a.split, false, st);
     const cudaError_t e = launch_rows<DT>(row_search_kernel<DT, true, true>, a, a.n_rows, false, st);
     if (e != cudaSuccess) return e;
     RowSearchArgs open = a;
     open.split = kOpenSplit;
-    const int64_t clusters = a.n_rows < a.num_sms ? a.n_rows : a.num_sms;
+    const int64_t slots = (int64_t)a.num_sms * 4 / kOpenSplit, clusters = a.n_rows < slots ? a.n_rows : slots;
     return launch_rows<DT>(open_rows_kernel<DT>, open, clusters * kOpenSplit, true, st);
 }
 
