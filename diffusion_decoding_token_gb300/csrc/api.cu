@@ -713,8 +713,9 @@ static dlm_status distill_prepare(dlm::DistillArgs& a, const void* student, dlm_
     a.temperature = temperature;
     a.weights = weights;
     a.dev_status = dev_status;
-    a.split = dlm::distill_split(dtype, n_rows, vocab, sm_count());
-    if (n_rows > 0x7fffffffLL / a.split) return DLM_ERR_INVALID_ARG;
+    a.inv_t = 1.0 / (double)temperature;
+    a.scale = (float)(1.4426950408889634 * a.inv_t);
+    if (n_rows > 0x7fffffffLL / 8) return DLM_ERR_INVALID_ARG;  // up to 8 CTAs per row
     return DLM_OK;
 }
 
@@ -743,6 +744,7 @@ dlm_status dlm_distill_loss(const void* student, dlm_dtype dtype, int64_t n_rows
     a.teacher_lse = teacher_lse;
     a.loss = loss;
     a.state = state;
+    dlm::distill_plan(a, dtype, sm_count());
     return from_cuda(dlm::launch_distill_loss(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -761,6 +763,7 @@ dlm_status dlm_distill_grad(const void* student, dlm_dtype dtype, int64_t n_rows
     a.grad_loss = grad_loss;
     a.grad = grad;
     a.grad_stride = grad_stride;
+    dlm::distill_plan(a, dtype, sm_count());
     return from_cuda(dlm::launch_distill_grad(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -779,6 +782,7 @@ dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows
     a.loss = loss;
     a.grad = grad;
     a.grad_stride = grad_stride;
+    dlm::distill_plan(a, dtype, sm_count());
     return from_cuda(dlm::launch_distill_loss(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 

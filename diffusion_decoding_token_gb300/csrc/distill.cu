@@ -7,16 +7,32 @@
 //   loss   = w [ sum_j p_j (ln p_j - ln q_{id_j}) + p_rest (ln p_rest - ln q_rest) ]
 //   dl/ds_v = w / T (q_v - p_v)                  v listed (p_v: all its entries)
 //   dl/ds_v = w / T q_v (1 - p_rest / q_rest)    otherwise (p_rest = 0: w / T q_v)
+//
 // Everything the gradient needs of a row is its maximum, 1 / sum, the factor
 // of the tokens that are not listed, and the list: `state` holds it between
 // the two calls.
 //
-// The loss reads the row once (HBM-bound).  q_rest = 1 - sum q_id would lose
-// all digits for a peaked student, so the sum over the tokens that are not
-// listed is taken apart from the start: a bitmap of the CTA's slice in shared
-// memory marks the listed ones, and one byte of it answers for a whole vector.
-// The gradient is written for every token as if none were listed, and then the
-// listed ones are written over (the block barrier between orders the two).
+// All three are bound by HBM: the loss by one read of the row, the gradient by a
+// read and a write.
+//  * distill_stream_kernel streams a row through registers for its loss.
+//  * The step needs the row twice, once for its sums and once for the gradient:
+//    distill_row_kernel holds it on chip in between.  A cluster's CTAs copy a
+//    slice each (about 40 KB, five CTAs per SM) into shared memory with
+//    asynchronous copies, read the teacher's list while those are on their way,
+//    add up their slice, exchange sums through distributed shared memory and
+//    write their slice's gradient.  The gradient alone is the same without the
+//    sums.  How long a CTA lives decides (its slice takes its share of the SM's
+//    shared memory meanwhile), so its reductions share five barriers, and only
+//    one thread of a row does 64-bit arithmetic on the sums.
+//  * Rows that eight CTAs can not hold (above 1.5 MB) are streamed twice.
+//
+// q_rest = 1 - sum q_id would lose all digits for a peaked student, so the sum
+// over the tokens that are not listed is taken apart from the start: the row
+// kernel takes the listed logits out of its slice (-inf in their place), the
+// stream kernel marks them in a bitmap, one byte of which answers for a whole
+// vector.  The gradient is written for every token as if none were listed, and
+// then the listed ones are written over (the block barrier between orders the
+// two).
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
@@ -37,55 +53,52 @@ constexpr float kUnit = 5.684341886080802e-14f;  // 2^-44
 struct Sums {
     float mx, ref, all, rest;
 };
+// What a warp or a CTA knows of a row: its sums and its share of the loss,
+// part = sum w_j (t_j - s_j) / T and w = sum w_j over its listed entries (the
+// teacher's weights before they are normalised).
+struct Share {
+    Sums q;
+    float part, w;
+};
 
-__device__ __forceinline__ void merge(Sums& a, const Sums& b, float c) {
-    const float r = fmaxf(a.ref, b.ref);
-    const float ea = ex2((a.ref - r) * c), eb = ex2((b.ref - r) * c);
-    a.all = a.all * ea + b.all * eb;
-    a.rest = a.rest * ea + b.rest * eb;
-    a.ref = r;
-    a.mx = max_nan(a.mx, b.mx);
-}
-
-// Merge over the warp in a fixed order (lower lane first), all lanes agree.
-__device__ __forceinline__ void warp_merge(Sums& a, float c) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        Sums b;
-        b.mx = __shfl_xor_sync(DLM_FULL_MASK, a.mx, o);
-        b.ref = __shfl_xor_sync(DLM_FULL_MASK, a.ref, o);
-        b.all = __shfl_xor_sync(DLM_FULL_MASK, a.all, o);
-        b.rest = __shfl_xor_sync(DLM_FULL_MASK, a.rest, o);
-        if (threadIdx.x & o) {
-            merge(b, a, c);
-            a = b;
-        } else {
-            merge(a, b, c);
-        }
-    }
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(DLM_FULL_MASK, v, o);
+    return v;
 }
+
+// The sum over the lanes in a fixed order, all lanes get it: a common reference
+// first, then plain sums.
+__device__ __forceinline__ Share warp_share(Share a, float c) {
+    const float ref = warp_max_nan(a.q.ref);
+    a.q.mx = warp_max_nan(a.q.mx);
+    const float up = ex2((a.q.ref - ref) * c);
+    a.q.all = warp_sum(a.q.all * up);
+    a.q.rest = warp_sum(a.q.rest * up);
+    a.q.ref = ref;
+    a.part = warp_sum(a.part);
+    a.w = warp_sum(a.w);
+    return a;
+}
+
+__device__ __forceinline__ Share no_share() { return Share{Sums{-INFINITY, -FLT_MAX, 0.f, 0.f}, 0.f, 0.f}; }
 
 struct Shared {
-    Sums warp[kWarps];
-    Sums cta;
-    Sums row;
-    uint64_t scan[kWarps];
-    float fscan[kWarps];
-    double dscan[kWarps];
-    float m, inv, tail;       // the row's state
-    float p_rest;
-    int any;                  // listed entries in range
-    int bad;                  // a teacher logit was NaN or +inf
-    int repeated;             // an id is listed more than once
+    Share warp[kWarps];
+    Share cta;
+    float list_max[kWarps];
+    uint64_t list_sum[kWarps];
+    int flags;                // kAny, kBad, kTwice
 };
+enum : int { kAny = 1, kBad = 2, kTwice = 4 };  // an entry; a teacher logit is NaN or +inf; an id may be listed twice
 
 // The list in shared memory.
 struct List {
     int32_t* id;     // -1: no entry
     float* t;        // teacher logit
-    float* p;        // teacher probability
+    float* p;        // teacher weight, not normalised
     float* s;        // student logit (entries of this CTA's slice)
-    uint32_t* bits;  // the listed tokens of this CTA's slice
+    uint32_t* bits;  // stream kernel: the listed tokens of this CTA's slice
 };
 
 __host__ __device__ inline size_t shared_bytes() { return (sizeof(Shared) + 15) & ~(size_t)15; }
@@ -101,6 +114,9 @@ __device__ __forceinline__ List carve(unsigned char* p, int k) {
     return l;
 }
 
+// Bytes of shared memory before a slice.
+__host__ __device__ inline size_t slice_offset(int k) { return (shared_bytes() + (size_t)k * 16 + 15) & ~(size_t)15; }
+
 __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
     switch (a.teacher_dtype) {
     case DLM_BF16: return Row<DLM_BF16>::scalar(a.teacher, i);
@@ -109,58 +125,63 @@ __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
     }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* scratch) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(DLM_FULL_MASK, v, o);
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double s = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += scratch[w];
-    __syncthreads();
-    return s;
+// ln x for x >= 1 to 2^-36: the float logarithm's error is what x 2^-y is off 1
+// by, with 2^-y from the integer weights.  (64-bit arithmetic has a 64th of the
+// 32-bit rate here: a double logarithm by every thread of a CTA took 7 us.)
+__device__ __forceinline__ double log_exact(float x) {
+    const float y = fmaxf(0.f, __log2f(x));
+    const double d = (double)x * ((double)weight44_of(y, 0.f) * (double)kUnit) - 1.0;
+    return (double)y * 0.6931471805599453 + (d - 0.5 * d * d);
 }
 
-// Reads the row's list and turns the teacher's logits into probabilities.
-// lse_t is used when rest.  Returns the natural log of the teacher's
-// normaliser (t / T - log_z = ln p).
-__device__ double read_list(const DistillArgs& a, const List& l, Shared& sh, int64_t r, bool rest, float lse_t) {
-    const int t = threadIdx.x, K = a.k;
+// The list in two steps with a barrier after each.  First: entries into shared
+// memory, their maximum per warp.  (sh.flags has been zeroed.)
+__device__ __forceinline__ void list_load(const DistillArgs& a, const List& l, Shared& sh, int64_t r, float lse_t) {
     float mx = -INFINITY;
-    bool any = false, bad = false;
-    for (int j = t; j < K; j += kThreads) {
-        int id = a.ids[r * K + j];
+    int flags = fabsf(lse_t) < INFINITY ? 0 : kBad;
+    for (int j = threadIdx.x; j < a.k; j += kThreads) {
+        int id = a.ids[r * a.k + j];
         if (id >= a.vocab) {
             id = -1;
             raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
         }
-        const float x = teacher_at(a, r * K + j);
+        const float x = teacher_at(a, r * a.k + j);
         if (id >= 0) {
-            any = true;
-            bad |= !(x < INFINITY);  // +inf or NaN
+            flags |= x < INFINITY ? (x > -INFINITY ? kAny : 0) : kBad;
             mx = fmaxf(mx, x);
         }
         l.id[j] = id < 0 ? -1 : id;
         l.t[j] = x;
     }
-    if (rest) bad |= !(fabsf(lse_t) < INFINITY);
-    mx = block_max_nan(mx, sh.fscan);
-    any = __syncthreads_or(any);
-    bad = __syncthreads_or(bad);
-    const double inv_t = 1.0 / (double)a.temperature;
-    const bool none = mx == -INFINITY;  // no entry, or only such that carry nothing
-    const WeightScale ws = weight_scale(none ? 0.f : mx, a.temperature);
+    mx = warp_max_nan(mx);
+    flags = __reduce_or_sync(DLM_FULL_MASK, flags);
+    if ((threadIdx.x & 31) == 0) {
+        sh.list_max[threadIdx.x >> 5] = mx;
+        if (flags) atomicOr(&sh.flags, flags);
+    }
+}
+
+// Second: the teacher's weights, 2^-(y + lo) each, relative to the list's
+// maximum or (rest) to the teacher's log-sum-exp.  The integer weight serves the
+// sum, which p_rest is the difference of 1 and; the float keeps all its digits
+// for a small one.
+__device__ __forceinline__ float list_max(const Shared& sh) {
+    float mx = sh.list_max[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sh.list_max[w]);
+    return mx;
+}
+__device__ __forceinline__ void list_weigh(const DistillArgs& a, const List& l, Shared& sh, bool rest, float lse_t) {
+    const float mx = list_max(sh);
+    const WeightScale ws = weight_scale(mx > -INFINITY ? mx : 0.f, a.temperature);
     uint64_t sum = 0;
-    for (int j = t; j < K; j += kThreads) {
+    for (int j = threadIdx.x; j < a.k; j += kThreads) {
         float p = 0.f;
         if (l.id[j] >= 0) {
-            // p (before the renormalisation) = 2^-(y + lo); the integer weight
-            // serves the sum, which p_rest is the difference of 1 and, and the
-            // float keeps all its digits for a small p
             float y, lo;
             if (rest) {
                 // a lse_t below the logits (p above 1) counts as p = 1
-                const double d = fmax(0.0, ((double)lse_t - (double)l.t[j] * inv_t) * 1.4426950408889634);
+                const double d = fmax(0.0, ((double)lse_t - (double)l.t[j] * a.inv_t) * 1.4426950408889634);
                 y = (float)d;
                 lo = y < INFINITY ? (float)(d - (double)y) : 0.f;
             } else {
@@ -171,22 +192,84 @@ __device__ double read_list(const DistillArgs& a, const List& l, Shared& sh, int
         }
         l.p[j] = p;
     }
-    uint64_t total;
-    block_scan(sum, sh.scan, total);
-    double log_z = lse_t;
-    if (!rest) {
-        const float inv = total ? 1.0f / ((float)total * kUnit) : 0.f;
-        for (int j = t; j < K; j += kThreads) l.p[j] *= inv;
-        log_z = (double)mx * inv_t + log((double)total * (double)kUnit);
+    sum = (uint64_t)warp_sum_ll((long long)sum);
+    if ((threadIdx.x & 31) == 0) sh.list_sum[threadIdx.x >> 5] = sum;
+}
+
+// What follows from the list as a whole (after the second barrier).
+struct Teacher {
+    uint64_t sum;    // of the weights, in 2^-44
+    float inv;       // 1 / sum, or 1 when the rest is a class: weight to probability
+    float p_rest;
+    bool any, bad, twice;
+};
+__device__ __forceinline__ Teacher list_total(const Shared& sh, bool rest) {
+    Teacher t;
+    t.sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) t.sum += sh.list_sum[w];
+    const uint64_t one = 1ull << kWeightBits;
+    t.inv = rest ? 1.f : t.sum ? 1.0f / ((float)t.sum * kUnit) : 0.f;
+    t.p_rest = rest && t.sum < one ? (float)(one - t.sum) * kUnit : 0.f;
+    t.any = sh.flags & kAny;
+    t.bad = sh.flags & kBad;
+    t.twice = sh.flags & kTwice;
+    return t;
+}
+
+// The listed tokens of a slice [e0, e1) in its bitmap (zeroed before).
+__device__ __forceinline__ void mark_listed(const List& l, int K, int64_t e0, int64_t e1) {
+    for (int j = threadIdx.x; j < K; j += kThreads) {
+        const int64_t id = l.id[j];
+        if (id >= e0 && id < e1) atomicOr(&l.bits[(id - e0) >> 5], 1u << ((id - e0) & 31));
     }
-    if (t == 0) {
-        sh.any = any && !none;
-        sh.bad = bad;
-        const uint64_t one = 1ull << kWeightBits;
-        sh.p_rest = rest && total < one ? (float)(one - total) * kUnit : 0.f;
+}
+
+// The row's loss (one thread): q relative to the row's maximum, the share of
+// the loss over the whole list, and the list's maximum.
+__device__ float row_loss(const DistillArgs& a, const Teacher& tch, float weight, const Share& row, bool rest,
+                          float lse_t, float list_mx) {
+    const Sums& q = row.q;
+    // ln p_j = t_j / T - log_z, ln q_j = s_j / T - lse_s
+    const double lse_s = (double)q.mx * a.inv_t + log_exact(q.all);
+    const double log_z = rest ? (double)lse_t
+                              : (double)list_mx * a.inv_t + log_exact(fmaxf((float)tch.sum * kUnit, 1.f));
+    double v = (double)tch.inv * ((double)row.part + (double)row.w * (lse_s - log_z));
+    if (tch.p_rest > 0.f) {
+        // ln p_rest - ln q_rest = ln(all / rest) - ln(1 / p_rest)
+        v += q.rest > 0.f ? (double)tch.p_rest * (log_exact(q.all / q.rest) - log_exact(1.f / tch.p_rest)) : INFINITY;
     }
-    __syncthreads();
-    return log_z;
+    return (float)((double)weight * v);
+}
+
+__device__ __forceinline__ void write_state(float* state, float m, float inv, float tail, float lse_t, bool rest) {
+    if (!state) return;
+    state[0] = m;
+    state[1] = inv;
+    state[2] = tail;
+    state[3] = lse_t;
+    state[4] = rest ? 1.f : 0.f;
+    state[5] = state[6] = state[7] = 0.f;
+}
+
+// What the gradient needs of a row: 1 / sum (0: no gradient) and the factor of
+// the tokens that are not listed.  q is relative to the row's maximum.
+__device__ __forceinline__ bool row_factors(const Teacher& tch, const Sums& q, bool rest, float& inv, float& tail) {
+    const bool fine = q.mx > -INFINITY && q.mx < INFINITY && !tch.bad;
+    inv = rest || tch.any ? 1.f / q.all : 0.f;
+    tail = rest ? (q.rest > 0.f ? 1.f - tch.p_rest * (q.all / q.rest) : 0.f) : 1.f;
+    if (!fine) inv = tail = NAN;
+    return fine;
+}
+
+// The loss and the state of a row (one thread).
+__device__ void finish_loss(const DistillArgs& a, const Shared& sh, const Teacher& tch, int64_t r, float weight,
+                            const Share& row, bool rest, float lse_t, bool fine, float inv, float tail) {
+    float v = NAN;
+    if (fine) v = rest || tch.any ? row_loss(a, tch, weight, row, rest, lse_t, list_max(sh)) : 0.f;
+    a.loss[r] = v;
+    if (!fine) raise_status(a.dev_status, DLM_DEV_NONFINITE);
+    write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, row.q.mx, inv, tail, lse_t, rest);
 }
 
 // Sums of vectors [v0, v1) of a row (kThreads threads; the whole CTA calls).
@@ -250,25 +333,30 @@ __device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c,
     return a;
 }
 
-// The row's sums over all the CTAs of its cluster, in every CTA.
-__device__ Sums merge_row(const Cluster& cl, Shared& sh, Sums a, float c) {
+// The row's sums over all the CTAs of its cluster, relative to its maximum, in
+// every thread: threads to warps, warps to the CTA, a cluster barrier, and every
+// warp adds up the CTAs for itself.  (The caller keeps the CTA alive until the
+// others have read its share: a second cluster barrier.)
+__device__ __forceinline__ Share merge_row(const Cluster& cl, Shared& sh, Share a, float c) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    warp_merge(a, c);
+    a = warp_share(a, c);
     if (lane == 0) sh.warp[warp] = a;
     __syncthreads();
-    if (warp == 0) {
-        a = lane < kWarps ? sh.warp[lane] : Sums{-INFINITY, -FLT_MAX, 0.f, 0.f};
-        warp_merge(a, c);
-        if (lane == 0) sh.cta = a;
+    if (cl.split > 1) {
+        if (warp == 0) {
+            a = warp_share(lane < kWarps ? sh.warp[lane] : no_share(), c);
+            if (lane == 0) sh.cta = a;
+        }
+        cl.sync();
+        a = lane < cl.split ? *cl.at(&sh.cta, lane) : no_share();
+    } else {
+        a = lane < kWarps ? sh.warp[lane] : no_share();
     }
-    cl.sync();
-    if (warp == 0) {
-        a = lane < cl.split ? *cl.at(&sh.cta, lane) : Sums{-INFINITY, -FLT_MAX, 0.f, 0.f};
-        warp_merge(a, c);
-        if (lane == 0) sh.row = a;
-    }
-    cl.sync();
-    return sh.row;
+    a = warp_share(a, c);
+    const float up = ex2((a.q.ref - a.q.mx) * c);
+    a.q.all *= up;
+    a.q.rest *= up;
+    return a;
 }
 
 // One float to storage.
@@ -336,22 +424,26 @@ __device__ void stream_grad(const char* row, char* out, int64_t V, int v0, int v
     }
 }
 
-// The listed tokens of this CTA's slice [e0, e1): g (q_v - p_v), once per
-// token (the first of its entries writes, p_v adds up all of them).
+// The listed tokens of this CTA's slice [e0, e1): g (q_v - p_v).  An id that
+// is listed more than once (`twice`: maybe) is written by its first entry, with
+// the sum of all of them.
 template <int DT>
-__device__ void write_listed(const List& l, int K, char* out, int64_t e0, int64_t e1, float m, float c, float inv,
-                             float g) {
+__device__ __forceinline__ void write_listed(const List& l, int K, char* out, int64_t e0, int64_t e1, float m, float c,
+                                             float inv, float inv_p, bool twice, float g) {
     for (int j = threadIdx.x; j < K; j += kThreads) {
         const int id = l.id[j];
         if (id < e0 || id >= e1) continue;
-        float p = 0.f;
+        float p = l.p[j];
         bool first = true;
-        for (int i = 0; i < K; ++i) {
-            if (l.id[i] != id) continue;
-            first &= i >= j;
-            p += l.p[i];
+        if (twice) {
+            p = 0.f;
+            for (int i = 0; i < K; ++i) {
+                if (l.id[i] != id) continue;
+                first &= i >= j;
+                p += l.p[i];
+            }
         }
-        if (first) store_elem<DT>(out, id, g * (inv * ex2((l.s[j] - m) * c) - p));
+        if (first) store_elem<DT>(out, id, g * (inv * ex2((l.s[j] - m) * c) - p * inv_p));
     }
 }
 
@@ -372,9 +464,10 @@ struct Slice {
     }
 };
 
-// GRAD: the gradient in the same launch, of the sum of the row losses.
+// The loss of a row, and with GRAD (rows too long for distill_row_kernel) the
+// gradient of the sum of the row losses.
 template <int DT, bool REST, bool GRAD>
-__global__ void __launch_bounds__(kThreads) distill_loss_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const DistillArgs a) {
     extern __shared__ __align__(16) unsigned char s_raw[];
     Shared& sh = *reinterpret_cast<Shared*>(s_raw);
     const List l = carve(s_raw, a.k);
@@ -388,79 +481,63 @@ __global__ void __launch_bounds__(kThreads) distill_loss_kernel(const DistillArg
     char* out = GRAD ? static_cast<char*>(a.grad) + r * a.grad_stride * Row<DT>::ESZ : nullptr;
     const Slice<DT> sl(V, cl);
     const float weight = a.weights ? a.weights[r] : 1.f;
-    const float c = (float)(1.4426950408889634 / (double)a.temperature);
-    float* state = a.state ? a.state + r * DLM_DISTILL_STATE : nullptr;
+    const float lse_t = REST ? a.teacher_lse[r] : 0.f;
+    const float c = a.scale;
     if (weight == 0.f) {  // the row has no loss: it is not read
         if (cl.rank == 0 && t == 0) {
             a.loss[r] = 0.f;
-            if (state)
-                for (int i = 0; i < DLM_DISTILL_STATE; ++i) state[i] = 0.f;
+            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, 0.f, 0.f, 0.f, 0.f, false);
         }
         if (GRAD) stream_grad<DT>(row, out, V, sl.v0, sl.v1, 0.f, c, 0.f);
         return;
     }
-    const float lse_t = REST ? a.teacher_lse[r] : 0.f;
-    const double log_z = read_list(a, l, sh, r, REST, lse_t);
-    if (REST) {
-        const int words = (int)((sl.e1 - sl.e0 + 31) / 32);
-        for (int i = t; i < words; i += kThreads) l.bits[i] = 0;
-        __syncthreads();
-        for (int j = t; j < K; j += kThreads) {
-            const int64_t id = l.id[j];
-            if (id >= sl.e0 && id < sl.e1) atomicOr(&l.bits[(id - sl.e0) >> 5], 1u << ((id - sl.e0) & 31));
-        }
-        __syncthreads();
+    if (t == 0) sh.flags = 0;
+    if (REST)
+        for (int i = t; i < (int)((sl.e1 - sl.e0 + 31) / 32); i += kThreads) l.bits[i] = 0;
+    __syncthreads();
+    list_load(a, l, sh, r, lse_t);
+    __syncthreads();
+    if (REST) mark_listed(l, K, sl.e0, sl.e1);
+    // the listed logits are asked for now and used after the stream
+    constexpr int kMine = (DLM_MAX_TOPK + kThreads - 1) / kThreads;
+    float mine[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int j = t + i * kThreads, id = j < K ? l.id[j] : -1;
+        mine[i] = id >= sl.e0 && id < sl.e1 ? Row<DT>::scalar(row, id) : 0.f;
     }
-    const Sums q = merge_row(cl, sh, stream_sums<DT, REST>(row, V, sl.v0, sl.v1, c, l.bits), c);
-    const bool fine = q.mx > -INFINITY && q.mx < INFINITY && !sh.bad;
-    // sums relative to the row's maximum
-    const float up = ex2((q.ref - q.mx) * c);
-    const float all = q.all * up, rest = q.rest * up;
-    const float p_rest = REST ? sh.p_rest : 0.f;
-    const bool teaches = REST || sh.any;
-    float inv = teaches ? 1.f / all : 0.f;
-    float tail = REST ? (rest > 0.f ? 1.f - p_rest * (all / rest) : 0.f) : 1.f;
-    if (!fine) inv = tail = NAN;
-    if (cl.rank == 0) {
-        const double inv_t = 1.0 / (double)a.temperature;
-        const double lse_s = (double)q.mx * inv_t + log((double)all);
-        double v = 0;
-        for (int j = t; j < K; j += kThreads) {
-            const float p = l.p[j];
-            if (l.id[j] >= 0 && p > 0.f)
-                v += (double)p * (((double)l.t[j] - (double)Row<DT>::scalar(row, l.id[j])) * inv_t - log_z + lse_s);
-        }
-        v = block_sum(v, sh.dscan);
-        if (t == 0) {
-            if (p_rest > 0.f) v += (double)p_rest * (log((double)p_rest) - log((double)rest / (double)all));
-            if (!teaches) v = 0;
-            a.loss[r] = fine ? (float)((double)weight * v) : NAN;
-            if (!fine) raise_status(a.dev_status, DLM_DEV_NONFINITE);
-            if (state) {
-                state[0] = q.mx;
-                state[1] = inv;
-                state[2] = tail;
-                state[3] = lse_t;
-                state[4] = REST ? 1.f : 0.f;
-                state[5] = state[6] = state[7] = 0.f;
-            }
+    list_weigh(a, l, sh, REST, lse_t);
+    if (REST) __syncthreads();
+    Share mine_all;
+    mine_all.q = stream_sums<DT, REST>(row, V, sl.v0, sl.v1, c, l.bits);
+    mine_all.part = mine_all.w = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int j = t + i * kThreads, id = j < K ? l.id[j] : -1;
+        if (id < sl.e0 || id >= sl.e1) continue;
+        l.s[j] = mine[i];
+        const float p = l.p[j];
+        if (p > 0.f) {
+            mine_all.part += p * (float)(((double)l.t[j] - (double)mine[i]) * a.inv_t);
+            mine_all.w += p;
         }
     }
+    const Share all = merge_row(cl, sh, mine_all, c);
+    const Teacher tch = list_total(sh, REST);
+    float inv, tail;
+    const bool fine = row_factors(tch, all.q, REST, inv, tail);
+    if (cl.rank == 0 && t == 0) finish_loss(a, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
     if (GRAD) {
-        for (int j = t; j < K; j += kThreads) {
-            const int id = l.id[j];
-            if (id >= sl.e0 && id < sl.e1) l.s[j] = Row<DT>::scalar(row, id);
-        }
-        cl.sync();  // in place: the first CTA has read its logits of every slice
         const float g = weight / a.temperature;
-        stream_grad<DT>(row, out, V, sl.v0, sl.v1, q.mx, c, g * inv * tail);
+        stream_grad<DT>(row, out, V, sl.v0, sl.v1, all.q.mx, c, g * inv * tail);
         __syncthreads();
-        if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, q.mx, c, inv, g);
+        if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, all.q.mx, c, inv, tch.inv, true, g);
     }
+    if (cl.split > 1) cl.sync();  // (this CTA's share has been read)
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(kThreads) distill_stream_grad_kernel(const DistillArgs a) {
     extern __shared__ __align__(16) unsigned char s_raw[];
     Shared& sh = *reinterpret_cast<Shared*>(s_raw);
     const List l = carve(s_raw, a.k);
@@ -474,37 +551,202 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
     char* out = static_cast<char*>(a.grad) + r * a.grad_stride * Row<DT>::ESZ;
     const Slice<DT> sl(V, cl);
     const float g = (a.weights ? a.weights[r] : 1.f) * (a.grad_loss ? a.grad_loss[r] : 1.f) / a.temperature;
-    const float c = (float)(1.4426950408889634 / (double)a.temperature);
+    const float c = a.scale;
     const float* state = a.state + r * DLM_DISTILL_STATE;
     const float m = state[0], inv = state[1], tail = state[2];
+    const bool rest = state[4] != 0.f;
     if (g == 0.f || inv == 0.f) {
         stream_grad<DT>(row, out, V, sl.v0, sl.v1, m, c, 0.f);
         return;
     }
-    read_list(a, l, sh, r, state[4] != 0.f, state[3]);
+    if (t == 0) sh.flags = 0;
+    __syncthreads();
+    list_load(a, l, sh, r, state[3]);
+    __syncthreads();
+    list_weigh(a, l, sh, rest, state[3]);
     for (int j = t; j < K; j += kThreads) {
         const int id = l.id[j];
         if (id >= sl.e0 && id < sl.e1) l.s[j] = Row<DT>::scalar(row, id);
     }
     __syncthreads();
+    const Teacher tch = list_total(sh, rest);
     stream_grad<DT>(row, out, V, sl.v0, sl.v1, m, c, g * inv * tail);
     __syncthreads();
-    write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, g);
+    write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, true, g);
 }
 
-// Shared memory of a CTA: the list, and with `bits` the bitmap of its slice.
-size_t smem_bytes(int64_t V, int k, int split, bool bits) {
+// ---- the row on chip --------------------------------------------------------
+
+// Takes element e out of a slice in shared memory: -inf in its place.  False if
+// -inf was there (an id listed twice, or a logit that carries nothing).
+template <int DT>
+__device__ __forceinline__ bool take_out(uint4* data, int e) {
+    if constexpr (DT == DLM_F32) {
+        return atomicExch(reinterpret_cast<uint32_t*>(data) + e, 0xff800000u) != 0xff800000u;
+    } else {
+        uint32_t* w = reinterpret_cast<uint32_t*>(data) + (e >> 1);
+        const int shift = (e & 1) * 16;
+        const uint32_t half = 0xffffu << shift, gone = Row<DT>::kNegInf << shift;
+        uint32_t old = *w, seen;
+        do {
+            seen = old;
+            if ((seen & half) == gone) return false;
+            old = atomicCAS(w, seen, (seen & ~half) | gone);
+        } while (old != seen);
+        return true;
+    }
+}
+
+// SUMS: loss and the gradient of the losses' sum; else the gradient from the
+// state (REST says nothing there).
+template <int DT, bool REST, bool SUMS>
+__global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillArgs a) {
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    constexpr int EPV = Row<DT>::EPV;
+    Shared& sh = *reinterpret_cast<Shared*>(s_raw);
+    const List l = carve(s_raw, a.k);
+    const int t = threadIdx.x, K = a.k;
+    Cluster cl;
+    cl.split = a.split;
+    const int64_t r = blockIdx.x / a.split;
+    cl.rank = (int)(blockIdx.x - r * a.split);
+    const int64_t V = a.vocab;
+    const char* row = static_cast<const char*>(a.student) + r * a.row_stride * Row<DT>::ESZ;
+    char* out = static_cast<char*>(a.grad) + r * a.grad_stride * Row<DT>::ESZ;
+    const Slice<DT> sl(V, cl);
+    const int n = sl.v1 - sl.v0, whole = (int)min((int64_t)sl.v1, V / EPV) - sl.v0;  // vectors; those not cut by V
+    uint4* data = reinterpret_cast<uint4*>(s_raw + slice_offset(K));
+    const float c = a.scale;
+    const float weight = a.weights ? a.weights[r] : 1.f;
+    float g = weight / a.temperature, m = 0.f, inv = 0.f, tail = 0.f, lse_t = 0.f;
+    bool rest = REST;
+    if (SUMS) {
+        if (REST) lse_t = a.teacher_lse[r];
+    } else {
+        const float* state = a.state + r * DLM_DISTILL_STATE;
+        m = state[0];
+        inv = state[1];
+        tail = state[2];
+        lse_t = state[3];
+        rest = state[4] != 0.f;
+        if (a.grad_loss) g *= a.grad_loss[r];
+    }
+    if (SUMS ? weight == 0.f : (g == 0.f || inv == 0.f)) {  // no gradient: the row is not read
+        if (SUMS && cl.rank == 0 && t == 0) a.loss[r] = 0.f;
+        stream_grad<DT>(row, out, V, sl.v0, sl.v1, 0.f, c, 0.f);
+        return;
+    }
+    // the slice: every thread copies, and later reads, its own vectors
+    const uint4* src = reinterpret_cast<const uint4*>(row) + sl.v0;
+    for (int v = t; v < n; v += kThreads) {
+        if (v < whole)
+            cp_async16(data + v, src + v);
+        else
+            data[v] = load_vec<DT>(row, V, sl.v0 + v);
+    }
+    if (t == 0) sh.flags = 0;
+    __syncthreads();
+    list_load(a, l, sh, r, lse_t);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // the list's weights, and this slice's listed logits
+    list_weigh(a, l, sh, rest, lse_t);
+    for (int j = t; j < K; j += kThreads) {
+        const int id = l.id[j];
+        if (id >= sl.e0 && id < sl.e1) l.s[j] = Row<DT>::scalar(data, (int64_t)id - sl.e0);
+    }
+    __syncthreads();
+    if (SUMS) {
+        Share mine = no_share();
+        f2 listed = pack2(0.f, 0.f), others = pack2(0.f, 0.f);
+        bool twice = false;
+        float top = -INFINITY;
+        for (int j = t; j < K; j += kThreads) {
+            const int id = l.id[j];
+            if (id < sl.e0 || id >= sl.e1) continue;
+            const float s = l.s[j], p = l.p[j];
+            if (p > 0.f) {
+                mine.part += p * (float)(((double)l.t[j] - (double)s) * a.inv_t);
+                mine.w += p;
+            }
+            // one of its entries takes it along (the teacher's logit has been used)
+            const bool took = take_out<DT>(data, (int)(id - sl.e0));
+            l.t[j] = took ? 1.f : 0.f;
+            if (took) top = max_nan(top, s);
+            twice |= !took;
+        }
+        if (twice) atomicOr(&sh.flags, (int)kTwice);
+        __syncthreads();
+        for (int v = t; v < n; v += kThreads) top = max_nan(top, Row<DT>::vmax(data[v]));
+        const float ref = top > -INFINITY ? top : 0.f;  // nothing but -inf: weights of 0
+        mine.q.mx = top;
+        mine.q.ref = top > -INFINITY ? top : -FLT_MAX;
+        const f2 r2 = pack2(ref, ref), c2 = pack2(c, c);
+        float own = 0.f;
+        for (int j = t; j < K; j += kThreads) {
+            const int id = l.id[j];
+            if (id >= sl.e0 && id < sl.e1 && l.t[j] != 0.f) own += ex2((l.s[j] - ref) * c);
+        }
+        for (int v = t; v < n; v += kThreads) {
+            float z[EPV];
+            Row<DT>::unpack(data[v], z);
+            f2 e[EPV / 2];
+#pragma unroll
+            for (int p = 0; p < EPV / 2; ++p) e[p] = ex2x2(mul2(sub2(pack2(z[2 * p], z[2 * p + 1]), r2), c2));
+#pragma unroll
+            for (int h = EPV / 4; h; h >>= 1)
+#pragma unroll
+                for (int p = 0; p < h; ++p) e[p] = add2(e[p], e[p + h]);
+            others = add2(others, e[0]);
+        }
+        mine.q.rest = hsum2(others);
+        mine.q.all = own + mine.q.rest;
+        const Share all = merge_row(cl, sh, mine, c);
+        if (cl.split > 1) cg::this_cluster().barrier_arrive();  // the others' shares have been read
+        const Teacher tch = list_total(sh, REST);
+        const bool fine = row_factors(tch, all.q, REST, inv, tail);
+        m = all.q.mx;
+        if (cl.rank == 0 && t == 0) finish_loss(a, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
+    }
+    const Teacher tch = list_total(sh, rest);
+    const float scale = g * inv * tail;
+    uint4* dst = reinterpret_cast<uint4*>(out) + sl.v0;
+    for (int v = t; v < n; v += kThreads) {
+        float z[EPV];
+        Row<DT>::unpack(data[v], z);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) z[e] = scale == 0.f ? 0.f : scale * ex2((z[e] - m) * c);
+        if (v < whole) {
+            st_row(dst + v, pack<DT>(z));
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                const int64_t i = (int64_t)(sl.v0 + v) * EPV + e;
+                if (i < V) store_elem<DT>(out, i, z[e]);
+            }
+        }
+    }
+    __syncthreads();
+    if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, SUMS ? tch.twice : true, g);
+    if (SUMS && cl.split > 1) cg::this_cluster().barrier_wait();
+}
+
+// Shared memory of a CTA that streams: the list, and with `bits` the bitmap of
+// its slice.
+size_t stream_bytes(int64_t V, int k, int split, bool bits) {
     size_t n = shared_bytes() + (size_t)k * 16;
     if (bits) n += (size_t)((V + split - 1) / split + 64) / 32 * 4 + 16;
     return n;
 }
 
+// The largest slice that a CTA can hold, and the one it should: five CTAs per SM.
+constexpr int kMaxSlice = 190 * 1024, kGoodSlice = 39 * 1024;
+constexpr int kMostShared = 227 * 1024;
+
 template <typename F>
-cudaError_t launch_rows(F kernel, const DistillArgs& a, bool bits, cudaStream_t st) {
-    const size_t smem = smem_bytes(a.vocab, a.k, a.split, bits);
+cudaError_t launch_rows(F kernel, const DistillArgs& a, size_t smem, cudaStream_t st) {
     if (smem > 48 * 1024) {  // the same limit whatever the call's size: calls may run side by side
-        const int most = (int)smem_bytes(DLM_MAX_SEARCH_VOCAB, DLM_MAX_TOPK, 1, true);
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -522,39 +764,57 @@ cudaError_t launch_rows(F kernel, const DistillArgs& a, bool bits, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int DT>
+template <int DT, bool REST>
 cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
-    if (a.grad)
-        return a.teacher_lse ? launch_rows(distill_loss_kernel<DT, true, true>, a, true, st)
-                             : launch_rows(distill_loss_kernel<DT, false, true>, a, false, st);
-    return a.teacher_lse ? launch_rows(distill_loss_kernel<DT, true, false>, a, true, st)
-                         : launch_rows(distill_loss_kernel<DT, false, false>, a, false, st);
+    const size_t smem = stream_bytes(a.vocab, a.k, a.split, REST);
+    if (!a.grad) return launch_rows(distill_stream_kernel<DT, REST, false>, a, smem, st);
+    if (a.slice_vecs == 0) return launch_rows(distill_stream_kernel<DT, REST, true>, a, smem, st);
+    return launch_rows(distill_row_kernel<DT, REST, true>, a, slice_offset(a.k) + (size_t)a.slice_vecs * 16, st);
+}
+
+template <int DT>
+cudaError_t launch_grad(const DistillArgs& a, cudaStream_t st) {
+    if (a.slice_vecs == 0)
+        return launch_rows(distill_stream_grad_kernel<DT>, a, stream_bytes(a.vocab, a.k, a.split, false), st);
+    return launch_rows(distill_row_kernel<DT, false, false>, a, slice_offset(a.k) + (size_t)a.slice_vecs * 16, st);
 }
 
 }  // namespace
 
-// CTAs per row: a row is split over a cluster when the rows alone do not fill
-// the GPU and each thread still gets a batch of vectors.
-int distill_split(int dtype, int64_t n_rows, int64_t vocab, int num_sms) {
-    const int64_t nv = vocab / (dtype == DLM_F32 ? 4 : 8);
+// CTAs per row, and for the gradient vectors per slice (0: the row is streamed).
+// A slice of about 40 KB lets five CTAs share an SM; rows too few to fill the
+// GPU are cut finer, down to 8 KB.  The loss alone splits a row only when the
+// rows do not fill the GPU and each thread still gets two batches of vectors.
+void distill_plan(DistillArgs& a, int dtype, int num_sms) {
+    const int epv = dtype == DLM_F32 ? 4 : 8, unit = 32 / epv;
+    const int64_t nv = (a.vocab + epv - 1) / epv;
     int split = 1;
-    while (split < 8 && n_rows * split < 2LL * num_sms && nv / (split * 2) >= 2LL * kThreads) split *= 2;
-    return split;
+    a.slice_vecs = 0;
+    if (a.grad) {
+        auto slice = [&](int n) { return ((nv + n - 1) / n + unit - 1) / unit * unit; };
+        while (split < 8 && slice(split) * 16 > kGoodSlice) split *= 2;
+        while (split < 8 && a.n_rows * split < 2LL * num_sms && slice(split) * 16 > 8 * 1024) split *= 2;
+        if (slice(split) * 16 <= kMaxSlice) a.slice_vecs = (int)slice(split);
+    } else {
+        while (split < 8 && a.n_rows * split < 2LL * num_sms && nv / (split * 2) >= 2LL * kThreads) split *= 2;
+    }
+    a.split = split;
 }
 
 cudaError_t launch_distill_loss(const DistillArgs& a, int dtype, cudaStream_t st) {
+    const bool rest = a.teacher_lse != nullptr;
     switch (dtype) {
-    case DLM_BF16: return launch_loss<DLM_BF16>(a, st);
-    case DLM_F16: return launch_loss<DLM_F16>(a, st);
-    default: return launch_loss<DLM_F32>(a, st);
+    case DLM_BF16: return rest ? launch_loss<DLM_BF16, true>(a, st) : launch_loss<DLM_BF16, false>(a, st);
+    case DLM_F16: return rest ? launch_loss<DLM_F16, true>(a, st) : launch_loss<DLM_F16, false>(a, st);
+    default: return rest ? launch_loss<DLM_F32, true>(a, st) : launch_loss<DLM_F32, false>(a, st);
     }
 }
 
 cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t st) {
     switch (dtype) {
-    case DLM_BF16: return launch_rows(distill_grad_kernel<DLM_BF16>, a, false, st);
-    case DLM_F16: return launch_rows(distill_grad_kernel<DLM_F16>, a, false, st);
-    default: return launch_rows(distill_grad_kernel<DLM_F32>, a, false, st);
+    case DLM_BF16: return launch_grad<DLM_BF16>(a, st);
+    case DLM_F16: return launch_grad<DLM_F16>(a, st);
+    default: return launch_grad<DLM_F32>(a, st);
     }
 }
 

@@ -250,6 +250,9 @@ struct DistillArgs {
     const void* student;
     int64_t n_rows, vocab, row_stride;
     int split;                // CTAs per row (thread-block cluster size)
+    int slice_vecs;           // 16-byte vectors of a row per CTA; 0: the row is streamed
+    float scale;              // log2(e) / temperature
+    double inv_t;             // 1 / temperature
     const int32_t* ids;       // [n_rows][k]
     const void* teacher;      // [n_rows][k]
     int teacher_dtype;
@@ -264,7 +267,7 @@ struct DistillArgs {
     int64_t grad_stride;
     uint32_t* dev_status;
 };
-int distill_split(int dtype, int64_t n_rows, int64_t vocab, int num_sms);
+void distill_plan(DistillArgs& a, int dtype, int num_sms);  // split and slice_vecs
 cudaError_t launch_distill_loss(const DistillArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
 
