@@ -84,13 +84,13 @@ __device__ __forceinline__ Share warp_share(Share a, float c) {
 __device__ __forceinline__ Share no_share() { return Share{Sums{-INFINITY, -FLT_MAX, 0.f, 0.f}, 0.f, 0.f}; }
 
 struct Shared {
-    Share warp[kWarps];
-    Share cta;
+    Share part[8 * kWarps];   // every warp's of every CTA of the cluster
     float list_max[kWarps];
     uint64_t list_sum[kWarps];
-    int flags;                // kAny, kBad, kTwice
+    int flags[kWarps];        // kAny, kBad
+    int twice[kWarps];        // an id may be listed twice
 };
-enum : int { kAny = 1, kBad = 2, kTwice = 4 };  // an entry; a teacher logit is NaN or +inf; an id may be listed twice
+enum : int { kAny = 1, kBad = 2 };  // an entry; a teacher logit is NaN or +inf
 
 // The list in shared memory.
 struct List {
@@ -98,6 +98,7 @@ struct List {
     float* t;        // teacher logit
     float* p;        // teacher weight, not normalised
     float* s;        // student logit (entries of this CTA's slice)
+    uint32_t* own;   // row kernel: this entry took its token out of the slice
     uint32_t* bits;  // stream kernel: the listed tokens of this CTA's slice
 };
 
@@ -110,12 +111,12 @@ __device__ __forceinline__ List carve(unsigned char* p, int k) {
     l.t = reinterpret_cast<float*>(l.id + k);
     l.p = l.t + k;
     l.s = l.p + k;
-    l.bits = reinterpret_cast<uint32_t*>(l.s + k);
+    l.own = l.bits = reinterpret_cast<uint32_t*>(l.s + k);
     return l;
 }
 
 // Bytes of shared memory before a slice.
-__host__ __device__ inline size_t slice_offset(int k) { return (shared_bytes() + (size_t)k * 16 + 15) & ~(size_t)15; }
+__host__ __device__ inline size_t slice_offset(int k) { return (shared_bytes() + (size_t)k * 20 + 15) & ~(size_t)15; }
 
 __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
     switch (a.teacher_dtype) {
@@ -135,17 +136,20 @@ __device__ __forceinline__ double log_exact(float x) {
 }
 
 // The list in two steps with a barrier after each.  First: entries into shared
-// memory, their maximum per warp.  (sh.flags has been zeroed.)
-__device__ __forceinline__ void list_load(const DistillArgs& a, const List& l, Shared& sh, int64_t r, float lse_t) {
+// memory, their maximum per warp.  A thread's first entry may have been asked
+// for before (id0, x0).
+__device__ __forceinline__ void list_load(const DistillArgs& a, const List& l, Shared& sh, int64_t r, float lse_t,
+                                          int id0, float x0) {
     float mx = -INFINITY;
     int flags = fabsf(lse_t) < INFINITY ? 0 : kBad;
     for (int j = threadIdx.x; j < a.k; j += kThreads) {
-        int id = a.ids[r * a.k + j];
+        const bool first = j < kThreads;
+        int id = first ? id0 : a.ids[r * a.k + j];
+        const float x = first ? x0 : teacher_at(a, r * a.k + j);
         if (id >= a.vocab) {
             id = -1;
             raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
         }
-        const float x = teacher_at(a, r * a.k + j);
         if (id >= 0) {
             flags |= x < INFINITY ? (x > -INFINITY ? kAny : 0) : kBad;
             mx = fmaxf(mx, x);
@@ -157,7 +161,7 @@ __device__ __forceinline__ void list_load(const DistillArgs& a, const List& l, S
     flags = __reduce_or_sync(DLM_FULL_MASK, flags);
     if ((threadIdx.x & 31) == 0) {
         sh.list_max[threadIdx.x >> 5] = mx;
-        if (flags) atomicOr(&sh.flags, flags);
+        sh.flags[threadIdx.x >> 5] = flags;
     }
 }
 
@@ -201,7 +205,7 @@ struct Teacher {
     uint64_t sum;    // of the weights, in 2^-44
     float inv;       // 1 / sum, or 1 when the rest is a class: weight to probability
     float p_rest;
-    bool any, bad, twice;
+    bool any, bad;
 };
 __device__ __forceinline__ Teacher list_total(const Shared& sh, bool rest) {
     Teacher t;
@@ -211,9 +215,11 @@ __device__ __forceinline__ Teacher list_total(const Shared& sh, bool rest) {
     const uint64_t one = 1ull << kWeightBits;
     t.inv = rest ? 1.f : t.sum ? 1.0f / ((float)t.sum * kUnit) : 0.f;
     t.p_rest = rest && t.sum < one ? (float)(one - t.sum) * kUnit : 0.f;
-    t.any = sh.flags & kAny;
-    t.bad = sh.flags & kBad;
-    t.twice = sh.flags & kTwice;
+    int flags = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) flags |= sh.flags[w];
+    t.any = flags & kAny;
+    t.bad = flags & kBad;
     return t;
 }
 
@@ -334,29 +340,42 @@ __device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c,
 }
 
 // The row's sums over all the CTAs of its cluster, relative to its maximum, in
-// every thread: threads to warps, warps to the CTA, a cluster barrier, and every
-// warp adds up the CTAs for itself.  (The caller keeps the CTA alive until the
-// others have read its share: a second cluster barrier.)
+// every thread.  Each warp leaves its share in every CTA (a remote store needs
+// no answer), one barrier later each warp adds up all of them for itself, and
+// nothing remote is read, so no CTA has to outlive another.  started()
+// comes before: no share is sent to a CTA that does not run yet.
 __device__ __forceinline__ Share merge_row(const Cluster& cl, Shared& sh, Share a, float c) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     a = warp_share(a, c);
-    if (lane == 0) sh.warp[warp] = a;
-    __syncthreads();
     if (cl.split > 1) {
-        if (warp == 0) {
-            a = warp_share(lane < kWarps ? sh.warp[lane] : no_share(), c);
-            if (lane == 0) sh.cta = a;
-        }
+        cg::this_cluster().barrier_wait();
+        if (lane < cl.split) *cl.at(&sh.part[cl.rank * kWarps + warp], lane) = a;
         cl.sync();
-        a = lane < cl.split ? *cl.at(&sh.cta, lane) : no_share();
     } else {
-        a = lane < kWarps ? sh.warp[lane] : no_share();
+        if (lane == 0) sh.part[warp] = a;
+        __syncthreads();
+    }
+    const int n = cl.split * kWarps;
+    a = lane < n ? sh.part[lane] : no_share();
+    for (int i = lane + 32; i < n; i += 32) {
+        const Share b = sh.part[i];
+        const float ref = fmaxf(a.q.ref, b.q.ref), ea = ex2((a.q.ref - ref) * c), eb = ex2((b.q.ref - ref) * c);
+        a.q.all = a.q.all * ea + b.q.all * eb;
+        a.q.rest = a.q.rest * ea + b.q.rest * eb;
+        a.q.ref = ref;
+        a.q.mx = max_nan(a.q.mx, b.q.mx);
+        a.part += b.part;
+        a.w += b.w;
     }
     a = warp_share(a, c);
     const float up = ex2((a.q.ref - a.q.mx) * c);
     a.q.all *= up;
     a.q.rest *= up;
     return a;
+}
+// The cluster's CTAs run (before merge_row; every thread).
+__device__ __forceinline__ void started(const Cluster& cl) {
+    if (cl.split > 1) cg::this_cluster().barrier_arrive();
 }
 
 // One float to storage.
@@ -370,23 +389,33 @@ __device__ __forceinline__ void store_elem(void* row, int64_t i, float x) {
         static_cast<__half*>(row)[i] = __float2half_rn(x);
 }
 
+// scale * 2^((z - m) c) of a vector, in storage.
+struct Slope {
+    f2 m, c, scale;
+    __device__ Slope(float m1, float c1, float s1) : m(pack2(m1, m1)), c(pack2(c1, c1)), scale(pack2(s1, s1)) {}
+};
 template <int DT>
-__device__ __forceinline__ uint4 pack(const float (&x)[Row<DT>::EPV]) {
-    uint4 w;
-    uint32_t* r = reinterpret_cast<uint32_t*>(&w);
+__device__ __forceinline__ uint4 slope_of(uint4 w, const Slope& s) {
+    constexpr int EPV = Row<DT>::EPV;
+    float z[EPV];
+    Row<DT>::unpack(w, z);
+    uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int p = 0; p < EPV / 2; ++p) {
+        float x, y;
+        unpack2(mul2(ex2x2(mul2(sub2(pack2(z[2 * p], z[2 * p + 1]), s.m), s.c)), s.scale), x, y);
         if constexpr (DT == DLM_F32) {
-            r[i] = __float_as_uint(x[i]);
+            r[2 * p] = __float_as_uint(x);
+            r[2 * p + 1] = __float_as_uint(y);
         } else if constexpr (DT == DLM_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            r[i] = *reinterpret_cast<const uint32_t*>(&h);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            r[p] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
-            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-            r[i] = *reinterpret_cast<const uint32_t*>(&h);
+            const __half2 h = __floats2half2_rn(x, y);
+            r[p] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
-    return w;
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // scale * 2^((z - m) c) for vectors [v0, v1) of the row; scale = 0 writes
@@ -396,13 +425,8 @@ template <int DT>
 __device__ void stream_grad(const char* row, char* out, int64_t V, int v0, int v1, float m, float c, float scale) {
     constexpr int EPV = Row<DT>::EPV;
     const int whole = (int)min((int64_t)v1, V / EPV);
-    auto value = [&](uint4 w) {
-        float z[EPV];
-        Row<DT>::unpack(w, z);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) z[e] = scale * ex2((z[e] - m) * c);
-        return pack<DT>(z);
-    };
+    const Slope slope(m, c, scale);
+    auto value = [&](uint4 w) { return slope_of<DT>(w, slope); };
     const uint4* src = reinterpret_cast<const uint4*>(row);
     uint4* dst = reinterpret_cast<uint4*>(out);
     int v = v0 + (int)threadIdx.x;
@@ -433,7 +457,7 @@ __device__ __forceinline__ void write_listed(const List& l, int K, char* out, in
     for (int j = threadIdx.x; j < K; j += kThreads) {
         const int id = l.id[j];
         if (id < e0 || id >= e1) continue;
-        float p = l.p[j];
+        float p = l.p[j], s = l.s[j];
         bool first = true;
         if (twice) {
             p = 0.f;
@@ -441,9 +465,10 @@ __device__ __forceinline__ void write_listed(const List& l, int K, char* out, in
                 if (l.id[i] != id) continue;
                 first &= i >= j;
                 p += l.p[i];
+                s = max_nan(s, l.s[i]);  // (one of them has the logit, the others it or -inf)
             }
         }
-        if (first) store_elem<DT>(out, id, g * (inv * ex2((l.s[j] - m) * c) - p * inv_p));
+        if (first) store_elem<DT>(out, id, g * (inv * ex2((s - m) * c) - p * inv_p));
     }
 }
 
@@ -480,6 +505,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
     const char* row = static_cast<const char*>(a.student) + r * a.row_stride * Row<DT>::ESZ;
     char* out = GRAD ? static_cast<char*>(a.grad) + r * a.grad_stride * Row<DT>::ESZ : nullptr;
     const Slice<DT> sl(V, cl);
+    const int id0 = t < K ? a.ids[r * K + t] : -1;
+    const float x0 = t < K ? teacher_at(a, r * K + t) : 0.f;
     const float weight = a.weights ? a.weights[r] : 1.f;
     const float lse_t = REST ? a.teacher_lse[r] : 0.f;
     const float c = a.scale;
@@ -491,11 +518,10 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
         if (GRAD) stream_grad<DT>(row, out, V, sl.v0, sl.v1, 0.f, c, 0.f);
         return;
     }
-    if (t == 0) sh.flags = 0;
+    started(cl);
     if (REST)
         for (int i = t; i < (int)((sl.e1 - sl.e0 + 31) / 32); i += kThreads) l.bits[i] = 0;
-    __syncthreads();
-    list_load(a, l, sh, r, lse_t);
+    list_load(a, l, sh, r, lse_t, id0, x0);
     __syncthreads();
     if (REST) mark_listed(l, K, sl.e0, sl.e1);
     // the listed logits are asked for now and used after the stream
@@ -533,7 +559,6 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
         __syncthreads();
         if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, all.q.mx, c, inv, tch.inv, true, g);
     }
-    if (cl.split > 1) cl.sync();  // (this CTA's share has been read)
 }
 
 template <int DT>
@@ -559,9 +584,7 @@ __global__ void __launch_bounds__(kThreads) distill_stream_grad_kernel(const Dis
         stream_grad<DT>(row, out, V, sl.v0, sl.v1, m, c, 0.f);
         return;
     }
-    if (t == 0) sh.flags = 0;
-    __syncthreads();
-    list_load(a, l, sh, r, state[3]);
+    list_load(a, l, sh, r, state[3], t < K ? a.ids[r * K + t] : -1, t < K ? teacher_at(a, r * K + t) : 0.f);
     __syncthreads();
     list_weigh(a, l, sh, rest, state[3]);
     for (int j = t; j < K; j += kThreads) {
@@ -577,12 +600,13 @@ __global__ void __launch_bounds__(kThreads) distill_stream_grad_kernel(const Dis
 
 // ---- the row on chip --------------------------------------------------------
 
-// Takes element e out of a slice in shared memory: -inf in its place.  False if
-// -inf was there (an id listed twice, or a logit that carries nothing).
+// Takes element e out of a slice in shared memory: its value, and -inf in its
+// place.  -inf if that was there already (an id listed twice, or a logit that
+// carries nothing).
 template <int DT>
-__device__ __forceinline__ bool take_out(uint4* data, int e) {
+__device__ __forceinline__ float take_out(uint4* data, int e) {
     if constexpr (DT == DLM_F32) {
-        return atomicExch(reinterpret_cast<uint32_t*>(data) + e, 0xff800000u) != 0xff800000u;
+        return __uint_as_float(atomicExch(reinterpret_cast<uint32_t*>(data) + e, 0xff800000u));
     } else {
         uint32_t* w = reinterpret_cast<uint32_t*>(data) + (e >> 1);
         const int shift = (e & 1) * 16;
@@ -590,10 +614,10 @@ __device__ __forceinline__ bool take_out(uint4* data, int e) {
         uint32_t old = *w, seen;
         do {
             seen = old;
-            if ((seen & half) == gone) return false;
             old = atomicCAS(w, seen, (seen & ~half) | gone);
         } while (old != seen);
-        return true;
+        const uint16_t bits = (uint16_t)(seen >> shift);
+        return Row<DT>::scalar(&bits, 0);
     }
 }
 
@@ -617,6 +641,8 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     const int n = sl.v1 - sl.v0, whole = (int)min((int64_t)sl.v1, V / EPV) - sl.v0;  // vectors; those not cut by V
     uint4* data = reinterpret_cast<uint4*>(s_raw + slice_offset(K));
     const float c = a.scale;
+    const int id0 = t < K ? a.ids[r * K + t] : -1;
+    const float x0 = t < K ? teacher_at(a, r * K + t) : 0.f;
     const float weight = a.weights ? a.weights[r] : 1.f;
     float g = weight / a.temperature, m = 0.f, inv = 0.f, tail = 0.f, lse_t = 0.f;
     bool rest = REST;
@@ -636,57 +662,38 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
         stream_grad<DT>(row, out, V, sl.v0, sl.v1, 0.f, c, 0.f);
         return;
     }
+    if (SUMS) started(cl);
     // the slice: every thread copies, and later reads, its own vectors
     const uint4* src = reinterpret_cast<const uint4*>(row) + sl.v0;
-    for (int v = t; v < n; v += kThreads) {
-        if (v < whole)
-            cp_async16(data + v, src + v);
-        else
-            data[v] = load_vec<DT>(row, V, sl.v0 + v);
-    }
-    if (t == 0) sh.flags = 0;
-    __syncthreads();
-    list_load(a, l, sh, r, lse_t);
+    for (int v = t; v < whole; v += kThreads) cp_async16(data + v, src + v);
+    if (whole < n && t == 0) data[whole] = load_vec<DT>(row, V, sl.v0 + whole);  // the row's last, cut vector
+    list_load(a, l, sh, r, lse_t, id0, x0);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    // the list's weights, and this slice's listed logits
-    list_weigh(a, l, sh, rest, lse_t);
-    for (int j = t; j < K; j += kThreads) {
-        const int id = l.id[j];
-        if (id >= sl.e0 && id < sl.e1) l.s[j] = Row<DT>::scalar(data, (int64_t)id - sl.e0);
-    }
-    __syncthreads();
     if (SUMS) {
-        Share mine = no_share();
-        f2 listed = pack2(0.f, 0.f), others = pack2(0.f, 0.f);
+        // the listed tokens leave the slice; one entry of each has its logit
         bool twice = false;
         float top = -INFINITY;
         for (int j = t; j < K; j += kThreads) {
             const int id = l.id[j];
             if (id < sl.e0 || id >= sl.e1) continue;
-            const float s = l.s[j], p = l.p[j];
-            if (p > 0.f) {
-                mine.part += p * (float)(((double)l.t[j] - (double)s) * a.inv_t);
-                mine.w += p;
-            }
-            // one of its entries takes it along (the teacher's logit has been used)
-            const bool took = take_out<DT>(data, (int)(id - sl.e0));
-            l.t[j] = took ? 1.f : 0.f;
-            if (took) top = max_nan(top, s);
+            const float s = take_out<DT>(data, (int)(id - sl.e0));
+            const bool took = !(s == -INFINITY);
+            l.s[j] = s;
+            l.own[j] = took;
             twice |= !took;
+            if (took) top = max_nan(top, s);
         }
-        if (twice) atomicOr(&sh.flags, (int)kTwice);
+        twice = __any_sync(DLM_FULL_MASK, twice);
+        if ((t & 31) == 0) sh.twice[t >> 5] = twice;
         __syncthreads();
         for (int v = t; v < n; v += kThreads) top = max_nan(top, Row<DT>::vmax(data[v]));
         const float ref = top > -INFINITY ? top : 0.f;  // nothing but -inf: weights of 0
+        Share mine = no_share();
         mine.q.mx = top;
         mine.q.ref = top > -INFINITY ? top : -FLT_MAX;
         const f2 r2 = pack2(ref, ref), c2 = pack2(c, c);
-        float own = 0.f;
-        for (int j = t; j < K; j += kThreads) {
-            const int id = l.id[j];
-            if (id >= sl.e0 && id < sl.e1 && l.t[j] != 0.f) own += ex2((l.s[j] - ref) * c);
-        }
+        f2 others = pack2(0.f, 0.f);
         for (int v = t; v < n; v += kThreads) {
             float z[EPV];
             Row<DT>::unpack(data[v], z);
@@ -700,35 +707,57 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             others = add2(others, e[0]);
         }
         mine.q.rest = hsum2(others);
+        // the list's weights and this slice's share of the loss
+        list_weigh(a, l, sh, rest, lse_t);
+        float own = 0.f;
+        for (int j = t; j < K; j += kThreads) {
+            const int id = l.id[j];
+            if (id < sl.e0 || id >= sl.e1) continue;
+            float s = l.s[j];
+            if (l.own[j]) {
+                own += ex2((s - ref) * c);
+            } else {  // another entry has this token's logit, or it is -inf
+                for (int i = 0; i < K; ++i)
+                    if (l.id[i] == id && l.own[i]) s = l.s[i];
+            }
+            const float p = l.p[j];
+            if (p > 0.f) {
+                mine.part += p * (float)(((double)l.t[j] - (double)s) * a.inv_t);
+                mine.w += p;
+            }
+        }
         mine.q.all = own + mine.q.rest;
         const Share all = merge_row(cl, sh, mine, c);
-        if (cl.split > 1) cg::this_cluster().barrier_arrive();  // the others' shares have been read
         const Teacher tch = list_total(sh, REST);
         const bool fine = row_factors(tch, all.q, REST, inv, tail);
         m = all.q.mx;
         if (cl.rank == 0 && t == 0) finish_loss(a, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
+    } else {
+        list_weigh(a, l, sh, rest, lse_t);
+        for (int j = t; j < K; j += kThreads) {
+            const int id = l.id[j];
+            if (id >= sl.e0 && id < sl.e1) l.s[j] = Row<DT>::scalar(data, (int64_t)id - sl.e0);
+        }
+        __syncthreads();
     }
     const Teacher tch = list_total(sh, rest);
     const float scale = g * inv * tail;
     uint4* dst = reinterpret_cast<uint4*>(out) + sl.v0;
-    for (int v = t; v < n; v += kThreads) {
-        float z[EPV];
-        Row<DT>::unpack(data[v], z);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e) z[e] = scale == 0.f ? 0.f : scale * ex2((z[e] - m) * c);
-        if (v < whole) {
-            st_row(dst + v, pack<DT>(z));
-        } else {
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) {
-                const int64_t i = (int64_t)(sl.v0 + v) * EPV + e;
-                if (i < V) store_elem<DT>(out, i, z[e]);
-            }
-        }
+    const Slope slope(m, c, scale);
+#pragma unroll 2
+    for (int v = t; v < whole; v += kThreads) st_row(dst + v, slope_of<DT>(data[v], slope));
+    if (whole < n) {  // the row's last, cut vector
+        for (int64_t i = (int64_t)(sl.v0 + whole) * EPV + t; i < V; i += kThreads)
+            store_elem<DT>(out, i, scale * ex2((Row<DT>::scalar(data, i - sl.e0) - m) * c));
     }
     __syncthreads();
-    if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, SUMS ? tch.twice : true, g);
-    if (SUMS && cl.split > 1) cg::this_cluster().barrier_wait();
+    if (inv != 0.f) {
+        int twice = !SUMS;
+        if (SUMS)
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) twice |= sh.twice[w];
+        write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, twice, g);
+    }
 }
 
 // Shared memory of a CTA that streams: the list, and with `bits` the bitmap of

@@ -24,7 +24,7 @@
 #include <string.h>
 #define DLM_HD inline
 #else
-#define DLM_HD __host__ __device__ __forceinline__
+#define DLM_HD __device__ __forceinline__
 #endif
 
 namespace dlm {
