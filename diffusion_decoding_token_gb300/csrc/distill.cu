@@ -668,6 +668,8 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     for (int v = t; v < whole; v += kThreads) cp_async16(data + v, src + v);
     if (whole < n && t == 0) data[whole] = load_vec<DT>(row, V, sl.v0 + whole);  // the row's last, cut vector
     list_load(a, l, sh, r, lse_t, id0, x0);
+    __syncthreads();
+    list_weigh(a, l, sh, rest, lse_t);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (SUMS) {
@@ -707,8 +709,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             others = add2(others, e[0]);
         }
         mine.q.rest = hsum2(others);
-        // the list's weights and this slice's share of the loss
-        list_weigh(a, l, sh, rest, lse_t);
+        // this slice's share of the loss
         float own = 0.f;
         for (int j = t; j < K; j += kThreads) {
             const int id = l.id[j];
@@ -733,7 +734,6 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
         m = all.q.mx;
         if (cl.rank == 0 && t == 0) finish_loss(a, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
     } else {
-        list_weigh(a, l, sh, rest, lse_t);
         for (int j = t; j < K; j += kThreads) {
             const int id = l.id[j];
             if (id >= sl.e0 && id < sl.e1) l.s[j] = Row<DT>::scalar(data, (int64_t)id - sl.e0);

@@ -114,7 +114,9 @@ struct Ctrl {
     uint64_t lo_side, hi_side;
     int hits[2][kWarps];
     uint32_t first[kWarps];
-    float wmax[kWarps];   // the first pass's maximum of each warp
+    float wmax[kWarps];   // the first pass's maximum of each warp, and its smallest
+    float wmin[kWarps];   // (finite) run maximum
+    int bins[kThreads];
     float fscan[kWarps];
     uint64_t scan[kWarps];
 };
@@ -154,15 +156,16 @@ __device__ __forceinline__ Smem carve(unsigned char* p, int nb) {
     s.bsum = s.sub + nb * kRuns;
     s.bties = reinterpret_cast<uint32_t*>(s.bsum + nb);
     p += shared_space(nb);
-    s.fine = reinterpret_cast<uint64_t*>(p);
-    p += sizeof(uint64_t) * kFine;
     s.bmass = reinterpret_cast<uint64_t*>(p);
     s.runs = reinterpret_cast<uint16_t*>(p);
+    p += sizeof(uint64_t) * nb;
+    s.fine = reinterpret_cast<uint64_t*>(p);
     return s;
 }
 
-size_t smem_bytes(int nb) {
-    return ctrl_bytes() + sizeof(uint64_t) * (kCap + kFine + (size_t)nb) + shared_space(nb);
+// (`fine` only where a bracket is worked)
+size_t smem_bytes(int nb, bool fine) {
+    return ctrl_bytes() + sizeof(uint64_t) * (kCap + (fine ? kFine : 0) + (size_t)nb) + shared_space(nb);
 }
 
 // 64-bit sum in shared memory by two native 32-bit atomics: the carry of the
@@ -223,48 +226,41 @@ __device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
 __device__ __forceinline__ uint64_t candidate(float z, uint32_t i) { return ((uint64_t)(~key_of(z)) << 32) | i; }
 __device__ __forceinline__ float candidate_value(uint64_t c) { return key_value(~(uint32_t)(c >> 32)); }
 
-// A threshold that at least k of the n floats of `sub` reach and few more
-// (-inf when fewer than k are finite).  Each step cuts the interval into nine:
-// warp w counts what reaches the w-th inner border, so a step is one look at
-// `sub` and one barrier, and three or four steps bring the count within a
-// quarter of k.
-__device__ float threshold_for(const float* sub, int n, int k, float m, Ctrl* c) {
+// A threshold that at least k of the n floats of `values` reach and few more
+// (-inf when fewer than k are finite): counts in kThreads bins between the
+// smallest and the largest, one barrier, and every warp adds the bins up from
+// the top for itself.  (A search by bisection took a barrier a step; under a
+// streaming load each cost the CTA about 1000 cycles.)  c->bins is zero before.
+__device__ float threshold_for(const float* values, int n, int k, float lo, float hi, Ctrl* c) {
     if (n < k) return -INFINITY;
-    if (k == 1) return m;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float lo = m;
-    int at = 0;  // how many reach lo
-    for (int i = lane; i < n; i += 32) {  // every warp for itself
-        const float x = sub[i];
-        at += x > -INFINITY;
-        if (x > -INFINITY) lo = fminf(lo, x);
-    }
-    lo = -warp_max_nan(-lo);
-    at = __reduce_add_sync(DLM_FULL_MASK, at);
-    if (at < k) return -INFINITY;
-    float hi = m;
-    const int most = k + max(8, k / 4);
-    for (int step = 0; step < 12 && at > most; ++step) {
-        const float width = (hi - lo) * (1.f / (kWarps + 1));
-        const float mid = lo + width * (float)(warp + 1);
-        int h = 0;
-        for (int i = lane; i < n; i += 32) h += sub[i] >= mid;
-        h = __reduce_add_sync(DLM_FULL_MASK, h);
-        if (lane == 0) c->hits[step & 1][warp] = h;
-        __syncthreads();
-        const float base = lo;
-        int top = -1;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const int hw = c->hits[step & 1][w];
-            if (hw >= k) top = w, at = hw;
-        }
-        if (top >= 0) lo = base + width * (float)(top + 1);
-        if (top < kWarps - 1) hi = base + width * (float)(top + 2);
-        if (!(width > 0.f)) break;
+    const int lane = threadIdx.x & 31;
+    const float scale = hi > lo ? fminf((float)kThreads / (hi - lo), 1e30f) : 0.f;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const float x = values[i];
+        if (x > -INFINITY) atomicAdd(&c->bins[min(kThreads - 1, max(0, (int)((x - lo) * scale)))], 1);
     }
     __syncthreads();
-    return lo;
+    constexpr int PER = kThreads / 32;
+    int v[PER], mine = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) mine += v[j] = c->bins[kThreads - 1 - (lane * PER + j)];
+    int run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(DLM_FULL_MASK, run, o);
+        if (lane >= o) run += x;
+    }
+    const uint32_t who = __ballot_sync(DLM_FULL_MASK, run >= k);
+    if (!who) return -INFINITY;
+    int at = 0, seen = run - mine;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        if (seen < k) at = kThreads - 1 - (lane * PER + j);
+        seen += v[j];
+    }
+    at = __shfl_sync(DLM_FULL_MASK, at, __ffs(who) - 1);
+    // a little below the bin's edge, so that nothing of it is lost to rounding
+    return lo + (scale > 0.f ? (float)at / scale : 0.f) - 1e-6f * (fabsf(lo) + fabsf(hi));
 }
 
 // Keeps of the n > kThreads candidates in buf the first k of the order and few
@@ -277,10 +273,16 @@ __device__ int top_candidates(const Smem& s, int n, int k) {
     Ctrl* c = s.c;
     float* values = reinterpret_cast<float*>(s.wbuf);
     uint64_t* out = s.wbuf + kCap / 2;
-    for (int i = t; i < n; i += kThreads) values[i] = candidate_value(s.buf[i]);
+    float lo = INFINITY;
+    for (int i = t; i < n; i += kThreads) {
+        const float x = candidate_value(s.buf[i]);
+        values[i] = x;
+        lo = fminf(lo, x);
+    }
     if (t == 0) c->runs = 0;
-    __syncthreads();
-    const float least = threshold_for(values, n, k, c->ws.m, c);
+    c->bins[t] = 0;
+    lo = -block_max_nan(-lo, c->fscan);  // (its barriers order the rest too)
+    const float least = threshold_for(values, n, k, lo, c->ws.m, c);
     for (int i = t; i < n; i += kThreads)
         if (values[i] >= least) {
             const uint32_t at = atomicAdd(&c->runs, 1u);
@@ -359,9 +361,38 @@ __device__ void gather_runs(const char* row, int64_t V, int nsub, const Smem& s,
             v[j] = at < n ? (int)s.runs[at] * 32 + lane : -1;
             if (at < n) w[j] = load_vec<DT>(row, V, v[j]);
         }
+        uint32_t mask = 0;  // elements that go into the list, a bit each
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (v[j] >= 0) push<DT>(w[j], (uint32_t)(v[j] * EPV), least, INFINITY, s.buf, kCap, &c->count);
+        for (int j = 0; j < kAhead; ++j) {
+            if (v[j] < 0) continue;
+            float z[EPV];
+            Row<DT>::unpack(w[j], z);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) mask |= (uint32_t)(z[e] >= least && z[e] > -INFINITY) << (j * EPV + e);
+        }
+        const int mine = __popc(mask);
+        int inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(DLM_FULL_MASK, inc, o);
+            if (lane >= o) inc += x;
+        }
+        uint32_t at = 0;
+        if (lane == 31) at = atomicAdd(&c->count, (uint32_t)inc);
+        at = __shfl_sync(DLM_FULL_MASK, at, 31) + (uint32_t)(inc - mine);
+        if (!mask) continue;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            if (!((mask >> (j * EPV)) & ((1u << EPV) - 1u))) continue;
+            float z[EPV];
+            Row<DT>::unpack(w[j], z);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e)
+                if ((mask >> (j * EPV + e)) & 1u) {
+                    if (at < (uint32_t)kCap) s.buf[at] = candidate(z[e], (uint32_t)(v[j] * EPV + e));
+                    ++at;
+                }
+        }
     }
     __syncthreads();
 }
@@ -383,10 +414,11 @@ __device__ __noinline__ void gather_slice(const char* row, int64_t V, int b0, in
 // Run maxima of batches [b0, b1), and with `sums` each batch's sum of
 // 2^((z - ref) c), ref the batch's maximum (a batch of -inf only sums to 0).
 // The next batch is loaded while one is summed, and the first while `begin` finds
-// out the scale (0: no sums; negative: leave).  Returns the warp's maximum.
+// out the scale (0: no sums; negative: leave).  Returns the warp's maximum, and
+// in `low` its smallest run maximum that is finite.
 template <int DT, typename F>
 __device__ __forceinline__ float scan_rows(const char* row, int64_t V, int b0, int b1, F begin, float* sub,
-                                           float* bsum) {
+                                           float* bsum, float& low) {
     constexpr int EPV = Row<DT>::EPV;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto fetch = [&](int b, uint4 (&w)[kRuns]) {
@@ -416,6 +448,8 @@ __device__ __forceinline__ float scan_rows(const char* row, int64_t V, int b0, i
         if (lane == 0) *reinterpret_cast<float4*>(sub + b * kRuns) = make_float4(m[0], m[1], m[2], m[3]);
         const float ref = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
         most = max_nan(most, ref);
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) low = fminf(low, m[i] > -INFINITY ? m[i] : INFINITY);
         if (!sums) continue;
         const float r = ref > -INFINITY ? ref : 0.f;  // -inf - 0 stays -inf: weight 0
         const f2 r2 = pack2(r, r), c2 = pack2(c, c);
@@ -1540,7 +1574,7 @@ __device__ void write_topk(const RowSearchArgs& a, const Smem& s, int n, int64_t
 // the batch sums.  Returns the verdict.
 template <int DT>
 __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem& s, const char* row, int64_t V, int nb,
-                                             int64_t o, bool whole) {
+                                             int64_t o, bool whole, float low) {
     Ctrl* c = s.c;
     const int t = threadIdx.x, nsub = nb * kRuns;
     const int k = c->top_k;
@@ -1553,7 +1587,7 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
         least = -INFINITY;
     } else if (k > 0) {
         // (more than the runs: a list from a threshold that a sample gives)
-        least = k <= DLM_MAX_TOPK ? threshold_for(s.sub, nsub, k, m, c) : -INFINITY;
+        least = k == 1 ? m : k <= DLM_MAX_TOPK ? threshold_for(s.sub, nsub, k, low, m, c) : -INFINITY;
         if (!(least > -INFINITY)) return k <= kListTopk ? kList : kRadix;
     } else if (by_least) {
         least = z_least;
@@ -1564,7 +1598,7 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
         nucleus_target(c, rule, 0, lo, hi);
         least = m;
         if (hi > kOne) {  // more than the largest logit alone
-            least = threshold_for(s.sub, nsub, min(kListRuns, nb), m, c);
+            least = threshold_for(s.sub, nsub, min(kListRuns, nb), low, m, c);
             // what the runs' maxima hold of the nucleus: a list of the runs
             // that is far short of it is not made
             float v = 0.f;
@@ -1826,6 +1860,8 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
     // Every logit of a short row fits the list, if a filter makes one.  A
     // top-k within the list needs no sums, and min-p without top-p neither.
     bool filtered = true, whole = false, sums = true;
+    c->bins[t] = 0;
+    float low = INFINITY;
     const float most = scan_rows<DT>(w.row, V, w.b0, w.b1, [&]() {
         if (t == 0) load_settings<SAMPLE>(a, o, c);
         __syncthreads();
@@ -1834,7 +1870,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
         whole = V <= kCap && filtered;
         sums = !SAMPLE || (c->top_k == 0 && !whole && (c->top_p < 1.f || c->least == 0));
         return sums ? c->ws.c_hi : 0.f;
-    }, s.sub, s.bsum);
+    }, s.sub, s.bsum, low);
     if (SAMPLE && c->bad) {
         if (cl.rank == 0 && t == 0) {
             write_none(a, o);
@@ -1843,15 +1879,22 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
         return;
     }
     const int k = c->top_k;
-    if ((t & 31) == 0) c->wmax[t >> 5] = most;
+    if ((t & 31) == 0) {
+        c->wmax[t >> 5] = most;
+        c->wmin[t >> 5] = low;
+    }
     cl.sync();
 
     if (cl.rank == 0) {
         float m = -INFINITY;
+        low = INFINITY;
         for (int rk = 0; rk < cl.split; ++rk) {
-            const float* wm = cl.at(c->wmax, rk);
+            const float *wm = cl.at(c->wmax, rk), *wl = cl.at(c->wmin, rk);
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) m = max_nan(m, wm[i]);
+            for (int i = 0; i < kWarps; ++i) {
+                m = max_nan(m, wm[i]);
+                low = fminf(low, wl[i]);
+            }
         }
         for (int rk = 1; rk < cl.split; ++rk) {  // the other slices' maxima and sums
             const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
@@ -1895,11 +1938,11 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
                 __syncthreads();
             }
             if constexpr (SAMPLE) {
-                verdict = sample_leader<DT>(a, s, w.row, V, nb, o, whole);
+                verdict = sample_leader<DT>(a, s, w.row, V, nb, o, whole, low);
                 if (verdict == kTier1 && filtered) verdict = place_bracket<DT>(w.row, V, s);
                 if (verdict == kList) verdict = place_list<DT>(w.row, V, k, s);
             } else {
-                const float least = whole ? -INFINITY : threshold_for(s.sub, nb * kRuns, k, m, c);
+                const float least = whole ? -INFINITY : threshold_for(s.sub, nb * kRuns, k, low, m, c);
                 verdict = kRadix;
                 if (!whole && !(least > -INFINITY)) {
                     verdict = place_list<DT>(w.row, V, k, s);
@@ -2018,17 +2061,17 @@ __global__ void __launch_bounds__(kThreads, 4) open_rows_kernel(const RowSearchA
 }
 
 template <int DT>
-size_t smem_for(int64_t V) {
+size_t smem_for(int64_t V, bool fine) {
     constexpr int BEL = kBatchVecs * Row<DT>::EPV;
-    return smem_bytes((int)((V + BEL - 1) / BEL));
+    return smem_bytes((int)((V + BEL - 1) / BEL), fine);
 }
 
 template <int DT, typename F>
-cudaError_t launch_rows(F kernel, const RowSearchArgs& a, int64_t grid, bool programmatic, cudaStream_t st) {
-    const size_t smem = smem_for<DT>(a.vocab);
+cudaError_t launch_rows(F kernel, const RowSearchArgs& a, int64_t grid, bool fine, bool programmatic, cudaStream_t st) {
+    const size_t smem = smem_for<DT>(a.vocab, fine);
     if (smem > 47 * 1024) {  // (static shared memory on top) the same limit whatever the call's size: calls may run side by side
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem_for<DT>(DLM_MAX_SEARCH_VOCAB));
+                                                   (int)smem_for<DT>(DLM_MAX_SEARCH_VOCAB, true));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -2060,18 +2103,18 @@ cudaError_t launch_sample(const RowSearchArgs& a, cudaStream_t st) {
     // rows of fewer batches than two per warp are finished where they are: a
     // pass over one takes its CTA less than a launch does
     if (a.split > 1 || a.vocab <= 2 * kWarps * kBatchVecs * Row<DT>::EPV)
-        return launch_rows<DT>(row_search_kernel<DT, true, false>, a, a.n_rows * a.split, false, st);
-    const cudaError_t e = launch_rows<DT>(row_search_kernel<DT, true, true>, a, a.n_rows, false, st);
+        return launch_rows<DT>(row_search_kernel<DT, true, false>, a, a.n_rows * a.split, true, false, st);
+    const cudaError_t e = launch_rows<DT>(row_search_kernel<DT, true, true>, a, a.n_rows, false, false, st);
     if (e != cudaSuccess) return e;
     RowSearchArgs open = a;
     open.split = kOpenSplit;
     const int64_t slots = (int64_t)a.num_sms * 4 / kOpenSplit, clusters = a.n_rows < slots ? a.n_rows : slots;
-    return launch_rows<DT>(open_rows_kernel<DT>, open, clusters * kOpenSplit, true, st);
+    return launch_rows<DT>(open_rows_kernel<DT>, open, clusters * kOpenSplit, true, true, st);
 }
 
 template <int DT>
 cudaError_t launch_topk(const RowSearchArgs& a, cudaStream_t st) {
-    return launch_rows<DT>(row_search_kernel<DT, false, false>, a, a.n_rows * a.split, false, st);
+    return launch_rows<DT>(row_search_kernel<DT, false, false>, a, a.n_rows * a.split, false, false, st);
 }
 
 }  // namespace
