@@ -57,6 +57,7 @@ constexpr int kListTopk = 1700;        // largest top-k whose list a sample's th
 constexpr uint64_t kOne = 1ull << kWeightBits;
 constexpr int kBins = 2048;            // radix bins of a pass over the whole row
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // ordered key of -inf
+static_assert(kCap == 8 * kThreads, "the longest list that is sorted");
 static_assert(kFine % kThreads == 0 && kFine >= kThreads, "whole bins per thread");
 static_assert(kCap >= 2 * DLM_MAX_TOPK, "a candidate list holds the largest top-k and ties");
 
@@ -114,14 +115,14 @@ struct Ctrl {
     uint64_t lo_side, hi_side;
     int hits[2][kWarps];
     uint32_t first[kWarps];
-    float wmax[kWarps];   // the first pass's maximum of each warp, and its smallest
-    float wmin[kWarps];   // (finite) run maximum
+    float wmax[8 * kWarps];  // the first pass's maximum of each warp of the cluster,
+    float wmin[8 * kWarps];  // and its smallest (finite) run maximum
     int bins[kThreads];
     float fscan[kWarps];
     uint64_t scan[kWarps];
 };
 
-// Shared memory of a CTA.  buf[kCap] holds candidates or radix bins; wbuf[kCap]
+// Shared memory of a CTA.  tab: the weights' table.  buf[kCap] holds candidates or radix bins; wbuf[kCap]
 // their weights, and behind buf the rest of a bracket's tokens.  sub[4 nb] and
 // bsum[nb], the first pass's run maxima and batch sums, and bties[nb] of the
 // radix search are used when wbuf is not and share its space.  fine[kFine]: the
@@ -129,6 +130,7 @@ struct Ctrl {
 // batches' mass; while runs are read again the list of them lies there.
 struct Smem {
     Ctrl* c;
+    uint64_t* tab;
     uint64_t* buf;
     uint64_t* wbuf;
     uint64_t* fine;
@@ -149,6 +151,8 @@ __device__ __forceinline__ Smem carve(unsigned char* p, int nb) {
     Smem s;
     s.c = reinterpret_cast<Ctrl*>(p);
     p += ctrl_bytes();
+    s.tab = reinterpret_cast<uint64_t*>(p);
+    p += sizeof(uint64_t) * 256;
     s.buf = reinterpret_cast<uint64_t*>(p);
     p += sizeof(uint64_t) * kCap;
     s.wbuf = reinterpret_cast<uint64_t*>(p);
@@ -165,7 +169,7 @@ __device__ __forceinline__ Smem carve(unsigned char* p, int nb) {
 
 // (`fine` only where a bracket is worked)
 size_t smem_bytes(int nb, bool fine) {
-    return ctrl_bytes() + sizeof(uint64_t) * (kCap + (fine ? kFine : 0) + (size_t)nb) + shared_space(nb);
+    return ctrl_bytes() + sizeof(uint64_t) * (256 + kCap + (fine ? kFine : 0) + (size_t)nb) + shared_space(nb);
 }
 
 // 64-bit sum in shared memory by two native 32-bit atomics: the carry of the
@@ -177,11 +181,69 @@ __device__ __forceinline__ void shared_add(uint64_t* p, uint64_t v) {
     if (hi) atomicAdd(half + 1, hi);
 }
 
-// Sort buf[0, n) ascending (n <= kBracketCap).  Short lists by rank (every thread
-// counts the smaller ones, broadcast reads, two barriers), longer ones by a
-// bitonic network padded to a power of two: each warp has an eighth of it, and
-// only the steps that reach past an eighth (6 of 66 for 2048) need the block's
-// barrier.
+// buf[0, 256 E) ascending: a bitonic network with E elements per thread in
+// registers.  Steps within a thread's elements need nothing, steps within a
+// warp's 32 E elements go by shuffles, and only those that reach further (6 of
+// 66 for 2048) through shared memory.  (With every step in shared memory 2048
+// elements took 91000 cycles.)
+template <int E>
+__device__ void bitonic(uint64_t* buf) {
+    const int lane = threadIdx.x & 31, base = threadIdx.x * E;
+    constexpr int M = kThreads * E;
+    uint64_t x[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = buf[base + e];
+    for (int k = 2; k <= M; k <<= 1) {
+        if (k > 32 * E) {
+            __syncthreads();  // (the loads, or the last round's, are done)
+#pragma unroll
+            for (int e = 0; e < E; ++e) buf[base + e] = x[e];
+            __syncthreads();
+            for (int j = k >> 1; j >= 32 * E; j >>= 1) {
+#pragma unroll
+                for (int q = 0; q < E / 2; ++q) {
+                    const int i = threadIdx.x + q * kThreads, lo = 2 * i - (i & (j - 1)), hi = lo + j;
+                    const uint64_t u = buf[lo], v = buf[hi];
+                    const bool swap = (u > v) == ((lo & k) == 0);
+                    buf[lo] = swap ? v : u;
+                    buf[hi] = swap ? u : v;
+                }
+                __syncthreads();
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = buf[base + e];
+        }
+        for (int j = min(k >> 1, 16 * E); j >= E; j >>= 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const uint64_t y = __shfl_xor_sync(DLM_FULL_MASK, x[e], j / E);
+                const bool up = ((base + e) & k) == 0, low = (lane & (j / E)) == 0;
+                x[e] = (up == low) == (x[e] < y) ? x[e] : y;
+            }
+        }
+#pragma unroll
+        for (int j = E / 2; j > 0; j >>= 1) {
+            if (2 * j > k) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (e & j) continue;
+                const bool up = ((base + e) & k) == 0;
+                const uint64_t u = x[e], v = x[e + j];
+                const bool swap = (u > v) == up;
+                x[e] = swap ? v : u;
+                x[e + j] = swap ? u : v;
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < E; ++e) buf[base + e] = x[e];
+    __syncthreads();
+}
+
+// Sort buf[0, n) ascending (n <= kCap).  Short lists by rank (every thread
+// counts the smaller ones, broadcast reads, two barriers), longer ones by the
+// network, padded to a power of two.
 __device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
     if (n <= kThreads) {
         const int i = threadIdx.x;
@@ -194,32 +256,15 @@ __device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
         __syncthreads();
         return;
     }
-    int m = 512;
-    while (m < n) m <<= 1;
+    const int m = n <= 2 * kThreads ? 2 * kThreads : n <= 4 * kThreads ? 4 * kThreads : 8 * kThreads;
     for (int i = n + threadIdx.x; i < m; i += kThreads) buf[i] = ~0ull;
     __syncthreads();
-    const int lane = threadIdx.x & 31, seg = m / kWarps, first = (threadIdx.x >> 5) * seg;
-    auto step = [&](int i, int k, int j) {
-        const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
-        const uint64_t a = buf[lo], b = buf[hi];
-        if ((a > b) == ((lo & k) == 0)) {
-            buf[lo] = b;
-            buf[hi] = a;
-        }
-    };
-    for (int k = 2; k <= m; k <<= 1) {
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            if (2 * j <= seg) {
-                for (int i = first / 2 + lane; i < (first + seg) / 2; i += 32) step(i, k, j);
-                __syncwarp();
-            } else {
-                if (2 * j == k) __syncthreads();  // (the steps before it were the warps' own)
-                for (int i = threadIdx.x; i < m / 2; i += kThreads) step(i, k, j);
-                __syncthreads();
-            }
-        }
-    }
-    __syncthreads();
+    if (m == 2 * kThreads)
+        bitonic<2>(buf);
+    else if (m == 4 * kThreads)
+        bitonic<4>(buf);
+    else
+        bitonic<8>(buf);
 }
 
 // A candidate: sorts by logit descending, then position ascending.
@@ -1275,7 +1320,9 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, b
     Ctrl* c = s.c;
     const int t = threadIdx.x;
     uint64_t total = 0, above = 0, n = 0;
-    for (int rk = 0; rk < cl.split; ++rk) {
+#pragma unroll
+    for (int rk = 0; rk < 8; ++rk) {
+        if (rk >= cl.split) break;
         const Ctrl* rc = cl.at(c, rk);
         total += rc->whole;
         above += rc->top;
@@ -1342,7 +1389,9 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, b
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         v[j] = 0;
-        for (int rk = 0; rk < cl.split; ++rk) v[j] += cl.at(s.fine, rk)[t * PER + j];
+#pragma unroll
+        for (int rk = 0; rk < 8; ++rk)  // all of them on their way at once
+            if (rk < cl.split) v[j] += cl.at(s.fine, rk)[t * PER + j];
         sum += v[j];
     }
     uint64_t m = block_scan(sum, c->scan, inside);
@@ -1518,11 +1567,7 @@ __device__ __forceinline__ void join_lists(const Cluster& cl, const Smem& s, uin
 }
 
 __device__ __forceinline__ void join_masses(const Cluster& cl, const Smem& s, int nb, int per) {
-    for (int rk = 1; rk < cl.split; ++rk) {
-        const int x0 = min(nb, rk * per), x1 = min(nb, x0 + per);
-        const uint64_t* rm = cl.at(s.bmass, rk);
-        for (int i = x0 + (int)threadIdx.x; i < x1; i += kThreads) s.bmass[i] = rm[i];
-    }
+    for (int i = per + (int)threadIdx.x; i < nb; i += kThreads) s.bmass[i] = cl.at(s.bmass, i / per)[i];
     __syncthreads();
 }
 
@@ -1643,7 +1688,7 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
 
 // A row's settings into ctrl (one thread of each CTA of its cluster).
 template <bool SAMPLE>
-__device__ __forceinline__ void load_settings(const RowSearchArgs& a, int64_t o, Ctrl* c) {
+__device__ __forceinline__ void load_settings(const RowSearchArgs& a, int64_t o, Ctrl* c, const uint64_t* tab) {
     float T = a.temperature, p = a.top_p, least = a.min_p;
     int k = a.k;
     bool bad = false;
@@ -1665,6 +1710,7 @@ __device__ __forceinline__ void load_settings(const RowSearchArgs& a, int64_t o,
     c->min_p = least;
     c->least = bad ? 0 : least < 1.f ? scale_ceil(kOne, least) : kOne;
     c->ws = weight_scale(0.f, bad ? 1.f : T);
+    c->ws.tab = tab;
 }
 
 __device__ __forceinline__ void write_none(const RowSearchArgs& a, int64_t o) {
@@ -1699,7 +1745,8 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
     const char* row = w.row;
     Ctrl* c = s.c;
     const Ctrl* c0 = cl.at(c, 0);
-    const WeightScale ws = c0->ws;
+    WeightScale ws = c0->ws;
+    ws.tab = s.tab;  // (this CTA's)
     if constexpr (SAMPLE) {
         while (verdict == kTier1 || verdict == kTier2) {
             const float z_lo = c0->z_lo, z_hi = c0->z_hi, per_bin = (float)kFine / (z_hi - z_lo);
@@ -1803,11 +1850,7 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
         cl.sync();
         if (cl.rank == 0) {
             join_masses(cl, s, nb, w.per);
-            for (int rk = 1; rk < cl.split; ++rk) {
-                const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
-                const uint32_t* rt = cl.at(s.bties, rk);
-                for (int i = x0 + t; i < x1; i += kThreads) s.bties[i] = rt[i];
-            }
+            for (int i = w.per + t; i < nb; i += kThreads) s.bties[i] = cl.at(s.bties, i / w.per)[i];
             if (t == 0) {
                 c->cut_key = cut_key;
                 c->cut_ties = cut_ties;
@@ -1861,17 +1904,23 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
     // top-k within the list needs no sums, and min-p without top-p neither.
     bool filtered = true, whole = false, sums = true;
     c->bins[t] = 0;
+    static_assert(kThreads == 256, "one entry of the table per thread");
+    s.tab[t] = kPow2Neg[t];
     float low = INFINITY;
+    // the maxima and sums go straight to the first CTA, which has to run by then
+    if (cl.split > 1) cg::this_cluster().barrier_arrive();
     const float most = scan_rows<DT>(w.row, V, w.b0, w.b1, [&]() {
-        if (t == 0) load_settings<SAMPLE>(a, o, c);
+        if (t == 0) load_settings<SAMPLE>(a, o, c, s.tab);
         __syncthreads();
         if (SAMPLE && c->bad) return -1.f;
         filtered = c->top_k > 0 || c->top_p < 1.f || c->least > 0;
         whole = V <= kCap && filtered;
         sums = !SAMPLE || (c->top_k == 0 && !whole && (c->top_p < 1.f || c->least == 0));
+        if (cl.split > 1) cg::this_cluster().barrier_wait();
         return sums ? c->ws.c_hi : 0.f;
-    }, s.sub, s.bsum, low);
+    }, cl.at(s.sub, 0), cl.at(s.bsum, 0), low);
     if (SAMPLE && c->bad) {
+        if (cl.split > 1) cg::this_cluster().barrier_wait();
         if (cl.rank == 0 && t == 0) {
             write_none(a, o);
             raise_status(a.dev_status, DLM_DEV_BAD_PARAM);
@@ -1880,30 +1929,20 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
     }
     const int k = c->top_k;
     if ((t & 31) == 0) {
-        c->wmax[t >> 5] = most;
-        c->wmin[t >> 5] = low;
+        cl.at(c, 0)->wmax[cl.rank * kWarps + (t >> 5)] = most;
+        cl.at(c, 0)->wmin[cl.rank * kWarps + (t >> 5)] = low;
     }
     cl.sync();
 
     if (cl.rank == 0) {
         float m = -INFINITY;
         low = INFINITY;
-        for (int rk = 0; rk < cl.split; ++rk) {
-            const float *wm = cl.at(c->wmax, rk), *wl = cl.at(c->wmin, rk);
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                m = max_nan(m, wm[i]);
-                low = fminf(low, wl[i]);
-            }
+        for (int i = t & 31; i < cl.split * kWarps; i += 32) {  // every warp for itself
+            m = max_nan(m, c->wmax[i]);
+            low = fminf(low, c->wmin[i]);
         }
-        for (int rk = 1; rk < cl.split; ++rk) {  // the other slices' maxima and sums
-            const int x0 = min(nb, rk * w.per), x1 = min(nb, x0 + w.per);
-            const float* rs = cl.at(s.sub, rk);
-            const float* rb = cl.at(s.bsum, rk);
-            for (int i = x0 * kRuns + t; i < x1 * kRuns; i += kThreads) s.sub[i] = rs[i];
-            if (sums)
-                for (int i = x0 + t; i < x1; i += kThreads) s.bsum[i] = rb[i];
-        }
+        m = warp_max_nan(m);
+        low = -warp_max_nan(-low);
         if (t == 0) c->ws.m = m;
         __syncthreads();
         int verdict = kDone;
@@ -2000,6 +2039,7 @@ __global__ void __launch_bounds__(kThreads, 4) open_rows_kernel(const RowSearchA
     constexpr int BEL = kBatchVecs * Row<DT>::EPV;
     const Smem s = carve(s_raw, (int)((a.vocab + BEL - 1) / BEL));
     Ctrl* c = s.c;
+    s.tab[t] = kPow2Neg[t];
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the first launch's marks
     int64_t from = 0;  // rows looked at, from `place` on, that are not open any more
     while (true) {
@@ -2048,7 +2088,7 @@ __global__ void __launch_bounds__(kThreads, 4) open_rows_kernel(const RowSearchA
         const Work w(a, cl, q, a.gather ? r : q, Row<DT>::ESZ, BEL);
         const int verdict = (int)(mark >> 24) & 7;
         if (t == 0) {  // every CTA of the cluster keeps the row's settings
-            load_settings<true>(a, w.o, c);
+            load_settings<true>(a, w.o, c, s.tab);
             c->ws.m = *(const volatile float*)(a.prob + w.o);
             c->bin_lo = (int)(mark >> 12) & 0xfff;
             c->bin_hi = (int)mark & 0xfff;

@@ -104,9 +104,11 @@ static const uint64_t kPow2Neg[256] = {
     0x08164d1f3bc0ull, 0x0810b40a1d81ull, 0x080b1ed4fd9aull, 0x08058d7d2d5eull,
 };
 
-// The row's constants: the maximum and log2(e) / T as a sum of two floats.
+// The row's constants: the maximum and log2(e) / T as a sum of two floats, and
+// where the table lies (a kernel's copy in shared memory, or the constant one).
 struct WeightScale {
     float m, c_hi, c_lo;
+    const uint64_t* tab;
 };
 
 // log2(e) / T to 2^-47: a float quotient and its remainder's.
@@ -116,6 +118,7 @@ DLM_HD WeightScale weight_scale(float m, float temperature) {
     s.m = m;
     s.c_hi = kHi / temperature;
     s.c_lo = (fmaf(-s.c_hi, temperature, kHi) + kLo) / temperature;
+    s.tab = kPow2Neg;
     return s;
 }
 
@@ -133,7 +136,7 @@ DLM_HD float weight_exponent(float z, const WeightScale& s, float& lo) {
 }
 
 // 2^-(y + e) in units of 2^-44, y >= 0 and e small against 2^-9.
-DLM_HD uint64_t weight44_of(float y, float e) {
+DLM_HD uint64_t weight44_of(float y, float e, const uint64_t* table = kPow2Neg) {
     if (!(y < kWeightCut)) return 0;
     constexpr float kMagic = 49152.0f;  // 1.5 * 2^15: its last place is 2^-8
     const float t = y + kMagic;
@@ -151,7 +154,7 @@ DLM_HD uint64_t weight44_of(float y, float e) {
     const float gf = (float)g;
     const int g3 = (int)(gf * gf * gf * 5.5145374e-25f);  // 2^-78 / 6
     const int q = g2 - g - g3;
-    const uint64_t tab = kPow2Neg[k & 255];
+    const uint64_t tab = table[k & 255];
     const uint64_t w = tab + (uint64_t)(((int64_t)(tab >> 13) * q) >> 26);
     const int n = k >> 8;
     return (w + ((1ull << n) >> 1)) >> n;
@@ -161,7 +164,7 @@ DLM_HD uint64_t weight44_of(float y, float e) {
 DLM_HD uint64_t weight44(float z, const WeightScale& s) {
     float e;
     const float y = weight_exponent(z, s, e);
-    return weight44_of(y, e);
+    return weight44_of(y, e, s.tab);
 }
 
 // floor(f * s) for a float f in [0, 1): f = mantissa * 2^-shift exactly.
