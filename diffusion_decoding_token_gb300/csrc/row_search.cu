@@ -71,6 +71,11 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // What one row's CTA (the first of its cluster) and the others share.
+// weight44 as a call: where it is met once or rarely, fifty instructions inline
+// cost more to fetch than to run (a row that takes the long way runs most of its
+// code once, and waited for instructions more than for anything but barriers).
+__device__ __noinline__ uint64_t weight_call(float z, const WeightScale ws) { return weight44(z, ws); }
+
 // What is to be done for a row: nothing more, a pass of tier 1 or 2, a list of
 // everything above a threshold, a pass of tier 1 around min-p's cut, or the
 // radix search.
@@ -637,7 +642,7 @@ __device__ __noinline__ void keep_candidates(const Smem& s, int n, ListRule rule
     const int per = (K + kThreads - 1) / kThreads, i0 = min(K, t * per), i1 = min(K, i0 + per);
     uint64_t sum = 0;
     for (int i = i0; i < i1; ++i) {
-        const uint64_t w = weight44(candidate_value(s.buf[i]), c->ws);
+        const uint64_t w = weight_call(candidate_value(s.buf[i]), c->ws);
         s.wbuf[i] = w;
         sum += w;
     }
@@ -746,7 +751,7 @@ __device__ __noinline__ void radix_pass(const char* row, int64_t V, int b0, int 
             if (key <= floor_key || (shift + bits < 32 && (key >> (shift + bits)) != prefix)) continue;
             const uint32_t bin = (key >> shift) & mask;
             if constexpr (MASS) {
-                const uint64_t w = weight44(z[e], ws);
+                const uint64_t w = weight_call(z[e], ws);
                 const uint32_t wl = (uint32_t)w;
                 const uint32_t old = atomicAdd(&lo[bin], wl);
                 const uint32_t up = (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u);
@@ -847,7 +852,7 @@ __device__ __noinline__ void mass_cut(const Cluster& cl, const Smem& s, const ch
                          uint32_t& ties) {
     uint32_t* lo = reinterpret_cast<uint32_t*>(s.buf);
     const Ctrl* c0 = cl.at(s.c, 0);
-    const uint64_t w_floor = floor_key > kKeyNegInf ? weight44(key_value(floor_key), ws) : 0;
+    const uint64_t w_floor = floor_key > kKeyNegInf ? weight_call(key_value(floor_key), ws) : 0;
     uint32_t prefix = 0;
     uint64_t above = 0, target = ~0ull, total = 0;
     for (int l = 0; l < 3; ++l) {
@@ -871,7 +876,7 @@ __device__ __noinline__ void mass_cut(const Cluster& cl, const Smem& s, const ch
         cl.sync();
     }
     key = prefix;
-    const uint64_t w = weight44(key_value(key), ws);  // > 0: its bin had mass
+    const uint64_t w = weight_call(key_value(key), ws);  // > 0: its bin had mass
     ties = (uint32_t)((target - above + w - 1) / w);
 }
 
@@ -892,7 +897,7 @@ __device__ __noinline__ void batch_masses(const char* row, int64_t V, int b0, in
             for (int e = 0; e < EPV; ++e) {
                 const uint32_t key = key_of(z[e]);
                 if (key > cut_key) {
-                    const uint64_t w = weight44(z[e], ws);
+                    const uint64_t w = weight_call(z[e], ws);
                     m += w >= least ? w : 0ull;
                 }
                 ties += key == cut_key;
@@ -976,7 +981,7 @@ __device__ __noinline__ void walk_batch(const char* row, int64_t V, Ctrl* c) {
         const uint32_t key = key_of(z[e]);
         const bool tie = key == cut_key;
         const bool stays = key > cut_key || (tie && rank < cut_ties && (uint32_t)(at + e) <= c->cut_last);
-        w[e] = stays ? weight44(z[e], ws) : 0ull;
+        w[e] = stays ? weight_call(z[e], ws) : 0ull;
         if (w[e] < c->least) w[e] = 0;
         rank += tie;
         sum += w[e];
@@ -1012,7 +1017,7 @@ __device__ __noinline__ int first_kept(const char* row, int64_t V, int nb, const
             const uint32_t key = key_of(z[e]);
             const bool in = key > c->cut_key || (key == c->cut_key && c->cut_ties > 0 &&
                                                  (uint32_t)((v0 + lane) * EPV + e) <= c->cut_last);
-            if (in && (c->least == 0 || weight44(z[e], ws) >= c->least)) e0 = e;
+            if (in && (c->least == 0 || weight_call(z[e], ws) >= c->least)) e0 = e;
         }
         const uint32_t who = __ballot_sync(DLM_FULL_MASK, e0 < EPV);
         if (who) {
@@ -1068,11 +1073,16 @@ __device__ __noinline__ float sample_row(const char* row, int64_t V, const Smem&
     const int nsub = (int)((V + 32 * EPV - 1) / (32 * EPV));
     const int n = min(nsub, kSampleTokens / (32 * EPV));
     const float c32 = c->ws.c_hi * 32.f, m = c->ws.m;
-#pragma unroll 4
+    const int stride = nsub / n;
+    auto fetch = [&](int i) { return i < n ? load_vec<DT>(row, V, i * stride * 32 + lane) : make_uint4(0, 0, 0, 0); };
+    uint4 w0 = fetch(warp), w1 = fetch(warp + kWarps), w2 = fetch(warp + 2 * kWarps);
+#pragma unroll 1
     for (int i = warp; i < n; i += kWarps) {
-        const int run = (int)((int64_t)i * nsub / n);
         float z[EPV];
-        Row<DT>::unpack(load_vec<DT>(row, V, run * 32 + lane), z);
+        Row<DT>::unpack(w0, z);
+        w0 = w1;
+        w1 = w2;
+        w2 = fetch(i + 3 * kWarps);
 #pragma unroll
         for (int e = 0; e < EPV; ++e) {
             if (!(z[e] > -INFINITY)) continue;
@@ -1206,62 +1216,59 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
     const float z_min = fmaxf(ws.m - 99.f / ws.c_hi, -FLT_MAX);  // a weight of 2^-99 counts as 0
     const SplitScale sp{pack2(ws.m, ws.m), pack2(-ws.c_hi, -ws.c_hi), pack2(-ws.c_lo, -ws.c_lo)};
     uint64_t whole = 0, top = 0, sum = 0;
-    uint4 next[kRuns];  // the next batch is loaded while one is summed
-    if (b0 + warp < b1) {
-#pragma unroll
-        for (int i = 0; i < kRuns; ++i) next[i] = load_vec<DT>(row, V, (b0 + warp) * kBatchVecs + i * 32 + lane);
-    }
-    for (int b = b0 + warp; b < b1; b += kWarps) {
-        uint64_t above = 0;
-        uint4 w4[kRuns];
-        const int v0 = b * kBatchVecs + lane;
-#pragma unroll
-        for (int i = 0; i < kRuns; ++i) w4[i] = next[i];
-        if (b + kWarps < b1) {
-#pragma unroll
-            for (int i = 0; i < kRuns; ++i) next[i] = load_vec<DT>(row, V, v0 + kWarps * kBatchVecs + i * 32);
-        }
+    // a run at a time (one copy of the code), two more on their way: the warp's
+    // i-th run is run i % 4 of its batch i / 4
+    const int runs = b0 + warp < b1 ? ((b1 - b0 - warp + kWarps - 1) / kWarps) * kRuns : 0;
+    auto vec_of = [&](int i) { return ((b0 + warp + (i / kRuns) * kWarps) * kRuns + i % kRuns) * 32 + lane; };
+    auto fetch = [&](int i) { return i < runs ? load_vec<DT>(row, V, vec_of(i)) : make_uint4(0, 0, 0, 0); };
+    uint4 w1 = fetch(0), w2 = fetch(1);
+    uint64_t above = 0;
+#pragma unroll 1
+    for (int i = 0; i < runs; ++i) {
+        const uint4 w0 = w1;
+        w1 = w2;
+        w2 = fetch(i + 2);
+        float z[EPV];
+        Row<DT>::unpack(w0, z);
         uint32_t mask = 0;  // tokens inside, a bit each
+        if constexpr (EXACT) {
 #pragma unroll
-        for (int i = 0; i < kRuns; ++i) {
-            float z[EPV];
-            Row<DT>::unpack(w4[i], z);
-            if constexpr (EXACT) {
-#pragma unroll
-                for (int e = 0; e < EPV; ++e) {
-                    const uint64_t w = weight44(z[e], ws);
-                    const bool up = z[e] >= z_hi;
-                    above += up ? w : 0ull;
-                    whole += w;
-                    mask |= (uint32_t)(!up && z[e] >= z_lo) << (i * EPV + e);
-                }
-            } else {
-                f2 up[EPV / 2], all[EPV / 2];
-#pragma unroll
-                for (int p = 0; p < EPV / 2; ++p) {
-                    const float x = fmaxf(z[2 * p], z_min), y = fmaxf(z[2 * p + 1], z_min);
-                    all[p] = weight_split(pack2(x, y), sp);
-                    float wx, wy;
-                    unpack2(all[p], wx, wy);
-                    const bool ux = x >= z_hi, uy = y >= z_hi;
-                    up[p] = pack2(ux ? wx : 0.f, uy ? wy : 0.f);
-                    mask |= (uint32_t)(!ux && x >= z_lo) << (i * EPV + 2 * p);
-                    mask |= (uint32_t)(!uy && y >= z_lo) << (i * EPV + 2 * p + 1);
-                }
-#pragma unroll
-                for (int h = EPV / 4; h; h >>= 1)
-#pragma unroll
-                    for (int p = 0; p < h; ++p) {
-                        up[p] = add2(up[p], up[p + h]);
-                        all[p] = add2(all[p], all[p + h]);
-                    }
-                above += __float2ull_rn(hsum2(up[0]) * 0x1p44f);
-                whole += __float2ull_rn(hsum2(all[0]) * 0x1p44f);
+            for (int e = 0; e < EPV; ++e) {
+                const uint64_t w = weight_call(z[e], ws);
+                const bool up = z[e] >= z_hi;
+                above += up ? w : 0ull;
+                whole += w;
+                mask |= (uint32_t)(!up && z[e] >= z_lo) << e;
             }
+        } else {
+            f2 up[EPV / 2], all[EPV / 2];
+#pragma unroll
+            for (int p = 0; p < EPV / 2; ++p) {
+                const float x = fmaxf(z[2 * p], z_min), y = fmaxf(z[2 * p + 1], z_min);
+                all[p] = weight_split(pack2(x, y), sp);
+                float wx, wy;
+                unpack2(all[p], wx, wy);
+                const bool ux = x >= z_hi, uy = y >= z_hi;
+                up[p] = pack2(ux ? wx : 0.f, uy ? wy : 0.f);
+                mask |= (uint32_t)(!ux && x >= z_lo) << (2 * p);
+                mask |= (uint32_t)(!uy && y >= z_lo) << (2 * p + 1);
+            }
+#pragma unroll
+            for (int h = EPV / 4; h; h >>= 1)
+#pragma unroll
+                for (int p = 0; p < h; ++p) {
+                    up[p] = add2(up[p], up[p + h]);
+                    all[p] = add2(all[p], all[p + h]);
+                }
+            above += __float2ull_rn(hsum2(up[0]) * 0x1p44f);
+            whole += __float2ull_rn(hsum2(all[0]) * 0x1p44f);
         }
-        top += above;
-        above = (uint64_t)warp_sum_ll((long long)above);
-        if (lane == 0) bmass[b] = above;
+        if (i % kRuns == kRuns - 1) {
+            top += above;
+            above = (uint64_t)warp_sum_ll((long long)above);
+            if (lane == 0) bmass[b0 + warp + (i / kRuns) * kWarps] = above;
+            above = 0;
+        }
         if (!__any_sync(DLM_FULL_MASK, mask != 0)) continue;
         const int mine = __popc(mask);
         int inc = mine;
@@ -1273,13 +1280,12 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
         uint32_t at = 0;
         if (lane == 31) at = atomicAdd(&c->count, (uint32_t)inc);
         at = __shfl_sync(DLM_FULL_MASK, at, 31) + (uint32_t)(inc - mine);
-        while (mask) {
-            const int bit = __ffs(mask) - 1;
-            mask &= mask - 1;
-            const int64_t pos = (int64_t)(v0 + (bit / EPV) * 32) * EPV + bit % EPV;
-            if (at < (uint32_t)kBracketCap) dst[at] = candidate(Row<DT>::scalar(row, pos), (uint32_t)pos);
-            ++at;
-        }
+#pragma unroll
+        for (int e = 0; e < EPV; ++e)
+            if ((mask >> e) & 1u) {
+                if (at < (uint32_t)kBracketCap) dst[at] = candidate(z[e], (uint32_t)(vec_of(i) * EPV + e));
+                ++at;
+            }
     }
     block_scan(whole, c->scan, sum);
     if (threadIdx.x == 0) c->whole = sum;
@@ -1304,7 +1310,7 @@ __device__ __noinline__ void bin_tokens(const Smem& s, float z_hi, float per_bin
         const uint64_t e = i < n ? s.buf[i] : 0;
         const uint32_t like = __match_any_sync(DLM_FULL_MASK, i < n ? (uint32_t)(e >> 32) : 0xffffffffu);
         if (i < n && __ffs(like) - 1 == (t & 31))
-            shared_add(&s.fine[fine_bin(e, z_hi, per_bin)], weight44(candidate_value(e), ws) * __popc(like));
+            shared_add(&s.fine[fine_bin(e, z_hi, per_bin)], weight_call(candidate_value(e), ws) * __popc(like));
     }
     __syncthreads();
 }
@@ -1371,7 +1377,7 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, b
     if (c->by_min) {
         if (n > (uint64_t)kBracketCap) return kRadix;
         // the cut has to be inside the bracket (the logits' estimate was near)
-        if (weight44(fminf(c->z_hi, c->ws.m), c->ws) < c->least || weight44(c->z_lo, c->ws) >= c->least) return kRadix;
+        if (weight_call(fminf(c->z_hi, c->ws.m), c->ws) < c->least || weight_call(c->z_lo, c->ws) >= c->least) return kRadix;
         __syncthreads();
         return kDone;
     }
@@ -1415,7 +1421,7 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, b
     // (a bin's lowest logit, and what else is in it, decides min-p)
     if (c->least > 0) {
         const float z = c->z_hi - (float)(c->last_bin + 1) / (float)kFine * (c->z_hi - c->z_lo) * 1.0001f;
-        if (weight44(z, c->ws) < c->least) return miss(kToMin);
+        if (weight_call(z, c->ws) < c->least) return miss(kToMin);
     }
     return kDone;
 }
@@ -1436,7 +1442,7 @@ __device__ __noinline__ void keep_tokens(const Cluster& cl, const Smem& s, const
         const uint64_t e = s.buf[i];
         const int bin = by_min ? 0 : fine_bin(e, z_hi, per_bin);
         if (by_min || bin < f0) {
-            const uint64_t w = weight44(candidate_value(e), ws);
+            const uint64_t w = weight_call(candidate_value(e), ws);
             if (w >= least) shared_add(&s.bmass[(uint32_t)e / BEL], w);
         } else if (bin <= f1) {
             const uint32_t at = atomicAdd(count, 1u);
@@ -1477,7 +1483,7 @@ __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const
         };
         if (n <= kThreads) {
             const uint64_t mine = t < n ? s.fine[t] : ~0ull;
-            const uint64_t w = t < n ? weight44(candidate_value(mine), c->ws) : 0ull;
+            const uint64_t w = t < n ? weight_call(candidate_value(mine), c->ws) : 0ull;
             if (t < n) s.buf[t] = w;
             __syncthreads();
             if (t < n) {
@@ -1490,10 +1496,10 @@ __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const
             sort_u64(s.fine, n);
             const int per = (n + kThreads - 1) / kThreads, i0 = min(n, t * per), i1 = min(n, i0 + per);
             uint64_t mine = 0, all;
-            for (int i = i0; i < i1; ++i) mine += weight44(candidate_value(s.fine[i]), c->ws);
+            for (int i = i0; i < i1; ++i) mine += weight_call(candidate_value(s.fine[i]), c->ws);
             uint64_t m0 = before_bin + block_scan(mine, c->scan, all);
             for (int i = i0; i < i1; ++i) {
-                const uint64_t w = weight44(candidate_value(s.fine[i]), c->ws);
+                const uint64_t w = weight_call(candidate_value(s.fine[i]), c->ws);
                 crossing(s.fine[i], m0, w);
                 m0 += w;
             }
@@ -1858,7 +1864,7 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
                 c->ties_before = 0;
             }
             __syncthreads();
-            uint64_t w_tie = cut_key > kKeyNegInf && cut_ties > 0 ? weight44(key_value(cut_key), ws) : 0;
+            uint64_t w_tie = cut_key > kKeyNegInf && cut_ties > 0 ? weight_call(key_value(cut_key), ws) : 0;
             if (w_tie < c->least) w_tie = 0;
             find_batch(s, nb, w_tie, cut_ties);
             if (c->u > 0.f) {
