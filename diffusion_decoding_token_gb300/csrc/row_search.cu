@@ -21,8 +21,10 @@
 // than that from the target is the answer, otherwise the next tier looks:
 //   0  the first pass's batch sums (off by 2^-18; no filter only);
 //   1  one more pass with the exponent split into integer and fraction (2^-20.8);
-//   2  the same pass with integer weights (2^-36).
-// The passes of tiers 1 and 2 find the nucleus' end by a bracket: a sample of
+//   2  the same with the fraction's power from a table of exact values, summed
+//      as integers, and a small correction in 32 bits (2^-27);
+//   3  the same with integer weights (2^-36).
+// The passes of tiers 1 to 3 find the nucleus' end by a bracket: a sample of
 // the row says between which two logits it must lie, the pass sums what is
 // above, lists what is inside, and the list is sorted.  What the bracket
 // misses (ties by the thousand, a top-k beyond the list) goes to a search by
@@ -51,7 +53,7 @@ constexpr int kFine = 1024;            // bins that a bracket's tokens are sorte
 constexpr int kListRuns = 128;         // run maxima that open a nucleus' candidate list
 constexpr int kBracketSide = 1200;     // tokens on either side of its middle
 constexpr int kSampleTokens = 16384;   // the sample that places a bracket
-constexpr int kOpenSplit = 2;          // CTAs per row that the first launch left open
+constexpr int kOpenSplit = 4;          // CTAs per row that the first launch left open
 constexpr int kTries = 4;              // brackets that a row gets
 constexpr int kListTopk = 1700;        // largest top-k whose list a sample's threshold can be trusted with
 constexpr uint64_t kOne = 1ull << kWeightBits;
@@ -76,10 +78,10 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 // code once, and waited for instructions more than for anything but barriers).
 __device__ __noinline__ uint64_t weight_call(float z, const WeightScale ws) { return weight44(z, ws); }
 
-// What is to be done for a row: nothing more, a pass of tier 1 or 2, a list of
-// everything above a threshold, a pass of tier 1 around min-p's cut, or the
+// What is to be done for a row: nothing more, a pass of tier 1, 2 or 3, a list
+// of everything above a threshold, a pass of tier 1 around min-p's cut, or the
 // radix search.
-enum Verdict : int { kRadix = 0, kDone = 1, kTier1 = 2, kTier2 = 3, kList = 4, kMinP = 5 };
+enum Verdict : int { kRadix = 0, kDone = 1, kTier1 = 2, kTier2 = 3, kTier3 = 4, kList = 5, kMinP = 6 };
 
 struct Ctrl {
     WeightScale ws;
@@ -452,10 +454,17 @@ __device__ void gather_runs(const char* row, int64_t V, int nsub, const Smem& s,
 template <int DT>
 __device__ __noinline__ void gather_slice(const char* row, int64_t V, int b0, int b1, float least, uint64_t* dst,
                                           uint32_t* count) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int s = b0 * kRuns + warp; s < b1 * kRuns; s += kWarps) {
-        const int v = s * 32 + lane;
-        push<DT>(load_vec<DT>(row, V, v), (uint32_t)(v * Row<DT>::EPV), least, INFINITY, dst, kCap, count);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, end = b1 * kRuns;
+    auto fetch = [&](int i) { return i < end ? load_vec<DT>(row, V, i * 32 + lane) : make_uint4(0, 0, 0, 0); };
+    int i = b0 * kRuns + warp;
+    uint4 w0 = fetch(i), w1 = fetch(i + kWarps), w2 = fetch(i + 2 * kWarps);
+#pragma unroll 1
+    for (; i < end; i += kWarps) {
+        const uint4 w = w0;
+        w0 = w1;
+        w1 = w2;
+        w2 = fetch(i + 3 * kWarps);
+        push<DT>(w, (uint32_t)((i * 32 + lane) * Row<DT>::EPV), least, INFINITY, dst, kCap, count);
     }
 }
 
@@ -1052,6 +1061,44 @@ __device__ __forceinline__ f2 weight_split(f2 z, const SplitScale& s) {
                  __int_as_float(__float_as_int(y) + (__float_as_int(ty) << 23)));
 }
 
+// Two weights as T 2^-n + a correction in 32 bits: 32 y = k + r, T = 2^(-j / 32)
+// with j = k mod 32, n = k div 32, T = table value M 2^-24 + lo exactly, so the
+// weight is (M << 20) >> n in units of 2^-44 plus (M 2^-24 (2^(-r / 32) - 1) + lo)
+// 2^-n, whose error is below 2^-28 of the weight.  `tab`: this lane's column of
+// the 32 values as floats M 2^-24, `tab + 1024` of the lo (a copy per bank).
+struct FineScale {
+    f2 m, nc_hi, nc_lo;  // the maximum, and minus 32 log2(e) / T in two floats
+    const float* tab;
+};
+__device__ __forceinline__ void weight_fine(f2 z, const FineScale& s, uint64_t (&hi)[2], f2& lo) {
+    const f2 magic = pack2(12582912.0f, 12582912.0f);
+    const f2 d = sub2(s.m, z);
+    const f2 b = sub2(d, s.m);
+    const f2 err = sub2(sub2(s.m, sub2(d, b)), add2(z, b));
+    const f2 t = fma2(d, s.nc_hi, magic);  // magic - k
+    f2 f = fma2(d, s.nc_hi, sub2(magic, t));
+    f = fma2(d, s.nc_lo, f);
+    f = fma2(err, s.nc_hi, f);
+    const f2 x = mul2(f, pack2(0.021660849392498291f, 0.021660849392498291f));  // ln 2 / 32
+    // e^x - 1 = x + x^2 / 2 + x^3 / 6 + x^4 / 24, |x| < 0.011
+    f2 q = fma2(x, pack2(1.f / 24, 1.f / 24), pack2(1.f / 6, 1.f / 6));
+    q = fma2(q, x, pack2(0.5f, 0.5f));
+    q = fma2(q, x, pack2(1.f, 1.f));
+    q = mul2(q, x);
+    float tt[2], qq[2], l[2];
+    unpack2(t, tt[0], tt[1]);
+    unpack2(q, qq[0], qq[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int k = 0x4b400000 - __float_as_int(tt[i]), j = k & 31, n = k >> 5;
+        const float v = s.tab[j * 32];
+        const uint32_t m = (__float_as_uint(v) & 0x7fffffu) | 0x800000u;  // v is in [1/2, 1)
+        hi[i] = ((uint64_t)m << 20) >> n;
+        l[i] = fmaf(v, qq[i], s.tab[1024 + j * 32]) * __int_as_float((127 - n) << 23);
+    }
+    lo = pack2(l[0], l[1]);
+}
+
 // The smallest logit that min-p can keep (or one a little lower: the weights
 // decide).
 __device__ __forceinline__ float min_p_logit(const Ctrl* c) {
@@ -1207,14 +1254,27 @@ __device__ __forceinline__ void set_bracket(Ctrl* c, int verdict) {
 
 // One pass over a slice: bmass[b] the mass of batch b at z >= z_hi, c->whole
 // the slice's whole mass, and the tokens of [z_lo, z_hi) into dst, c->count of
-// them (which may exceed kBracketCap).  EXACT: integer weights, else weight_split summed over a vector in 32 bits.
-template <int DT, bool EXACT>
+// them (which may exceed kBracketCap).  TIER 1: weight_split summed over a vector
+// in 32 bits, 2: weight_fine (its table in `fine`), 3: integer weights.
+template <int DT, int TIER>
 __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, int b1, float z_lo, float z_hi,
-                                          const WeightScale ws, uint64_t* bmass, Ctrl* c, uint64_t* dst) {
+                                          const WeightScale ws, uint64_t* bmass, Ctrl* c, uint64_t* dst,
+                                          float* fine) {
     constexpr int EPV = Row<DT>::EPV;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float z_min = fmaxf(ws.m - 99.f / ws.c_hi, -FLT_MAX);  // a weight of 2^-99 counts as 0
+    // a weight of 2^-60 counts as 0
+    const float z_min = fmaxf(ws.m - 60.f / ws.c_hi, -FLT_MAX), c32 = -32.f * ws.c_hi, d32 = -32.f * ws.c_lo;
     const SplitScale sp{pack2(ws.m, ws.m), pack2(-ws.c_hi, -ws.c_hi), pack2(-ws.c_lo, -ws.c_lo)};
+    const FineScale fs{pack2(ws.m, ws.m), pack2(c32, c32), pack2(d32, d32), fine + lane};
+    if (TIER == 2) {
+        for (int i = threadIdx.x; i < 1024; i += kThreads) {
+            const uint64_t v = ws.tab[(i >> 5) * 8];
+            const uint32_t m = min((uint32_t)(v >> 20), 0xffffffu);
+            fine[i] = (float)m * 0x1p-24f;
+            fine[1024 + i] = (float)(uint32_t)(v - ((uint64_t)m << 20)) * 0x1p-44f;
+        }
+        __syncthreads();
+    }
     uint64_t whole = 0, top = 0, sum = 0;
     // a run at a time (one copy of the code), two more on their way: the warp's
     // i-th run is run i % 4 of its batch i / 4
@@ -1231,7 +1291,7 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
         float z[EPV];
         Row<DT>::unpack(w0, z);
         uint32_t mask = 0;  // tokens inside, a bit each
-        if constexpr (EXACT) {
+        if constexpr (TIER == 3) {
 #pragma unroll
             for (int e = 0; e < EPV; ++e) {
                 const uint64_t w = weight_call(z[e], ws);
@@ -1240,6 +1300,26 @@ __device__ __noinline__ void bracket_pass(const char* row, int64_t V, int b0, in
                 whole += w;
                 mask |= (uint32_t)(!up && z[e] >= z_lo) << e;
             }
+        } else if constexpr (TIER == 2) {
+            f2 up = pack2(0.f, 0.f), all = pack2(0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < EPV / 2; ++p) {
+                const float x = fmaxf(z[2 * p], z_min), y = fmaxf(z[2 * p + 1], z_min);
+                uint64_t w[2];
+                f2 lo;
+                weight_fine(pack2(x, y), fs, w, lo);
+                const bool ux = x >= z_hi, uy = y >= z_hi;
+                above += (ux ? w[0] : 0ull) + (uy ? w[1] : 0ull);
+                whole += w[0] + w[1];
+                float lx, ly;
+                unpack2(lo, lx, ly);
+                all = add2(all, lo);
+                up = add2(up, pack2(ux ? lx : 0.f, uy ? ly : 0.f));
+                mask |= (uint32_t)(!ux && x >= z_lo) << (2 * p);
+                mask |= (uint32_t)(!uy && y >= z_lo) << (2 * p + 1);
+            }
+            above += (uint64_t)__float2ll_rn(hsum2(up) * 0x1p44f);
+            whole += (uint64_t)__float2ll_rn(hsum2(all) * 0x1p44f);
         } else {
             f2 up[EPV / 2], all[EPV / 2];
 #pragma unroll
@@ -1322,7 +1402,7 @@ __device__ __noinline__ void bin_tokens(const Smem& s, float z_hi, float per_bin
 // ctrl then has the bins that may hold it (first_bin, last_bin), the mass before
 // them (left) and the targets; else another bracket is set and it is a tier's,
 // or kRadix.
-__device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, bool last_tier) {
+__device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, int tier) {
     Ctrl* c = s.c;
     const int t = threadIdx.x;
     uint64_t total = 0, above = 0, n = 0;
@@ -1334,9 +1414,11 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, b
         above += rc->top;
         n = max(n, (uint64_t)rc->count);
     }
-    // integer weights 2^-37; else, in 2^-24, ex2 4, the fraction's roundings and
-    // the conversion 2, three levels of additions 3
-    const uint64_t err = last_tier ? (total >> 36) + (uint64_t)nb : (total >> 24) * 9 + (uint64_t)nb;
+    // tier 1, in 2^-24: ex2 4, the fraction's roundings and the conversion 2,
+    // three levels of additions 3.  Tier 2, in 2^-24 of a correction that is at
+    // most 2^-6.5 of its weight: the table's product 2, the power 2, the
+    // exponent's roundings 2, additions 4.  Tier 3: integer weights, 2^-37
+    const uint64_t err = (tier == kTier1 ? (total >> 24) * 9 : total >> (tier == kTier2 ? 27 : 36)) + 4 * (uint64_t)nb;
     const float p = c->top_p;
     const uint64_t x = p < 1.f ? scale_ceil(total, p) : ~0ull;
     const uint64_t off = p < 1.f ? (uint64_t)((float)err * 2.0001f * p * (1.f - p)) + 2 : 0;  // rounded up
@@ -1366,7 +1448,7 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, b
             c->tries += 1;
         }
         __syncthreads();
-        return c->tries < kTries ? (last_tier ? kTier2 : kTier1) : kRadix;
+        return c->tries < kTries ? tier : (int)kRadix;
     };
     if (t == 0) {
         c->total = total;
@@ -1456,7 +1538,7 @@ __device__ __noinline__ void keep_tokens(const Cluster& cl, const Smem& s, const
 // whatever its distance from a border.  Returns the next verdict.
 template <int DT>
 __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const char* row, int64_t V, int nb,
-                                    int64_t o, bool last_tier) {
+                                    int64_t o, int tier) {
     constexpr int BEL = kBatchVecs * Row<DT>::EPV;
     Ctrl* c = s.c;
     const int t = threadIdx.x;
@@ -1530,7 +1612,7 @@ __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const
             c->tries += 1;
         }
         __syncthreads();
-        return c->tries < kTries ? (last_tier ? kTier2 : kTier1) : kRadix;
+        return c->tries < kTries ? tier : (int)kRadix;
     }
     const bool first = c->u == 0.f;
     if (!first) {
@@ -1550,11 +1632,11 @@ __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const
     // prob to be within 2^-17
     const uint64_t off = slack + err / 2 + 1;
     bool done = c->token >= 0;
-    if (done && !last_tier)
+    if (done && tier != kTier3)
         done = slack <= (c->mass >> 17) && (first || (c->lo_side + off <= c->left && c->left + off < c->hi_side)) &&
                candidate(c->z, (uint32_t)c->token) <= sure;
     if (t == 0 && done) write_token(a, c, o, c->token, c->z, c->mass);
-    return done ? kDone : last_tier ? kRadix : kTier2;
+    return done ? (int)kDone : tier == kTier3 ? (int)kRadix : tier + 1;
 }
 
 // The other slices' lists behind the first CTA's own (`count` of them may
@@ -1754,19 +1836,22 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
     WeightScale ws = c0->ws;
     ws.tab = s.tab;  // (this CTA's)
     if constexpr (SAMPLE) {
-        while (verdict == kTier1 || verdict == kTier2) {
+        while (verdict >= kTier1 && verdict <= kTier3) {
             const float z_lo = c0->z_lo, z_hi = c0->z_hi, per_bin = (float)kFine / (z_hi - z_lo);
             const bool bins = c->top_p < 1.f && !c0->by_min;
             if (t == 0) c->count = 0;
             __syncthreads();
+            float* fine = reinterpret_cast<float*>(s.fine);
             if (verdict == kTier1)
-                bracket_pass<DT, false>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf);
+                bracket_pass<DT, 1>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf, fine);
+            else if (verdict == kTier2)
+                bracket_pass<DT, 2>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf, fine);
             else
-                bracket_pass<DT, true>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf);
+                bracket_pass<DT, 3>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf, fine);
             if (bins) bin_tokens(s, z_hi, per_bin, ws);
             cl.sync();
             if (cl.rank == 0) {
-                const int next = find_end(cl, s, nb, verdict == kTier2);
+                const int next = find_end(cl, s, nb, verdict);
                 if (t == 0) c->verdict = next;
             }
             cl.sync();
@@ -1775,7 +1860,7 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
                 cl.sync();
                 if (cl.rank == 0) {
                     join_masses(cl, s, nb, w.per);
-                    const int next = end_row<DT>(a, s, row, V, nb, o, verdict == kTier2);
+                    const int next = end_row<DT>(a, s, row, V, nb, o, verdict);
                     __syncthreads();
                     if (t == 0) c->verdict = next;
                 }
