@@ -255,6 +255,65 @@ def test_sample_is_the_same_on_every_launch_and_in_a_graph(dlm):
         assert torch.equal(out.token, first.token) and torch.equal(out.prob, first.prob)
 
 
+@pytest.mark.parametrize("f", [dict(), dict(top_p=0.95), dict(top_p=0.9, temperature=0.7), dict(min_p=1e-3)], ids=str)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_sample_next_to_a_border(dlm, kind, f):
+    # u chosen so that u * mass lies 1e-10 .. 1e-8 of the mass from a border of
+    # the running sum, on both sides: 32-bit sums (1e-7) can not tell, the
+    # integer weights (1e-11) can
+    n = 24
+    z = ref.rows(n, 20011, kind, seed=91, sigma=1.0, boosted=0.0)
+    u, g = np.zeros(n, np.float32), np.random.default_rng(5)
+    for r, row in enumerate(ref.host(z)):
+        at, w = ref.kept(row, f.get("temperature", 1.0), 0, f.get("top_p", 1.0), f.get("min_p", 0.0))
+        borders = np.cumsum(w)[:-1] / w.sum()
+        near = borders.astype(np.float32)
+        off = near.astype(np.float64) - borders
+        ok = (np.abs(off) > 1e-10) & (np.abs(off) < 1e-8) & ((off > 0) == (r % 2 == 0))
+        u[r] = g.choice(near[ok])
+    check_sample(dlm, z, u.astype(np.float64), **f)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+def test_sample_rows_listed_twice(dlm, gather):
+    # enough rows for one CTA each, so that the open ones go to the second launch
+    n, vocab = 700, 20011
+    z = ref.rows(n, vocab, "bf16", seed=17, sigma=1.0, boosted=0.2)
+    g = np.random.default_rng(6)
+    index = g.integers(0, n, n).astype(np.int32)
+    u = g.random(n).astype(np.float32)
+    d = on_gpu(z)
+    r = dlm.row_sample(d, torch.from_numpy(u).cuda(), top_p=0.95, row_index=torch.from_numpy(index).cuda(), gather=gather)
+    zz = ref.host(z)
+    for i in g.choice(n, 120, replace=False):
+        o = i if gather else index[i]
+        assert int(r.token[o]) == ref.sample(zz[index[i]], float(u[o]), top_p=0.95)[0]
+
+
+def test_two_streams_at_once(dlm):
+    z = [on_gpu(ref.rows(400, 20011, "bf16", seed=s, boosted=0.3)) for s in (1, 2)]
+    u = torch.rand(400, device="cuda")
+    want = [dlm.row_sample(x, u, top_p=0.95).token.clone() for x in z]
+    streams = [torch.cuda.Stream() for _ in z]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for x, st in zip(z, streams):
+            with torch.cuda.stream(st):
+                got.append(dlm.row_sample(x, u, top_p=0.95).token)
+    torch.cuda.synchronize()
+    for i, t in enumerate(got):
+        assert torch.equal(t, want[i % 2])
+
+
+@pytest.mark.parametrize("kind,vocab", [("f32", 1048575), ("bf16", 1000001)])
+def test_largest_vocabularies(dlm, kind, vocab):
+    z = ref.rows(2, vocab, kind, seed=3)
+    check_topk(dlm, z, 300)
+    for f in (dict(), dict(top_p=0.9), dict(top_k=40, min_p=0.01)):
+        check_sample(dlm, z, np.array([0.31, 0.87]), **f)
+
+
 def test_refusals(dlm):
     z = on_gpu(ref.rows(4, 100, "f32", seed=1))
     u = torch.zeros(4, device="cuda")
