@@ -119,9 +119,10 @@ def lib():
         E, U = ctypes.c_int, ctypes.c_uint32
         L.dlm_row_topk.argtypes = [P, E, I64, I64, I64, P, I64, I32, F, P, P, P, P, U, P]
         L.dlm_row_sample.argtypes = [P, E, I64, I64, I64, P, I64, P, ctypes.POINTER(SampleParams), P, P, P, P, P, U, P]
-        L.dlm_distill_loss.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, F, P, P, P, P, P]
-        L.dlm_distill_grad.argtypes = [P, E, I64, I64, I64, P, P, E, I32, F, P, P, P, P, I64, P, P]
-        L.dlm_distill_step.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, F, P, P, P, I64, P, P]
+        D = ctypes.c_double
+        L.dlm_distill_loss.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, D, P, P, P, P, P]
+        L.dlm_distill_grad.argtypes = [P, E, I64, I64, I64, P, P, E, I32, D, P, P, P, P, I64, P, P]
+        L.dlm_distill_step.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, D, P, P, P, I64, P, P]
         for f in ("dlm_row_topk", "dlm_row_sample", "dlm_distill_loss", "dlm_distill_grad", "dlm_distill_step",
                   "dlm_row_stats", "dlm_select_threshold", "dlm_depcap_boundary", "dlm_cap_select",
                   "dlm_dapd_graph_mis", "dlm_dapd_graph", "dlm_dapd_select", "dlm_select_topk",

@@ -692,11 +692,11 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
 // Checks shared by the distillation calls.
 static dlm_status distill_prepare(dlm::DistillArgs& a, const void* student, dlm_dtype dtype, int64_t n_rows,
                                   int64_t vocab, int64_t row_stride, const int32_t* ids, const void* teacher,
-                                  dlm_dtype teacher_dtype, int32_t k, float temperature, const float* weights,
+                                  dlm_dtype teacher_dtype, int32_t k, double temperature, const float* weights,
                                   uint32_t* dev_status) {
     if (!dtype_ok(dtype) || !dtype_ok(teacher_dtype)) return DLM_ERR_UNSUPPORTED;
     if (n_rows < 0 || vocab < 1 || vocab > DLM_MAX_SEARCH_VOCAB || row_stride < vocab || k < 1 || k > DLM_MAX_TOPK ||
-        !temperature_ok(temperature))
+        !temperature_ok((float)temperature))
         return DLM_ERR_INVALID_ARG;
     if (n_rows == 0) return DLM_OK;
     if (!student || !ids || !teacher) return DLM_ERR_INVALID_ARG;
@@ -710,11 +710,14 @@ static dlm_status distill_prepare(dlm::DistillArgs& a, const void* student, dlm_
     a.teacher = teacher;
     a.teacher_dtype = teacher_dtype;
     a.k = k;
-    a.temperature = temperature;
     a.weights = weights;
     a.dev_status = dev_status;
-    a.inv_t = 1.0 / (double)temperature;
-    a.scale = (float)(1.4426950408889634 * a.inv_t);
+    a.inv_t = 1.0 / temperature;
+    // rounded down, so that the rest is positive: -inf times both is -inf
+    const double scale = 1.4426950408889634 * a.inv_t;
+    a.scale = (float)scale;
+    if ((double)a.scale >= scale) a.scale = nextafterf(a.scale, 0.f);
+    a.scale_lo = (float)(scale - (double)a.scale);
     if (n_rows > 0x7fffffffLL / 8) return DLM_ERR_INVALID_ARG;  // up to 8 CTAs per row
     return DLM_OK;
 }
@@ -734,7 +737,7 @@ static dlm_status distill_grad_ok(const dlm::DistillArgs& a, dlm_dtype dtype, co
 
 dlm_status dlm_distill_loss(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                             const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
-                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            const float* teacher_lse, double temperature, const float* weights, float* loss,
                             float* state, uint32_t* dev_status, dlm_stream_t stream) {
     dlm::DistillArgs a{};
     const dlm_status st = distill_prepare(a, student, dtype, n_rows, vocab, row_stride, ids, teacher, teacher_dtype,
@@ -750,7 +753,7 @@ dlm_status dlm_distill_loss(const void* student, dlm_dtype dtype, int64_t n_rows
 
 dlm_status dlm_distill_grad(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                             const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
-                            float temperature, const float* weights, const float* state, const float* grad_loss,
+                            double temperature, const float* weights, const float* state, const float* grad_loss,
                             void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
     dlm::DistillArgs a{};
     dlm_status st = distill_prepare(a, student, dtype, n_rows, vocab, row_stride, ids, teacher, teacher_dtype, k,
@@ -769,7 +772,7 @@ dlm_status dlm_distill_grad(const void* student, dlm_dtype dtype, int64_t n_rows
 
 dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                             const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
-                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            const float* teacher_lse, double temperature, const float* weights, float* loss,
                             void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
     dlm::DistillArgs a{};
     dlm_status st = distill_prepare(a, student, dtype, n_rows, vocab, row_stride, ids, teacher, teacher_dtype, k,

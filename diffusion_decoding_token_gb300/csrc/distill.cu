@@ -53,12 +53,11 @@ constexpr float kUnit = 5.684341886080802e-14f;  // 2^-44
 struct Sums {
     float mx, ref, all, rest;
 };
-// What a warp or a CTA knows of a row: its sums and its share of the loss,
-// part = sum w_j (t_j - s_j) / T and w = sum w_j over its listed entries (the
-// teacher's weights before they are normalised).
+// What a warp or a CTA knows of a row: its sums, and whether an id of its slice
+// may be listed twice.
 struct Share {
     Sums q;
-    float part, w;
+    int twice;
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -76,19 +75,19 @@ __device__ __forceinline__ Share warp_share(Share a, float c) {
     a.q.all = warp_sum(a.q.all * up);
     a.q.rest = warp_sum(a.q.rest * up);
     a.q.ref = ref;
-    a.part = warp_sum(a.part);
-    a.w = warp_sum(a.w);
+    a.twice = __any_sync(DLM_FULL_MASK, a.twice);
     return a;
 }
 
-__device__ __forceinline__ Share no_share() { return Share{Sums{-INFINITY, -FLT_MAX, 0.f, 0.f}, 0.f, 0.f}; }
+__device__ __forceinline__ Share no_share() { return Share{Sums{-INFINITY, -FLT_MAX, 0.f, 0.f}, 0}; }
 
 struct Shared {
     Share part[8 * kWarps];   // every warp's of every CTA of the cluster
     float list_max[kWarps];
     uint64_t list_sum[kWarps];
     int flags[kWarps];        // kAny, kBad
-    int twice[kWarps];        // an id may be listed twice
+    float sum[kWarps];
+    uint64_t listed[kWarps];
 };
 enum : int { kAny = 1, kBad = 2 };  // an entry; a teacher logit is NaN or +inf
 
@@ -97,7 +96,7 @@ struct List {
     int32_t* id;     // -1: no entry
     float* t;        // teacher logit
     float* p;        // teacher weight, not normalised
-    float* s;        // student logit (entries of this CTA's slice)
+    float* s;        // student logit (entries of this CTA's slice; the first CTA has all of them)
     uint32_t* own;   // row kernel: this entry took its token out of the slice
     uint32_t* bits;  // stream kernel: the listed tokens of this CTA's slice
 };
@@ -177,7 +176,7 @@ __device__ __forceinline__ float list_max(const Shared& sh) {
 }
 __device__ __forceinline__ void list_weigh(const DistillArgs& a, const List& l, Shared& sh, bool rest, float lse_t) {
     const float mx = list_max(sh);
-    const WeightScale ws = weight_scale(mx > -INFINITY ? mx : 0.f, a.temperature);
+    const WeightScale ws{mx > -INFINITY ? mx : 0.f, a.scale, a.scale_lo, kPow2Neg};
     uint64_t sum = 0;
     for (int j = threadIdx.x; j < a.k; j += kThreads) {
         float p = 0.f;
@@ -191,8 +190,9 @@ __device__ __forceinline__ void list_weigh(const DistillArgs& a, const List& l, 
             } else {
                 y = weight_exponent(l.t[j], ws, lo);
             }
-            sum += weight44_of(y, lo);
-            p = y < INFINITY ? exp2f(-y) * fmaf(lo, -kLn2, 1.0f) : 0.f;
+            const uint64_t w = weight44_of(y, lo);
+            sum += w;
+            p = y < 16.f ? (float)w * kUnit : y < INFINITY ? exp2f(-y) * fmaf(lo, -kLn2, 1.0f) : 0.f;
         }
         l.p[j] = p;
     }
@@ -223,29 +223,105 @@ __device__ __forceinline__ Teacher list_total(const Shared& sh, bool rest) {
     return t;
 }
 
-// The listed tokens of a slice [e0, e1) in its bitmap (zeroed before).
-__device__ __forceinline__ void mark_listed(const List& l, int K, int64_t e0, int64_t e1) {
+// The listed tokens of a slice [e0, e1) in its bitmap (zeroed before); whether
+// this thread met one that was marked already.
+__device__ __forceinline__ int mark_listed(const List& l, int K, int64_t e0, int64_t e1) {
+    int twice = 0;
     for (int j = threadIdx.x; j < K; j += kThreads) {
         const int64_t id = l.id[j];
-        if (id >= e0 && id < e1) atomicOr(&l.bits[(id - e0) >> 5], 1u << ((id - e0) & 31));
+        if (id < e0 || id >= e1) continue;
+        const uint32_t bit = 1u << ((id - e0) & 31);
+        twice |= (atomicOr(&l.bits[(id - e0) >> 5], bit) & bit) != 0;
     }
+    return twice;
 }
 
-// The row's loss (one thread): q relative to the row's maximum, the share of
-// the loss over the whole list, and the list's maximum.
-__device__ float row_loss(const DistillArgs& a, const Teacher& tch, float weight, const Share& row, bool rest,
-                          float lse_t, float list_mx) {
-    const Sums& q = row.q;
-    // ln p_j = t_j / T - log_z, ln q_j = s_j / T - lse_s
+// p (x - 1 + e^-x) for x = ln p - ln q, q = p e^-x.
+__device__ __forceinline__ float class_term(float p, float x, float q) {
+    if (!(p > 0.f)) return q;
+    if (!(fabsf(x) < 1.f)) return p * (x - 1.f) + q;
+    // x^2 (1/2! - x/3! + x^2/4! - ...)
+    float r = 1.f / 39916800;
+    r = fmaf(-x, r, 1.f / 3628800);
+    r = fmaf(-x, r, 1.f / 362880);
+    r = fmaf(-x, r, 1.f / 40320);
+    r = fmaf(-x, r, 1.f / 5040);
+    r = fmaf(-x, r, 1.f / 720);
+    r = fmaf(-x, r, 1.f / 120);
+    r = fmaf(-x, r, 1.f / 24);
+    r = fmaf(-x, r, 1.f / 6);
+    r = fmaf(-x, r, 0.5f);
+    return p * (x * x * r);
+}
+
+// The row's loss, by the first CTA, which has all of the list's student logits;
+// q relative to the row's maximum.  sum p x over the classes, x = ln p - ln q,
+// loses its digits when student and teacher are near (every x is small, of
+// either sign, and off by the log-sum-exps' rounding): with q = p e^-x it is
+// sum p (x - 1 + e^-x) + sum p - sum q, whose terms are positive and of second
+// order in x, and sum p - sum q is known exactly: 0 with the rest as a class,
+// q_rest without.  For that the listed part of q's sum is added up once more,
+// from integer weights.  (A list with repeats counts its q twice; it takes the
+// plain sum, in 64 bits.)  A list of up to kAlone entries is one warp's work:
+// `threads` is 32 then, and only warp 0 calls.  Thread 0 has the result.
+constexpr int kAlone = 128;
+
+__device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const Teacher& tch, const Share& row,
+                          bool rest, float lse_t, int threads) {
+    Sums q = row.q;
+    const int t = threadIdx.x;
+    const WeightScale ws{q.mx, a.scale, a.scale_lo, kPow2Neg};
+    if (!row.twice) {
+        uint64_t listed = 0;
+        for (int j = t; j < a.k; j += threads)
+            if (l.id[j] >= 0) listed += weight44(l.s[j], ws);
+        listed = (uint64_t)warp_sum_ll((long long)listed);
+        if (threads > 32) {
+            if ((t & 31) == 0) sh.listed[t >> 5] = listed;
+            __syncthreads();
+            listed = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) listed += sh.listed[w];
+        }
+        q.all = (float)listed * kUnit + q.rest;
+    }
     const double lse_s = (double)q.mx * a.inv_t + log_exact(q.all);
     const double log_z = rest ? (double)lse_t
-                              : (double)list_mx * a.inv_t + log_exact(fmaxf((float)tch.sum * kUnit, 1.f));
-    double v = (double)tch.inv * ((double)row.part + (double)row.w * (lse_s - log_z));
-    if (tch.p_rest > 0.f) {
-        // ln p_rest - ln q_rest = ln(all / rest) - ln(1 / p_rest)
-        v += q.rest > 0.f ? (double)tch.p_rest * (log_exact(q.all / q.rest) - log_exact(1.f / tch.p_rest)) : INFINITY;
+                              : (double)list_max(sh) * a.inv_t + log_exact(fmaxf((float)tch.sum * kUnit, 1.f));
+    const double shift = lse_s - log_z;
+    // ln p_rest - ln q_rest = ln(all / rest) - ln(1 / p_rest)
+    const float q_rest = q.rest / q.all;
+    double x_rest = 0;
+    if (tch.p_rest > 0.f)
+        x_rest = q.rest > 0.f ? log_exact(q.all / q.rest) - log_exact(1.f / tch.p_rest) : (double)INFINITY;
+    if (row.twice) {
+        double v = 0;
+        if (t == 0) {
+            for (int j = 0; j < a.k; ++j)
+                if (l.id[j] >= 0 && l.p[j] > 0.f)
+                    v += (double)(l.p[j] * tch.inv) * (((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift);
+            if (tch.p_rest > 0.f) v += (double)tch.p_rest * x_rest;
+        }
+        return (float)v;
     }
-    return (float)((double)weight * v);
+    float v = 0.f;
+    const float inv_q = 1.f / q.all;
+    for (int j = t; j < a.k; j += threads) {
+        if (l.id[j] < 0) continue;
+        const float x = (float)(((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift);
+        v += class_term(l.p[j] * tch.inv, x, inv_q * exp2f((l.s[j] - q.mx) * a.scale));
+    }
+    v = warp_sum(v);
+    if (threads > 32) {
+        if ((t & 31) == 0) sh.sum[t >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v += sh.sum[w];
+    }
+    if (!rest) return v + q_rest;
+    const uint64_t one = 1ull << kWeightBits;
+    return v + class_term(tch.p_rest, (float)x_rest, q_rest) + (tch.sum > one ? (float)(tch.sum - one) * kUnit : 0.f);
 }
 
 __device__ __forceinline__ void write_state(float* state, float m, float inv, float tail, float lse_t, bool rest) {
@@ -268,25 +344,36 @@ __device__ __forceinline__ bool row_factors(const Teacher& tch, const Sums& q, b
     return fine;
 }
 
-// The loss and the state of a row (one thread).
-__device__ void finish_loss(const DistillArgs& a, const Shared& sh, const Teacher& tch, int64_t r, float weight,
-                            const Share& row, bool rest, float lse_t, bool fine, float inv, float tail) {
+// The loss and the state of a row (the first CTA).
+__device__ __forceinline__ void finish_loss(const DistillArgs& a, const List& l, Shared& sh, const Teacher& tch, int64_t r,
+                                            float weight, const Share& row, bool rest, float lse_t, bool fine, float inv,
+                                            float tail) {
+    const bool alone = a.k <= kAlone;
+    if (alone && threadIdx.x >= 32) return;
     float v = NAN;
-    if (fine) v = rest || tch.any ? row_loss(a, tch, weight, row, rest, lse_t, list_max(sh)) : 0.f;
+    if (fine) v = rest || tch.any ? weight * row_loss(a, l, sh, tch, row, rest, lse_t, alone ? 32 : kThreads) : 0.f;
+    if (threadIdx.x != 0) return;
     a.loss[r] = v;
     if (!fine) raise_status(a.dev_status, DLM_DEV_NONFINITE);
     write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, row.q.mx, inv, tail, lse_t, rest);
 }
 
+// 2^((z - ref) c) with c in two floats (one float's rounding, the same for every
+// token, would show in the loss's seventh digit).
+__device__ __forceinline__ f2 weights_of(f2 z, f2 ref, f2 c, f2 c_lo) {
+    const f2 d = sub2(z, ref);
+    return ex2x2(fma2(d, c, mul2(d, c_lo)));  // the large product inside the fma: one rounding of it less
+}
+
 // Sums of vectors [v0, v1) of a row (kThreads threads; the whole CTA calls).
-template <int DT, bool REST>
-__device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c, const uint32_t* bits) {
+template <int DT>
+__device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c, float c_lo, const uint32_t* bits) {
     constexpr int EPV = Row<DT>::EPV;
     Sums a;
     a.mx = -INFINITY;
     a.ref = -FLT_MAX;
     f2 all = pack2(0.f, 0.f), rest = pack2(0.f, 0.f);
-    const f2 c2 = pack2(c, c);
+    const f2 c2 = pack2(c, c), lo2 = pack2(c_lo, c_lo);
     const int whole = (int)min((int64_t)v1, V / EPV);
     auto add = [&](uint4 w, int v) {
         const float m = Row<DT>::vmax(w);
@@ -302,8 +389,8 @@ __device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c,
         const f2 r2 = pack2(a.ref, a.ref);
         f2 e[EPV / 2];
 #pragma unroll
-        for (int p = 0; p < EPV / 2; ++p) e[p] = ex2x2(mul2(sub2(pack2(z[2 * p], z[2 * p + 1]), r2), c2));
-        if (REST) {
+        for (int p = 0; p < EPV / 2; ++p) e[p] = weights_of(pack2(z[2 * p], z[2 * p + 1]), r2, c2, lo2);
+        {
             const int at = (v - v0) * EPV;  // first token of the vector, from the slice's start
             const uint32_t in = (bits[at >> 5] >> (at & 31)) & ((1u << EPV) - 1u);
             if (in) {
@@ -348,7 +435,6 @@ __device__ __forceinline__ Share merge_row(const Cluster& cl, Shared& sh, Share 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     a = warp_share(a, c);
     if (cl.split > 1) {
-        cg::this_cluster().barrier_wait();
         if (lane < cl.split) *cl.at(&sh.part[cl.rank * kWarps + warp], lane) = a;
         cl.sync();
     } else {
@@ -364,8 +450,7 @@ __device__ __forceinline__ Share merge_row(const Cluster& cl, Shared& sh, Share 
         a.q.rest = a.q.rest * ea + b.q.rest * eb;
         a.q.ref = ref;
         a.q.mx = max_nan(a.q.mx, b.q.mx);
-        a.part += b.part;
-        a.w += b.w;
+        a.twice |= b.twice;
     }
     a = warp_share(a, c);
     const float up = ex2((a.q.ref - a.q.mx) * c);
@@ -373,9 +458,13 @@ __device__ __forceinline__ Share merge_row(const Cluster& cl, Shared& sh, Share 
     a.q.rest *= up;
     return a;
 }
-// The cluster's CTAs run (before merge_row; every thread).
+// The cluster's CTAs run: every thread says so first and, before it stores into
+// another CTA, waits for the others.
 __device__ __forceinline__ void started(const Cluster& cl) {
     if (cl.split > 1) cg::this_cluster().barrier_arrive();
+}
+__device__ __forceinline__ void all_started(const Cluster& cl) {
+    if (cl.split > 1) cg::this_cluster().barrier_wait();
 }
 
 // One float to storage.
@@ -519,11 +608,11 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
         return;
     }
     started(cl);
-    if (REST)
-        for (int i = t; i < (int)((sl.e1 - sl.e0 + 31) / 32); i += kThreads) l.bits[i] = 0;
+    for (int i = t; i < (int)((sl.e1 - sl.e0 + 31) / 32); i += kThreads) l.bits[i] = 0;
     list_load(a, l, sh, r, lse_t, id0, x0);
     __syncthreads();
-    if (REST) mark_listed(l, K, sl.e0, sl.e1);
+    Share mine_all;
+    mine_all.twice = mark_listed(l, K, sl.e0, sl.e1);
     // the listed logits are asked for now and used after the stream
     constexpr int kMine = (DLM_MAX_TOPK + kThreads - 1) / kThreads;
     float mine[kMine];
@@ -533,28 +622,23 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
         mine[i] = id >= sl.e0 && id < sl.e1 ? Row<DT>::scalar(row, id) : 0.f;
     }
     list_weigh(a, l, sh, REST, lse_t);
-    if (REST) __syncthreads();
-    Share mine_all;
-    mine_all.q = stream_sums<DT, REST>(row, V, sl.v0, sl.v1, c, l.bits);
-    mine_all.part = mine_all.w = 0.f;
+    __syncthreads();
+    mine_all.q = stream_sums<DT>(row, V, sl.v0, sl.v1, c, a.scale_lo, l.bits);
+    all_started(cl);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
         const int j = t + i * kThreads, id = j < K ? l.id[j] : -1;
         if (id < sl.e0 || id >= sl.e1) continue;
         l.s[j] = mine[i];
-        const float p = l.p[j];
-        if (p > 0.f) {
-            mine_all.part += p * (float)(((double)l.t[j] - (double)mine[i]) * a.inv_t);
-            mine_all.w += p;
-        }
+        if (cl.rank != 0) cl.at(l.s, 0)[j] = mine[i];
     }
     const Share all = merge_row(cl, sh, mine_all, c);
     const Teacher tch = list_total(sh, REST);
     float inv, tail;
     const bool fine = row_factors(tch, all.q, REST, inv, tail);
-    if (cl.rank == 0 && t == 0) finish_loss(a, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
+    if (cl.rank == 0) finish_loss(a, l, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
     if (GRAD) {
-        const float g = weight / a.temperature;
+        const float g = weight * (float)a.inv_t;
         stream_grad<DT>(row, out, V, sl.v0, sl.v1, all.q.mx, c, g * inv * tail);
         __syncthreads();
         if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, all.q.mx, c, inv, tch.inv, true, g);
@@ -575,7 +659,7 @@ __global__ void __launch_bounds__(kThreads) distill_stream_grad_kernel(const Dis
     const char* row = static_cast<const char*>(a.student) + r * a.row_stride * Row<DT>::ESZ;
     char* out = static_cast<char*>(a.grad) + r * a.grad_stride * Row<DT>::ESZ;
     const Slice<DT> sl(V, cl);
-    const float g = (a.weights ? a.weights[r] : 1.f) * (a.grad_loss ? a.grad_loss[r] : 1.f) / a.temperature;
+    const float g = (a.weights ? a.weights[r] : 1.f) * (a.grad_loss ? a.grad_loss[r] : 1.f) * (float)a.inv_t;
     const float c = a.scale;
     const float* state = a.state + r * DLM_DISTILL_STATE;
     const float m = state[0], inv = state[1], tail = state[2];
@@ -644,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     const int id0 = t < K ? a.ids[r * K + t] : -1;
     const float x0 = t < K ? teacher_at(a, r * K + t) : 0.f;
     const float weight = a.weights ? a.weights[r] : 1.f;
-    float g = weight / a.temperature, m = 0.f, inv = 0.f, tail = 0.f, lse_t = 0.f;
+    float g = weight * (float)a.inv_t, m = 0.f, inv = 0.f, tail = 0.f, lse_t = 0.f;
     bool rest = REST;
     if (SUMS) {
         if (REST) lse_t = a.teacher_lse[r];
@@ -672,6 +756,9 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     list_weigh(a, l, sh, rest, lse_t);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
+    Share row_share = no_share();
+    row_share.twice = 1;
+    bool ok = true;
     if (SUMS) {
         // the listed tokens leave the slice; one entry of each has its logit
         bool twice = false;
@@ -686,22 +773,20 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             twice |= !took;
             if (took) top = max_nan(top, s);
         }
-        twice = __any_sync(DLM_FULL_MASK, twice);
-        if ((t & 31) == 0) sh.twice[t >> 5] = twice;
         __syncthreads();
         for (int v = t; v < n; v += kThreads) top = max_nan(top, Row<DT>::vmax(data[v]));
         const float ref = top > -INFINITY ? top : 0.f;  // nothing but -inf: weights of 0
         Share mine = no_share();
         mine.q.mx = top;
         mine.q.ref = top > -INFINITY ? top : -FLT_MAX;
-        const f2 r2 = pack2(ref, ref), c2 = pack2(c, c);
+        const f2 r2 = pack2(ref, ref), c2 = pack2(c, c), lo2 = pack2(a.scale_lo, a.scale_lo);
         f2 others = pack2(0.f, 0.f);
         for (int v = t; v < n; v += kThreads) {
             float z[EPV];
             Row<DT>::unpack(data[v], z);
             f2 e[EPV / 2];
 #pragma unroll
-            for (int p = 0; p < EPV / 2; ++p) e[p] = ex2x2(mul2(sub2(pack2(z[2 * p], z[2 * p + 1]), r2), c2));
+            for (int p = 0; p < EPV / 2; ++p) e[p] = weights_of(pack2(z[2 * p], z[2 * p + 1]), r2, c2, lo2);
 #pragma unroll
             for (int h = EPV / 4; h; h >>= 1)
 #pragma unroll
@@ -709,8 +794,9 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             others = add2(others, e[0]);
         }
         mine.q.rest = hsum2(others);
-        // this slice's share of the loss
+        // the listed tokens' weights; their logits to the first CTA
         float own = 0.f;
+        all_started(cl);
         for (int j = t; j < K; j += kThreads) {
             const int id = l.id[j];
             if (id < sl.e0 || id >= sl.e1) continue;
@@ -721,18 +807,16 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
                 for (int i = 0; i < K; ++i)
                     if (l.id[i] == id && l.own[i]) s = l.s[i];
             }
-            const float p = l.p[j];
-            if (p > 0.f) {
-                mine.part += p * (float)(((double)l.t[j] - (double)s) * a.inv_t);
-                mine.w += p;
-            }
+            if (cl.rank != 0 || !l.own[j]) cl.at(l.s, 0)[j] = s;
         }
         mine.q.all = own + mine.q.rest;
+        mine.twice = twice;
         const Share all = merge_row(cl, sh, mine, c);
         const Teacher tch = list_total(sh, REST);
         const bool fine = row_factors(tch, all.q, REST, inv, tail);
         m = all.q.mx;
-        if (cl.rank == 0 && t == 0) finish_loss(a, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
+        row_share = all;
+        ok = fine;
     } else {
         for (int j = t; j < K; j += kThreads) {
             const int id = l.id[j];
@@ -751,13 +835,9 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             store_elem<DT>(out, i, scale * ex2((Row<DT>::scalar(data, i - sl.e0) - m) * c));
     }
     __syncthreads();
-    if (inv != 0.f) {
-        int twice = !SUMS;
-        if (SUMS)
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) twice |= sh.twice[w];
-        write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, twice, g);
-    }
+    if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, row_share.twice, g);
+    // (last: the gradient does not wait for it)
+    if (SUMS && cl.rank == 0) finish_loss(a, l, sh, tch, r, weight, row_share, REST, lse_t, ok, inv, tail);
 }
 
 // Shared memory of a CTA that streams: the list, and with `bits` the bitmap of
@@ -795,7 +875,7 @@ cudaError_t launch_rows(F kernel, const DistillArgs& a, size_t smem, cudaStream_
 
 template <int DT, bool REST>
 cudaError_t launch_loss(const DistillArgs& a, cudaStream_t st) {
-    const size_t smem = stream_bytes(a.vocab, a.k, a.split, REST);
+    const size_t smem = stream_bytes(a.vocab, a.k, a.split, true);
     if (!a.grad) return launch_rows(distill_stream_kernel<DT, REST, false>, a, smem, st);
     if (a.slice_vecs == 0) return launch_rows(distill_stream_kernel<DT, REST, true>, a, smem, st);
     return launch_rows(distill_row_kernel<DT, REST, true>, a, slice_offset(a.k) + (size_t)a.slice_vecs * 16, st);

@@ -251,14 +251,13 @@ struct DistillArgs {
     int64_t n_rows, vocab, row_stride;
     int split;                // CTAs per row (thread-block cluster size)
     int slice_vecs;           // 16-byte vectors of a row per CTA; 0: the row is streamed
-    float scale;              // log2(e) / temperature
+    float scale, scale_lo;    // log2(e) / temperature in two floats
     double inv_t;             // 1 / temperature
     const int32_t* ids;       // [n_rows][k]
     const void* teacher;      // [n_rows][k]
     int teacher_dtype;
     int k;
     const float* teacher_lse; // [n_rows], nullable: renormalised over the list
-    float temperature;
     const float* weights;     // [n_rows], nullable: 1
     const float* grad_loss;   // [n_rows], nullable: 1 (gradient call)
     float* loss;

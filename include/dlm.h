@@ -797,17 +797,17 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
 
 dlm_status dlm_distill_loss(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                             const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
-                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            const float* teacher_lse, double temperature, const float* weights, float* loss,
                             float* state, uint32_t* dev_status, dlm_stream_t stream);
 
 dlm_status dlm_distill_grad(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                             const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
-                            float temperature, const float* weights, const float* state, const float* grad_loss,
+                            double temperature, const float* weights, const float* state, const float* grad_loss,
                             void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
 
 dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                             const int32_t* ids, const void* teacher, dlm_dtype teacher_dtype, int32_t k,
-                            const float* teacher_lse, float temperature, const float* weights, float* loss,
+                            const float* teacher_lse, double temperature, const float* weights, float* loss,
                             void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
 
 #ifdef __cplusplus

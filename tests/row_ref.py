@@ -71,7 +71,7 @@ def distill(row, ids, teacher, weight=1.0, temperature=1.0, teacher_lse=None):
     """(loss, gradient, per-token error scale of the gradient): the scale is
     what a relative error of 1 in q (more for far tokens, see below), p and
     the factor of the unlisted tokens together would change, for tolerances."""
-    t = float(np.float32(temperature))
+    t = float(temperature)
     held = (ids >= 0) & (ids < len(row))
     ids, a = ids[held], teacher[held] / t
     y = row / t

@@ -61,10 +61,10 @@ def distill(L, call="loss", student=X, dtype=1, n=4, vocab=100, stride=104, ids=
             loss=X, state=X, grad=Y, gstride=104):
     head = (student, dtype, n, vocab, stride, ids, teacher, tdtype, k)
     if call == "loss":
-        return L.dlm_distill_loss(*head, None, F(t), None, loss, state, None, None)
+        return L.dlm_distill_loss(*head, None, ctypes.c_double(t), None, loss, state, None, None)
     if call == "grad":
-        return L.dlm_distill_grad(*head, F(t), None, state, None, grad, gstride, None, None)
-    return L.dlm_distill_step(*head, None, F(t), None, loss, grad, gstride, None, None)
+        return L.dlm_distill_grad(*head, ctypes.c_double(t), None, state, None, grad, gstride, None, None)
+    return L.dlm_distill_step(*head, None, ctypes.c_double(t), None, loss, grad, gstride, None, None)
 
 
 @pytest.mark.parametrize("call", ["loss", "grad", "step"])
