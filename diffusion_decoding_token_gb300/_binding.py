@@ -222,11 +222,12 @@ def row_stats(cur: torch.Tensor, prev: torch.Tensor | None = None, *, row_index:
 
 def _on(device, call, *args) -> None:
     """Run a C call on the current stream of the tensors' device."""
-    if device.index == torch.cuda.current_device():
-        status = call(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = call(*args, torch._C._cuda_getCurrentRawStream(device.index))
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != 0:
         _check(status)
 
@@ -238,7 +239,8 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 def _rows_arg(t: torch.Tensor, name: str) -> None:
     if not t.is_cuda:
         raise ValueError("libdlm takes CUDA tensors only")
-    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1 and t.shape[1] > 1:
         raise ValueError(f"{name} must be [rows, V] with contiguous rows")
 
 
@@ -367,8 +369,7 @@ def _distill_args(student, ids, teacher, weights, teacher_lse=None):
 def _grad_out(student, out):
     if out is None:
         # rows at the student's stride, which is a multiple of 16 bytes
-        rows, V = student.shape
-        return torch.empty((rows, _stride(student)), dtype=student.dtype, device=student.device)[:, :V]
+        return torch.empty_strided(student.shape, (_stride(student), 1), dtype=student.dtype, device=student.device)
     _rows_arg(out, "the gradient")
     if out.shape != student.shape or out.dtype != student.dtype or out.device != student.device:
         raise ValueError("the gradient must match the student in shape, dtype and device")

@@ -636,7 +636,7 @@ static dlm_status row_search_prepare(dlm::RowSearchArgs& a, const void* logits, 
     return DLM_OK;
 }
 
-static bool temperature_ok(float t) { return t >= DLM_MIN_TEMPERATURE && isfinite(t); }
+static bool temperature_ok(float t) { return t >= DLM_MIN_TEMPERATURE && t <= DLM_MAX_TEMPERATURE; }
 
 dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                         const int32_t* row_index, int64_t n_src_rows, int32_t k, float temperature, float* values,
@@ -673,6 +673,11 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
                                              dev_status, flags);
     if (st != DLM_OK || n_rows == 0) return st;
     if (!uniform || !token || !prob) return DLM_ERR_INVALID_ARG;
+    // both launches read these, and the first one writes token and prob
+    for (const void* in : {(const void*)uniform, (const void*)lse, (const void*)params->temperature_rows,
+                           (const void*)params->top_k_rows, (const void*)params->top_p_rows,
+                           (const void*)params->min_p_rows})
+        if (in == token || in == prob) return DLM_ERR_INVALID_ARG;
     a.uniform = uniform;
     a.temperature = params->temperature;
     a.k = params->top_k;

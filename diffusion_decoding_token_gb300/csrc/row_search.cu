@@ -72,7 +72,6 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// What one row's CTA (the first of its cluster) and the others share.
 // weight44 as a call: where it is met once or rarely, fifty instructions inline
 // cost more to fetch than to run (a row that takes the long way runs most of its
 // code once, and waited for instructions more than for anything but barriers).
@@ -83,6 +82,7 @@ __device__ __noinline__ uint64_t weight_call(float z, const WeightScale ws) { re
 // radix search.
 enum Verdict : int { kRadix = 0, kDone = 1, kTier1 = 2, kTier2 = 3, kTier3 = 4, kList = 5, kMinP = 6 };
 
+// What one row's CTA (the first of its cluster) and the others share.
 struct Ctrl {
     WeightScale ws;
     float top_p, min_p, u;
@@ -351,7 +351,7 @@ __device__ int top_candidates(const Smem& s, int n, int k) {
 // Push the elements z >= least of one loaded vector of each lane (positions
 // from pos0 on) into the list dst of `cap` entries, its length in *count.
 template <int DT>
-__device__ __forceinline__ void push(uint4 w, uint32_t pos0, float least, float below, uint64_t* dst, uint32_t cap,
+__device__ __forceinline__ void push(uint4 w, uint32_t pos0, float least, uint64_t* dst, uint32_t cap,
                                      uint32_t* count) {
     constexpr int EPV = Row<DT>::EPV;
     const int lane = threadIdx.x & 31;
@@ -359,7 +359,7 @@ __device__ __forceinline__ void push(uint4 w, uint32_t pos0, float least, float 
     Row<DT>::unpack(w, z);
     uint32_t mine = 0;
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) mine |= (uint32_t)(z[e] >= least && z[e] < below && z[e] > -INFINITY) << e;
+    for (int e = 0; e < EPV; ++e) mine |= (uint32_t)(z[e] >= least && z[e] > -INFINITY) << e;
     if (!__any_sync(DLM_FULL_MASK, mine != 0)) return;
     const int n = __popc(mine);
     int inc = n;
@@ -464,7 +464,7 @@ __device__ __noinline__ void gather_slice(const char* row, int64_t V, int b0, in
         w0 = w1;
         w1 = w2;
         w2 = fetch(i + 3 * kWarps);
-        push<DT>(w, (uint32_t)((i * 32 + lane) * Row<DT>::EPV), least, INFINITY, dst, kCap, count);
+        push<DT>(w, (uint32_t)((i * 32 + lane) * Row<DT>::EPV), least, dst, kCap, count);
     }
 }
 
@@ -1786,7 +1786,7 @@ __device__ __forceinline__ void load_settings(const RowSearchArgs& a, int64_t o,
         if (a.top_p_rows) p = a.top_p_rows[o];
         if (a.min_p_rows) least = a.min_p_rows[o];
         const float u = a.uniform[o];
-        bad = !(T == 0.f || (T >= DLM_MIN_TEMPERATURE && T <= FLT_MAX)) || k < 0 || !(p > 0.f && p <= 1.f) ||
+        bad = !(T == 0.f || (T >= DLM_MIN_TEMPERATURE && T <= DLM_MAX_TEMPERATURE)) || k < 0 || !(p > 0.f && p <= 1.f) ||
               !(least >= 0.f && least <= 1.f) || !(u >= 0.f && u < 1.f);
         c->u = u;
         if (T == 0.f) k = 1, T = 1.f, p = 1.f, least = 0.f;  // the argmax
@@ -2069,6 +2069,9 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
             }
             if constexpr (SAMPLE) {
                 verdict = sample_leader<DT>(a, s, w.row, V, nb, o, whole, low);
+                // logits so far from 0 that tiers 1 and 2 can not tell "60 powers
+                // of 2 below the maximum" from the maximum itself
+                if (verdict == kTier1 && fabsf(m) * c->ws.c_hi > 60.f * 1048576.f) verdict = kRadix;
                 if (verdict == kTier1 && filtered) verdict = place_bracket<DT>(w.row, V, s);
                 if (verdict == kList) verdict = place_list<DT>(w.row, V, k, s);
             } else {

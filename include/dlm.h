@@ -679,7 +679,7 @@ dlm_status dlm_revocable_step(const int32_t* argmax, const float* conf, const fl
  * logits, dtype, n_rows, vocab, row_stride, row_index, n_src_rows : as in
  *               dlm_row_stats_ex; vocab <= DLM_MAX_SEARCH_VOCAB.
  * k           : 1 <= k <= DLM_MAX_TOPK (may exceed vocab).
- * temperature : >= DLM_MIN_TEMPERATURE, finite; enters lse only.
+ * temperature : DLM_MIN_TEMPERATURE .. DLM_MAX_TEMPERATURE; enters lse only.
  * values, ids : float / int32 [.][k] outputs; lse: nullable float output.
  *               Row r processed is stored at o = q, or at o = r with
  *               DLM_ROWS_GATHER (the only flag).
@@ -690,6 +690,7 @@ dlm_status dlm_revocable_step(const int32_t* argmax, const float* conf, const fl
 #define DLM_MAX_TOPK 1024
 #define DLM_MAX_SEARCH_VOCAB 1048575 /* 2^20 - 1: a row's mass in units of 2^-44 fits 64 bits */
 #define DLM_MIN_TEMPERATURE 1e-4f
+#define DLM_MAX_TEMPERATURE 1e30f    /* log2(e) / T stays a normal number in two floats */
 
 dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
                         const int32_t* row_index, int64_t n_src_rows, int32_t k, float temperature, float* values,
@@ -719,14 +720,16 @@ dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int
  *               lse and outputs at o = q, or o = r with DLM_ROWS_GATHER).
  * uniform     : float [.], 0 <= u < 1.
  * params      : the call's settings; a non-null *_rows array gives row o's own.
- *               temperature 0 or in [DLM_MIN_TEMPERATURE, FLT_MAX], top_k >= 0,
- *               0 < top_p <= 1, 0 <= min_p <= 1.  Scalars are checked on the
- *               host; a row whose own settings or u are out of range gets
- *               token -1, prob 0 and sets DLM_DEV_BAD_PARAM.
+ *               temperature 0 or DLM_MIN_TEMPERATURE .. DLM_MAX_TEMPERATURE,
+ *               top_k >= 0, 0 < top_p <= 1, 0 <= min_p <= 1.  Scalars are
+ *               checked on the host; a row whose own settings or u are out of
+ *               range gets token -1, prob 0 and sets DLM_DEV_BAD_PARAM.
  * lse         : nullable float [.] (dlm_row_stats' lse); with conf, conf[o] =
  *               exp(z_token - lse[o]): the token's unfiltered probability at
  *               temperature 1, which the selection rules take.  Both or none.
- * token, prob : int32 / float outputs.  A row that holds NaN or +inf, or -inf
+ * token, prob : int32 / float outputs, which hold notes between the call's two
+ *               launches: they are valid when its work has ended, and may not
+ *               overlap uniform, the settings or lse.  A row that holds NaN or +inf, or -inf
  *               only, gets token -1, prob 0 (conf 0) and sets DLM_DEV_NONFINITE.
  */
 typedef struct dlm_sample_params {
@@ -778,7 +781,7 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  * teacher     : [n_rows][k] logits of teacher_dtype (values of empty entries
  *               are not used); teacher_lse: nullable float [n_rows],
  *               ln sum_v exp(t_v / T) of the whole teacher row (dlm_row_topk).
- * temperature : T >= DLM_MIN_TEMPERATURE, finite.
+ * temperature : DLM_MIN_TEMPERATURE <= T <= DLM_MAX_TEMPERATURE.
  * weights     : nullable float [n_rows] (1).  A row of weight 0 is not read:
  *               loss 0, gradient 0.
  * loss        : float [n_rows] output.

@@ -306,6 +306,27 @@ def test_two_streams_at_once(dlm):
         assert torch.equal(t, want[i % 2])
 
 
+@pytest.mark.parametrize("n,vocab", [(6, 20012), (330, 20012), (330, 3000)])
+@pytest.mark.parametrize("f", [dict(top_p=0.9, temperature=1e-4), dict(top_p=0.3, temperature=1e-4), dict(temperature=1e-4), dict(min_p=1e-6, temperature=1e-4),
+                               dict(top_p=0.9, temperature=0.01), dict(top_p=0.5, temperature=1e30),
+                               dict(min_p=0.5, temperature=1e30), dict(temperature=1e30),
+                               dict(top_k=3000, temperature=1e-4)], ids=str)
+def test_sample_far_from_zero(dlm, n, vocab, f):
+    # logits whose place is far above the temperature: a step of the type is
+    # many powers of e, and thousands of tokens share the maximum
+    g = np.random.default_rng(11)
+    z = torch.zeros((n, vocab), dtype=torch.float32)
+    z[0::6] = 1e6 - torch.from_numpy((g.random((n // 6, vocab)) > 0.8).astype(np.float32))
+    z[1::6] = -1e30
+    z[1::6, ::3] = -0.999e30
+    z[2::6] = 1e5 + torch.from_numpy(g.integers(0, 64, (n // 6, vocab)).astype(np.float32)) / 128
+    z[3::6] = 1000 + torch.from_numpy(g.integers(0, 64, (n // 6, vocab)).astype(np.float32)) / 16384
+    z[4::6] = torch.from_numpy(g.normal(0, 1e-4, (n // 6, vocab)).astype(np.float32))
+    z[5::6] = 3e38
+    z[5::6, 1::2] = -3e38
+    check_sample(dlm, z, g.random(n), **f)
+
+
 @pytest.mark.parametrize("kind,vocab", [("f32", 1048575), ("bf16", 1000001)])
 def test_largest_vocabularies(dlm, kind, vocab):
     z = ref.rows(2, vocab, kind, seed=3)
@@ -323,7 +344,7 @@ def test_refusals(dlm):
         dlm.row_topk(z, dlm.MAX_TOPK + 1)
     with pytest.raises(dlm.DlmError):
         dlm.row_topk(z, 4, temperature=0.0)
-    for bad in (dict(temperature=-1.0), dict(temperature=float("nan")), dict(top_k=-1), dict(top_p=0.0),
+    for bad in (dict(temperature=-1.0), dict(temperature=2e30), dict(temperature=float("nan")), dict(top_k=-1), dict(top_p=0.0),
                 dict(top_p=1.5), dict(min_p=-0.1), dict(min_p=1.1)):
         with pytest.raises(dlm.DlmError):
             dlm.row_sample(z, u, **bad)

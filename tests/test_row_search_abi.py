@@ -19,6 +19,7 @@ def L():
 
 X = P(0x100000)
 Y = P(0x10000000)
+U = P(0x400000)
 
 
 def topk(L, logits=X, dtype=1, n=4, vocab=100, stride=104, index=None, n_src=0, k=8, t=1.0, values=X, ids=X, flags=0):
@@ -30,14 +31,14 @@ def test_topk(L):
     assert topk(L, dtype=5) == UNSUP
     for kw in (dict(logits=None), dict(n=-1), dict(vocab=0), dict(vocab=105), dict(vocab=1 << 20, stride=1 << 20),
                dict(n_src=-1), dict(n_src=3), dict(k=0), dict(k=1025), dict(t=0.0), dict(t=5e-5), dict(t=float("inf")),
-               dict(t=float("nan")), dict(t=-1.0), dict(values=None), dict(ids=None), dict(flags=1), dict(flags=4),
+               dict(t=float("nan")), dict(t=-1.0), dict(t=2e30), dict(values=None), dict(ids=None), dict(flags=1), dict(flags=4),
                dict(n=1 << 31)):
         assert topk(L, **kw) == INVALID, kw
     assert topk(L, logits=P(0x100008)) == ALIGN
     assert topk(L, stride=101) == ALIGN
 
 
-def sample(L, u=X, t=1.0, k=0, p=1.0, m=0.0, lse=None, conf=None, token=X, prob=X, n=4, rows=None, params=True, **kw):
+def sample(L, u=U, t=1.0, k=0, p=1.0, m=0.0, lse=None, conf=None, token=P(0x200000), prob=P(0x300000), n=4, rows=None, params=True, **kw):
     from diffusion_decoding_token_gb300._binding import SampleParams
     prm = SampleParams(t, k, p, m, *(rows or (None,) * 4))
     a = dict(dtype=1, vocab=100, stride=104, flags=0) | kw
@@ -48,9 +49,10 @@ def sample(L, u=X, t=1.0, k=0, p=1.0, m=0.0, lse=None, conf=None, token=X, prob=
 def test_sample(L):
     assert sample(L, n=0) == 0 and sample(L, n=0, t=0.0) == 0
     assert sample(L, dtype=3) == UNSUP
-    for kw in (dict(params=False), dict(u=None), dict(t=-0.1), dict(t=1e-5), dict(t=float("nan")), dict(k=-1),
+    for kw in (dict(params=False), dict(u=None), dict(t=-0.1), dict(t=1e-5), dict(t=2e30), dict(t=float("nan")), dict(k=-1),
                dict(p=0.0), dict(p=1.01), dict(p=float("nan")), dict(m=-0.1), dict(m=1.01), dict(lse=X), dict(conf=X),
-               dict(token=None), dict(prob=None), dict(vocab=200), dict(flags=2 | 8)):
+               dict(token=None), dict(prob=None), dict(vocab=200), dict(flags=2 | 8), dict(prob=U), dict(token=U),
+               dict(rows=(None, None, None, 0x200000)), dict(rows=(None, 0x300000, None, None))):
         assert sample(L, **kw) == INVALID, kw
     # a setting that comes per row is not checked here
     assert sample(L, n=0, t=-1.0, k=-1, p=7.0, m=7.0, rows=(0x1000,) * 4) == 0
@@ -71,7 +73,7 @@ def distill(L, call="loss", student=X, dtype=1, n=4, vocab=100, stride=104, ids=
 def test_distill(L, call):
     assert distill(L, call, n=0) == 0
     assert distill(L, call, dtype=3) == UNSUP and distill(L, call, tdtype=9) == UNSUP
-    for kw in (dict(student=None), dict(ids=None), dict(teacher=None), dict(k=0), dict(k=1025), dict(t=0.0),
+    for kw in (dict(student=None), dict(ids=None), dict(teacher=None), dict(k=0), dict(k=1025), dict(t=0.0), dict(t=2e30),
                dict(t=float("nan")), dict(n=-1), dict(vocab=0), dict(vocab=105), dict(vocab=1 << 20, stride=1 << 20)):
         assert distill(L, call, **kw) == INVALID, kw
     assert distill(L, call, student=P(0x100002)) == ALIGN
