@@ -331,14 +331,12 @@ def row_sample(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.0, 
     dev = logits.device
     _same(uniform, (m,), torch.float32, dev, "uniform")
     _same(lse, (m,), torch.float32, dev, "lse")
-    prm = SampleParams(1.0, 0, 1.0, 0.0, None, None, None, None)
-    for name, v, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+    settings, rows = [temperature, top_k, top_p, min_p], [None] * 4
+    for j, v in enumerate(settings):
         if isinstance(v, torch.Tensor):
-            _same(v, (m,), dtype, dev, name)
-            setattr(prm, name + "_rows", v.data_ptr())
-        else:
-            setattr(prm, name, v)
+            _same(v, (m,), torch.int32 if j == 1 else torch.float32, dev, ("temperature", "top_k", "top_p", "min_p")[j])
+            settings[j], rows[j] = 0, v.data_ptr()
+    prm = SampleParams(*settings, *rows)
     if out is None:
         f = dict(dtype=torch.float32, device=dev)
         out = RowSample(torch.empty(m, dtype=torch.int32, device=dev), torch.empty(m, **f),

@@ -262,7 +262,8 @@ __device__ __forceinline__ float class_term(float p, float x, float q) {
 // order in x, and sum p - sum q is known exactly: 0 with the rest as a class,
 // q_rest without.  For that the listed part of q's sum is added up once more,
 // from integer weights.  (A list with repeats counts its q twice; it takes the
-// plain sum, in 64 bits.)  A list of up to kAlone entries is one warp's work:
+// plain sum, in 64 bits over the lanes: by one thread it took 30 us for 256
+// entries.)  A list of up to kAlone entries is one warp's work:
 // `threads` is 32 then, and only warp 0 calls.  Thread 0 has the result.
 constexpr int kAlone = 128;
 
@@ -296,12 +297,19 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
         x_rest = q.rest > 0.f ? log_exact(q.all / q.rest) - log_exact(1.f / tch.p_rest) : (double)INFINITY;
     if (row.twice) {
         double v = 0;
-        if (t == 0) {
-            for (int j = 0; j < a.k; ++j)
-                if (l.id[j] >= 0 && l.p[j] > 0.f)
-                    v += (double)(l.p[j] * tch.inv) * (((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift);
-            if (tch.p_rest > 0.f) v += (double)tch.p_rest * x_rest;
+        for (int j = t; j < a.k; j += threads)
+            if (l.id[j] >= 0 && l.p[j] > 0.f)
+                v += (double)(l.p[j] * tch.inv) * (((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(DLM_FULL_MASK, v, o);
+        if (threads > 32) {
+            if ((t & 31) == 0) sh.listed[t >> 5] = (uint64_t)__double_as_longlong(v);
+            __syncthreads();
+            v = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) v += __longlong_as_double((long long)sh.listed[w]);
         }
+        if (tch.p_rest > 0.f) v += (double)tch.p_rest * x_rest;
         return (float)v;
     }
     float v = 0.f;
