@@ -49,6 +49,7 @@ constexpr int kRuns = 4;               // runs (of 32 vectors) per batch
 constexpr int kBatchVecs = 32 * kRuns;
 constexpr int kCap = 2048;             // candidates held in shared memory
 constexpr int kBracketCap = 2 * kCap;  // tokens of a bracket (the weights' space too)
+constexpr int kSortBins = 1024;        // bins of a sort
 constexpr int kFine = 1024;            // bins that a bracket's tokens are sorted into
 constexpr int kListRuns = 128;         // run maxima that open a nucleus' candidate list
 constexpr int kBracketSide = 1200;     // tokens on either side of its middle
@@ -248,10 +249,17 @@ __device__ void bitonic(uint64_t* buf) {
     __syncthreads();
 }
 
-// Sort buf[0, n) ascending (n <= kCap).  Short lists by rank (every thread
-// counts the smaller ones, broadcast reads, two barriers), longer ones by the
-// network, padded to a power of two.
-__device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
+// Sort buf[0, n) ascending (n <= kCap, entries differ).  Short lists by rank
+// (every thread counts the smaller ones, broadcast reads, two barriers), longer
+// ones by bins: the upper words between the smallest and the largest in
+// kSortBins equal steps, the bins' starts from a scan, and each entry's rank
+// among its bin's.  Where many share a bin (ties), or there is no room for bins,
+// the network, padded to a power of two.  `space` holds kSortBins words that
+// are free, or is null.  (The 1000 largest of 61 rows of 100003 floats take
+// 48 us, 66 with the network alone; top_k = 1500 of 512 rows of 152064, 370 and
+// 415.  4 KB of their own for the bins cost the kernels more, 517 us for 482 at
+// 2048 rows of 126464: four CTAs' shared memory leaves that much less cache.)
+__device__ __noinline__ void sort_u64(uint64_t* buf, int n, void* space, Ctrl* c) {
     if (n <= kThreads) {
         const int i = threadIdx.x;
         const uint64_t v = i < n ? buf[i] : 0;
@@ -262,6 +270,69 @@ __device__ __noinline__ void sort_u64(uint64_t* buf, int n) {
         if (i < n) buf[r] = v;
         __syncthreads();
         return;
+    }
+    if (space) {
+        constexpr int E = kCap / kThreads, PER = kSortBins / kThreads;
+        const int t = threadIdx.x;
+        uint32_t* bins = static_cast<uint32_t*>(space);
+        uint64_t x[E];
+        uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int i = t + e * kThreads;
+            x[e] = i < n ? buf[i] : ~0ull;
+            if (i < n) lo = min(lo, (uint32_t)(x[e] >> 32)), hi = max(hi, (uint32_t)(x[e] >> 32));
+        }
+        lo = __reduce_min_sync(DLM_FULL_MASK, lo);
+        hi = __reduce_max_sync(DLM_FULL_MASK, hi);
+        if ((t & 31) == 0) c->hits[0][t >> 5] = (int)lo, c->hits[1][t >> 5] = (int)hi;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) bins[t + j * kThreads] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) lo = min(lo, (uint32_t)c->hits[0][w]), hi = max(hi, (uint32_t)c->hits[1][w]);
+        // (float conversion and product are monotone, so bins are in order)
+        const float step = (kSortBins - 0.5f) / ((float)(hi - lo) + 1.f);
+        uint32_t at[E], most = 0;  // bin, and place in it
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (t + e * kThreads >= n) continue;
+            const uint32_t bin = min((uint32_t)kSortBins - 1, (uint32_t)((float)((uint32_t)(x[e] >> 32) - lo) * step));
+            const uint32_t place = atomicAdd(&bins[bin], 1u);
+            at[e] = bin << 16 | place;
+            most = max(most, place);
+        }
+        if (!__syncthreads_or(most >= 64)) {
+            uint32_t v[PER], sum = 0;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) sum += v[j] = bins[t * PER + j];
+            uint64_t all;
+            uint32_t run = (uint32_t)block_scan((uint64_t)sum, c->scan, all);
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {  // start and length
+                bins[t * PER + j] = run << 16 | v[j];
+                run += v[j];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (t + e * kThreads < n) buf[(bins[at[e] >> 16] >> 16) + (at[e] & 0xffffu)] = x[e];
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (t + e * kThreads >= n) continue;
+                const uint32_t bin = bins[at[e] >> 16], i0 = bin >> 16, i1 = i0 + (bin & 0xffffu);
+                uint32_t r = i0;
+                for (uint32_t i = i0; i < i1; ++i) r += buf[i] < x[e];
+                at[e] = r;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (t + e * kThreads < n) buf[at[e]] = x[e];
+            __syncthreads();
+            return;
+        }
     }
     const int m = n <= 2 * kThreads ? 2 * kThreads : n <= 4 * kThreads ? 4 * kThreads : 8 * kThreads;
     for (int i = n + threadIdx.x; i < m; i += kThreads) buf[i] = ~0ull;
@@ -726,7 +797,8 @@ __device__ __noinline__ void pick_candidate(const RowSearchArgs& a, const Smem& 
     }
     for (int i = t; i < n; i += kThreads) s.buf[i] = (s.buf[i] << 32) | (uint32_t)i;
     __syncthreads();
-    sort_u64(s.buf, n);
+    constexpr int kRoom = kCap - kSortBins / 2;  // (bins behind the weights)
+    sort_u64(s.buf, n, n <= kRoom ? s.wbuf + kRoom : nullptr, c);
     const int per = (n + kThreads - 1) / kThreads, i0 = min(n, t * per), i1 = min(n, i0 + per);
     uint64_t sum = 0, total;
     for (int i = i0; i < i1; ++i) sum += s.wbuf[(uint32_t)s.buf[i]];
@@ -1575,7 +1647,7 @@ __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const
                 crossing(mine, m0, w);
             }
         } else {
-            sort_u64(s.fine, n);
+            sort_u64(s.fine, n, s.buf, c);
             const int per = (n + kThreads - 1) / kThreads, i0 = min(n, t * per), i1 = min(n, i0 + per);
             uint64_t mine = 0, all;
             for (int i = i0; i < i1; ++i) mine += weight_call(candidate_value(s.fine[i]), c->ws);
@@ -1766,7 +1838,7 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
     if (c->count > (uint32_t)kCap) return other;
     const uint32_t n = k > 0 ? (uint32_t)top_candidates(s, (int)c->count, k) : c->count;
     if (n <= (uint32_t)kThreads) return decide_small(a, s, (int)n, rule, o) ? kDone : other;
-    sort_u64(s.buf, (int)n);
+    sort_u64(s.buf, (int)n, s.wbuf, c);
     keep_candidates(s, (int)n, rule);
     const int kept = c->n;
     if (kept <= 0) return other;
@@ -1881,7 +1953,7 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
             const int n = (int)c->count, k = c->top_k;
             const bool fits = n >= k && n <= kCap;
             if (fits) {
-                sort_u64(s.buf, n);
+                sort_u64(s.buf, n, s.wbuf, c);
                 if constexpr (!SAMPLE) {
                     write_topk(a, s, k, o);
                 } else {
@@ -1918,7 +1990,7 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
                     __syncthreads();
                 }
                 const int n = (int)c->count;
-                sort_u64(s.buf, n);
+                sort_u64(s.buf, n, s.wbuf, c);
                 if constexpr (!SAMPLE) {
                     write_topk(a, s, min(n, k), o);
                 } else {
@@ -2083,7 +2155,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
                     gather_runs<DT>(w.row, V, nb * kRuns, s, least);
                     if (c->count <= (uint32_t)kCap) {
                         const int n = top_candidates(s, (int)c->count, k);
-                        sort_u64(s.buf, n);
+                        sort_u64(s.buf, n, s.wbuf, c);
                         write_topk(a, s, min(n, k), o);
                         verdict = kDone;
                     }
