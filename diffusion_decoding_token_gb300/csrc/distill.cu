@@ -15,6 +15,9 @@
 // All three are bound by HBM: the loss by one read of the row, the gradient by a
 // read and a write.
 //  * distill_stream_kernel streams a row through registers for its loss.
+//    512 rows of 126464 bf16 tokens, 64 teacher logits: 38 us with an empty L2
+//    (3.4 TB/s of 6.8; 3.4 CTAs per SM, each with 16 KB on its way).  Two CTAs
+//    per row took 46 us.
 //  * The step needs the row twice, once for its sums and once for the gradient:
 //    distill_row_kernel holds it on chip in between.  A cluster's CTAs copy a
 //    slice each (about 40 KB, five CTAs per SM) into shared memory with
@@ -22,17 +25,20 @@
 //    add up their slice, exchange sums through distributed shared memory and
 //    write their slice's gradient.  The gradient alone is the same without the
 //    sums.  How long a CTA lives decides (its slice takes its share of the SM's
-//    shared memory meanwhile), so its reductions share five barriers, and only
-//    one thread of a row does 64-bit arithmetic on the sums.
+//    shared memory meanwhile), so its reductions share five barriers, only the
+//    first CTA does 64-bit arithmetic on the sums, and last.
+//    2048 rows of 152064 bf16 tokens, a quarter of them without a loss: 228 us,
+//    4.8 TB/s of the 1.09 GB that it reads and writes.  Streamed twice (the
+//    second read from L2) it took 269 us at best, slices of 77 KB 308 us, 128
+//    threads 231 us.
 //  * Rows that eight CTAs can not hold (above 1.5 MB) are streamed twice.
 //
 // q_rest = 1 - sum q_id would lose all digits for a peaked student, so the sum
-// over the tokens that are not listed is taken apart from the start: the row
-// kernel takes the listed logits out of its slice (-inf in their place), the
-// stream kernel marks them in a bitmap, one byte of which answers for a whole
-// vector.  The gradient is written for every token as if none were listed, and
-// then the listed ones are written over (the block barrier between orders the
-// two).
+// over the tokens that are not listed is taken apart from the start: listed
+// logits are taken out (-inf in their place), by the row kernel in its slice, by
+// the stream kernel with a bitmap, one byte of which answers for a whole vector.
+// The gradient is written for every token as if none were listed, and then the
+// listed ones are written over (the block barrier between orders the two).
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
@@ -223,17 +229,42 @@ __device__ __forceinline__ Teacher list_total(const Shared& sh, bool rest) {
     return t;
 }
 
-// The listed tokens of a slice [e0, e1) in its bitmap (zeroed before); whether
-// this thread met one that was marked already.
-__device__ __forceinline__ int mark_listed(const List& l, int K, int64_t e0, int64_t e1) {
-    int twice = 0;
-    for (int j = threadIdx.x; j < K; j += kThreads) {
-        const int64_t id = l.id[j];
+// The entries that a thread of the stream kernel looks after, j = t, t + kThreads, ...:
+// those in the CTA's slice, and of them the first of each token.
+constexpr int kMine = (DLM_MAX_TOPK + kThreads - 1) / kThreads;
+struct Mine {
+    uint32_t in, own;  // a bit per entry
+    float s[kMine];    // their logits
+};
+
+// The listed tokens of a slice [e0, e1) in its bitmap (zeroed before).
+__device__ __forceinline__ void mark_listed(const List& l, int K, int64_t e0, int64_t e1, Mine& mine) {
+    mine.in = mine.own = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        const int j = threadIdx.x + i * kThreads;
+        const int64_t id = j < K ? l.id[j] : -1;
         if (id < e0 || id >= e1) continue;
         const uint32_t bit = 1u << ((id - e0) & 31);
-        twice |= (atomicOr(&l.bits[(id - e0) >> 5], bit) & bit) != 0;
+        mine.in |= 1u << i;
+        mine.own |= (uint32_t)((atomicOr(&l.bits[(id - e0) >> 5], bit) & bit) == 0) << i;
     }
-    return twice;
+}
+
+// A vector without the elements of the mask: -inf in their place.
+template <int DT>
+__device__ __forceinline__ uint4 without(uint4 w, uint32_t mask) {
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == DLM_F32) {
+            if ((mask >> i) & 1u) x[i] = 0xff800000u;
+        } else {
+            if ((mask >> (2 * i)) & 1u) x[i] = (x[i] & 0xffff0000u) | Row<DT>::kNegInf;
+            if ((mask >> (2 * i + 1)) & 1u) x[i] = (x[i] & 0xffffu) | (uint32_t)Row<DT>::kNegInf << 16;
+        }
+    }
+    return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
 // p (x - 1 + e^-x) for x = ln p - ln q, q = p e^-x.
@@ -373,64 +404,93 @@ __device__ __forceinline__ f2 weights_of(f2 z, f2 ref, f2 c, f2 c_lo) {
     return ex2x2(fma2(d, c, mul2(d, c_lo)));  // the large product inside the fma: one rounding of it less
 }
 
-// Sums of vectors [v0, v1) of a row (kThreads threads; the whole CTA calls).
+// Sums of vectors [v0, v1) of a row (kThreads threads; the whole CTA calls).  The
+// listed tokens are taken out of the vectors first, so that a batch's arithmetic
+// is straight code with one test for a new reference (with a branch on the mask
+// in each vector's, 512 rows of 126464 tokens took 40 us, not 38; the slice's
+// first 16 to 128 KB asked into L2 before the list is read changed nothing); a thread adds those
+// that it looks after at the end.
 template <int DT>
-__device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c, float c_lo, const uint32_t* bits) {
+__device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c, float c_lo, const uint32_t* bits,
+                            const Mine& mine) {
     constexpr int EPV = Row<DT>::EPV;
     Sums a;
     a.mx = -INFINITY;
     a.ref = -FLT_MAX;
-    f2 all = pack2(0.f, 0.f), rest = pack2(0.f, 0.f);
+    f2 rest = pack2(0.f, 0.f);
     const f2 c2 = pack2(c, c), lo2 = pack2(c_lo, c_lo);
     const int whole = (int)min((int64_t)v1, V / EPV);
-    auto add = [&](uint4 w, int v) {
-        const float m = Row<DT>::vmax(w);
+    auto add = [&](auto& w, const int (&v)[sizeof(w) / 16]) {
+        constexpr int N = sizeof(w) / 16;
+        uint32_t in[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const int at = (v[u] - v0) * EPV;  // first token of the vector, from the slice's start
+            in[u] = (bits[at >> 5] >> (at & 31)) & ((1u << EPV) - 1u);
+        }
+        float m = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            if (in[u]) w[u] = without<DT>(w[u], in[u]);
+            m = max_nan(m, Row<DT>::vmax(w[u]));
+        }
         a.mx = max_nan(a.mx, m);
         if ((m - a.ref) * c > kRebase) {
             const float e = ex2((a.ref - m) * c);
-            all = mul2(all, pack2(e, e));
             rest = mul2(rest, pack2(e, e));
             a.ref = m;
         }
-        float z[EPV];
-        Row<DT>::unpack(w, z);
         const f2 r2 = pack2(a.ref, a.ref);
-        f2 e[EPV / 2];
+        f2 sum[N];
 #pragma unroll
-        for (int p = 0; p < EPV / 2; ++p) e[p] = weights_of(pack2(z[2 * p], z[2 * p + 1]), r2, c2, lo2);
-        {
-            const int at = (v - v0) * EPV;  // first token of the vector, from the slice's start
-            const uint32_t in = (bits[at >> 5] >> (at & 31)) & ((1u << EPV) - 1u);
-            if (in) {
+        for (int u = 0; u < N; ++u) {
+            float z[EPV];
+            Row<DT>::unpack(w[u], z);
+            f2 e[EPV / 2];
 #pragma unroll
-                for (int p = 0; p < EPV / 2; ++p) {
-                    float x, y;
-                    unpack2(e[p], x, y);
-                    const float lx = (in >> (2 * p)) & 1u ? x : 0.f, ly = (in >> (2 * p + 1)) & 1u ? y : 0.f;
-                    all = add2(all, pack2(lx, ly));
-                    rest = add2(rest, pack2(x - lx, y - ly));
-                }
-                return;
-            }
+            for (int p = 0; p < EPV / 2; ++p) e[p] = weights_of(pack2(z[2 * p], z[2 * p + 1]), r2, c2, lo2);
+#pragma unroll
+            for (int h = EPV / 4; h; h >>= 1)
+#pragma unroll
+                for (int p = 0; p < h; ++p) e[p] = add2(e[p], e[p + h]);
+            sum[u] = e[0];
         }
 #pragma unroll
-        for (int h = EPV / 4; h; h >>= 1)
+        for (int h = N / 2; h; h >>= 1)
 #pragma unroll
-            for (int p = 0; p < h; ++p) e[p] = add2(e[p], e[p + h]);
-        rest = add2(rest, e[0]);
+            for (int u = 0; u < h; ++u) sum[u] = add2(sum[u], sum[u + h]);
+        rest = add2(rest, sum[0]);
     };
     int v = v0 + (int)threadIdx.x;
     const uint4* vec = reinterpret_cast<const uint4*>(row);
     for (; v + (kUnroll - 1) * kThreads < whole; v += kUnroll * kThreads) {
         uint4 w[kUnroll];
+        int at[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) w[u] = ld_row(vec + v + u * kThreads);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) add(w[u], v + u * kThreads);
+        for (int u = 0; u < kUnroll; ++u) at[u] = v + u * kThreads, w[u] = ld_row(vec + at[u]);
+        add(w, at);
     }
-    for (; v < v1; v += kThreads) add(v < whole ? ld_row(vec + v) : load_vec<DT>(row, V, v), v);
+    for (; v < v1; v += kThreads) {
+        uint4 w[1] = {v < whole ? ld_row(vec + v) : load_vec<DT>(row, V, v)};
+        const int at[1] = {v};
+        add(w, at);
+    }
     a.rest = hsum2(rest);
-    a.all = hsum2(all) + a.rest;  // `all` held the listed ones so far
+    float listed = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        if (!((mine.own >> i) & 1u)) continue;
+        const float z = mine.s[i];
+        a.mx = max_nan(a.mx, z);
+        if ((z - a.ref) * c > kRebase) {
+            const float e = ex2((a.ref - z) * c);
+            listed *= e;
+            a.rest *= e;
+            a.ref = z;
+        }
+        listed += ex2((z - a.ref) * c);
+    }
+    a.all = listed + a.rest;
     return a;
 }
 
@@ -619,28 +679,26 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
     for (int i = t; i < (int)((sl.e1 - sl.e0 + 31) / 32); i += kThreads) l.bits[i] = 0;
     list_load(a, l, sh, r, lse_t, id0, x0);
     __syncthreads();
-    Share mine_all;
-    mine_all.twice = mark_listed(l, K, sl.e0, sl.e1);
+    Mine mine;
+    mark_listed(l, K, sl.e0, sl.e1, mine);
     // the listed logits are asked for now and used after the stream
-    constexpr int kMine = (DLM_MAX_TOPK + kThreads - 1) / kThreads;
-    float mine[kMine];
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const int j = t + i * kThreads, id = j < K ? l.id[j] : -1;
-        mine[i] = id >= sl.e0 && id < sl.e1 ? Row<DT>::scalar(row, id) : 0.f;
-    }
+    for (int i = 0; i < kMine; ++i)
+        mine.s[i] = (mine.in >> i) & 1u ? Row<DT>::scalar(row, l.id[t + i * kThreads]) : 0.f;
     list_weigh(a, l, sh, REST, lse_t);
     __syncthreads();
-    mine_all.q = stream_sums<DT>(row, V, sl.v0, sl.v1, c, a.scale_lo, l.bits);
+    Share share;
+    share.q = stream_sums<DT>(row, V, sl.v0, sl.v1, c, a.scale_lo, l.bits, mine);
+    share.twice = mine.in != mine.own;
     all_started(cl);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-        const int j = t + i * kThreads, id = j < K ? l.id[j] : -1;
-        if (id < sl.e0 || id >= sl.e1) continue;
-        l.s[j] = mine[i];
-        if (cl.rank != 0) cl.at(l.s, 0)[j] = mine[i];
+        if (!((mine.in >> i) & 1u)) continue;
+        const int j = t + i * kThreads;
+        l.s[j] = mine.s[i];
+        if (cl.rank != 0) cl.at(l.s, 0)[j] = mine.s[i];
     }
-    const Share all = merge_row(cl, sh, mine_all, c);
+    const Share all = merge_row(cl, sh, share, c);
     const Teacher tch = list_total(sh, REST);
     float inv, tail;
     const bool fine = row_factors(tch, all.q, REST, inv, tail);
