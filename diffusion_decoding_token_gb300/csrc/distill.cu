@@ -823,22 +823,21 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     Share row_share = no_share();
-    row_share.twice = 1;
     bool ok = true;
+    // the listed tokens leave the slice; one entry of each has its logit
+    bool twice = false;
+    float top = -INFINITY;
+    for (int j = t; j < K; j += kThreads) {
+        const int id = l.id[j];
+        if (id < sl.e0 || id >= sl.e1) continue;
+        const float s = take_out<DT>(data, (int)(id - sl.e0));
+        const bool took = !(s == -INFINITY);
+        l.s[j] = s;
+        l.own[j] = took;
+        twice |= !took;
+        if (took) top = max_nan(top, s);
+    }
     if (SUMS) {
-        // the listed tokens leave the slice; one entry of each has its logit
-        bool twice = false;
-        float top = -INFINITY;
-        for (int j = t; j < K; j += kThreads) {
-            const int id = l.id[j];
-            if (id < sl.e0 || id >= sl.e1) continue;
-            const float s = take_out<DT>(data, (int)(id - sl.e0));
-            const bool took = !(s == -INFINITY);
-            l.s[j] = s;
-            l.own[j] = took;
-            twice |= !took;
-            if (took) top = max_nan(top, s);
-        }
         __syncthreads();
         for (int v = t; v < n; v += kThreads) top = max_nan(top, Row<DT>::vmax(data[v]));
         const float ref = top > -INFINITY ? top : 0.f;  // nothing but -inf: weights of 0
@@ -884,11 +883,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
         row_share = all;
         ok = fine;
     } else {
-        for (int j = t; j < K; j += kThreads) {
-            const int id = l.id[j];
-            if (id >= sl.e0 && id < sl.e1) l.s[j] = Row<DT>::scalar(data, (int64_t)id - sl.e0);
-        }
-        __syncthreads();
+        row_share.twice = __syncthreads_or(twice);
     }
     const Teacher tch = list_total(sh, rest);
     const float scale = g * inv * tail;
