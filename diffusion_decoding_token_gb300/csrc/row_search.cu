@@ -34,6 +34,15 @@
 // one CTA per row the rows that need another pass are left to a second launch
 // that works each with a cluster: alone, a CTA would be at such a row long after
 // all the others have ended.
+//
+// Measured (empty L2, 2048 bf16 rows of 152064 unless said; the rows' bytes at the
+// card's 6.8 TB/s take 92 us): the 64 largest 149 us, 4.2 TB/s (the pass over the
+// rows alone 105 to 111; a list is made while its CTA reads nothing); settings of
+// their own per row, a fifth of them open, 263 us; top_p = 0.95 at temperature 1
+// over rows of 126464, two of five of them flat, 485 us; 32 of those rows at 0.7
+// and 0.9, 65 us, a chain of a dozen steps of 1 to 8 us each; 32 rows of 1024,
+// 13 us.  Four CTAs per SM (64 registers): three took 157, five and six 165 and
+// 236 with spills.
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
@@ -253,12 +262,16 @@ __device__ void bitonic(uint64_t* buf) {
 // (every thread counts the smaller ones, broadcast reads, two barriers), longer
 // ones by bins: the upper words between the smallest and the largest in
 // kSortBins equal steps, the bins' starts from a scan, and each entry's rank
-// among its bin's.  Where many share a bin (ties), or there is no room for bins,
-// the network, padded to a power of two.  `space` holds kSortBins words that
-// are free, or is null.  (The 1000 largest of 61 rows of 100003 floats take
-// 48 us, 66 with the network alone; top_k = 1500 of 512 rows of 152064, 370 and
-// 415.  4 KB of their own for the bins cost the kernels more, 517 us for 482 at
-// 2048 rows of 126464: four CTAs' shared memory leaves that much less cache.)
+// among its bin's.  Equal steps of a candidate's word are narrow near 0, which
+// suits a list's tail and an outlier; where logits of both signs are listed the
+// steps are equal in the logit (651 rows of 1611, k = 575: 30 us for 54; with all
+// lists so, the 1000 largest of 61 rows of 100003 floats take 50 us, not 44).
+// Where many share a bin (ties), or there is no room for bins, the network,
+// padded to a power of two (62 us for those 1000 largest; top_k = 1500 of 512
+// rows of 152064: 415 us, 370 with bins).  `space` holds kSortBins words that are
+// free, or is null.  (4 KB of their own for the bins cost the kernels more, 517
+// us for 482 at 2048 rows of 126464: four CTAs' shared memory leaves that much
+// less cache.)
 __device__ __noinline__ void sort_u64(uint64_t* buf, int n, void* space, Ctrl* c) {
     if (n <= kThreads) {
         const int i = threadIdx.x;
@@ -291,13 +304,15 @@ __device__ __noinline__ void sort_u64(uint64_t* buf, int n, void* space, Ctrl* c
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) lo = min(lo, (uint32_t)c->hits[0][w]), hi = max(hi, (uint32_t)c->hits[1][w]);
-        // (float conversion and product are monotone, so bins are in order)
-        const float step = (kSortBins - 0.5f) / ((float)(hi - lo) + 1.f);
+        // (conversion, difference and product are monotone, so bins are in order)
+        const bool both = (lo ^ hi) >> 31;
+        auto place_of = [&](uint32_t word) { return both ? -key_value(~word) : (float)word; };
+        const float from = place_of(lo), step = (kSortBins - 0.5f) / fmaxf(place_of(hi) - from, 1e-30f);
         uint32_t at[E], most = 0;  // bin, and place in it
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if (t + e * kThreads >= n) continue;
-            const uint32_t bin = min((uint32_t)kSortBins - 1, (uint32_t)((float)((uint32_t)(x[e] >> 32) - lo) * step));
+            const uint32_t bin = min((uint32_t)kSortBins - 1, (uint32_t)((place_of((uint32_t)(x[e] >> 32)) - from) * step));
             const uint32_t place = atomicAdd(&bins[bin], 1u);
             at[e] = bin << 16 | place;
             most = max(most, place);
