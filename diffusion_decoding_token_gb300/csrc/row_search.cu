@@ -38,11 +38,11 @@
 // Measured (empty L2, 2048 bf16 rows of 152064 unless said; the rows' bytes at the
 // card's 6.8 TB/s take 92 us): the 64 largest 149 us, 4.2 TB/s (the pass over the
 // rows alone 105 to 111; a list is made while its CTA reads nothing); settings of
-// their own per row, a fifth of them open, 263 us; top_p = 0.95 at temperature 1
-// over rows of 126464, two of five of them flat, 485 us; 32 of those rows at 0.7
-// and 0.9, 65 us, a chain of a dozen steps of 1 to 8 us each; 32 rows of 1024,
-// 13 us.  Four CTAs per SM (64 registers): three took 157, five and six 165 and
-// 236 with spills.
+// their own per row 263 us; top_p = 0.95 at temperature 1 over rows of 126464, two
+// of five of them flat, 485 us; 32 of those rows at 0.7 and 0.9, 65 us, a chain of
+// a dozen steps of 1 to 8 us each; 32 rows of 1024, 13 us.  Four CTAs per SM (64
+// registers): three took 157 us for the first of these, five and six 165 and 236
+// with spills.
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
