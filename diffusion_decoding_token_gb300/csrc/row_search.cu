@@ -1484,6 +1484,21 @@ __device__ __noinline__ void bin_tokens(const Smem& s, float z_hi, float per_bin
     __syncthreads();
 }
 
+// The cluster's bins added up in the first CTA: each CTA takes its share of them.
+// (By the first CTA alone, 32 remote loads per thread, 32 rows of 126464 take
+// 57.6 us instead of 55.5.)
+__device__ __noinline__ void merge_bins(const Cluster& cl, const Smem& s) {
+    const int per = kFine / cl.split;
+    for (int i = cl.rank * per + (int)threadIdx.x; i < (cl.rank + 1) * per; i += kThreads) {
+        uint64_t v[8], sum = 0;
+#pragma unroll
+        for (int rk = 0; rk < 8; ++rk) v[rk] = rk < cl.split ? cl.at(s.fine, rk)[i] : 0;
+#pragma unroll
+        for (int rk = 0; rk < 8; ++rk) sum += v[rk];
+        cl.at(s.fine, 0)[i] = sum;
+    }
+}
+
 // After a pass, in the first CTA: where the row ends.  Every weight of the
 // pass is off by the share err / total at most, so a sum over part of the mass
 // and that part's share of the whole differ by 2 share (1 - share) err at most
@@ -1565,10 +1580,7 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, i
     uint64_t v[PER], sum = 0, inside;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        v[j] = 0;
-#pragma unroll
-        for (int rk = 0; rk < 8; ++rk)  // all of them on their way at once
-            if (rk < cl.split) v[j] += cl.at(s.fine, rk)[t * PER + j];
+        v[j] = s.fine[t * PER + j];
         sum += v[j];
     }
     uint64_t m = block_scan(sum, c->scan, inside);
@@ -1939,6 +1951,10 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
                 bracket_pass<DT, 3>(row, V, w.b0, w.b1, z_lo, z_hi, ws, s.bmass, c, s.buf, fine);
             if (bins) bin_tokens(s, z_hi, per_bin, ws);
             cl.sync();
+            if (bins && cl.split > 1) {
+                merge_bins(cl, s);
+                cl.sync();
+            }
             if (cl.rank == 0) {
                 const int next = find_end(cl, s, nb, verdict);
                 if (t == 0) c->verdict = next;
