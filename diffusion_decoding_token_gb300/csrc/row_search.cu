@@ -1192,31 +1192,48 @@ __device__ __forceinline__ float min_p_logit(const Ctrl* c) {
     return c->ws.m + (1.0001f * __logf(c->min_p) - 1e-5f) / (c->ws.c_hi * kLn2) - 1e-6f * fabsf(c->ws.m);
 }
 
+// The cluster's bins added up in the first CTA: each CTA takes its share of them.
+// (By the first CTA alone, 32 remote loads per thread for a bracket's, 32 rows of
+// 126464 take 57.6 us instead of 55.5.)
+template <typename T>
+__device__ __noinline__ void merge_bins(const Cluster& cl, T* bins, int n) {
+    const int per = n / cl.split;
+    for (int i = cl.rank * per + (int)threadIdx.x; i < (cl.rank + 1) * per; i += kThreads) {
+        T v[8], sum = 0;
+#pragma unroll
+        for (int rk = 0; rk < 8; ++rk) v[rk] = rk < cl.split ? cl.at(bins, rk)[i] : 0;
+#pragma unroll
+        for (int rk = 0; rk < 8; ++rk) sum += v[rk];
+        cl.at(bins, 0)[i] = sum;
+    }
+}
+
 // A sample of `tokens` of the row in buf's kBins words: per 1/32 of an exponent below the
 // maximum the weights relative to the bin's upper end, in 2^-16 (between 0.97
 // and 1 each, so the bin counts its tokens too).  Returns how many of the row's
 // tokens one of the sample stands for.
+// The cluster's CTAs take a share each (merge_bins adds them up).
 template <int DT>
-__device__ __noinline__ float sample_row(const char* row, int64_t V, const Smem& s, int tokens) {
+__device__ __noinline__ float sample_row(const Cluster& cl, const char* row, int64_t V, const Smem& s, int tokens,
+                                         float m, float c_hi) {
     constexpr int EPV = Row<DT>::EPV;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const Ctrl* c = s.c;
+    const int t = threadIdx.x, lane = t & 31, warps = kWarps * cl.split, warp = cl.rank * kWarps + (t >> 5);
     uint32_t* bins = reinterpret_cast<uint32_t*>(s.buf);
     for (int i = t; i < kBins; i += kThreads) bins[i] = 0;
     __syncthreads();
     const int nsub = (int)((V + 32 * EPV - 1) / (32 * EPV));
     const int n = min(nsub, tokens / (32 * EPV));
-    const float c32 = c->ws.c_hi * 32.f, m = c->ws.m;
+    const float c32 = c_hi * 32.f;
     const int stride = nsub / n;
     auto fetch = [&](int i) { return i < n ? load_vec<DT>(row, V, i * stride * 32 + lane) : make_uint4(0, 0, 0, 0); };
-    uint4 w0 = fetch(warp), w1 = fetch(warp + kWarps), w2 = fetch(warp + 2 * kWarps);
+    uint4 w0 = fetch(warp), w1 = fetch(warp + warps), w2 = fetch(warp + 2 * warps);
 #pragma unroll 1
-    for (int i = warp; i < n; i += kWarps) {
+    for (int i = warp; i < n; i += warps) {
         float z[EPV];
         Row<DT>::unpack(w0, z);
         w0 = w1;
         w1 = w2;
-        w2 = fetch(i + 3 * kWarps);
+        w2 = fetch(i + 3 * warps);
 #pragma unroll
         for (int e = 0; e < EPV; ++e) {
             if (!(z[e] > -INFINITY)) continue;
@@ -1234,17 +1251,17 @@ __device__ __noinline__ float sample_row(const char* row, int64_t V, const Smem&
 // to that, and the bracket takes the kBracketSide tokens on either side.  On a
 // flat row of 152064 tokens that is three to four standard deviations of the
 // sample; where few tokens hold the mass it reaches up to the largest.  When
-// min-p's cut is higher the bracket is put around it.  One CTA; sets c->bin_lo,
-// c->bin_hi and returns kTier1 or kMinP.
-template <int DT>
-__device__ __noinline__ int place_bracket(const char* row, int64_t V, const Smem& s) {
+// min-p's cut is higher the bracket is put around it.  `scale`: how many tokens one
+// of the sample stands for.  One CTA; sets c->bin_lo, c->bin_hi and returns
+// kTier1 or kMinP.
+__device__ __noinline__ int place_bracket(const Smem& s, float scale) {
     constexpr int PER = kBins / kThreads;
     const int t = threadIdx.x;
     Ctrl* c = s.c;
     const uint32_t* bins = reinterpret_cast<const uint32_t*>(s.buf);
     const bool by_least = c->least > 0;
     const int cut = by_least ? (int)fminf((c->ws.m - min_p_logit(c)) * c->ws.c_hi * 32.f, (float)(kBins - 2)) : kBins;
-    float want = 0.f, scale = 1.f;
+    float want = 0.f;
     if (t == 0) {  // for a sample that does not reach it
         c->left = 0;
         c->bin_lo = kBins;
@@ -1252,7 +1269,6 @@ __device__ __noinline__ int place_bracket(const char* row, int64_t V, const Smem
         c->batch = kBins;
     }
     if (c->top_p < 1.f) {
-        scale = sample_row<DT>(row, V, s, kSampleTokens);
         // thread t takes bins from the lowest weights up
         float mass = 0.f;
         uint64_t tokens = 0;  // in 2^-16, a little short
@@ -1306,15 +1322,11 @@ __device__ __noinline__ int place_bracket(const char* row, int64_t V, const Smem
 // A threshold that about sqrt(k kCap) of the row's logits reach, between k and
 // the list's length by three standard deviations of the sample.  One CTA; sets
 // c->bin_lo and returns kList, or kRadix when no bin is near.
-template <int DT>
-__device__ __noinline__ int place_list(const char* row, int64_t V, int k, const Smem& s) {
+__device__ __noinline__ int place_list(int k, const Smem& s, float scale) {
     constexpr int PER = kBins / kThreads;
     const int t = threadIdx.x;
     Ctrl* c = s.c;
     const uint32_t* bins = reinterpret_cast<const uint32_t*>(s.buf);
-    // half the sample is enough for the largest k of dlm_row_topk (48 and 44 us
-    // for the 1000 largest of 61 rows of 100003 floats)
-    const float scale = sample_row<DT>(row, V, s, k <= DLM_MAX_TOPK ? kSampleTokens / 2 : kSampleTokens);
     if (t == 0) c->bin_lo = 0;
     uint64_t tokens = 0, all;
 #pragma unroll
@@ -1482,21 +1494,6 @@ __device__ __noinline__ void bin_tokens(const Smem& s, float z_hi, float per_bin
             shared_add(&s.fine[fine_bin(e, z_hi, per_bin)], weight_call(candidate_value(e), ws) * __popc(like));
     }
     __syncthreads();
-}
-
-// The cluster's bins added up in the first CTA: each CTA takes its share of them.
-// (By the first CTA alone, 32 remote loads per thread, 32 rows of 126464 take
-// 57.6 us instead of 55.5.)
-__device__ __noinline__ void merge_bins(const Cluster& cl, const Smem& s) {
-    const int per = kFine / cl.split;
-    for (int i = cl.rank * per + (int)threadIdx.x; i < (cl.rank + 1) * per; i += kThreads) {
-        uint64_t v[8], sum = 0;
-#pragma unroll
-        for (int rk = 0; rk < 8; ++rk) v[rk] = rk < cl.split ? cl.at(s.fine, rk)[i] : 0;
-#pragma unroll
-        for (int rk = 0; rk < 8; ++rk) sum += v[rk];
-        cl.at(s.fine, 0)[i] = sum;
-    }
 }
 
 // After a pass, in the first CTA: where the row ends.  Every weight of the
@@ -1952,7 +1949,7 @@ __device__ __forceinline__ void finish_row(const RowSearchArgs& a, const Cluster
             if (bins) bin_tokens(s, z_hi, per_bin, ws);
             cl.sync();
             if (bins && cl.split > 1) {
-                merge_bins(cl, s);
+                merge_bins(cl, s.fine, kFine);
                 cl.sync();
             }
             if (cl.rank == 0) {
@@ -2130,6 +2127,7 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
     }
     cl.sync();
 
+    int found = kDone;
     if (cl.rank == 0) {
         float m = -INFINITY;
         low = INFINITY;
@@ -2177,13 +2175,11 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
                 // logits so far from 0 that tiers 1 and 2 can not tell "60 powers
                 // of 2 below the maximum" from the maximum itself
                 if (verdict == kTier1 && fabsf(m) * c->ws.c_hi > 60.f * 1048576.f) verdict = kRadix;
-                if (verdict == kTier1 && filtered) verdict = place_bracket<DT>(w.row, V, s);
-                if (verdict == kList) verdict = place_list<DT>(w.row, V, k, s);
             } else {
                 const float least = whole ? -INFINITY : threshold_for(s.sub, nb * kRuns, k, low, m, c);
                 verdict = kRadix;
                 if (!whole && !(least > -INFINITY)) {
-                    verdict = place_list<DT>(w.row, V, k, s);
+                    verdict = kList;
                 } else {
                     gather_runs<DT>(w.row, V, nb * kRuns, s, least);
                     if (c->count <= (uint32_t)kCap) {
@@ -2195,27 +2191,49 @@ __global__ void __launch_bounds__(kThreads, 4) row_search_kernel(const RowSearch
                 }
             }
         }
-        if (DEFER) {
-            if (t == 0 && verdict != kDone) {
-                const bool placed = verdict == kMinP || verdict == kList || (verdict == kTier1 && filtered);
-                const uint32_t bins = placed ? (uint32_t)c->bin_lo << 12 | (uint32_t)(verdict == kList ? 0 : c->bin_hi) : 0u;
-                a.token[o] = (int32_t)(kOpenMark | (uint32_t)verdict << 24 | bins);
-                a.prob[o] = m;
-            }
+        found = verdict;
+        if (t == 0) c->verdict = verdict;
+    }
+    // a row that needs a bracket or a list's threshold: a sample of it by all its CTAs
+    if (!DEFER) {
+        cl.sync();
+        found = cl.at(c, 0)->verdict;
+        if (found == kDone) {
+            cl.sync();  // (the first CTA's ctrl has been read)
             return;
         }
-        if (t == 0) {
-            set_bracket(c, verdict);
-            c->verdict = verdict == kMinP ? kTier1 : verdict;
-        }
     }
-    if (DEFER) return;
+    int verdict = found;
+    if (verdict == kList || (verdict == kTier1 && filtered)) {
+        float scale = 1.f;
+        if (verdict == kList || c->top_p < 1.f) {
+            // half the sample is enough for the largest k of dlm_row_topk (48 and 44 us
+            // for the 1000 largest of 61 rows of 100003 floats)
+            const int tokens = verdict == kList && k <= DLM_MAX_TOPK ? kSampleTokens / 2 : kSampleTokens;
+            scale = sample_row<DT>(cl, w.row, V, s, tokens, cl.at(c, 0)->ws.m, c->ws.c_hi);
+            if (cl.split > 1) {
+                cl.sync();
+                merge_bins(cl, reinterpret_cast<uint32_t*>(s.buf), kBins);
+                cl.sync();
+            }
+        }
+        if (cl.rank == 0) verdict = verdict == kList ? place_list(k, s, scale) : place_bracket(s, scale);
+    }
+    if (DEFER) {
+        if (t == 0 && verdict != kDone) {
+            const bool placed = verdict == kMinP || verdict == kList || (verdict == kTier1 && filtered);
+            const uint32_t bins = placed ? (uint32_t)c->bin_lo << 12 | (uint32_t)(verdict == kList ? 0 : c->bin_hi) : 0u;
+            a.token[o] = (int32_t)(kOpenMark | (uint32_t)verdict << 24 | bins);
+            a.prob[o] = c->ws.m;
+        }
+        return;
+    }
+    if (cl.rank == 0 && t == 0) {
+        set_bracket(c, verdict);
+        c->verdict = verdict == kMinP ? kTier1 : verdict;
+    }
     cl.sync();
-    const int verdict = cl.at(c, 0)->verdict;
-    if (verdict == kDone)
-        cl.sync();  // (the first CTA's ctrl has been read)
-    else
-        finish_row<DT, SAMPLE>(a, cl, s, w, verdict);
+    finish_row<DT, SAMPLE>(a, cl, s, w, cl.at(c, 0)->verdict);
 }
 
 // The rows that row_search_kernel left open.  Which rows they are is not known
