@@ -39,7 +39,7 @@
 // card's 6.8 TB/s take 92 us): the 64 largest 149 us, 4.2 TB/s (the pass over the
 // rows alone 105 to 111; a list is made while its CTA reads nothing); settings of
 // their own per row 263 us; top_p = 0.95 at temperature 1 over rows of 126464, two
-// of five of them flat, 485 us; 32 of those rows at 0.7 and 0.9, 65 us, a chain of
+// of five of them flat, 482 us; 32 of those rows at 0.7 and 0.9, 61 us, a chain of
 // a dozen steps of 1 to 8 us each; 32 rows of 1024, 13 us.  Four CTAs per SM (64
 // registers): three took 157 us for the first of these, five and six 165 and 236
 // with spills.
