@@ -52,7 +52,6 @@ constexpr int kThreads = kRowThreads;
 constexpr int kWarps = kRowWarps;
 constexpr int kUnroll = 4;
 constexpr float kRebase = 12.0f;  // powers of 2 of headroom before a thread's reference moves
-constexpr float kUnit = 5.684341886080802e-14f;  // 2^-44
 
 // A slice's softmax sums relative to `ref`; `mx` is the exact maximum (NaN if
 // the slice holds one), `rest` the sum over the tokens that are not listed.
@@ -129,15 +128,6 @@ __device__ __forceinline__ float teacher_at(const DistillArgs& a, int64_t i) {
     case DLM_F16: return Row<DLM_F16>::scalar(a.teacher, i);
     default: return static_cast<const float*>(a.teacher)[i];
     }
-}
-
-// ln x for x >= 1 to 2^-36: the float logarithm's error is what x 2^-y is off 1
-// by, with 2^-y from the integer weights.  (64-bit arithmetic has a 64th of the
-// 32-bit rate here: a double logarithm by every thread of a CTA took 7 us.)
-__device__ __forceinline__ double log_exact(float x) {
-    const float y = fmaxf(0.f, __log2f(x));
-    const double d = (double)x * ((double)weight44_of(y, 0.f) * (double)kUnit) - 1.0;
-    return (double)y * 0.6931471805599453 + (d - 0.5 * d * d);
 }
 
 // The list in two steps with a barrier after each.  First: entries into shared
@@ -317,15 +307,14 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
         }
         q.all = (float)listed * kUnit + q.rest;
     }
-    const double lse_s = (double)q.mx * a.inv_t + log_exact(q.all);
+    const double log_all = log_exact(q.all), lse_s = (double)q.mx * a.inv_t + log_all;
     const double log_z = rest ? (double)lse_t
                               : (double)list_max(sh) * a.inv_t + log_exact(fmaxf((float)tch.sum * kUnit, 1.f));
     const double shift = lse_s - log_z;
-    // ln p_rest - ln q_rest = ln(all / rest) - ln(1 / p_rest)
+    // ln p_rest - ln q_rest, from three logarithms: a quotient of the sums has no limit
     const float q_rest = q.rest / q.all;
     double x_rest = 0;
-    if (tch.p_rest > 0.f)
-        x_rest = q.rest > 0.f ? log_exact(q.all / q.rest) - log_exact(1.f / tch.p_rest) : (double)INFINITY;
+    if (tch.p_rest > 0.f) x_rest = q.rest > 0.f ? log_exact(tch.p_rest) + log_all - log_exact(q.rest) : (double)INFINITY;
     if (row.twice) {
         double v = 0;
         for (int j = t; j < a.k; j += threads)

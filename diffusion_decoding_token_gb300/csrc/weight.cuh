@@ -30,6 +30,7 @@
 namespace dlm {
 
 constexpr int kWeightBits = 44;       // one unit is 2^-44 of the largest weight
+constexpr float kUnit = 5.684341886080802e-14f;  // 2^-44
 constexpr float kWeightCut = 46.0f;   // below 2^-46 a weight rounds to 0
 
 // round(2^44 * 2^(-j/256))
@@ -165,6 +166,28 @@ DLM_HD uint64_t weight44(float z, const WeightScale& s) {
     float e;
     const float y = weight_exponent(z, s, e);
     return weight44_of(y, e, s.tab);
+}
+
+// ln x to 2^-36 for any normal x > 0: with x = m 2^e and m in [1, 2), the float
+// logarithm y of m is off by what m 2^-y is off 1 by, 2^-y from the integer
+// weights.  (Of x itself that product would have no digits left: from x = 2^25 on
+// the logarithm was off by more than 2^-18, from 2^46 on by 1.5.  64-bit arithmetic
+// has a 64th of the 32-bit rate here: a double logarithm by every thread of a CTA
+// took 7 us.)
+DLM_HD double log_exact(float x) {
+#ifdef __CUDA_ARCH__
+    const uint32_t b = __float_as_uint(x);
+    const float m = __uint_as_float((b & 0x7fffffu) | 0x3f800000u), y = fmaxf(0.f, __log2f(m));
+#else
+    uint32_t b;
+    memcpy(&b, &x, 4);
+    const uint32_t mb = (b & 0x7fffffu) | 0x3f800000u;
+    float m;
+    memcpy(&m, &mb, 4);
+    const float y = fmaxf(0.f, log2f(m));
+#endif
+    const double d = (double)m * ((double)weight44_of(y, 0.f) * (double)kUnit) - 1.0;
+    return ((double)((int)(b >> 23) - 127) + (double)y) * 0.6931471805599453 + (d - 0.5 * d * d);
 }
 
 // floor(f * s) for a float f in [0, 1): f = mantissa * 2^-shift exactly.

@@ -1,0 +1,143 @@
+"""Distillation where a student's mass lies in its list by tens of nats, or in one
+token: loss and gradient against 64-bit numpy that works with logarithms.
+
+Tolerances.  A row's two sums of exponentials (listed, not listed) are each
+within 2^-18 of themselves (ex2 2^-22, exponents of up to ~20 relative to the
+sum's own largest rounded three times at 2^-24, additions), and logarithms of
+them within that.  So the loss is within |w| 2^-17 sum p, and 2^-21 of itself for
+its own roundings.  An unlisted token's gradient w / T (q_v - p_rest e_v / rest)
+is within 2^-17 of its two terms, more where the token lies far below the largest
+unlisted one (row_ref.distill has that factor).  A listed token's q - p is within
+2^-17 of q + p, and where q is above 1/2 within 2^-17 of (1 - q) + |1 - p|, of
+which it is the difference too.  Half a step of the gradient's type is added.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import row_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dlm():
+    import diffusion_decoding_token_gb300 as d
+    d.lib()
+    return d
+
+
+def log_sum_exp(y):
+    return y.max() + math.log(np.exp(y - y.max()).sum()) if len(y) and y.max() > -np.inf else -np.inf
+
+
+def definition(row, ids, teacher, t, lse):
+    """(loss, gradient, the gradient's error scale) of a row of weight 1."""
+    held = ids >= 0
+    ids, a = ids[held], teacher[held] / t
+    with np.errstate(divide="ignore"):
+        y = row / t
+        log_q = y - log_sum_exp(y)
+        log_p = a - (log_sum_exp(a) if lse is None else lse)
+        out = np.ones(len(row), bool)
+        out[ids] = False
+        p, q = np.exp(log_p), np.exp(log_q)
+        loss = sum(p[j] * (log_p[j] - log_q[ids[j]]) for j in range(len(p)) if p[j] > 0)
+        far = lambda e: np.maximum(1.0, 0.53 + 0.0165 * np.minimum(e / math.log(2), 1e4))  # noqa: E731
+        grad, scale = q.copy(), q * far(y.max() - y)
+        total = np.zeros(len(row))
+        np.add.at(total, ids, p)
+        grad -= total
+        scale += total
+        if q.max() > 0.5 and not out[q.argmax()]:  # one token holds the row: its complement counts
+            v = int(q.argmax())
+            others = math.exp(log_sum_exp(np.delete(y, v)) - log_sum_exp(y))  # 1 - q
+            less = 1 - total[v] if lse is not None else math.fsum(p[ids != v])
+            grad[v], scale[v] = less - others, abs(less) + others
+        if lse is not None:
+            p_rest = max(0.0, 1 - math.fsum(p))
+            log_rest = log_sum_exp(y[out])
+            if p_rest > 0:
+                loss += p_rest * (math.log(p_rest) - (log_rest - log_sum_exp(y)))
+            if p_rest > 0 and log_rest > -np.inf:
+                e = np.exp(y[out] - log_rest)
+                grad[out] -= p_rest * e
+                scale[out] += p_rest * e * far(y[out].max() - y[out])
+    return loss, grad / t, (scale + 2.0 ** (17 - 126)) / t, max(1.0, p.sum())
+
+
+def half_step(x, dtype):
+    f = torch.finfo(dtype)
+    return np.maximum(np.abs(x) * f.eps / 2, f.tiny * f.eps / 2)
+
+
+def on_gpu(z):
+    wide = torch.full((z.shape[0], z.stride(0)), float("nan"), dtype=z.dtype, device="cuda")
+    d = wide[:, :z.shape[1]]
+    d.copy_(z)
+    return d
+
+
+def check(dlm, z, ids, top, lse, t=1.0):
+    d, cuda = on_gpu(z), lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    status = dlm.new_status()
+    kw = dict(teacher_lse=cuda(lse), temperature=t, status=status)
+    out = dlm.distill_loss(d, cuda(ids), cuda(top), **kw)
+    g1 = dlm.distill_grad(d, cuda(ids), cuda(top), out.state, temperature=t, status=status)
+    loss2, g2 = dlm.distill_step(d, cuda(ids), cuda(top), **kw)
+    assert int(status.item()) == 0
+    zz = ref.host(z)
+    for r in range(len(zz)):
+        want, grad, scale, mass = definition(zz[r], ids[r], top[r].astype(np.float64), t, None if lse is None else float(lse[r]))
+        for name, got in (("loss", float(out.loss[r])), ("step", float(loss2[r]))):
+            if math.isinf(want):
+                assert got == want, (name, r, got, want)
+            else:
+                assert abs(got - want) <= 2.0 ** -17 * mass + 2.0 ** -21 * (1 + abs(want)), (name, r, got, want)
+        for name, g in (("grad", g1), ("step", g2)):
+            x = ref.host(g[r])
+            bad = ~(np.abs(x - grad) <= scale * 2.0 ** -17 + half_step(grad, z.dtype))
+            assert not bad.any(), (name, r, np.nonzero(bad)[0][:5], x[bad][:5], grad[bad][:5])
+
+
+def flat_teacher(n, vocab, kind, k, seed, gap, t=1.0, rest_mass=0.5, hole=0.0):
+    """Students whose listed logits lie `gap` temperatures above all others, the
+    list all over the row (one entry of a cluster's each slice at a height of its
+    own), against a teacher that gives the others `rest_mass`."""
+    g = np.random.default_rng(seed)
+    z = ref.rows(n, vocab, kind, seed, sigma=0.5, boosted=0.0)
+    ids = np.stack([np.linspace(0, vocab - 1, k).astype(np.int32) for _ in range(n)])
+    host = ref.host(z)
+    for r in range(n):
+        host[r] = host[r] * t
+        host[r, ids[r]] += gap * t * np.where(np.arange(k) % 3 == 1, 0.9, 1.0)
+        if hole:
+            gone = g.random(vocab) < hole
+            gone[ids[r]] = False
+            host[r, gone] = -np.inf
+    z.copy_(torch.from_numpy(host.astype(np.float32)).to(z.dtype))
+    top = g.normal(0, t, (n, k)).astype(np.float32)
+    a = top.astype(np.float64) / t
+    lse = np.array([log_sum_exp(x) - math.log1p(-rest_mass) for x in a], np.float32)
+    return z, ids, top, lse
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("gap", [20, 30, 40, 60])
+@pytest.mark.parametrize("n,vocab,k", [(3, 3000, 12), (2, 40001, 64), (1, 126464, 200)])
+def test_list_far_above_the_rest(dlm, kind, gap, n, vocab, k):
+    check(dlm, *flat_teacher(n, vocab, kind, k, gap, gap))
+
+
+@pytest.mark.parametrize("gap", [30, 60])
+@pytest.mark.parametrize("kind,vocab", [("f32", 500001), ("bf16", 1000003)])
+def test_list_far_above_the_rest_of_a_long_row(dlm, kind, vocab, gap):
+    check(dlm, *flat_teacher(1, vocab, kind, 40, gap, gap))
+
+
+def test_repeats_far_above_the_rest(dlm):
+    z, ids, top, lse = flat_teacher(3, 5000, "f32", 20, 3, 45)
+    ids[:, 3] = ids[:, 4]
+    check(dlm, z, ids, top, lse)

@@ -51,3 +51,33 @@ def test_weights_against_long_double(tmp_path, flags):
                     "-o", str(exe), str(src)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+LOG_PROGRAM = r'''
+#include "weight.cuh"
+#include <cstdio>
+#include <cstdlib>
+using namespace dlm;
+int main() {
+    srand48(3);
+    long double worst = 0;
+    auto look = [&](float x) { worst = fmaxl(worst, fabsl((long double)log_exact(x) - logl((long double)x))); };
+    for (int e = -126; e <= 127; ++e)
+        for (int i = 0; i < 2000; ++i) look(ldexpf(1.0f + (float)drand48() * (1.0f - 0x1p-23f), e));
+    for (int e = -126; e <= 127; ++e) look(ldexpf(1.0f, e)), look(ldexpf(1.0f + 0x1p-23f, e)), look(ldexpf(2.0f - 0x1p-23f, e));
+    printf("worst %.3Lg\n", worst);
+    return worst > 0x1p-36L || log_exact(1.0f) != 0.0;
+}
+'''
+
+
+@pytest.mark.parametrize("flags", [[], ["-ffp-contract=off"]])
+def test_logarithm_against_long_double(tmp_path, flags):
+    # the row's sums and their quotients: any normal float
+    src = tmp_path / "l.cpp"
+    src.write_text(LOG_PROGRAM)
+    exe = tmp_path / "l"
+    subprocess.run(["g++", "-O1", "-std=c++17", *flags, "-I", os.path.join(ROOT, "diffusion_decoding_token_gb300", "csrc"),
+                    "-o", str(exe), str(src)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
