@@ -8,8 +8,8 @@
 //   dl/ds_v = w / T (q_v - p_v)                  v listed (p_v: all its entries)
 //   dl/ds_v = w / T q_v (1 - p_rest / q_rest)    otherwise (p_rest = 0: w / T q_v)
 //
-// Everything the gradient needs of a row is its maximum, 1 / sum, the factor
-// of the tokens that are not listed, and the list: `state` holds it between
+// Everything the gradient needs of a row is its maximum, 1 / sum, reference and
+// factor of the tokens that are not listed, and the list: `state` holds it between
 // the two calls.
 //
 // All three are bound by HBM: the loss by one read of the row, the gradient by a
@@ -53,16 +53,15 @@ constexpr int kWarps = kRowWarps;
 constexpr int kUnroll = 4;
 constexpr float kRebase = 12.0f;  // powers of 2 of headroom before a thread's reference moves
 
-// A slice's softmax sums relative to `ref`; `mx` is the exact maximum (NaN if
-// the slice holds one), `rest` the sum over the tokens that are not listed.
-struct Sums {
-    float mx, ref, all, rest;
-};
-// What a warp or a CTA knows of a row: its sums, and whether an id of its slice
-// may be listed twice.
-struct Share {
-    Sums q;
-    int twice;
+// What a thread, a warp or a CTA knows of a row: the softmax sums of its slice over
+// the listed tokens, relative to the largest of them `ref` (-inf: none), and over
+// the others, relative to `rest_ref` (NaN where there is one).  Two references,
+// since a student's list may lie far above the rest: with one, the rest's weights
+// were subnormal or 0 from 83 nats on, and the quotients that p_rest is multiplied
+// by overflowed.  The sign of `listed` says whether an id may be listed twice.
+// (16 bytes: one store into another CTA, one load.)
+struct __align__(16) Share {
+    float ref, listed, rest_ref, rest;
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -71,20 +70,35 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// The sum over the lanes in a fixed order, all lanes get it: a common reference
-// first, then plain sums.
-__device__ __forceinline__ Share warp_share(Share a, float c) {
-    const float ref = warp_max_nan(a.q.ref);
-    a.q.mx = warp_max_nan(a.q.mx);
-    const float up = ex2((a.q.ref - ref) * c);
-    a.q.all = warp_sum(a.q.all * up);
-    a.q.rest = warp_sum(a.q.rest * up);
-    a.q.ref = ref;
-    a.twice = __any_sync(DLM_FULL_MASK, a.twice);
-    return a;
+__device__ __forceinline__ float or_zero(float ref) { return ref > -INFINITY ? ref : 0.f; }
+__device__ __forceinline__ bool is_twice(float listed) { return __float_as_uint(listed) >> 31; }
+
+// A sum that is relative to `ref` relative to `to` (-inf: nothing, and 0).
+__device__ __forceinline__ float rebased(float sum, float ref, float to, float c) {
+    return sum * ex2((ref - or_zero(to)) * c);
 }
 
-__device__ __forceinline__ Share no_share() { return Share{Sums{-INFINITY, -FLT_MAX, 0.f, 0.f}, 0}; }
+// The sum over the lanes in a fixed order, all lanes get it: common references
+// first, then plain sums.
+__device__ __forceinline__ Share warp_share(Share a, float c) {
+    Share b;
+    b.ref = warp_max_nan(a.ref);
+    b.rest_ref = warp_max_nan(a.rest_ref);
+    const bool twice = __any_sync(DLM_FULL_MASK, is_twice(a.listed));
+    b.listed = warp_sum(rebased(fabsf(a.listed), a.ref, b.ref, c));
+    b.rest = warp_sum(rebased(a.rest, a.rest_ref, b.rest_ref, c));
+    if (twice) b.listed = -b.listed;
+    return b;
+}
+
+__device__ __forceinline__ Share no_share() { return Share{-INFINITY, 0.f, -INFINITY, 0.f}; }
+
+// What is known of a whole row: its maximum, all sums relative to that, and the
+// others' sum relative to its own reference, whose weight relative to the maximum
+// is `up`.
+struct Total {
+    float mx, all, rest_ref, rest, up;
+};
 
 struct Shared {
     Share part[8 * kWarps];   // every warp's of every CTA of the cluster
@@ -93,6 +107,8 @@ struct Shared {
     int flags[kWarps];        // kAny, kBad
     float sum[kWarps];
     uint64_t listed[kWarps];
+    Total row;                // row kernel: kept for the loss, which comes last
+    float weight, lse_t;
 };
 enum : int { kAny = 1, kBad = 2 };  // an entry; a teacher logit is NaN or +inf
 
@@ -288,12 +304,11 @@ __device__ __forceinline__ float class_term(float p, float x, float q) {
 // `threads` is 32 then, and only warp 0 calls.  Thread 0 has the result.
 constexpr int kAlone = 128;
 
-__device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const Teacher& tch, const Share& row,
-                          bool rest, float lse_t, int threads) {
-    Sums q = row.q;
+__device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const Teacher& tch, Total q,
+                          bool rest, float lse_t, bool twice, int threads) {
     const int t = threadIdx.x;
     const WeightScale ws{q.mx, a.scale, a.scale_lo, kPow2Neg};
-    if (!row.twice) {
+    if (!twice) {
         uint64_t listed = 0;
         for (int j = t; j < a.k; j += threads)
             if (l.id[j] >= 0) listed += weight44(l.s[j], ws);
@@ -305,17 +320,20 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) listed += sh.listed[w];
         }
-        q.all = (float)listed * kUnit + q.rest;
+        q.all = (float)listed * kUnit + q.rest * q.up;
     }
     const double log_all = log_exact(q.all), lse_s = (double)q.mx * a.inv_t + log_all;
     const double log_z = rest ? (double)lse_t
                               : (double)list_max(sh) * a.inv_t + log_exact(fmaxf((float)tch.sum * kUnit, 1.f));
     const double shift = lse_s - log_z;
     // ln p_rest - ln q_rest, from three logarithms: a quotient of the sums has no limit
-    const float q_rest = q.rest / q.all;
+    const float q_rest = q.rest * q.up / q.all;
     double x_rest = 0;
-    if (tch.p_rest > 0.f) x_rest = q.rest > 0.f ? log_exact(tch.p_rest) + log_all - log_exact(q.rest) : (double)INFINITY;
-    if (row.twice) {
+    if (tch.p_rest > 0.f)
+        x_rest = q.rest > 0.f ? log_exact(tch.p_rest) + log_all - log_exact(q.rest) +
+                                    ((double)q.mx - (double)q.rest_ref) * a.inv_t
+                              : (double)INFINITY;
+    if (twice) {
         double v = 0;
         for (int j = t; j < a.k; j += threads)
             if (l.id[j] >= 0 && l.p[j] > 0.f)
@@ -352,38 +370,49 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
     return v + class_term(tch.p_rest, (float)x_rest, q_rest) + (tch.sum > one ? (float)(tch.sum - one) * kUnit : 0.f);
 }
 
-__device__ __forceinline__ void write_state(float* state, float m, float inv, float tail, float lse_t, bool rest) {
+__device__ __forceinline__ void write_state(float* state, float m, float inv, float base, float tail, float lse_t,
+                                            bool rest) {
     if (!state) return;
     state[0] = m;
     state[1] = inv;
     state[2] = tail;
     state[3] = lse_t;
     state[4] = rest ? 1.f : 0.f;
-    state[5] = state[6] = state[7] = 0.f;
+    state[5] = base;
+    state[6] = state[7] = 0.f;
 }
 
-// What the gradient needs of a row: 1 / sum (0: no gradient) and the factor of
-// the tokens that are not listed.  q is relative to the row's maximum.
-__device__ __forceinline__ bool row_factors(const Teacher& tch, const Sums& q, bool rest, float& inv, float& tail) {
-    const bool fine = q.mx > -INFINITY && q.mx < INFINITY && !tch.bad;
+// What the gradient needs of a row: 1 / sum (0: no gradient), and of the tokens
+// that are not listed a reference and the factor of their weights relative to it,
+// q_v - p_v = tail 2^((z - base) c).
+__device__ __forceinline__ bool row_fine(const Teacher& tch, const Total& q) {
+    return q.mx > -INFINITY && q.mx < INFINITY && !tch.bad;
+}
+__device__ __forceinline__ void row_factors(const Teacher& tch, const Total& q, bool rest, float& inv, float& base,
+                                            float& tail) {
     inv = rest || tch.any ? 1.f / q.all : 0.f;
-    tail = rest ? (q.rest > 0.f ? 1.f - tch.p_rest * (q.all / q.rest) : 0.f) : 1.f;
-    if (!fine) inv = tail = NAN;
-    return fine;
+    base = q.mx;
+    tail = inv;
+    if (rest) {
+        tail = 0.f;
+        if (q.rest > 0.f) {
+            base = q.rest_ref;
+            tail = inv * q.up - tch.p_rest / q.rest;
+        }
+    }
+    if (!row_fine(tch, q)) inv = tail = NAN;
 }
 
-// The loss and the state of a row (the first CTA).
+// The loss of a row (the first CTA).
 __device__ __forceinline__ void finish_loss(const DistillArgs& a, const List& l, Shared& sh, const Teacher& tch, int64_t r,
-                                            float weight, const Share& row, bool rest, float lse_t, bool fine, float inv,
-                                            float tail) {
-    const bool alone = a.k <= kAlone;
+                                            float weight, const Total& row, bool rest, float lse_t, bool twice) {
+    const bool alone = a.k <= kAlone, fine = row_fine(tch, row);
     if (alone && threadIdx.x >= 32) return;
     float v = NAN;
-    if (fine) v = rest || tch.any ? weight * row_loss(a, l, sh, tch, row, rest, lse_t, alone ? 32 : kThreads) : 0.f;
+    if (fine) v = rest || tch.any ? weight * row_loss(a, l, sh, tch, row, rest, lse_t, twice, alone ? 32 : kThreads) : 0.f;
     if (threadIdx.x != 0) return;
     a.loss[r] = v;
     if (!fine) raise_status(a.dev_status, DLM_DEV_NONFINITE);
-    write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, row.q.mx, inv, tail, lse_t, rest);
 }
 
 // 2^((z - ref) c) with c in two floats (one float's rounding, the same for every
@@ -400,12 +429,11 @@ __device__ __forceinline__ f2 weights_of(f2 z, f2 ref, f2 c, f2 c_lo) {
 // first 16 to 128 KB asked into L2 before the list is read changed nothing); a thread adds those
 // that it looks after at the end.
 template <int DT>
-__device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c, float c_lo, const uint32_t* bits,
+__device__ Share stream_sums(const char* row, int64_t V, int v0, int v1, float c, float c_lo, const uint32_t* bits,
                             const Mine& mine) {
     constexpr int EPV = Row<DT>::EPV;
-    Sums a;
-    a.mx = -INFINITY;
-    a.ref = -FLT_MAX;
+    Share a = no_share();
+    float top = -INFINITY, ref = -FLT_MAX;
     f2 rest = pack2(0.f, 0.f);
     const f2 c2 = pack2(c, c), lo2 = pack2(c_lo, c_lo);
     const int whole = (int)min((int64_t)v1, V / EPV);
@@ -423,13 +451,13 @@ __device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c,
             if (in[u]) w[u] = without<DT>(w[u], in[u]);
             m = max_nan(m, Row<DT>::vmax(w[u]));
         }
-        a.mx = max_nan(a.mx, m);
-        if ((m - a.ref) * c > kRebase) {
-            const float e = ex2((a.ref - m) * c);
+        top = max_nan(top, m);
+        if ((m - ref) * c > kRebase) {
+            const float e = ex2((ref - m) * c);
             rest = mul2(rest, pack2(e, e));
-            a.ref = m;
+            ref = m;
         }
-        const f2 r2 = pack2(a.ref, a.ref);
+        const f2 r2 = pack2(ref, ref);
         f2 sum[N];
 #pragma unroll
         for (int u = 0; u < N; ++u) {
@@ -464,31 +492,22 @@ __device__ Sums stream_sums(const char* row, int64_t V, int v0, int v1, float c,
         const int at[1] = {v};
         add(w, at);
     }
-    a.rest = hsum2(rest);
-    float listed = 0.f;
+    a.rest_ref = top;
+    a.rest = rebased(hsum2(rest), ref, top, c);
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        if (!((mine.own >> i) & 1u)) continue;
-        const float z = mine.s[i];
-        a.mx = max_nan(a.mx, z);
-        if ((z - a.ref) * c > kRebase) {
-            const float e = ex2((a.ref - z) * c);
-            listed *= e;
-            a.rest *= e;
-            a.ref = z;
-        }
-        listed += ex2((z - a.ref) * c);
-    }
-    a.all = listed + a.rest;
+    for (int i = 0; i < kMine; ++i)
+        if ((mine.own >> i) & 1u) a.ref = max_nan(a.ref, mine.s[i]);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        if ((mine.own >> i) & 1u) a.listed += ex2((mine.s[i] - or_zero(a.ref)) * c);
     return a;
 }
 
-// The row's sums over all the CTAs of its cluster, relative to its maximum, in
-// every thread.  Each warp leaves its share in every CTA (a remote store needs
+// The row's sums over all the CTAs of its cluster, in every thread.  Each warp leaves its share in every CTA (a remote store needs
 // no answer), one barrier later each warp adds up all of them for itself, and
 // nothing remote is read, so no CTA has to outlive another.  started()
 // comes before: no share is sent to a CTA that does not run yet.
-__device__ __forceinline__ Share merge_row(const Cluster& cl, Shared& sh, Share a, float c) {
+__device__ __forceinline__ Total merge_row(const Cluster& cl, Shared& sh, Share a, float c, bool& twice) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     a = warp_share(a, c);
     if (cl.split > 1) {
@@ -502,18 +521,22 @@ __device__ __forceinline__ Share merge_row(const Cluster& cl, Shared& sh, Share 
     a = lane < n ? sh.part[lane] : no_share();
     for (int i = lane + 32; i < n; i += 32) {
         const Share b = sh.part[i];
-        const float ref = fmaxf(a.q.ref, b.q.ref), ea = ex2((a.q.ref - ref) * c), eb = ex2((b.q.ref - ref) * c);
-        a.q.all = a.q.all * ea + b.q.all * eb;
-        a.q.rest = a.q.rest * ea + b.q.rest * eb;
-        a.q.ref = ref;
-        a.q.mx = max_nan(a.q.mx, b.q.mx);
-        a.twice |= b.twice;
+        const float ref = max_nan(a.ref, b.ref), rest_ref = max_nan(a.rest_ref, b.rest_ref);
+        const float listed = rebased(fabsf(a.listed), a.ref, ref, c) + rebased(fabsf(b.listed), b.ref, ref, c);
+        a.listed = is_twice(a.listed) || is_twice(b.listed) ? -listed : listed;
+        a.rest = rebased(a.rest, a.rest_ref, rest_ref, c) + rebased(b.rest, b.rest_ref, rest_ref, c);
+        a.ref = ref;
+        a.rest_ref = rest_ref;
     }
     a = warp_share(a, c);
-    const float up = ex2((a.q.ref - a.q.mx) * c);
-    a.q.all *= up;
-    a.q.rest *= up;
-    return a;
+    Total q;
+    q.mx = max_nan(a.ref, a.rest_ref);
+    q.rest_ref = a.rest_ref;
+    q.rest = a.rest;
+    q.up = ex2((a.rest_ref - or_zero(q.mx)) * c);
+    q.all = rebased(fabsf(a.listed), a.ref, q.mx, c) + q.rest * q.up;
+    twice = is_twice(a.listed);
+    return q;
 }
 // The cluster's CTAs run: every thread says so first and, before it stores into
 // another CTA, waits for the others.
@@ -621,7 +644,7 @@ __device__ __forceinline__ void write_listed(const List& l, int K, char* out, in
 template <int DT>
 struct Slice {
     int v0, v1;       // vectors of this CTA
-    int64_t e0, e1;   // its tokens
+    int e0, e1;       // its tokens
     __device__ Slice(int64_t V, const Cluster& cl) {
         constexpr int EPV = Row<DT>::EPV;
         const int nv = (int)((V + EPV - 1) / EPV);
@@ -630,8 +653,8 @@ struct Slice {
         const int per = ((nv + cl.split - 1) / cl.split + unit - 1) / unit * unit;
         v0 = min(nv, cl.rank * per);
         v1 = min(nv, v0 + per);
-        e0 = (int64_t)v0 * EPV;
-        e1 = min(V, (int64_t)v1 * EPV);
+        e0 = v0 * EPV;
+        e1 = min((int)V, v1 * EPV);
     }
 };
 
@@ -659,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
     if (weight == 0.f) {  // the row has no loss: it is not read
         if (cl.rank == 0 && t == 0) {
             a.loss[r] = 0.f;
-            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, 0.f, 0.f, 0.f, 0.f, false);
+            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, 0.f, 0.f, 0.f, 0.f, 0.f, false);
         }
         if (GRAD) stream_grad<DT>(row, out, V, sl.v0, sl.v1, 0.f, c, 0.f);
         return;
@@ -676,9 +699,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
         mine.s[i] = (mine.in >> i) & 1u ? Row<DT>::scalar(row, l.id[t + i * kThreads]) : 0.f;
     list_weigh(a, l, sh, REST, lse_t);
     __syncthreads();
-    Share share;
-    share.q = stream_sums<DT>(row, V, sl.v0, sl.v1, c, a.scale_lo, l.bits, mine);
-    share.twice = mine.in != mine.own;
+    Share share = stream_sums<DT>(row, V, sl.v0, sl.v1, c, a.scale_lo, l.bits, mine);
+    if (mine.in != mine.own) share.listed = -share.listed;
     all_started(cl);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
@@ -687,16 +709,21 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
         l.s[j] = mine.s[i];
         if (cl.rank != 0) cl.at(l.s, 0)[j] = mine.s[i];
     }
-    const Share all = merge_row(cl, sh, share, c);
+    bool twice;
+    const Total all = merge_row(cl, sh, share, c, twice);
     const Teacher tch = list_total(sh, REST);
-    float inv, tail;
-    const bool fine = row_factors(tch, all.q, REST, inv, tail);
-    if (cl.rank == 0) finish_loss(a, l, sh, tch, r, weight, all, REST, lse_t, fine, inv, tail);
+    float inv, base, tail;
+    row_factors(tch, all, REST, inv, base, tail);
+    if (cl.rank == 0) {
+        if (t == 0)
+            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, all.mx, inv, base, tail, lse_t, REST);
+        finish_loss(a, l, sh, tch, r, weight, all, REST, lse_t, twice);
+    }
     if (GRAD) {
         const float g = weight * (float)a.inv_t;
-        stream_grad<DT>(row, out, V, sl.v0, sl.v1, all.q.mx, c, g * inv * tail);
+        stream_grad<DT>(row, out, V, sl.v0, sl.v1, base, c, g * tail);
         __syncthreads();
-        if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, all.q.mx, c, inv, tch.inv, true, g);
+        if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, all.mx, c, inv, tch.inv, true, g);
     }
 }
 
@@ -717,7 +744,7 @@ __global__ void __launch_bounds__(kThreads) distill_stream_grad_kernel(const Dis
     const float g = (a.weights ? a.weights[r] : 1.f) * (a.grad_loss ? a.grad_loss[r] : 1.f) * (float)a.inv_t;
     const float c = a.scale;
     const float* state = a.state + r * DLM_DISTILL_STATE;
-    const float m = state[0], inv = state[1], tail = state[2];
+    const float m = state[0], inv = state[1], tail = state[2], base = state[5];
     const bool rest = state[4] != 0.f;
     if (g == 0.f || inv == 0.f) {
         stream_grad<DT>(row, out, V, sl.v0, sl.v1, m, c, 0.f);
@@ -732,7 +759,7 @@ __global__ void __launch_bounds__(kThreads) distill_stream_grad_kernel(const Dis
     }
     __syncthreads();
     const Teacher tch = list_total(sh, rest);
-    stream_grad<DT>(row, out, V, sl.v0, sl.v1, m, c, g * inv * tail);
+    stream_grad<DT>(row, out, V, sl.v0, sl.v1, base, c, g * tail);
     __syncthreads();
     write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, true, g);
 }
@@ -783,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     const int id0 = t < K ? a.ids[r * K + t] : -1;
     const float x0 = t < K ? teacher_at(a, r * K + t) : 0.f;
     const float weight = a.weights ? a.weights[r] : 1.f;
-    float g = weight * (float)a.inv_t, m = 0.f, inv = 0.f, tail = 0.f, lse_t = 0.f;
+    float g = weight * (float)a.inv_t, m = 0.f, inv = 0.f, base = 0.f, tail = 0.f, lse_t = 0.f;
     bool rest = REST;
     if (SUMS) {
         if (REST) lse_t = a.teacher_lse[r];
@@ -794,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
         tail = state[2];
         lse_t = state[3];
         rest = state[4] != 0.f;
+        base = state[5];
         if (a.grad_loss) g *= a.grad_loss[r];
     }
     if (SUMS ? weight == 0.f : (g == 0.f || inv == 0.f)) {  // no gradient: the row is not read
@@ -811,8 +839,6 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     list_weigh(a, l, sh, rest, lse_t);
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    Share row_share = no_share();
-    bool ok = true;
     // the listed tokens leave the slice; one entry of each has its logit
     bool twice = false;
     float top = -INFINITY;
@@ -828,11 +854,9 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
     }
     if (SUMS) {
         __syncthreads();
-        for (int v = t; v < n; v += kThreads) top = max_nan(top, Row<DT>::vmax(data[v]));
-        const float ref = top > -INFINITY ? top : 0.f;  // nothing but -inf: weights of 0
-        Share mine = no_share();
-        mine.q.mx = top;
-        mine.q.ref = top > -INFINITY ? top : -FLT_MAX;
+        float high = -INFINITY;
+        for (int v = t; v < n; v += kThreads) high = max_nan(high, Row<DT>::vmax(data[v]));
+        const float ref = or_zero(high);  // nothing but -inf: weights of 0
         const f2 r2 = pack2(ref, ref), c2 = pack2(c, c), lo2 = pack2(a.scale_lo, a.scale_lo);
         f2 others = pack2(0.f, 0.f);
         for (int v = t; v < n; v += kThreads) {
@@ -847,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
                 for (int p = 0; p < h; ++p) e[p] = add2(e[p], e[p + h]);
             others = add2(others, e[0]);
         }
-        mine.q.rest = hsum2(others);
+        const float rest_sum = hsum2(others);
         // the listed tokens' weights; their logits to the first CTA
         float own = 0.f;
         all_started(cl);
@@ -856,38 +880,38 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             if (id < sl.e0 || id >= sl.e1) continue;
             float s = l.s[j];
             if (l.own[j]) {
-                own += ex2((s - ref) * c);
+                own += ex2((s - or_zero(top)) * c);
             } else {  // another entry has this token's logit, or it is -inf
                 for (int i = 0; i < K; ++i)
                     if (l.id[i] == id && l.own[i]) s = l.s[i];
             }
             if (cl.rank != 0 || !l.own[j]) cl.at(l.s, 0)[j] = s;
         }
-        mine.q.all = own + mine.q.rest;
-        mine.twice = twice;
-        const Share all = merge_row(cl, sh, mine, c);
-        const Teacher tch = list_total(sh, REST);
-        const bool fine = row_factors(tch, all.q, REST, inv, tail);
-        m = all.q.mx;
-        row_share = all;
-        ok = fine;
+        const Total all = merge_row(cl, sh, Share{top, twice ? -own : own, high, rest_sum}, c, twice);
+        row_factors(list_total(sh, REST), all, REST, inv, base, tail);
+        m = all.mx;
+        if (t == 0) {
+            sh.row = all;
+            sh.weight = weight;
+            sh.lse_t = lse_t;
+        }
     } else {
-        row_share.twice = __syncthreads_or(twice);
+        twice = __syncthreads_or(twice);
     }
     const Teacher tch = list_total(sh, rest);
-    const float scale = g * inv * tail;
+    const float scale = g * tail;
     uint4* dst = reinterpret_cast<uint4*>(out) + sl.v0;
-    const Slope slope(m, c, scale);
+    const Slope slope(base, c, scale);
 #pragma unroll 2
     for (int v = t; v < whole; v += kThreads) st_row(dst + v, slope_of<DT>(data[v], slope));
     if (whole < n) {  // the row's last, cut vector
         for (int64_t i = (int64_t)(sl.v0 + whole) * EPV + t; i < V; i += kThreads)
-            store_elem<DT>(out, i, scale * ex2((Row<DT>::scalar(data, i - sl.e0) - m) * c));
+            store_elem<DT>(out, i, scale * ex2((Row<DT>::scalar(data, i - sl.e0) - base) * c));
     }
     __syncthreads();
-    if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, row_share.twice, g);
+    if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, twice, g);
     // (last: the gradient does not wait for it)
-    if (SUMS && cl.rank == 0) finish_loss(a, l, sh, tch, r, weight, row_share, REST, lse_t, ok, inv, tail);
+    if (SUMS && cl.rank == 0) finish_loss(a, l, sh, list_total(sh, REST), r, sh.weight, sh.row, REST, sh.lse_t, twice);
 }
 
 // Shared memory of a CTA that streams: the list, and with `bits` the bitmap of

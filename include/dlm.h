@@ -756,13 +756,15 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  * ids[r][j]: softmax(teacher[r] / T) over the row's entries, or with
  * teacher_lse  p_j = exp(teacher[r][j] / T - teacher_lse[r]) and the rest of
  * the mass p_rest = max(0, 1 - sum_j p_j) as one more class, q_rest being the
- * student's mass outside the list (a weight below 2^-126 of the row's largest
- * counts as 0):
+ * student's mass outside the list.  Listed and other tokens are summed apart, each
+ * relative to their own largest weight, so q_rest may be far below the range of a
+ * float (a weight below 2^-126 of its sum's largest counts as 0):
  *   loss[r] = weights[r] * ( sum_j p_j (ln p_j - ln q_{ids_j})
  *                            [ + p_rest (ln p_rest - ln q_rest) ] )
  *   d loss[r] / d s_v = weights[r] / T * ( q_v - p_v )                  v listed
  *                     = weights[r] / T * q_v (1 - p_rest / q_rest)      otherwise
- * (p_rest = 0 without teacher_lse).  Multiply by T^2 through weights where a
+ * (p_rest = 0 without teacher_lse; p_rest > 0 without a finite logit outside the
+ * list: loss +inf, and those tokens' gradient 0).  Multiply by T^2 through weights where a
  * mix with another loss asks for it.
  *
  * A row's sum of exponentials is held in 32 bits (within 2^-18 of itself, 2^-21

@@ -62,7 +62,8 @@ def definition(row, ids, teacher, t, lse):
             if p_rest > 0:
                 loss += p_rest * (math.log(p_rest) - (log_rest - log_sum_exp(y)))
             if p_rest > 0 and log_rest > -np.inf:
-                e = np.exp(y[out] - log_rest)
+                e = np.exp(y[out] - y[out].max())  # (the logarithm itself has no digits left at -3e38)
+                e /= e.sum()
                 grad[out] -= p_rest * e
                 scale[out] += p_rest * e * far(y[out].max() - y[out])
     return loss, grad / t, (scale + 2.0 ** (17 - 126)) / t, max(1.0, p.sum())
@@ -80,22 +81,24 @@ def on_gpu(z):
     return d
 
 
-def check(dlm, z, ids, top, lse, t=1.0):
+def check(dlm, z, ids, top, lse, t=1.0, w=1.0):
     d, cuda = on_gpu(z), lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
     status = dlm.new_status()
-    kw = dict(teacher_lse=cuda(lse), temperature=t, status=status)
+    weights = torch.full((len(z),), w, device="cuda")
+    kw = dict(teacher_lse=cuda(lse), temperature=t, weights=weights, status=status)
     out = dlm.distill_loss(d, cuda(ids), cuda(top), **kw)
-    g1 = dlm.distill_grad(d, cuda(ids), cuda(top), out.state, temperature=t, status=status)
+    g1 = dlm.distill_grad(d, cuda(ids), cuda(top), out.state, temperature=t, weights=weights, status=status)
     loss2, g2 = dlm.distill_step(d, cuda(ids), cuda(top), **kw)
     assert int(status.item()) == 0
     zz = ref.host(z)
     for r in range(len(zz)):
         want, grad, scale, mass = definition(zz[r], ids[r], top[r].astype(np.float64), t, None if lse is None else float(lse[r]))
+        want, grad, scale = w * want, w * grad, w * scale
         for name, got in (("loss", float(out.loss[r])), ("step", float(loss2[r]))):
             if math.isinf(want):
                 assert got == want, (name, r, got, want)
             else:
-                assert abs(got - want) <= 2.0 ** -17 * mass + 2.0 ** -21 * (1 + abs(want)), (name, r, got, want)
+                assert abs(got - want) <= 2.0 ** -17 * w * mass + 2.0 ** -21 * (w + abs(want)), (name, r, got, want)
         for name, g in (("grad", g1), ("step", g2)):
             x = ref.host(g[r])
             bad = ~(np.abs(x - grad) <= scale * 2.0 ** -17 + half_step(grad, z.dtype))
@@ -140,4 +143,48 @@ def test_list_far_above_the_rest_of_a_long_row(dlm, kind, vocab, gap):
 def test_repeats_far_above_the_rest(dlm):
     z, ids, top, lse = flat_teacher(3, 5000, "f32", 20, 3, 45)
     ids[:, 3] = ids[:, 4]
+    check(dlm, z, ids, top, lse)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("gap,t", [(83, 1.0), (86, 1.0), (88, 0.125), (100, 1.0), (1000, 0.25), (40000, 0.01)])
+@pytest.mark.parametrize("n,vocab,k", [(3, 3000, 12), (1, 126464, 64)])
+def test_rest_below_the_range_of_a_float(dlm, kind, gap, t, n, vocab, k):
+    # the unlisted tokens' weights relative to the row's largest are subnormal, or
+    # 0 in 32 bits; a third of these tokens is masked
+    check(dlm, *flat_teacher(n, vocab, kind, k, 7, gap, t, hole=0.3), t=t)
+
+
+@pytest.mark.parametrize("kind,vocab", [("f32", 500001), ("bf16", 1000003)])
+@pytest.mark.parametrize("gap", [86, 100])
+def test_rest_below_the_range_of_a_float_in_a_long_row(dlm, kind, vocab, gap):
+    check(dlm, *flat_teacher(1, vocab, kind, 40, 9, gap, hole=0.3))
+
+
+@pytest.mark.parametrize("w", [1e30, 1e-30])
+def test_large_and_small_weights(dlm, w):
+    z, ids, top, lse = flat_teacher(2, 3000, "f32", 12, 11, 80, 1e-3, hole=0.3)
+    check(dlm, z, ids, top, lse, t=1e-3, w=float(np.float32(w)))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_rest_at_the_lowest_value(dlm, kind):
+    # every unlisted token is masked with the type's lowest value: the rest's
+    # probability is e^-3e38, its tokens share its gradient
+    z, ids, top, lse = flat_teacher(3, 3000, kind, 12, 13, 20)
+    keep = z.clone()
+    z[:] = torch.finfo(z.dtype).min
+    for r in range(3):
+        z[r, torch.from_numpy(ids[r]).long()] = keep[r, torch.from_numpy(ids[r]).long()]
+    z[2, ids[2, 1:].tolist()] = torch.finfo(z.dtype).min  # and of the list all but one
+    check(dlm, z, ids, top, lse)
+
+
+def test_no_rest_at_all(dlm):
+    # q_rest = 0 while the teacher has a rest: the loss is infinite, the listed
+    # tokens' gradient is what it is
+    z, ids, top, lse = flat_teacher(2, 3000, "f32", 12, 15, 20)
+    keep = z.clone()
+    z[0] = -float("inf")
+    z[0, torch.from_numpy(ids[0]).long()] = keep[0, torch.from_numpy(ids[0]).long()]
     check(dlm, z, ids, top, lse)
