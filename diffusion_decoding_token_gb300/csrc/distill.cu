@@ -58,7 +58,10 @@ constexpr float kRebase = 12.0f;  // powers of 2 of headroom before a thread's r
 // the others, relative to `rest_ref` (NaN where there is one).  Two references,
 // since a student's list may lie far above the rest: with one, the rest's weights
 // were subnormal or 0 from 83 nats on, and the quotients that p_rest is multiplied
-// by overflowed.  The sign of `listed` says whether an id may be listed twice.
+// by overflowed.  `listed` leaves one weight of 1, that of a token at `ref`, out: a
+// student that is sure of a token has 1 - q from the others' sum, which 1 + that
+// sum would have rounded away (and the gradient there is (1 - p) - (1 - q)).  Its
+// sign says whether an id may be listed twice.
 // (16 bytes: one store into another CTA, one load.)
 struct __align__(16) Share {
     float ref, listed, rest_ref, rest;
@@ -85,7 +88,9 @@ __device__ __forceinline__ Share warp_share(Share a, float c) {
     b.ref = warp_max_nan(a.ref);
     b.rest_ref = warp_max_nan(a.rest_ref);
     const bool twice = __any_sync(DLM_FULL_MASK, is_twice(a.listed));
-    b.listed = warp_sum(rebased(fabsf(a.listed), a.ref, b.ref, c));
+    // the first lane at the common reference leaves its 1 out for all
+    const bool first = (threadIdx.x & 31) == __ffs(__ballot_sync(DLM_FULL_MASK, a.ref == b.ref)) - 1;
+    b.listed = warp_sum(rebased(fabsf(a.listed) + (first ? 0.f : 1.f), a.ref, b.ref, c));
     b.rest = warp_sum(rebased(a.rest, a.rest_ref, b.rest_ref, c));
     if (twice) b.listed = -b.listed;
     return b;
@@ -93,11 +98,12 @@ __device__ __forceinline__ Share warp_share(Share a, float c) {
 
 __device__ __forceinline__ Share no_share() { return Share{-INFINITY, 0.f, -INFINITY, 0.f}; }
 
-// What is known of a whole row: its maximum, all sums relative to that, and the
-// others' sum relative to its own reference, whose weight relative to the maximum
-// is `up`.
+// What is known of a whole row: its maximum, the sum of all weights relative to
+// that, `away` the share of all but one listed token that is at the maximum (-1:
+// none is), and the others' sum relative to its own reference, whose weight
+// relative to the maximum is `up`.
 struct Total {
-    float mx, all, rest_ref, rest, up;
+    float mx, all, away, rest_ref, rest, up;
 };
 
 struct Shared {
@@ -186,23 +192,34 @@ __device__ __forceinline__ float list_max(const Shared& sh) {
     for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, sh.list_max[w]);
     return mx;
 }
+__device__ __forceinline__ WeightScale teacher_scale(const DistillArgs& a, const Shared& sh) {
+    return WeightScale{or_zero(list_max(sh)), a.scale, a.scale_lo, kPow2Neg};
+}
+// One entry's weight 2^-(y + lo) as an integer.
+__device__ __forceinline__ uint64_t teacher_weight(const DistillArgs& a, float x, const WeightScale& ws, bool rest,
+                                                   float lse_t, float& y, float& lo) {
+    if (!rest) {
+        y = weight_exponent(x, ws, lo);
+        return weight44_of(y, lo);
+    }
+    // a lse_t below the logits (p above 1) counts as p = 1
+    const double d = fmax(0.0, (double)lse_t - (double)x * a.inv_t), e = d * 1.4426950408889634;
+    y = (float)e;
+    lo = y < INFINITY ? (float)(e - (double)y) : 0.f;
+    // a teacher that is sure of a token: 1 - p by its series, to the last place (the
+    // table's weight is off by 2^-37 of p, 2^-20 of a 1 - p of 10^-5)
+    if (d < 0x1p-12)
+        return (1ull << kWeightBits) - (uint64_t)(d * (1.0 - d * (0.5 - d * (1.0 / 6))) * 17592186044416.0 + 0.5);
+    return weight44_of(y, lo);
+}
 __device__ __forceinline__ void list_weigh(const DistillArgs& a, const List& l, Shared& sh, bool rest, float lse_t) {
-    const float mx = list_max(sh);
-    const WeightScale ws{mx > -INFINITY ? mx : 0.f, a.scale, a.scale_lo, kPow2Neg};
+    const WeightScale ws = teacher_scale(a, sh);
     uint64_t sum = 0;
     for (int j = threadIdx.x; j < a.k; j += kThreads) {
         float p = 0.f;
         if (l.id[j] >= 0) {
             float y, lo;
-            if (rest) {
-                // a lse_t below the logits (p above 1) counts as p = 1
-                const double d = fmax(0.0, ((double)lse_t - (double)l.t[j] * a.inv_t) * 1.4426950408889634);
-                y = (float)d;
-                lo = y < INFINITY ? (float)(d - (double)y) : 0.f;
-            } else {
-                y = weight_exponent(l.t[j], ws, lo);
-            }
-            const uint64_t w = weight44_of(y, lo);
+            const uint64_t w = teacher_weight(a, l.t[j], ws, rest, lse_t, y, lo);
             sum += w;
             p = y < 16.f ? (float)w * kUnit : y < INFINITY ? exp2f(-y) * fmaf(lo, -kLn2, 1.0f) : 0.f;
         }
@@ -370,16 +387,17 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
     return v + class_term(tch.p_rest, (float)x_rest, q_rest) + (tch.sum > one ? (float)(tch.sum - one) * kUnit : 0.f);
 }
 
-__device__ __forceinline__ void write_state(float* state, float m, float inv, float base, float tail, float lse_t,
-                                            bool rest) {
+__device__ __forceinline__ void write_state(float* state, const Total& row, float inv, float base, float tail,
+                                            float lse_t, bool rest) {
     if (!state) return;
-    state[0] = m;
+    state[0] = row.mx;
     state[1] = inv;
     state[2] = tail;
     state[3] = lse_t;
     state[4] = rest ? 1.f : 0.f;
     state[5] = base;
-    state[6] = state[7] = 0.f;
+    state[6] = row.away;
+    state[7] = 0.f;
 }
 
 // What the gradient needs of a row: 1 / sum (0: no gradient), and of the tokens
@@ -494,12 +512,16 @@ __device__ Share stream_sums(const char* row, int64_t V, int v0, int v1, float c
     }
     a.rest_ref = top;
     a.rest = rebased(hsum2(rest), ref, top, c);
+    int at = kMine;
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
-        if ((mine.own >> i) & 1u) a.ref = max_nan(a.ref, mine.s[i]);
+        if ((mine.own >> i) & 1u) {
+            if (mine.s[i] > a.ref) at = i;
+            a.ref = max_nan(a.ref, mine.s[i]);
+        }
 #pragma unroll
     for (int i = 0; i < kMine; ++i)
-        if ((mine.own >> i) & 1u) a.listed += ex2((mine.s[i] - or_zero(a.ref)) * c);
+        if (((mine.own >> i) & 1u) && i != at) a.listed += ex2((mine.s[i] - or_zero(a.ref)) * c);
     return a;
 }
 
@@ -522,7 +544,8 @@ __device__ __forceinline__ Total merge_row(const Cluster& cl, Shared& sh, Share 
     for (int i = lane + 32; i < n; i += 32) {
         const Share b = sh.part[i];
         const float ref = max_nan(a.ref, b.ref), rest_ref = max_nan(a.rest_ref, b.rest_ref);
-        const float listed = rebased(fabsf(a.listed), a.ref, ref, c) + rebased(fabsf(b.listed), b.ref, ref, c);
+        const float a1 = b.ref > a.ref ? 1.f : 0.f, b1 = 1.f - a1;  // whose 1 counts now
+        const float listed = rebased(fabsf(a.listed) + a1, a.ref, ref, c) + rebased(fabsf(b.listed) + b1, b.ref, ref, c);
         a.listed = is_twice(a.listed) || is_twice(b.listed) ? -listed : listed;
         a.rest = rebased(a.rest, a.rest_ref, rest_ref, c) + rebased(b.rest, b.rest_ref, rest_ref, c);
         a.ref = ref;
@@ -534,7 +557,9 @@ __device__ __forceinline__ Total merge_row(const Cluster& cl, Shared& sh, Share 
     q.rest_ref = a.rest_ref;
     q.rest = a.rest;
     q.up = ex2((a.rest_ref - or_zero(q.mx)) * c);
-    q.all = rebased(fabsf(a.listed), a.ref, q.mx, c) + q.rest * q.up;
+    const float listed = fabsf(a.listed), rest = q.rest * q.up;
+    q.all = rebased(1.f + listed, a.ref, q.mx, c) + rest;
+    q.away = a.ref == q.mx ? (listed + rest) / q.all : -1.f;
     twice = is_twice(a.listed);
     return q;
 }
@@ -617,18 +642,37 @@ __device__ void stream_grad(const char* row, char* out, int64_t V, int v0, int v
     }
 }
 
-// The listed tokens of this CTA's slice [e0, e1): g (q_v - p_v).  An id that
-// is listed more than once (`twice`: maybe) is written by its first entry, with
-// the sum of all of them.
+// What the listed tokens' gradient needs of the row.
+struct Listed {
+    float m, inv, inv_p, away, lse_t;
+    bool twice, rest;
+};
+
+// 1 - p_v of the token that entry j lists, p_v close to 1 or not.
+__device__ __forceinline__ float teacher_away(const DistillArgs& a, const List& l, const Shared& sh, int j, const Listed& row) {
+    const WeightScale ws = teacher_scale(a, sh);
+    const int id = l.id[j];
+    const Teacher tch = list_total(sh, row.rest);
+    uint64_t w = 0;
+    float y, lo;
+    for (int i = row.twice ? 0 : j; i < (row.twice ? a.k : j + 1); ++i)
+        if (l.id[i] == id) w += teacher_weight(a, l.t[i], ws, row.rest, row.lse_t, y, lo);
+    return (float)(int64_t)((row.rest ? 1ull << kWeightBits : tch.sum) - w) * (row.rest ? kUnit : tch.inv * kUnit);
+}
+
+// The listed tokens of this CTA's slice [e0, e1): g (q_v - p_v), for a token that
+// the student is sure of g ((1 - p_v) - (1 - q_v)).  An id that is listed more than
+// once (`twice`: maybe) is written by its first entry, with the sum of all of them.
 template <int DT>
-__device__ __forceinline__ void write_listed(const List& l, int K, char* out, int64_t e0, int64_t e1, float m, float c,
-                                             float inv, float inv_p, bool twice, float g) {
+__device__ __forceinline__ void write_listed(const DistillArgs& a, const List& l, const Shared& sh, char* out, int e0,
+                                             int e1, const Listed& row, float g) {
+    const int K = a.k;
     for (int j = threadIdx.x; j < K; j += kThreads) {
         const int id = l.id[j];
         if (id < e0 || id >= e1) continue;
         float p = l.p[j], s = l.s[j];
         bool first = true;
-        if (twice) {
+        if (row.twice) {
             p = 0.f;
             for (int i = 0; i < K; ++i) {
                 if (l.id[i] != id) continue;
@@ -637,7 +681,11 @@ __device__ __forceinline__ void write_listed(const List& l, int K, char* out, in
                 s = max_nan(s, l.s[i]);  // (one of them has the logit, the others it or -inf)
             }
         }
-        if (first) store_elem<DT>(out, id, g * (inv * ex2((s - m) * c) - p * inv_p));
+        if (!first) continue;
+        const float q = row.inv * ex2((s - row.m) * a.scale);
+        float slope = q - p * row.inv_p;
+        if (q > 0.5f && s == row.m) slope = teacher_away(a, l, sh, j, row) - row.away;
+        store_elem<DT>(out, id, g * slope);
     }
 }
 
@@ -682,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
     if (weight == 0.f) {  // the row has no loss: it is not read
         if (cl.rank == 0 && t == 0) {
             a.loss[r] = 0.f;
-            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, 0.f, 0.f, 0.f, 0.f, 0.f, false);
+            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, Total{}, 0.f, 0.f, 0.f, 0.f, false);
         }
         if (GRAD) stream_grad<DT>(row, out, V, sl.v0, sl.v1, 0.f, c, 0.f);
         return;
@@ -716,14 +764,15 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
     row_factors(tch, all, REST, inv, base, tail);
     if (cl.rank == 0) {
         if (t == 0)
-            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, all.mx, inv, base, tail, lse_t, REST);
+            write_state(a.state ? a.state + r * DLM_DISTILL_STATE : nullptr, all, inv, base, tail, lse_t, REST);
         finish_loss(a, l, sh, tch, r, weight, all, REST, lse_t, twice);
     }
     if (GRAD) {
         const float g = weight * (float)a.inv_t;
         stream_grad<DT>(row, out, V, sl.v0, sl.v1, base, c, g * tail);
         __syncthreads();
-        if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, all.mx, c, inv, tch.inv, true, g);
+        if (inv != 0.f)
+            write_listed<DT>(a, l, sh, out, sl.e0, sl.e1, Listed{all.mx, inv, tch.inv, all.away, lse_t, true, REST}, g);
     }
 }
 
@@ -761,7 +810,7 @@ __global__ void __launch_bounds__(kThreads) distill_stream_grad_kernel(const Dis
     const Teacher tch = list_total(sh, rest);
     stream_grad<DT>(row, out, V, sl.v0, sl.v1, base, c, g * tail);
     __syncthreads();
-    write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, true, g);
+    write_listed<DT>(a, l, sh, out, sl.e0, sl.e1, Listed{m, inv, tch.inv, state[6], state[3], true, rest}, g);
 }
 
 // ---- the row on chip --------------------------------------------------------
@@ -874,13 +923,17 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
         const float rest_sum = hsum2(others);
         // the listed tokens' weights; their logits to the first CTA
         float own = 0.f;
+        bool first = true;
         all_started(cl);
         for (int j = t; j < K; j += kThreads) {
             const int id = l.id[j];
             if (id < sl.e0 || id >= sl.e1) continue;
             float s = l.s[j];
             if (l.own[j]) {
-                own += ex2((s - or_zero(top)) * c);
+                if (s == top && first)
+                    first = false;
+                else
+                    own += ex2((s - or_zero(top)) * c);
             } else {  // another entry has this token's logit, or it is -inf
                 for (int i = 0; i < K; ++i)
                     if (l.id[i] == id && l.own[i]) s = l.s[i];
@@ -896,6 +949,10 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             sh.lse_t = lse_t;
         }
     } else {
+        if (t == 0) {
+            sh.row.away = a.state[r * DLM_DISTILL_STATE + 6];
+            sh.lse_t = lse_t;
+        }
         twice = __syncthreads_or(twice);
     }
     const Teacher tch = list_total(sh, rest);
@@ -909,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
             store_elem<DT>(out, i, scale * ex2((Row<DT>::scalar(data, i - sl.e0) - base) * c));
     }
     __syncthreads();
-    if (inv != 0.f) write_listed<DT>(l, K, out, sl.e0, sl.e1, m, c, inv, tch.inv, twice, g);
+    if (inv != 0.f) write_listed<DT>(a, l, sh, out, sl.e0, sl.e1, Listed{m, inv, tch.inv, sh.row.away, sh.lse_t, twice, rest}, g);
     // (last: the gradient does not wait for it)
     if (SUMS && cl.rank == 0) finish_loss(a, l, sh, list_total(sh, REST), r, sh.weight, sh.row, REST, sh.lse_t, twice);
 }

@@ -767,9 +767,11 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  * list: loss +inf, and those tokens' gradient 0).  Multiply by T^2 through weights where a
  * mix with another loss asks for it.
  *
- * A row's sum of exponentials is held in 32 bits (within 2^-18 of itself, 2^-21
- * seen): a student that agrees with its teacher closer than that gets a loss
- * and a gradient that are rounding.
+ * A row's sums of exponentials are held in 32 bits (within 2^-18 of themselves,
+ * 2^-21 seen): a student that agrees with its teacher closer than that gets a loss
+ * and a gradient that are rounding.  Where the student is sure of a listed token
+ * (q above 1/2) its gradient is the difference of 1 - p and 1 - q, each to that
+ * accuracy of itself.
  *
  * dlm_distill_loss writes loss and, if given, the state that dlm_distill_grad
  * takes to write grad[r] = grad_loss[r] * d loss[r] / d s.  dlm_distill_step

@@ -188,3 +188,49 @@ def test_no_rest_at_all(dlm):
     z[0] = -float("inf")
     z[0, torch.from_numpy(ids[0]).long()] = keep[0, torch.from_numpy(ids[0]).long()]
     check(dlm, z, ids, top, lse)
+
+
+def peaked(n, vocab, kind, k, seed, rest, sure):
+    """Students and teachers sure of the same token of each row, 1 - q and 1 - p
+    about e^-sure each and of the same order."""
+    g = np.random.default_rng(seed)
+    z = ref.rows(n, vocab, kind, seed, boosted=0.0)
+    host = ref.host(z)
+    at = g.integers(vocab, size=n)
+    for r in range(n):
+        host[r, at[r]] = log_sum_exp(host[r]) + sure
+    z.copy_(torch.from_numpy(host.astype(np.float32)).to(z.dtype))
+    t = ref.host(z) + g.normal(0, 0.5, (n, vocab))
+    ids = np.argsort(-t, axis=1, kind="stable")[:, :k].astype(np.int32)
+    ids = ids[:, g.permutation(k)]
+    top = np.take_along_axis(t, ids.astype(np.int64), 1).astype(np.float32)
+    # (a little more than the log-sum-exp, so that rounding leaves no p above 1)
+    lse = np.array([log_sum_exp(x) + 6e-6 for x in t], np.float32) if rest else None
+    return z, ids, top, lse
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("sure", [5, 9, 13])
+@pytest.mark.parametrize("n,vocab,k", [(6, 2000, 16), (3, 40001, 300), (2, 126464, 64)])
+def test_rows_that_are_sure_of_a_token(dlm, kind, sure, rest, n, vocab, k):
+    check(dlm, *peaked(n, vocab, kind, k, sure, rest, sure))
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("kind,vocab", [("f32", 500001), ("bf16", 1000003)])
+def test_long_rows_that_are_sure_of_a_token(dlm, kind, vocab, rest):
+    check(dlm, *peaked(1, vocab, kind, 40, 5, rest, 11))
+
+
+@pytest.mark.parametrize("rest", [False, True])
+def test_sure_of_a_token_that_is_listed_in_parts(dlm, rest):
+    # the token's probability in three entries that add up to it
+    z, ids, top, lse = peaked(4, 3000, "f32", 20, 21, rest, 10)
+    for r in range(4):
+        j = int(top[r].argmax())
+        i = [x for x in range(20) if x != j][5:7]
+        ids[r, i] = ids[r, j]
+        top[r, i] = top[r, j] - np.float32(3.0)
+        top[r, j] += np.float32(math.log1p(-2 * math.exp(-3.0)))
+    check(dlm, z, ids, top, lse)
