@@ -195,6 +195,14 @@ __device__ __forceinline__ float list_max(const Shared& sh) {
 __device__ __forceinline__ WeightScale teacher_scale(const DistillArgs& a, const Shared& sh) {
     return WeightScale{or_zero(list_max(sh)), a.scale, a.scale_lo, kPow2Neg};
 }
+// A probability may be above 1 where lse_t lies below the logit (rounded, or
+// another row's): up to 2^8, so that the sum of a list fits 64 bits.
+constexpr double kMostP = 8 * 0.6931471805599453;
+// ln p - ln q of entry j; shift is the student's log-sum-exp less the teacher's.
+__device__ __forceinline__ double log_ratio(const DistillArgs& a, const List& l, int j, double shift, bool rest, double lse_s) {
+    if (rest && l.p[j] >= 256.f) return kMostP - ((double)l.s[j] * a.inv_t - lse_s);
+    return ((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift;
+}
 // One entry's weight 2^-(y + lo) as an integer.
 __device__ __forceinline__ uint64_t teacher_weight(const DistillArgs& a, float x, const WeightScale& ws, bool rest,
                                                    float lse_t, float& y, float& lo) {
@@ -202,15 +210,18 @@ __device__ __forceinline__ uint64_t teacher_weight(const DistillArgs& a, float x
         y = weight_exponent(x, ws, lo);
         return weight44_of(y, lo);
     }
-    // a lse_t below the logits (p above 1) counts as p = 1
-    const double d = fmax(0.0, (double)lse_t - (double)x * a.inv_t), e = d * 1.4426950408889634;
-    y = (float)e;
-    lo = y < INFINITY ? (float)(e - (double)y) : 0.f;
+    const double d = fmax(-kMostP, (double)lse_t - (double)x * a.inv_t);
     // a teacher that is sure of a token: 1 - p by its series, to the last place (the
     // table's weight is off by 2^-37 of p, 2^-20 of a 1 - p of 10^-5)
-    if (d < 0x1p-12)
-        return (1ull << kWeightBits) - (uint64_t)(d * (1.0 - d * (0.5 - d * (1.0 / 6))) * 17592186044416.0 + 0.5);
-    return weight44_of(y, lo);
+    if (fabs(d) < 0x1p-12) {
+        y = lo = 0.f;
+        return (1ull << kWeightBits) - (uint64_t)__double2ll_rn(d * (1.0 - d * (0.5 - d * (1.0 / 6))) * 17592186044416.0);
+    }
+    const int up = d < 0.0 ? 8 : 0;
+    const double e = d * 1.4426950408889634 + up;
+    y = (float)e;
+    lo = y < INFINITY ? (float)(e - (double)y) : 0.f;
+    return weight44_of(fmaxf(y, 0.f), lo) << up;
 }
 __device__ __forceinline__ void list_weigh(const DistillArgs& a, const List& l, Shared& sh, bool rest, float lse_t) {
     const WeightScale ws = teacher_scale(a, sh);
@@ -354,7 +365,7 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
         double v = 0;
         for (int j = t; j < a.k; j += threads)
             if (l.id[j] >= 0 && l.p[j] > 0.f)
-                v += (double)(l.p[j] * tch.inv) * (((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift);
+                v += (double)(l.p[j] * tch.inv) * log_ratio(a, l, j, shift, rest, lse_s);
 #pragma unroll
         for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(DLM_FULL_MASK, v, o);
         if (threads > 32) {
@@ -371,7 +382,7 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
     const float inv_q = 1.f / q.all;
     for (int j = t; j < a.k; j += threads) {
         if (l.id[j] < 0) continue;
-        const float x = (float)(((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift);
+        const float x = (float)log_ratio(a, l, j, shift, rest, lse_s);
         v += class_term(l.p[j] * tch.inv, x, inv_q * exp2f((l.s[j] - q.mx) * a.scale));
     }
     v = warp_sum(v);

@@ -789,6 +789,8 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  * teacher     : [n_rows][k] logits of teacher_dtype (values of empty entries
  *               are not used); teacher_lse: nullable float [n_rows],
  *               ln sum_v exp(t_v / T) of the whole teacher row (dlm_row_topk).
+ *               Where it lies below a listed logit p_j is above 1 (above 256: 256),
+ *               and p_rest is 0 where the list's sum reaches 1.
  * temperature : DLM_MIN_TEMPERATURE <= T <= DLM_MAX_TEMPERATURE.
  * weights     : nullable float [n_rows] (1).  A row of weight 0 is not read:
  *               loss 0, gradient 0.

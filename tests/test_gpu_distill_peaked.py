@@ -40,7 +40,7 @@ def definition(row, ids, teacher, t, lse):
     with np.errstate(divide="ignore"):
         y = row / t
         log_q = y - log_sum_exp(y)
-        log_p = a - (log_sum_exp(a) if lse is None else lse)
+        log_p = np.minimum(a - (log_sum_exp(a) if lse is None else lse), 8 * math.log(2))
         out = np.ones(len(row), bool)
         out[ids] = False
         p, q = np.exp(log_p), np.exp(log_q)
@@ -234,3 +234,14 @@ def test_sure_of_a_token_that_is_listed_in_parts(dlm, rest):
         top[r, i] = top[r, j] - np.float32(3.0)
         top[r, j] += np.float32(math.log1p(-2 * math.exp(-3.0)))
     check(dlm, z, ids, top, lse)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("less", [0.0, 1e-6, 1e-3, 0.3, 1.0, 5.0, 5.6, 40.0])
+def test_teacher_sums_below_their_logits(dlm, kind, less):
+    # probabilities above 1 are what the formula makes of them (up to 256): a
+    # rounded log-sum-exp of a teacher that is sure of a token gives 1 + 1e-6
+    z, ids, top, _ = peaked(5, 3000, kind, 16, 23, True, 9)
+    check(dlm, z, ids, top, (top.max(1) - less).astype(np.float32))
+    ids[:, 4] = ids[:, 5]
+    check(dlm, z, ids, top, (top.max(1) - less).astype(np.float32))
