@@ -650,13 +650,22 @@ struct ListRule {
     bool all_least;   // every token with a weight >= c->least is listed
 };
 
+// The mass of 2^20 - 1 weights of 1 leaves room for one more below 2^64; the margins
+// are larger.
+__device__ __forceinline__ uint64_t add_up_to_most(uint64_t a, uint64_t b) { return a + b < a ? ~0ull : a + b; }
+
+// Whether `left` lies inside [lo, hi) by more than `off`.
+__device__ __forceinline__ bool well_inside(uint64_t lo, uint64_t left, uint64_t hi, uint64_t off) {
+    return lo <= left && left < hi && left - lo >= off && hi - left > off;
+}
+
 // The nucleus' target mass, as the two ends of what it may be.
 __device__ __forceinline__ void nucleus_target(const Ctrl* c, const ListRule& rule, uint64_t listed, uint64_t& lo,
                                                uint64_t& hi) {
     const uint64_t e = rule.complete ? 0 : c->margin, s = rule.complete ? listed : c->total;
     const float p = c->top_p;
     lo = p < 1.f ? scale_ceil(s - e, p) : ~0ull;
-    hi = p < 1.f ? scale_ceil(s + e, p) : ~0ull;
+    hi = p < 1.f ? scale_ceil(add_up_to_most(s, e), p) : ~0ull;
 }
 
 // The row's token from a list of at most kThreads candidates, one thread each
@@ -1700,7 +1709,7 @@ __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const
     __syncthreads();
     find_batch(s, nb, 0, 0);
     // min-p ends the row only if its tokens are all inside the nucleus
-    if (c->by_min && c->top_p < 1.f && c->mass + 2 * err >= scale_ceil(c->total, c->top_p)) {
+    if (c->by_min && c->top_p < 1.f && add_up_to_most(c->mass, 2 * err) >= scale_ceil(c->total, c->top_p)) {
         __syncthreads();
         if (t == 0) {
             const float hi = c->z_hi, width = hi - c->z_lo;
@@ -1731,7 +1740,7 @@ __device__ __noinline__ int end_row(const RowSearchArgs& a, const Smem& s, const
     const uint64_t off = slack + err / 2 + 1;
     bool done = c->token >= 0;
     if (done && tier != kTier3)
-        done = slack <= (c->mass >> 17) && (first || (c->lo_side + off <= c->left && c->left + off < c->hi_side)) &&
+        done = slack <= (c->mass >> 17) && (first || well_inside(c->lo_side, c->left, c->hi_side, off)) &&
                candidate(c->z, (uint32_t)c->token) <= sure;
     if (t == 0 && done) write_token(a, c, o, c->token, c->z, c->mass);
     return done ? (int)kDone : tier == kTier3 ? (int)kRadix : tier + 1;
@@ -1854,7 +1863,7 @@ __device__ __forceinline__ int sample_leader(const RowSearchArgs& a, const Smem&
         // of the mass and u times the whole differ by at most 2 u (1 - u) e of
         // the mass from what they should: e / 2
         const uint64_t off = c->margin / 2 + 1;
-        const bool sure = c->token >= 0 && c->lo_side + off <= c->left && c->left + off < c->hi_side;
+        const bool sure = c->token >= 0 && well_inside(c->lo_side, c->left, c->hi_side, off);
         if (t == 0 && sure) write_token(a, c, o, c->token, c->z, c->mass);
         return sure ? kDone : kTier1;
     }
