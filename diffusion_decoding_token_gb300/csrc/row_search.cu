@@ -929,8 +929,10 @@ __device__ __noinline__ void count_cut(const Cluster& cl, const Smem& s, const c
         radix_pick(cl, s, prefix, radix_bits(l), above, (uint64_t)k);
         if (l == 0 && c0->total < (uint64_t)k) {  // fewer finite logits: all of them
             list = c0->total <= (uint64_t)kCap;
-            key = kKeyNegInf + 1;
-            ties = 0xffffffffu;
+            // (no ties at the lowest float: their number is not known, and where it is
+            // the maximum their weight is 1)
+            key = list ? kKeyNegInf + 1 : kKeyNegInf;
+            ties = 0;
             cl.sync();
             return;
         }

@@ -48,3 +48,16 @@ def test_mass_that_fills_64_bits(dlm, f, n):
     z = ref.rows(2, 1048575, "f32", seed=5, boosted=0.0)
     g = np.random.default_rng(9)
     check(dlm, z, np.arange(n) % 2, g.random(n), temperature=1e30, **f)
+
+
+@pytest.mark.parametrize("n", [3, 400])
+@pytest.mark.parametrize("f", [dict(top_k=3000, top_p=0.9), dict(top_k=3000, top_p=0.5), dict(top_k=3000),
+                               dict(top_k=3000, top_p=0.9, min_p=0.5), dict(top_k=2400, top_p=0.9),
+                               dict(top_k=9999, top_p=0.9), dict(top_p=0.9), dict()], ids=str)
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_rows_masked_with_the_lowest_value(dlm, kind, f, n):
+    g = np.random.default_rng(3)
+    z = torch.full((3, 40000), -float("inf"), dtype=ref.TYPES[kind])
+    for q, m in enumerate((2500, 2049, 30000)):
+        z[q, torch.from_numpy(g.permutation(40000)[:m])] = torch.finfo(z.dtype).min
+    check(dlm, z, np.arange(n) % 3, g.random(n), **f)
