@@ -244,10 +244,15 @@ def _rows_arg(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be [rows, V] with contiguous rows")
 
 
+def _padded(t: torch.Tensor) -> int:
+    """The columns of ``t`` rounded up to whole 16-byte vectors."""
+    epv = 16 // t.element_size()
+    return (t.shape[1] + epv - 1) // epv * epv
+
+
 def _stride(t: torch.Tensor) -> int:
     # a single row's stride is never used; torch reports any value for it
-    epv = 16 // t.element_size()
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + epv - 1) // epv * epv
+    return t.stride(0) if t.shape[0] > 1 else _padded(t)
 
 
 def _same(t: torch.Tensor | None, shape, dtype, device, name: str, dtypes=None) -> None:
@@ -366,8 +371,8 @@ def _distill_args(student, ids, teacher, weights, teacher_lse=None):
 
 def _grad_out(student, out):
     if out is None:
-        # rows at the student's stride, which is a multiple of 16 bytes
-        return torch.empty_strided(student.shape, (_stride(student), 1), dtype=student.dtype, device=student.device)
+        # rows of its own, not at the stride of the student, which may be a view of one position in many
+        return torch.empty_strided(student.shape, (_padded(student), 1), dtype=student.dtype, device=student.device)
     _rows_arg(out, "the gradient")
     if out.shape != student.shape or out.dtype != student.dtype or out.device != student.device:
         raise ValueError("the gradient must match the student in shape, dtype and device")

@@ -91,3 +91,14 @@ def test_distill(L, call):
         assert distill(L, call, grad=P(0x100000 + 208)) == INVALID
         assert distill(L, call, grad=P(0x100000 - 208)) == INVALID
         assert distill(L, call, grad=X, gstride=112) == INVALID
+
+
+def test_the_gradient_takes_its_own_memory_only():
+    # the student as one position of a model's [batch, positions, vocabulary]
+    import torch
+    from diffusion_decoding_token_gb300 import _binding
+    for dtype, vocab, padded in ((torch.float32, 1001, 1004), (torch.bfloat16, 1000, 1000), (torch.float16, 1001, 1008)):
+        student = torch.empty((4, 50, padded), dtype=dtype)[:, 7, :vocab]
+        grad = _binding._grad_out(student, None)
+        assert grad.shape == student.shape and grad.dtype == dtype and grad.stride() == (padded, 1)
+        assert grad.untyped_storage().nbytes() <= 4 * padded * grad.element_size()
