@@ -735,6 +735,12 @@ static dlm_status distill_grad_ok(const dlm::DistillArgs& a, dlm_dtype dtype, co
     const char* s0 = static_cast<const char*>(a.student);
     const char* g0 = static_cast<const char*>(grad);
     if (s0 == g0 && grad_stride == a.row_stride) return DLM_OK;
+    // rows that lie between the student's
+    if (grad_stride == a.row_stride) {
+        const int64_t stride = a.row_stride * esz, row = a.vocab * esz;
+        const int64_t from = ((reinterpret_cast<intptr_t>(g0) - reinterpret_cast<intptr_t>(s0)) % stride + stride) % stride;
+        if (from >= row && stride - from >= row) return DLM_OK;
+    }
     const char* s1 = s0 + ((a.n_rows - 1) * a.row_stride + a.vocab) * esz;
     const char* g1 = g0 + ((a.n_rows - 1) * grad_stride + a.vocab) * esz;
     return g0 < s1 && s0 < g1 ? DLM_ERR_INVALID_ARG : DLM_OK;

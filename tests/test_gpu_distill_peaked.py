@@ -245,3 +245,20 @@ def test_teacher_sums_below_their_logits(dlm, kind, less):
     check(dlm, z, ids, top, (top.max(1) - less).astype(np.float32))
     ids[:, 4] = ids[:, 5]
     check(dlm, z, ids, top, (top.max(1) - less).astype(np.float32))
+
+
+def test_gradient_rows_between_the_students(dlm):
+    # memory that holds both in turn overlaps nowhere
+    z, ids, top, lse = flat_teacher(6, 1003, "f32", 8, 25, 3)
+    cuda = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    want = dlm.distill_step(on_gpu(z), cuda(ids), cuda(top), teacher_lse=cuda(lse))
+    for first in (0, 1):
+        both = torch.full((6, 2, 1004), 7.0, device="cuda")
+        student, grad = both[:, first, :1003], both[:, 1 - first, :1003]
+        student.copy_(z)
+        loss, _ = dlm.distill_step(student, cuda(ids), cuda(top), teacher_lse=cuda(lse), grad=grad)
+        assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])
+        assert torch.equal(student.cpu(), z) and (both[:, :, 1003] == 7.0).all()
+    with pytest.raises(dlm.DlmError):  # the same stride, one vector of each row shared
+        wide = torch.zeros((6, 2, 1004), device="cuda").view(6, 2008)
+        dlm.distill_step(wide[:, :1003], cuda(ids), cuda(top), grad=wide[:, 1000:2003])
