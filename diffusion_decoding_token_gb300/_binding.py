@@ -265,6 +265,15 @@ def _same(t: torch.Tensor | None, shape, dtype, device, name: str, dtypes=None) 
         raise ValueError(f"{name} must be a contiguous {want} tensor of shape {tuple(shape)} on {device}")
 
 
+def _status_ptr(status: torch.Tensor | None, device) -> int | None:
+    """A status word that kernels on ``device`` may write."""
+    if status is None:
+        return None
+    if status.device != device or status.dtype not in (torch.int32, torch.uint32) or status.numel() < 1:
+        raise ValueError(f"status must be an int32 tensor on {device}")
+    return status.data_ptr()
+
+
 class RowTopk(NamedTuple):
     values: torch.Tensor
     ids: torch.Tensor
@@ -317,7 +326,7 @@ def row_topk(logits: torch.Tensor, k: int, *, temperature: float = 1.0, row_inde
         _same(out.ids, (m, k), torch.int32, dev, "out.ids")
         _same(out.lse, (m,), torch.float32, dev, "out.lse")
     _on(dev, lib().dlm_row_topk, _ptr(logits), _dt(logits), n, logits.shape[1], _stride(logits), _ptr(row_index),
-        logits.shape[0], int(k), float(temperature), _ptr(out.values), _ptr(out.ids), _ptr(out.lse), _ptr(status),
+        logits.shape[0], int(k), float(temperature), _ptr(out.values), _ptr(out.ids), _ptr(out.lse), _status_ptr(status, dev),
         ROWS_GATHER if gather else 0)
     return out
 
@@ -352,7 +361,7 @@ def row_sample(logits: torch.Tensor, uniform: torch.Tensor, *, temperature=1.0, 
         _same(out.conf, (m,), torch.float32, dev, "out.conf")
     _on(dev, lib().dlm_row_sample, _ptr(logits), _dt(logits), n, logits.shape[1], _stride(logits), _ptr(row_index),
         logits.shape[0], _ptr(uniform), ctypes.byref(prm), _ptr(lse), _ptr(out.token), _ptr(out.prob), _ptr(out.conf),
-        _ptr(status), ROWS_GATHER if gather else 0)
+        _status_ptr(status, dev), ROWS_GATHER if gather else 0)
     return out
 
 
@@ -397,7 +406,7 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
         _same(out.loss, (rows,), torch.float32, dev, "out.loss")
         _same(out.state, (rows, DISTILL_STATE), torch.float32, dev, "out.state")
     _on(dev, lib().dlm_distill_loss, *args, _ptr(teacher_lse), float(temperature), _ptr(weights), _ptr(out.loss),
-        _ptr(out.state), _ptr(status))
+        _ptr(out.state), _status_ptr(status, dev))
     return out
 
 
@@ -414,7 +423,7 @@ def distill_grad(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
     _same(grad_loss, (rows,), torch.float32, dev, "grad_loss")
     out = _grad_out(student, out)
     _on(dev, lib().dlm_distill_grad, *args, float(temperature), _ptr(weights), _ptr(state), _ptr(grad_loss), _ptr(out),
-        _stride(out), _ptr(status))
+        _stride(out), _status_ptr(status, dev))
     return out
 
 
@@ -433,7 +442,7 @@ def distill_step(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
         _same(loss, (rows,), torch.float32, dev, "loss")
     grad = _grad_out(student, grad)
     _on(dev, lib().dlm_distill_step, *args, _ptr(teacher_lse), float(temperature), _ptr(weights), _ptr(loss), _ptr(grad),
-        _stride(grad), _ptr(status))
+        _stride(grad), _status_ptr(status, dev))
     return loss, grad
 
 

@@ -61,3 +61,15 @@ def test_rows_masked_with_the_lowest_value(dlm, kind, f, n):
     for q, m in enumerate((2500, 2049, 30000)):
         z[q, torch.from_numpy(g.permutation(40000)[:m])] = torch.finfo(z.dtype).min
     check(dlm, z, np.arange(n) % 3, g.random(n), **f)
+
+
+def test_status_words_elsewhere_are_refused(dlm):
+    z, word = torch.zeros((2, 104), device="cuda"), torch.zeros(1, dtype=torch.int32)
+    i, t = torch.zeros((2, 4), dtype=torch.int32, device="cuda"), torch.zeros((2, 4), device="cuda")
+    for call in (lambda s: dlm.row_topk(z, 4, status=s), lambda s: dlm.row_sample(z, z[:, 0].contiguous(), status=s),
+                 lambda s: dlm.distill_loss(z, i, t, status=s), lambda s: dlm.distill_step(z, i, t, status=s),
+                 lambda s: dlm.distill_grad(z, i, t, torch.zeros((2, 8), device="cuda"), status=s)):
+        for bad in (word, torch.zeros(1, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")):
+            with pytest.raises(ValueError):
+                call(bad)
+        call(dlm.new_status())

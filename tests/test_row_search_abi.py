@@ -102,3 +102,15 @@ def test_the_gradient_takes_its_own_memory_only():
         grad = _binding._grad_out(student, None)
         assert grad.shape == student.shape and grad.dtype == dtype and grad.stride() == (padded, 1)
         assert grad.untyped_storage().nbytes() <= 4 * padded * grad.element_size()
+
+
+def test_a_status_word_is_on_the_kernels_device():
+    # (a host address would be written by the GPU)
+    import torch
+    from diffusion_decoding_token_gb300 import _binding
+    here, word = torch.device("cpu"), torch.zeros(1, dtype=torch.int32)
+    assert _binding._status_ptr(None, here) is None
+    assert _binding._status_ptr(word, here) == word.data_ptr()
+    for bad, device in ((word, torch.device("cuda", 0)), (word[:0], here), (word.long(), here), (word.float(), here)):
+        with pytest.raises(ValueError):
+            _binding._status_ptr(bad, device)
