@@ -673,11 +673,18 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
                                              dev_status, flags);
     if (st != DLM_OK || n_rows == 0) return st;
     if (!uniform || !token || !prob) return DLM_ERR_INVALID_ARG;
-    // both launches read these, and the first one writes token and prob
+    // both launches read the inputs, and the first one writes notes into token and prob:
+    // arrays of 4-byte entries, as many as the rows where that is known
+    const int64_t entries = (flags & DLM_ROWS_GATHER) || !row_index ? n_rows : n_src_rows > 0 ? n_src_rows : 1;
+    auto overlap = [&](const void* p, const void* q) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q), n = (uintptr_t)entries * 4;
+        return p && q && (x < y ? y - x < n : x - y < n);
+    };
     for (const void* in : {(const void*)uniform, (const void*)lse, (const void*)params->temperature_rows,
                            (const void*)params->top_k_rows, (const void*)params->top_p_rows,
-                           (const void*)params->min_p_rows})
-        if (in == token || in == prob) return DLM_ERR_INVALID_ARG;
+                           (const void*)params->min_p_rows, (const void*)conf})
+        if (overlap(in, token) || overlap(in, prob)) return DLM_ERR_INVALID_ARG;
+    if (overlap(token, prob)) return DLM_ERR_INVALID_ARG;
     a.uniform = uniform;
     a.temperature = params->temperature;
     a.k = params->top_k;

@@ -729,8 +729,10 @@ dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int
  *               temperature 1, which the selection rules take.  Both or none.
  * token, prob : int32 / float outputs, which hold notes between the call's two
  *               launches: they are valid when its work has ended, and may not
- *               overlap uniform, the settings or lse.  A row that holds NaN or +inf, or -inf
- *               only, gets token -1, prob 0 (conf 0) and sets DLM_DEV_NONFINITE.
+ *               overlap each other, uniform, the settings, lse or conf (refused as
+ *               far as their lengths are known).  conf may be lse's memory where no
+ *               row is listed twice.  A row that holds NaN or +inf, or -inf only,
+ *               gets token -1, prob 0 (conf 0) and sets DLM_DEV_NONFINITE.
  */
 typedef struct dlm_sample_params {
     float temperature;

@@ -114,3 +114,13 @@ def test_a_status_word_is_on_the_kernels_device():
     for bad, device in ((word, torch.device("cuda", 0)), (word[:0], here), (word.long(), here), (word.float(), here)):
         with pytest.raises(ValueError):
             _binding._status_ptr(bad, device)
+
+
+def test_sampled_tokens_and_their_inputs_do_not_overlap(L):
+    # n = 1000 entries of 4 bytes each; token at 0x200000, prob at 0x300000
+    at = lambda x: P(x)  # noqa: E731
+    for kw in (dict(u=at(0x200000 + 3996)), dict(u=at(0x200000 - 3996)), dict(u=at(0x300000 + 4)),
+               dict(prob=at(0x200000)), dict(prob=at(0x200000 + 2000)), dict(lse=X, conf=at(0x200000 + 4)),
+               dict(lse=X, conf=at(0x300000)), dict(lse=at(0x300000 + 3996), conf=Y),
+               dict(rows=(None, 0x200000 + 3996, None, None)), dict(rows=(0x300000 - 3996, None, None, None))):
+        assert sample(L, n=1000, **kw) == INVALID, kw
