@@ -1535,16 +1535,15 @@ __device__ __noinline__ int find_end(const Cluster& cl, const Smem& s, int nb, i
     const uint64_t x = p < 1.f ? scale_ceil(total, p) : ~0ull;
     const uint64_t off = p < 1.f ? (uint64_t)((float)err * 2.0001f * p * (1.f - p)) + 2 : 0;  // rounded up
     // another bracket: above this one or below (with a quarter of it), the
-    // middle of one that holds too many tokens, or the other filter's
-    enum { kUp, kDown, kMiddle, kToMin, kToNucleus };
+    // middle of one that holds too many tokens, or min-p's
+    enum { kUp, kDown, kMiddle, kToMin };
     auto miss = [&](int how) {
         __syncthreads();
         if (t == 0) {
             const float lo = c->z_lo, hi = c->z_hi, width = fmaxf(hi - lo, 1e-6f * fabsf(hi));
-            if (how == kUp || how == kToNucleus) {
+            if (how == kUp) {
                 c->z_lo = hi - 0.25f * width;
                 c->z_hi = hi + 2.f * width;
-                c->by_min = 0;
             } else if (how == kDown) {
                 c->z_lo = lo - 2.f * width;
                 c->z_hi = lo + 0.25f * width;
