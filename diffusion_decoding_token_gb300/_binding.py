@@ -396,7 +396,9 @@ def distill_loss(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
     column stride) against the teacher's top logits ``teacher`` at ``ids`` (both
     [rows, k]; a negative id is an empty entry), and the state that
     :func:`distill_grad` takes.  With ``teacher_lse`` the teacher's mass outside
-    the list is one more class, without it the list is renormalised."""
+    the list is one more class, without it the list is renormalised.  The result
+    carries no autograd graph, also of a student that requires a gradient:
+    that is :func:`distill_grad`'s or :func:`distill_step`'s output."""
     args = _distill_args(student, ids, teacher, weights, teacher_lse)
     rows, dev = student.shape[0], student.device
     if out is None:

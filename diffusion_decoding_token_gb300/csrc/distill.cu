@@ -8,9 +8,9 @@
 //   dl/ds_v = w / T (q_v - p_v)                  v listed (p_v: all its entries)
 //   dl/ds_v = w / T q_v (1 - p_rest / q_rest)    otherwise (p_rest = 0: w / T q_v)
 //
-// Everything the gradient needs of a row is its maximum, 1 / sum, reference and
-// factor of the tokens that are not listed, and the list: `state` holds it between
-// the two calls.
+// Everything the gradient needs of a row is its maximum, 1 / sum, the share of all
+// but the largest listed token, reference and factor of the tokens that are not
+// listed, and the list: `state` holds it between the two calls.
 //
 // All three are bound by HBM: the loss by one read of the row, the gradient by a
 // read and a write.
@@ -27,10 +27,12 @@
 //    sums.  How long a CTA lives decides (its slice takes its share of the SM's
 //    shared memory meanwhile), so its reductions share five barriers, only the
 //    first CTA does 64-bit arithmetic on the sums, and last.
-//    2048 rows of 152064 bf16 tokens, a quarter of them without a loss: 228 us,
-//    4.8 TB/s of the 1.09 GB that it reads and writes.  Streamed twice (the
-//    second read from L2) it took 269 us at best, slices of 77 KB 308 us, 128
-//    threads 231 us.
+//    2048 rows of 152064 bf16 tokens, a quarter of them without a loss: 221 us,
+//    4.9 TB/s of the 1.09 GB that it reads and writes (a call among others).
+//    Registers decide here: at 48 of them, with what only the loss needs at the
+//    end kept in shared memory, nothing spills; with 92 bytes of spills it took
+//    255 us.  Against 228 us then, streamed twice (the second read from L2) it took
+//    269 us at best, slices of 77 KB 308 us, 128 threads 231 us.
 //  * Rows that eight CTAs can not hold (above 1.5 MB) are streamed twice.
 //
 // q_rest = 1 - sum q_id would lose all digits for a peaked student, so the sum
@@ -55,7 +57,7 @@ constexpr float kRebase = 12.0f;  // powers of 2 of headroom before a thread's r
 
 // What a thread, a warp or a CTA knows of a row: the softmax sums of its slice over
 // the listed tokens, relative to the largest of them `ref` (-inf: none), and over
-// the others, relative to `rest_ref` (NaN where there is one).  Two references,
+// the others, relative to `rest_ref` (a NaN logit makes its reference NaN).  Two references,
 // since a student's list may lie far above the rest: with one, the rest's weights
 // were subnormal or 0 from 83 nats on, and the quotients that p_rest is multiplied
 // by overflowed.  `listed` leaves one weight of 1, that of a token at `ref`, out: a
@@ -536,10 +538,11 @@ __device__ Share stream_sums(const char* row, int64_t V, int v0, int v1, float c
     return a;
 }
 
-// The row's sums over all the CTAs of its cluster, in every thread.  Each warp leaves its share in every CTA (a remote store needs
-// no answer), one barrier later each warp adds up all of them for itself, and
-// nothing remote is read, so no CTA has to outlive another.  started()
-// comes before: no share is sent to a CTA that does not run yet.
+// The row's sums over all the CTAs of its cluster, in every thread.  Each warp leaves
+// its share in every CTA (a remote store needs no answer), one barrier later each
+// warp adds up all of them for itself, and nothing remote is read, so no CTA has to
+// outlive another.  started() comes before: no share is sent to a CTA that does not
+// run yet.
 __device__ __forceinline__ Total merge_row(const Cluster& cl, Shared& sh, Share a, float c, bool& twice) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     a = warp_share(a, c);

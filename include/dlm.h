@@ -714,7 +714,8 @@ dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int
  * not): the token is that of the real-number
  * definition unless u * sum lies within about 1e-11 of a border, and equal
  * inputs give equal tokens on every launch.  prob is within 2^-20 (relative),
- * and within 2^-17 where top_p keeps hundreds of tokens or more.
+ * within 2^-17 where top_p keeps hundreds of tokens or more, and without a filter
+ * within 2^-18 (its sum may come from 32 bits; 2^-21 seen).
  *
  * logits .. n_src_rows, flags : as in dlm_row_topk (row r's uniform, settings,
  *               lse and outputs at o = q, or o = r with DLM_ROWS_GATHER).
@@ -795,7 +796,8 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  *               and p_rest is 0 where the list's sum reaches 1.
  * temperature : DLM_MIN_TEMPERATURE <= T <= DLM_MAX_TEMPERATURE.
  * weights     : nullable float [n_rows] (1).  A row of weight 0 is not read:
- *               loss 0, gradient 0.
+ *               loss 0, gradient 0.  weights[r] / T (times grad_loss[r]) has to be
+ *               a finite float.
  * loss        : float [n_rows] output.
  * state       : float [n_rows][DLM_DISTILL_STATE], opaque; nullable in
  *               dlm_distill_loss.  dlm_distill_grad must get the ids, teacher,
@@ -805,8 +807,9 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  *               may be the student's memory itself (same base and stride), else
  *               it must not overlap it.  Elements past vocab are left alone.
  * dev_status  : DLM_DEV_NONFINITE for a row whose student logits hold NaN or
- *               +inf, or -inf only, or whose listed teacher logits (or
- *               teacher_lse) are NaN or +inf: loss and gradient are NaN there.
+ *               +inf, or -inf only, whose listed teacher logits are NaN or +inf, or
+ *               whose teacher_lse is not finite: loss and gradient are NaN there.
+ *               (dlm_distill_grad writes such a row's NaN and sets no status.)
  */
 #define DLM_DISTILL_STATE 8
 
