@@ -205,6 +205,8 @@ __device__ __forceinline__ double log_ratio(const DistillArgs& a, const List& l,
     if (rest && l.p[j] >= 256.f) return kMostP - ((double)l.s[j] * a.inv_t - lse_s);
     return ((double)l.t[j] - (double)l.s[j]) * a.inv_t + shift;
 }
+// 1 - e^-d for |d| < 2^-12.
+__device__ __forceinline__ double one_less_exp(double d) { return d * (1.0 - d * (0.5 - d * (1.0 / 6))); }
 // One entry's weight 2^-(y + lo) as an integer.
 __device__ __forceinline__ uint64_t teacher_weight(const DistillArgs& a, float x, const WeightScale& ws, bool rest,
                                                    float lse_t, float& y, float& lo) {
@@ -217,7 +219,7 @@ __device__ __forceinline__ uint64_t teacher_weight(const DistillArgs& a, float x
     // table's weight is off by 2^-37 of p, 2^-20 of a 1 - p of 10^-5)
     if (fabs(d) < 0x1p-12) {
         y = lo = 0.f;
-        return (1ull << kWeightBits) - (uint64_t)__double2ll_rn(d * (1.0 - d * (0.5 - d * (1.0 / 6))) * 17592186044416.0);
+        return (1ull << kWeightBits) - (uint64_t)__double2ll_rn(one_less_exp(d) * 17592186044416.0);
     }
     const int up = d < 0.0 ? 8 : 0;
     const double e = d * 1.4426950408889634 + up;
@@ -662,16 +664,27 @@ struct Listed {
     bool twice, rest;
 };
 
-// 1 - p_v of the token that entry j lists, p_v close to 1 or not.
+// 1 - p_v of the token that entry j lists, to all digits however near p_v is to 1:
+// without the rest the other entries' sum, with it the series of 1 - e^-d.  (A token
+// that is listed in parts, with the rest: one less the integer weights, to 2^-45.)
 __device__ __forceinline__ float teacher_away(const DistillArgs& a, const List& l, const Shared& sh, int j, const Listed& row) {
+    const int id = l.id[j], K = a.k;
+    if (!row.rest) {
+        float others = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < K; ++i) others += l.id[i] != id ? l.p[i] : 0.f;
+        return others * row.inv_p;
+    }
     const WeightScale ws = teacher_scale(a, sh);
-    const int id = l.id[j];
-    const Teacher tch = list_total(sh, row.rest);
-    uint64_t w = 0;
     float y, lo;
-    for (int i = row.twice ? 0 : j; i < (row.twice ? a.k : j + 1); ++i)
-        if (l.id[i] == id) w += teacher_weight(a, l.t[i], ws, row.rest, row.lse_t, y, lo);
-    return (float)(int64_t)((row.rest ? 1ull << kWeightBits : tch.sum) - w) * (row.rest ? kUnit : tch.inv * kUnit);
+    if (!row.twice) {
+        const double d = (double)row.lse_t - (double)l.t[j] * a.inv_t;
+        if (fabs(d) < 0x1p-12) return (float)one_less_exp(d);
+    }
+    uint64_t w = 0;
+    for (int i = row.twice ? 0 : j; i < (row.twice ? K : j + 1); ++i)
+        if (l.id[i] == id) w += teacher_weight(a, l.t[i], ws, true, row.lse_t, y, lo);
+    return (float)(int64_t)((1ull << kWeightBits) - w) * kUnit;
 }
 
 // The listed tokens of this CTA's slice [e0, e1): g (q_v - p_v), for a token that

@@ -711,9 +711,9 @@ dlm_status dlm_row_topk(const void* logits, dlm_dtype dtype, int64_t n_rows, int
  * prob = w_token / (sum over all kept).  temperature 0 takes the first maximum
  * (prob 1) whatever the filters.  The sums that decide are integers (64-bit
  * fixed point, weights to 2^-37; 32-bit sums decide only where their error can
- * not): the token is that of the real-number
- * definition unless u * sum lies within about 1e-11 of a border, and equal
- * inputs give equal tokens on every launch.  prob is within 2^-20 (relative),
+ * not): the token is that of the real-number definition unless u * sum (or top_p
+ * times its sum, or min_p) lies within about 1e-11 of a border, and equal inputs
+ * give equal tokens on every launch.  prob is within 2^-20 (relative),
  * within 2^-17 where top_p keeps hundreds of tokens or more, and without a filter
  * within 2^-18 (its sum may come from 32 bits; 2^-21 seen).
  *
@@ -774,7 +774,8 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  * 2^-21 seen): a student that agrees with its teacher closer than that gets a loss
  * and a gradient that are rounding.  Where the student is sure of a listed token
  * (q above 1/2) its gradient is the difference of 1 - p and 1 - q, each to that
- * accuracy of itself.
+ * accuracy of itself (but for weights that count as 0).  p_rest is 1 less a sum of
+ * integers in units of 2^-44, within 2^-34 (2^-38 where no list is long).
  *
  * dlm_distill_loss writes loss and, if given, the state that dlm_distill_grad
  * takes to write grad[r] = grad_loss[r] * d loss[r] / d s.  dlm_distill_step

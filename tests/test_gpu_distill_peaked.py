@@ -55,7 +55,8 @@ def definition(row, ids, teacher, t, lse):
             v = int(q.argmax())
             others = math.exp(log_sum_exp(np.delete(y, v)) - log_sum_exp(y))  # 1 - q
             less = 1 - total[v] if lse is not None else math.fsum(p[ids != v])
-            grad[v], scale[v] = less - others, abs(less) + others
+            # (each of the other weights may be one below 2^-126, which counts as 0)
+            grad[v], scale[v] = less - others, abs(less) + others + len(row) * 2.0 ** (17 - 126)
         if lse is not None:
             p_rest = max(0.0, 1 - math.fsum(p))
             log_rest = log_sum_exp(y[out])
@@ -262,3 +263,21 @@ def test_gradient_rows_between_the_students(dlm):
     with pytest.raises(dlm.DlmError):  # the same stride, one vector of each row shared
         wide = torch.zeros((6, 2, 1004), device="cuda").view(6, 2008)
         dlm.distill_step(wide[:, :1003], cuda(ids), cuda(top), grad=wide[:, 1000:2003])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("sure,t", [(18, 1.0), (24, 1.0), (40, 0.5)])
+@pytest.mark.parametrize("n,vocab,k", [(5, 2000, 16), (2, 40001, 700), (1, 500001, 40)])
+def test_rows_that_are_all_but_certain(dlm, kind, sure, t, n, vocab, k):
+    # 1 - p from 1e-8 to 1e-35: next to nothing in units of 2^-44
+    z, ids, top, _ = peaked(n, vocab, kind, k, sure, False, sure)
+    check(dlm, z, ids, top, None, t=t)
+    ids[:, 2] = ids[:, 3]
+    check(dlm, z, ids, top, None, t=t)
+
+
+def test_one_less_p_next_to_nothing(dlm):
+    # lse_t - t / T of 2^-18 to 2^-40 (a teacher whose logits lie around 0)
+    z, ids, top, _ = peaked(23, 2000, "f32", 16, 31, True, 12)
+    top -= top.max(1, keepdims=True)
+    check(dlm, z, ids, top, (2.0 ** -np.arange(18, 41)).astype(np.float32))
