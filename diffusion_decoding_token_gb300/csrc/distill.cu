@@ -305,9 +305,12 @@ __device__ __forceinline__ uint4 without(uint4 w, uint32_t mask) {
     return make_uint4(x[0], x[1], x[2], x[3]);
 }
 
-// p (x - 1 + e^-x) for x = ln p - ln q, q = p e^-x.
-__device__ __forceinline__ float class_term(float p, float x, float q) {
+// p (x - 1 + e^-x) for x = ln p - ln q, q = p e^-x.  (x of a token at the lowest float
+// may pass a float's range where p x does not.)
+__device__ __forceinline__ float class_term(float p, double x64, float q) {
     if (!(p > 0.f)) return q;
+    const float x = (float)x64;
+    if (!(fabsf(x) < INFINITY)) return (float)((double)p * x64);
     if (!(fabsf(x) < 1.f)) return p * (x - 1.f) + q;
     // x^2 (1/2! - x/3! + x^2/4! - ...)
     float r = 1.f / 39916800;
@@ -386,7 +389,7 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
     const float inv_q = 1.f / q.all;
     for (int j = t; j < a.k; j += threads) {
         if (l.id[j] < 0) continue;
-        const float x = (float)log_ratio(a, l, j, shift, rest, lse_s);
+        const double x = log_ratio(a, l, j, shift, rest, lse_s);
         v += class_term(l.p[j] * tch.inv, x, inv_q * exp2f((l.s[j] - q.mx) * a.scale));
     }
     v = warp_sum(v);
@@ -399,7 +402,7 @@ __device__ float row_loss(const DistillArgs& a, const List& l, Shared& sh, const
     }
     if (!rest) return v + q_rest;
     const uint64_t one = 1ull << kWeightBits;
-    return v + class_term(tch.p_rest, (float)x_rest, q_rest) + (tch.sum > one ? (float)(tch.sum - one) * kUnit : 0.f);
+    return v + class_term(tch.p_rest, x_rest, q_rest) + (tch.sum > one ? (float)(tch.sum - one) * kUnit : 0.f);
 }
 
 __device__ __forceinline__ void write_state(float* state, const Total& row, float inv, float base, float tail,

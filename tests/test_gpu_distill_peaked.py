@@ -281,3 +281,21 @@ def test_one_less_p_next_to_nothing(dlm):
     z, ids, top, _ = peaked(23, 2000, "f32", 16, 31, True, 12)
     top -= top.max(1, keepdims=True)
     check(dlm, z, ids, top, (2.0 ** -np.arange(18, 41)).astype(np.float32))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("listed", [False, True])
+def test_logarithms_beyond_a_float(dlm, kind, listed):
+    # ln q of -3e38 / 0.5 times a probability of 1e-5: a loss of 1e33
+    z, ids, top, lse = flat_teacher(3, 3000, kind, 12, 27, 20, t=0.5, rest_mass=0.0 if listed else 1e-5)
+    low = torch.finfo(z.dtype).min
+    if listed:
+        top[:, 3] = top.max(1) - np.float32(5.5)
+        z[torch.arange(3), torch.from_numpy(ids[:, 3]).long()] = low
+        check(dlm, z, ids, top, None, t=0.5)
+    keep = z.clone()
+    z[:] = low
+    for r in range(3):
+        z[r, torch.from_numpy(ids[r]).long()] = keep[r, torch.from_numpy(ids[r]).long()]
+    if not listed:
+        check(dlm, z, ids, top, lse, t=0.5)
