@@ -27,7 +27,7 @@
 //    sums.  How long a CTA lives decides (its slice takes its share of the SM's
 //    shared memory meanwhile), so its reductions share five barriers, only the
 //    first CTA does 64-bit arithmetic on the sums, and last.
-//    2048 rows of 152064 bf16 tokens, a quarter of them without a loss: 221 us,
+//    2048 rows of 152064 bf16 tokens, a quarter of them without a loss: 224 us,
 //    4.9 TB/s of the 1.09 GB that it reads and writes (a call among others).
 //    Registers decide here: at 48 of them, with what only the loss needs at the
 //    end kept in shared memory, nothing spills; with 92 bytes of spills it took
@@ -286,6 +286,19 @@ __device__ __forceinline__ void mark_listed(const List& l, int K, int64_t e0, in
         const uint32_t bit = 1u << ((id - e0) & 31);
         mine.in |= 1u << i;
         mine.own |= (uint32_t)((atomicOr(&l.bits[(id - e0) >> 5], bit) & bit) == 0) << i;
+    }
+}
+
+// Which entry of a token that is listed again marked it first goes by chance, and the
+// sums' last place by which thread holds it: the lowest entry has it.
+__device__ __forceinline__ void lowest_own(const List& l, int K, Mine& mine) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+        if (!((mine.in >> i) & 1u)) continue;
+        const int j = threadIdx.x + i * kThreads;
+        int at = 0;
+        while (l.id[at] != l.id[j]) ++at;
+        mine.own = (mine.own & ~(1u << i)) | (uint32_t)(at == j) << i;
     }
 }
 
@@ -776,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_stream_kernel(const Disti
     for (int i = 0; i < kMine; ++i)
         mine.s[i] = (mine.in >> i) & 1u ? Row<DT>::scalar(row, l.id[t + i * kThreads]) : 0.f;
     list_weigh(a, l, sh, REST, lse_t);
-    __syncthreads();
+    if (__syncthreads_or(mine.in != mine.own)) lowest_own(l, K, mine);
     Share share = stream_sums<DT>(row, V, sl.v0, sl.v1, c, a.scale_lo, l.bits, mine);
     if (mine.in != mine.own) share.listed = -share.listed;
     all_started(cl);
@@ -866,6 +879,26 @@ __device__ __forceinline__ float take_out(uint4* data, int e) {
     }
 }
 
+// Where a token of the slice is listed again, its lowest entry gets the logit that one
+// of them took by chance (as in lowest_own).  Returns the thread's largest.
+__device__ __forceinline__ float settle_own(const List& l, int K, int e0, int e1) {
+    for (int j = threadIdx.x; j < K; j += kThreads) {
+        const int id = l.id[j];
+        if (id < e0 || id >= e1 || !l.own[j]) continue;
+        int at = 0;
+        while (l.id[at] != id) ++at;
+        if (at == j) continue;
+        l.s[at] = l.s[j];
+        l.own[at] = 1;
+        l.own[j] = 0;
+    }
+    __syncthreads();
+    float top = -INFINITY;
+    for (int j = threadIdx.x; j < K; j += kThreads)
+        if (l.id[j] >= e0 && l.id[j] < e1 && l.own[j]) top = max_nan(top, l.s[j]);
+    return top;
+}
+
 // SUMS: loss and the gradient of the losses' sum; else the gradient from the
 // state (REST says nothing there).
 template <int DT, bool REST, bool SUMS>
@@ -932,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_row_kernel(const DistillA
         if (took) top = max_nan(top, s);
     }
     if (SUMS) {
-        __syncthreads();
+        if (__syncthreads_or(twice)) top = settle_own(l, K, sl.e0, sl.e1);
         float high = -INFINITY;
         for (int v = t; v < n; v += kThreads) high = max_nan(high, Row<DT>::vmax(data[v]));
         const float ref = or_zero(high);  // nothing but -inf: weights of 0

@@ -779,7 +779,8 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
  *
  * dlm_distill_loss writes loss and, if given, the state that dlm_distill_grad
  * takes to write grad[r] = grad_loss[r] * d loss[r] / d s.  dlm_distill_step
- * writes both in one launch, the gradient being that of sum_r loss[r].
+ * writes both in one launch, the gradient being that of sum_r loss[r].  Equal
+ * inputs give equal bits on every launch of a call.
  *
  * student     : [n_rows][row_stride] logits; alignment and dtypes as in
  *               dlm_row_stats, vocab <= DLM_MAX_SEARCH_VOCAB.  -inf logits

@@ -299,3 +299,23 @@ def test_logarithms_beyond_a_float(dlm, kind, listed):
         z[r, torch.from_numpy(ids[r]).long()] = keep[r, torch.from_numpy(ids[r]).long()]
     if not listed:
         check(dlm, z, ids, top, lse, t=0.5)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("kind,n,vocab,k", [("f32", 128, 2000, 700), ("bf16", 128, 2000, 64), ("f16", 16, 60000, 1000),
+                                            ("f32", 3, 500001, 300)])
+def test_repeats_give_the_same_bits_on_every_launch(dlm, kind, n, vocab, k, rest):
+    g = np.random.default_rng(33)
+    z, ids, top, lse = flat_teacher(n, vocab, kind, k, 29, 2, rest_mass=0.5)
+    ids = np.take_along_axis(ids, g.integers(0, k, (n, k)), 1)  # a third of the tokens is listed twice or more
+    d, cuda = on_gpu(z), lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    i, t, lse = cuda(ids), cuda(top), cuda(lse) if rest else None
+    bits = lambda x: x.contiguous().view(torch.uint8)  # noqa: E731
+    want = dlm.distill_loss(d, i, t, teacher_lse=lse), dlm.distill_step(d, i, t, teacher_lse=lse)
+    want_grad = dlm.distill_grad(d, i, t, want[0].state)
+    for _ in range(20):
+        out = dlm.distill_loss(d, i, t, teacher_lse=lse)
+        loss, grad = dlm.distill_step(d, i, t, teacher_lse=lse)
+        assert torch.equal(bits(out.loss), bits(want[0].loss)) and torch.equal(bits(out.state), bits(want[0].state))
+        assert torch.equal(bits(loss), bits(want[1][0])) and torch.equal(bits(grad), bits(want[1][1]))
+        assert torch.equal(bits(dlm.distill_grad(d, i, t, out.state)), bits(want_grad))
