@@ -12,7 +12,13 @@ After every forward pass, for the masked positions of the active block:
   min-p from given random numbers;
 * :func:`row_topk` -- the k largest logits of each row and its log-sum-exp;
 * :func:`distill_loss`, :func:`distill_grad`, :func:`distill_step` -- training a
-  student's rows on a teacher's top logits.
+  student's rows on a teacher's top logits;
+* :func:`row_logprob`, :func:`row_logprob_grad`, :func:`row_logprob_step` -- the
+  log-probability of one given token per row;
+* :func:`policy_loss`, :func:`policy_grad`, :func:`policy_step` -- the clipped
+  policy loss with a KL term;
+* :func:`preference_loss`, :func:`preference_grad`, :func:`preference_step` -- the
+  preference loss of paired sequences.
 
 All work runs in hand-written sm_103a kernels behind the C ABI of
 ``libdlm.so`` (``include/dlm.h``); this package only marshals CUDA tensors.
@@ -31,6 +37,11 @@ from ._binding import (  # noqa: F401
     MAX_TOPK,
     DistillLoss,
     DlmError,
+    PolicyLoss,
+    PolicyStep,
+    PreferenceLoss,
+    PreferenceStep,
+    RowLogprob,
     RowSample,
     RowStats,
     RowTopk,
@@ -49,6 +60,16 @@ from ._binding import (  # noqa: F401
     distill_step,
     lib,
     new_status,
+    policy_grad,
+    policy_loss,
+    policy_step,
+    preference_grad,
+    preference_loss,
+    preference_step,
+    preference_workspace,
+    row_logprob,
+    row_logprob_grad,
+    row_logprob_step,
     row_sample,
     row_stats,
     row_topk,
@@ -71,5 +92,8 @@ from .driver import SyntheticDecoder  # noqa: F401
 __all__ = [
     "row_stats", "select_threshold", "select_topk", "select_factor", "parallel_certificate", "depcap_boundary", "cap_select", "dapd_graph_mis", "dapd_graph", "dapd_select",
     "row_topk", "row_sample", "distill_loss", "distill_grad", "distill_step", "RowTopk", "RowSample", "DistillLoss",
+    "row_logprob", "row_logprob_grad", "row_logprob_step", "policy_loss", "policy_grad", "policy_step",
+    "preference_loss", "preference_grad", "preference_step", "preference_workspace",
+    "RowLogprob", "PolicyLoss", "PolicyStep", "PreferenceLoss", "PreferenceStep",
     "StepPlan", "alloc_row_stats", "cap_workspace", "dapd_workspace", "new_status", "RowStats", "DlmError", "lib",
 ]

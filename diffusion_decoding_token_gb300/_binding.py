@@ -54,6 +54,15 @@ class SampleParams(ctypes.Structure):
                 ("top_p_rows", ctypes.c_void_p), ("min_p_rows", ctypes.c_void_p)]
 
 
+class PolicyParams(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("dual_clip", ctypes.c_float),
+                ("kl_weight", ctypes.c_float), ("kl", ctypes.c_int32)]
+
+
+class PreferenceParams(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float), ("kind", ctypes.c_int32)]
+
+
 RULE_THRESHOLD, RULE_BOUNDARY, RULE_CAP = 1, 2, 4
 
 
@@ -123,6 +132,23 @@ def lib():
         L.dlm_distill_loss.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, D, P, P, P, P, P]
         L.dlm_distill_grad.argtypes = [P, E, I64, I64, I64, P, P, E, I32, D, P, P, P, P, I64, P, P]
         L.dlm_distill_step.argtypes = [P, E, I64, I64, I64, P, P, E, I32, P, D, P, P, P, I64, P, P]
+        rows = [P, E, I64, I64, I64]
+        L.dlm_row_logprob.argtypes = [*rows, P, I64, P, D, P, P, P, P, U, P]
+        L.dlm_row_logprob_grad.argtypes = [*rows, P, D, P, P, P, I64, P, P]
+        L.dlm_row_logprob_step.argtypes = [*rows, P, D, P, P, P, I64, P, P]
+        L.dlm_policy_loss.argtypes = [*rows, P, D, P, P, P, P, ctypes.POINTER(PolicyParams), P, P, P, P, P]
+        L.dlm_policy_grad.argtypes = [*rows, P, D, P, P, P, I64, P, P]
+        L.dlm_policy_step.argtypes = [*rows, P, D, P, P, P, P, ctypes.POINTER(PolicyParams), P, P, P, I64, P, P]
+        L.dlm_preference_workspace_size.restype = Z
+        L.dlm_preference_workspace_size.argtypes = [I64, I64]
+        pairs = [P, D, P, I64, P, P, P, P, ctypes.POINTER(PreferenceParams), P, P, P]
+        L.dlm_preference_loss.argtypes = [*rows, *pairs, P, P, P]
+        L.dlm_preference_grad.argtypes = [*rows, P, D, I64, P, P, P, I64, P, P]
+        L.dlm_preference_step.argtypes = [*rows, *pairs, P, I64, P, Z, P, P]
+        for f in ("dlm_row_logprob", "dlm_row_logprob_grad", "dlm_row_logprob_step", "dlm_policy_loss",
+                  "dlm_policy_grad", "dlm_policy_step", "dlm_preference_loss", "dlm_preference_grad",
+                  "dlm_preference_step"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("dlm_row_topk", "dlm_row_sample", "dlm_distill_loss", "dlm_distill_grad", "dlm_distill_step",
                   "dlm_row_stats", "dlm_select_threshold", "dlm_depcap_boundary", "dlm_cap_select",
                   "dlm_dapd_graph_mis", "dlm_dapd_graph", "dlm_dapd_select", "dlm_select_topk",
@@ -384,7 +410,7 @@ def _grad_out(student, out):
         return torch.empty_strided(student.shape, (_padded(student), 1), dtype=student.dtype, device=student.device)
     _rows_arg(out, "the gradient")
     if out.shape != student.shape or out.dtype != student.dtype or out.device != student.device:
-        raise ValueError("the gradient must match the student in shape, dtype and device")
+        raise ValueError("the gradient must match the logits in shape, dtype and device")
     return out
 
 
@@ -446,6 +472,270 @@ def distill_step(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
     _on(dev, lib().dlm_distill_step, *args, _ptr(teacher_lse), float(temperature), _ptr(weights), _ptr(loss), _ptr(grad),
         _stride(grad), _status_ptr(status, dev))
     return loss, grad
+
+
+class RowLogprob(NamedTuple):
+    logp: torch.Tensor
+    lse: torch.Tensor
+    state: torch.Tensor | None
+
+
+class PolicyLoss(NamedTuple):
+    loss: torch.Tensor
+    logp: torch.Tensor
+    state: torch.Tensor
+
+
+class PolicyStep(NamedTuple):
+    loss: torch.Tensor
+    logp: torch.Tensor
+    grad: torch.Tensor
+
+
+class PreferenceLoss(NamedTuple):
+    loss: torch.Tensor
+    score: torch.Tensor
+    logp: torch.Tensor
+    state: torch.Tensor
+
+
+class PreferenceStep(NamedTuple):
+    loss: torch.Tensor
+    score: torch.Tensor
+    logp: torch.Tensor
+    grad: torch.Tensor
+
+
+TOKEN_STATE = 8  # DLM_TOKEN_STATE
+_KL = {"k1": 1, "k2": 2, "k3": 3}                      # DLM_KL_*
+_PREF = {"sigmoid": 0, "hinge": 1, "ipo": 2}           # DLM_PREF_*
+
+
+def _token_rows(logits, tokens):
+    """The arguments that the calls over given tokens begin with, apart from the tokens."""
+    _rows_arg(logits, "logits")
+    rows = logits.shape[0]
+    _same(tokens, (rows,), torch.int32, logits.device, "tokens")
+    return _ptr(logits), _dt(logits), rows, logits.shape[1], _stride(logits)
+
+
+def _floats(n, device, *given):
+    """Per-row inputs: float32 tensors of ``n`` entries, or None."""
+    for name, t in given:
+        _same(t, (n,), torch.float32, device, name)
+
+
+def _new(shape, device):
+    return torch.empty(shape, dtype=torch.float32, device=device)
+
+
+def row_logprob(logits: torch.Tensor, tokens: torch.Tensor, *, temperature: float = 1.0,
+                row_index: torch.Tensor | None = None, gather: bool = False, with_state: bool = False,
+                out: RowLogprob | None = None, status: torch.Tensor | None = None) -> RowLogprob:
+    """dlm_row_logprob: the log-probability of one token per row of ``logits``
+    ([rows, V], unit column stride) and the row's log-sum-exp, both of
+    logits / temperature.  ``tokens`` is int32; a negative one is none (0 and 0).
+    ``with_state`` adds the state that :func:`row_logprob_grad` takes.
+    ``row_index`` and ``gather`` as in :func:`row_stats`."""
+    _rows_arg(logits, "logits")
+    row_index, n, m = _gathered(logits, row_index, gather)
+    dev = logits.device
+    _same(tokens, (m,), torch.int32, dev, "tokens")
+    if out is None:
+        out = RowLogprob(_new(m, dev), _new(m, dev), _new((m, TOKEN_STATE), dev) if with_state else None)
+    else:
+        _floats(m, dev, ("out.logp", out.logp), ("out.lse", out.lse))
+        _same(out.state, (m, TOKEN_STATE), torch.float32, dev, "out.state")
+    _on(dev, lib().dlm_row_logprob, _ptr(logits), _dt(logits), n, logits.shape[1], _stride(logits), _ptr(row_index),
+        logits.shape[0], _ptr(tokens), float(temperature), _ptr(out.logp), _ptr(out.lse), _ptr(out.state),
+        _status_ptr(status, dev), ROWS_GATHER if gather else 0)
+    return out
+
+
+def _token_grad(call, logits, tokens, state, up, up_shape, temperature, out, status, name, *pairs):
+    args = _token_rows(logits, tokens)
+    dev = logits.device
+    _same(state, (logits.shape[0], TOKEN_STATE), torch.float32, dev, "state")
+    _same(up, up_shape, torch.float32, dev, name)
+    out = _grad_out(logits, out)
+    _on(dev, call, *args, _ptr(tokens), float(temperature), *pairs, _ptr(state), _ptr(up), _ptr(out), _stride(out),
+        _status_ptr(status, dev))
+    return out
+
+
+def row_logprob_grad(logits: torch.Tensor, tokens: torch.Tensor, state: torch.Tensor,
+                     grad_logp: torch.Tensor | None = None, *, temperature: float = 1.0,
+                     out: torch.Tensor | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+    """dlm_row_logprob_grad: the gradient of sum_r grad_logp[r] * logp[r] with
+    respect to ``logits``, from the state of the :func:`row_logprob` call with the
+    same arguments.  ``out`` may be ``logits`` itself."""
+    return _token_grad(lib().dlm_row_logprob_grad, logits, tokens, state, grad_logp, logits.shape[:1], temperature, out,
+                       status, "grad_logp")
+
+
+def row_logprob_step(logits: torch.Tensor, tokens: torch.Tensor, weights: torch.Tensor | None = None, *,
+                     temperature: float = 1.0, logp: torch.Tensor | None = None, grad: torch.Tensor | None = None,
+                     status: torch.Tensor | None = None):
+    """dlm_row_logprob_step: (log-probability of each row's token, gradient of
+    sum_r weights[r] * logp[r]) in one launch; ``grad`` may be ``logits`` itself.
+    The loss of a likelihood bound has negative weights: ``-1 / t`` at masked
+    positions, 0 elsewhere."""
+    args = _token_rows(logits, tokens)
+    rows, dev = logits.shape[0], logits.device
+    _floats(rows, dev, ("weights", weights), ("logp", logp))
+    if logp is None:
+        logp = _new(rows, dev)
+    grad = _grad_out(logits, grad)
+    _on(dev, lib().dlm_row_logprob_step, *args, _ptr(tokens), float(temperature), _ptr(weights), _ptr(logp), _ptr(grad),
+        _stride(grad), _status_ptr(status, dev))
+    return logp, grad
+
+
+def _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip, kl_weight, kl, temperature):
+    args = _token_rows(logits, tokens)
+    if kl not in _KL:
+        raise ValueError(f"kl must be one of {sorted(_KL)}")
+    _floats(logits.shape[0], logits.device, ("advantages", advantages), ("old", old), ("ref", ref), ("weights", weights))
+    return (*args, _ptr(tokens), float(temperature), _ptr(advantages), _ptr(old), _ptr(ref), _ptr(weights),
+            ctypes.byref(PolicyParams(clip_low, clip_high, dual_clip, kl_weight, _KL[kl])))
+
+
+def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, advantages: torch.Tensor, *, old: torch.Tensor | None = None,
+                ref: torch.Tensor | None = None, clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                kl_weight: float = 0.0, kl: str = "k3", temperature: float = 1.0, weights: torch.Tensor | None = None,
+                out: PolicyLoss | None = None, status: torch.Tensor | None = None) -> PolicyLoss:
+    """dlm_policy_loss: the clipped policy loss of each row of ``logits`` ([rows, V],
+    unit column stride) for its token, with ``kl_weight`` times the KL estimate
+    ``kl`` ("k1", "k2", "k3") to the reference's log-probabilities ``ref``.  ``old``
+    holds the rollout policy's (None: the policy is the rollout's own).  Returns the
+    losses, the log-probabilities and the state that :func:`policy_grad` takes.
+    The result carries no autograd graph."""
+    args = _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip, kl_weight, kl,
+                        temperature)
+    rows, dev = logits.shape[0], logits.device
+    if out is None:
+        out = PolicyLoss(_new(rows, dev), _new(rows, dev), _new((rows, TOKEN_STATE), dev))
+    else:
+        _floats(rows, dev, ("out.loss", out.loss), ("out.logp", out.logp))
+        _same(out.state, (rows, TOKEN_STATE), torch.float32, dev, "out.state")
+    _on(dev, lib().dlm_policy_loss, *args, _ptr(out.loss), _ptr(out.logp), _ptr(out.state), _status_ptr(status, dev))
+    return out
+
+
+def policy_grad(logits: torch.Tensor, tokens: torch.Tensor, state: torch.Tensor, grad_loss: torch.Tensor | None = None, *,
+                temperature: float = 1.0, out: torch.Tensor | None = None,
+                status: torch.Tensor | None = None) -> torch.Tensor:
+    """dlm_policy_grad: the gradient of sum_r grad_loss[r] * loss[r] with respect to
+    ``logits``, from the state of the :func:`policy_loss` call with the same
+    arguments.  ``out`` may be ``logits`` itself."""
+    return _token_grad(lib().dlm_policy_grad, logits, tokens, state, grad_loss, logits.shape[:1], temperature, out, status,
+                       "grad_loss")
+
+
+def policy_step(logits: torch.Tensor, tokens: torch.Tensor, advantages: torch.Tensor, *, old: torch.Tensor | None = None,
+                ref: torch.Tensor | None = None, clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0,
+                kl_weight: float = 0.0, kl: str = "k3", temperature: float = 1.0, weights: torch.Tensor | None = None,
+                out: PolicyStep | None = None, status: torch.Tensor | None = None) -> PolicyStep:
+    """dlm_policy_step: :func:`policy_loss` and the gradient of the losses' sum in
+    one launch; ``out.grad`` may be ``logits`` itself.  Feed a model's own graph with
+    ``logits.backward(grad)``."""
+    args = _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip, kl_weight, kl,
+                        temperature)
+    rows, dev = logits.shape[0], logits.device
+    if out is None:
+        out = PolicyStep(_new(rows, dev), _new(rows, dev), _grad_out(logits, None))
+    else:
+        _floats(rows, dev, ("out.loss", out.loss), ("out.logp", out.logp))
+        _grad_out(logits, out.grad)
+    _on(dev, lib().dlm_policy_step, *args, _ptr(out.loss), _ptr(out.logp), _ptr(out.grad), _stride(out.grad),
+        _status_ptr(status, dev))
+    return out
+
+
+def _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta, label_smoothing, kind, temperature):
+    args = _token_rows(logits, tokens)
+    dev = logits.device
+    if kind not in _PREF:
+        raise ValueError(f"kind must be one of {sorted(_PREF)}")
+    if offsets.dim() != 1 or offsets.shape[0] % 2 != 1:
+        raise ValueError("offsets must have 2 * pairs + 1 entries")
+    _same(offsets, offsets.shape, torch.int32, dev, "offsets")
+    pairs = offsets.shape[0] // 2
+    _floats(logits.shape[0], dev, ("ref", ref), ("weights", weights))
+    _floats(pairs, dev, ("margins", margins), ("pair_weights", pair_weights))
+    return pairs, (*args, _ptr(tokens), float(temperature), _ptr(offsets), pairs, _ptr(ref), _ptr(weights), _ptr(margins),
+                   _ptr(pair_weights), ctypes.byref(PreferenceParams(beta, label_smoothing, _PREF[kind])))
+
+
+def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, offsets: torch.Tensor, *, ref: torch.Tensor | None = None,
+                    beta: float = 0.1, kind: str = "sigmoid", label_smoothing: float = 0.0,
+                    margins: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                    pair_weights: torch.Tensor | None = None, temperature: float = 1.0, out: PreferenceLoss | None = None,
+                    status: torch.Tensor | None = None) -> PreferenceLoss:
+    """dlm_preference_loss: the loss ``kind`` ("sigmoid", "hinge", "ipo") of pairs of
+    sequences.  Sequence s is the rows ``offsets[s]`` to ``offsets[s + 1]`` of
+    ``logits`` ([rows, V], unit column stride); pair i is sequence 2i, the chosen
+    one, and 2i + 1.  A sequence's score is the sum over its rows of ``weights`` times
+    the token's log-probability less the reference's ``ref`` (None: no reference).
+    Returns the pairs' losses, the scores, the log-probabilities and the state that
+    :func:`preference_grad` takes.  The result carries no autograd graph."""
+    pairs, args = _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta, label_smoothing, kind,
+                                   temperature)
+    rows, dev = logits.shape[0], logits.device
+    if out is None:
+        out = PreferenceLoss(_new(pairs, dev), _new(2 * pairs, dev), _new(rows, dev), _new((rows, TOKEN_STATE), dev))
+    else:
+        _floats(pairs, dev, ("out.loss", out.loss))
+        _floats(2 * pairs, dev, ("out.score", out.score))
+        _floats(rows, dev, ("out.logp", out.logp))
+        _same(out.state, (rows, TOKEN_STATE), torch.float32, dev, "out.state")
+    _on(dev, lib().dlm_preference_loss, *args, _ptr(out.loss), _ptr(out.score), _ptr(out.logp), _ptr(out.state),
+        _status_ptr(status, dev))
+    return out
+
+
+def preference_grad(logits: torch.Tensor, tokens: torch.Tensor, state: torch.Tensor, grad_loss: torch.Tensor | None = None,
+                    *, temperature: float = 1.0, out: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None) -> torch.Tensor:
+    """dlm_preference_grad: the gradient of sum_i grad_loss[i] * loss[i] (one entry
+    per pair) with respect to ``logits``, from the state of the
+    :func:`preference_loss` call with the same arguments.  ``out`` may be ``logits``
+    itself."""
+    shape = grad_loss.shape[:1] if grad_loss is not None else (0,)
+    return _token_grad(lib().dlm_preference_grad, logits, tokens, state, grad_loss, shape, temperature, out, status,
+                       "grad_loss", shape[0])
+
+
+def preference_workspace(rows: int, pairs: int, device) -> torch.Tensor:
+    """Scratch of :func:`preference_step` (calls sharing it must not overlap)."""
+    return torch.empty(lib().dlm_preference_workspace_size(rows, pairs), dtype=torch.uint8, device=device)
+
+
+def preference_step(logits: torch.Tensor, tokens: torch.Tensor, offsets: torch.Tensor, *, ref: torch.Tensor | None = None,
+                    beta: float = 0.1, kind: str = "sigmoid", label_smoothing: float = 0.0,
+                    margins: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                    pair_weights: torch.Tensor | None = None, temperature: float = 1.0, out: PreferenceStep | None = None,
+                    workspace: torch.Tensor | None = None, status: torch.Tensor | None = None) -> PreferenceStep:
+    """dlm_preference_step: :func:`preference_loss` and the gradient of the losses'
+    sum; ``out.grad`` may be ``logits`` itself.  ``workspace``:
+    :func:`preference_workspace` (None: a new one)."""
+    pairs, args = _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta, label_smoothing, kind,
+                                   temperature)
+    rows, dev = logits.shape[0], logits.device
+    if workspace is None:
+        workspace = preference_workspace(rows, pairs, dev)
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    if out is None:
+        out = PreferenceStep(_new(pairs, dev), _new(2 * pairs, dev), _new(rows, dev), _grad_out(logits, None))
+    else:
+        _floats(pairs, dev, ("out.loss", out.loss))
+        _floats(2 * pairs, dev, ("out.score", out.score))
+        _floats(rows, dev, ("out.logp", out.logp))
+        _grad_out(logits, out.grad)
+    _on(dev, lib().dlm_preference_step, *args, _ptr(out.loss), _ptr(out.score), _ptr(out.logp), _ptr(out.grad),
+        _stride(out.grad), _ptr(workspace), workspace.numel(), _status_ptr(status, dev))
+    return out
 
 
 PARTIAL_FLOATS = 8  # dlm_row_partial: 8 four-byte fields

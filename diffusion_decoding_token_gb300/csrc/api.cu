@@ -36,6 +36,27 @@ inline bool dtype_ok(int dt) { return dt == DLM_F32 || dt == DLM_BF16 || dt == D
 
 inline dlm_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DLM_OK : DLM_ERR_CUDA; }
 
+// Whether one of the outputs overlaps another or an input (4-byte entries).
+struct Span {
+    const void* p;
+    int64_t n;
+};
+inline bool overlap(const Span& x, const Span& y) {
+    if (!x.p || !y.p || x.n == 0 || y.n == 0) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return a < b ? b - a < (uintptr_t)x.n * 4 : a - b < (uintptr_t)y.n * 4;
+}
+template <int N, int M>
+bool overlapping(const Span (&outs)[N], const Span (&ins)[M]) {
+    for (int i = 0; i < N; ++i) {
+        for (int j = i + 1; j < N; ++j)
+            if (overlap(outs[i], outs[j])) return true;
+        for (const Span& in : ins)
+            if (overlap(outs[i], in)) return true;
+    }
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -701,6 +722,15 @@ dlm_status dlm_row_sample(const void* logits, dlm_dtype dtype, int64_t n_rows, i
     return from_cuda(dlm::launch_row_sample(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// log2(e) / temperature in two floats, the first rounded down, so that the second is
+// positive: -inf times both is -inf.
+static void split_scale(double inv_t, float& hi, float& lo) {
+    const double scale = 1.4426950408889634 * inv_t;
+    hi = (float)scale;
+    if ((double)hi >= scale) hi = nextafterf(hi, 0.f);
+    lo = (float)(scale - (double)hi);
+}
+
 // Checks shared by the distillation calls.
 static dlm_status distill_prepare(dlm::DistillArgs& a, const void* student, dlm_dtype dtype, int64_t n_rows,
                                   int64_t vocab, int64_t row_stride, const int32_t* ids, const void* teacher,
@@ -725,31 +755,28 @@ static dlm_status distill_prepare(dlm::DistillArgs& a, const void* student, dlm_
     a.weights = weights;
     a.dev_status = dev_status;
     a.inv_t = 1.0 / temperature;
-    // rounded down, so that the rest is positive: -inf times both is -inf
-    const double scale = 1.4426950408889634 * a.inv_t;
-    a.scale = (float)scale;
-    if ((double)a.scale >= scale) a.scale = nextafterf(a.scale, 0.f);
-    a.scale_lo = (float)(scale - (double)a.scale);
+    split_scale(a.inv_t, a.scale, a.scale_lo);
     if (n_rows > 0x7fffffffLL / 8) return DLM_ERR_INVALID_ARG;  // up to 8 CTAs per row
     return DLM_OK;
 }
 
-// The gradient's memory: aligned like the student's, and the same rows or none of them.
-static dlm_status distill_grad_ok(const dlm::DistillArgs& a, dlm_dtype dtype, const void* grad, int64_t grad_stride) {
-    if (!grad || grad_stride < a.vocab) return DLM_ERR_INVALID_ARG;
+// A gradient's memory: aligned like the logits', and the same rows or none of them.
+static dlm_status grad_rows_ok(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                               const void* grad, int64_t grad_stride) {
+    if (!grad || grad_stride < vocab) return DLM_ERR_INVALID_ARG;
     const int64_t esz = dtype_size(dtype);
     if (!aligned16(grad) || (grad_stride * esz) % 16 != 0) return DLM_ERR_ALIGNMENT;
-    const char* s0 = static_cast<const char*>(a.student);
+    const char* s0 = static_cast<const char*>(logits);
     const char* g0 = static_cast<const char*>(grad);
-    if (s0 == g0 && grad_stride == a.row_stride) return DLM_OK;
+    if (s0 == g0 && grad_stride == row_stride) return DLM_OK;
     // rows that lie between the student's
-    if (grad_stride == a.row_stride) {
-        const int64_t stride = a.row_stride * esz, row = a.vocab * esz;
+    if (grad_stride == row_stride) {
+        const int64_t stride = row_stride * esz, row = vocab * esz;
         const int64_t from = ((reinterpret_cast<intptr_t>(g0) - reinterpret_cast<intptr_t>(s0)) % stride + stride) % stride;
         if (from >= row && stride - from >= row) return DLM_OK;
     }
-    const char* s1 = s0 + ((a.n_rows - 1) * a.row_stride + a.vocab) * esz;
-    const char* g1 = g0 + ((a.n_rows - 1) * grad_stride + a.vocab) * esz;
+    const char* s1 = s0 + ((n_rows - 1) * row_stride + vocab) * esz;
+    const char* g1 = g0 + ((n_rows - 1) * grad_stride + vocab) * esz;
     return g0 < s1 && s0 < g1 ? DLM_ERR_INVALID_ARG : DLM_OK;
 }
 
@@ -778,7 +805,7 @@ dlm_status dlm_distill_grad(const void* student, dlm_dtype dtype, int64_t n_rows
                                     temperature, weights, dev_status);
     if (st != DLM_OK || n_rows == 0) return st;
     if (!state) return DLM_ERR_INVALID_ARG;
-    st = distill_grad_ok(a, dtype, grad, grad_stride);
+    st = grad_rows_ok(student, dtype, n_rows, vocab, row_stride, grad, grad_stride);
     if (st != DLM_OK) return st;
     a.state = const_cast<float*>(state);
     a.grad_loss = grad_loss;
@@ -797,7 +824,7 @@ dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows
                                     temperature, weights, dev_status);
     if (st != DLM_OK || n_rows == 0) return st;
     if (!loss) return DLM_ERR_INVALID_ARG;
-    st = distill_grad_ok(a, dtype, grad, grad_stride);
+    st = grad_rows_ok(student, dtype, n_rows, vocab, row_stride, grad, grad_stride);
     if (st != DLM_OK) return st;
     a.teacher_lse = teacher_lse;
     a.loss = loss;
@@ -805,6 +832,259 @@ dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows
     a.grad_stride = grad_stride;
     dlm::distill_plan(a, dtype, sm_count());
     return from_cuda(dlm::launch_distill_loss(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Checks shared by the calls over given tokens; fills everything but the outputs.
+static dlm_status token_prepare(dlm::TokenArgs& a, const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab,
+                                int64_t row_stride, const int32_t* tokens, double temperature, uint32_t* dev_status) {
+    if (!dtype_ok(dtype)) return DLM_ERR_UNSUPPORTED;
+    if (n_rows < 0 || vocab < 1 || vocab > DLM_MAX_SEARCH_VOCAB || row_stride < vocab || !temperature_ok((float)temperature))
+        return DLM_ERR_INVALID_ARG;
+    a = dlm::TokenArgs{};
+    if (n_rows == 0) return DLM_OK;
+    if (!logits || !tokens) return DLM_ERR_INVALID_ARG;
+    if (!aligned16(logits) || (row_stride * dtype_size(dtype)) % 16 != 0) return DLM_ERR_ALIGNMENT;
+    if (n_rows > 0x7fffffffLL / 8) return DLM_ERR_INVALID_ARG;  // up to 8 CTAs per row
+    a.logits = logits;
+    a.n_rows = n_rows;
+    a.vocab = vocab;
+    a.row_stride = row_stride;
+    a.tokens = tokens;
+    a.inv_t = 1.0 / temperature;
+    split_scale(a.inv_t, a.scale, a.scale_lo);
+    a.dev_status = dev_status;
+    a.num_sms = sm_count();
+    return DLM_OK;
+}
+
+static dlm_status token_run(const dlm::TokenArgs& a, dlm_dtype dtype, dlm_stream_t stream) {
+    return from_cuda(dlm::launch_token(a, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The gradient calls: from the state.
+static dlm_status token_grad(int op, const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab,
+                             int64_t row_stride, const int32_t* tokens, double temperature, int64_t n_up,
+                             const float* state, const float* up, void* grad, int64_t grad_stride, uint32_t* dev_status,
+                             dlm_stream_t stream) {
+    dlm::TokenArgs a;
+    dlm_status st = token_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!state) return DLM_ERR_INVALID_ARG;
+    if (!aligned16(state)) return DLM_ERR_ALIGNMENT;
+    st = grad_rows_ok(logits, dtype, n_rows, vocab, row_stride, grad, grad_stride);
+    if (st != DLM_OK) return st;
+    a.op = op;
+    a.state = const_cast<float*>(state);
+    a.grad_loss = up;
+    a.n_up = n_up;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return token_run(a, dtype, stream);
+}
+
+dlm_status dlm_row_logprob(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* row_index, int64_t n_src_rows, const int32_t* tokens, double temperature,
+                           float* logp, float* lse, float* state, uint32_t* dev_status, uint32_t flags,
+                           dlm_stream_t stream) {
+    if ((flags & ~DLM_ROWS_GATHER) || n_src_rows < 0) return DLM_ERR_INVALID_ARG;
+    if (!row_index && n_src_rows > 0 && n_rows > n_src_rows) return DLM_ERR_INVALID_ARG;
+    dlm::TokenArgs a;
+    const dlm_status st = token_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!logp || (state && row_index)) return DLM_ERR_INVALID_ARG;
+    if (state && !aligned16(state)) return DLM_ERR_ALIGNMENT;
+    a.gather = (flags & DLM_ROWS_GATHER) ? 1 : 0;
+    // arrays as long as the rows, where that is known
+    const int64_t n = a.gather || !row_index ? n_rows : n_src_rows > 0 ? n_src_rows : 1;
+    if (overlapping({{logp, n}, {lse, n}, {state, n * DLM_TOKEN_STATE}}, {{tokens, n}, {row_index, n_rows}}))
+        return DLM_ERR_INVALID_ARG;
+    a.op = dlm::kTokenLogprob;
+    a.sums = 1;
+    a.row_index = row_index;
+    a.n_src = n_src_rows;
+    a.logp = logp;
+    a.lse = lse;
+    a.state = state;
+    return token_run(a, dtype, stream);
+}
+
+dlm_status dlm_row_logprob_grad(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                                const int32_t* tokens, double temperature, const float* state, const float* grad_logp,
+                                void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
+    return token_grad(dlm::kTokenLogprob, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, n_rows, state,
+                      grad_logp, grad, grad_stride, dev_status, stream);
+}
+
+dlm_status dlm_row_logprob_step(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                                const int32_t* tokens, double temperature, const float* weights, float* logp, void* grad,
+                                int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::TokenArgs a;
+    dlm_status st = token_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!logp) return DLM_ERR_INVALID_ARG;
+    st = grad_rows_ok(logits, dtype, n_rows, vocab, row_stride, grad, grad_stride);
+    if (st != DLM_OK) return st;
+    if (overlapping({{logp, n_rows}}, {{tokens, n_rows}, {weights, n_rows}})) return DLM_ERR_INVALID_ARG;
+    a.op = dlm::kTokenLogprob;
+    a.sums = 1;
+    a.weights = weights;
+    a.logp = logp;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return token_run(a, dtype, stream);
+}
+
+// What the policy's loss and step share: settings, inputs and per-row outputs.
+static dlm_status policy_prepare(dlm::TokenArgs& a, const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab,
+                                 int64_t row_stride, const int32_t* tokens, double temperature, const float* advantages,
+                                 const float* old_logp, const float* ref_logp, const float* weights,
+                                 const dlm_policy_params* params, float* loss, float* logp, float* state,
+                                 uint32_t* dev_status) {
+    if (!params) return DLM_ERR_INVALID_ARG;
+    const dlm_policy_params& p = *params;
+    if (!(p.clip_low >= 0.f && p.clip_low <= 1.f) || !(p.clip_high >= 0.f) ||
+        !(p.dual_clip == 0.f || (p.dual_clip >= 1.f && p.dual_clip < INFINITY)) ||
+        !(p.kl_weight >= 0.f && p.kl_weight < INFINITY) || p.kl < DLM_KL_K1 || p.kl > DLM_KL_K3)
+        return DLM_ERR_INVALID_ARG;
+    const dlm_status st = token_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    if (!advantages || !loss || (p.kl_weight != 0.f && !ref_logp)) return DLM_ERR_INVALID_ARG;
+    if (state && !aligned16(state)) return DLM_ERR_ALIGNMENT;
+    if (overlapping({{loss, n_rows}, {logp, n_rows}, {state, n_rows * DLM_TOKEN_STATE}},
+                    {{tokens, n_rows}, {advantages, n_rows}, {old_logp, n_rows}, {ref_logp, n_rows}, {weights, n_rows}}))
+        return DLM_ERR_INVALID_ARG;
+    a.op = dlm::kTokenPolicy;
+    a.sums = 1;
+    a.advantages = advantages;
+    a.old_logp = old_logp;
+    a.ref_logp = p.kl_weight != 0.f ? ref_logp : nullptr;
+    a.weights = weights;
+    a.policy = dlm::PolicyRule{(float)(1.0 - (double)p.clip_low), (float)(1.0 + (double)p.clip_high), p.dual_clip,
+                               p.kl_weight, p.kl};
+    a.loss = loss;
+    a.logp = logp;
+    a.state = state;
+    return DLM_OK;
+}
+
+dlm_status dlm_policy_loss(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* tokens, double temperature, const float* advantages, const float* old_logp,
+                           const float* ref_logp, const float* weights, const dlm_policy_params* params, float* loss,
+                           float* logp, float* state, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::TokenArgs a;
+    const dlm_status st = policy_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, advantages,
+                                         old_logp, ref_logp, weights, params, loss, logp, state, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    return token_run(a, dtype, stream);
+}
+
+dlm_status dlm_policy_grad(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* tokens, double temperature, const float* state, const float* grad_loss,
+                           void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
+    return token_grad(dlm::kTokenPolicy, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, n_rows, state,
+                      grad_loss, grad, grad_stride, dev_status, stream);
+}
+
+dlm_status dlm_policy_step(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* tokens, double temperature, const float* advantages, const float* old_logp,
+                           const float* ref_logp, const float* weights, const dlm_policy_params* params, float* loss,
+                           float* logp, void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::TokenArgs a;
+    dlm_status st = policy_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, advantages,
+                                   old_logp, ref_logp, weights, params, loss, logp, nullptr, dev_status);
+    if (st != DLM_OK || n_rows == 0) return st;
+    st = grad_rows_ok(logits, dtype, n_rows, vocab, row_stride, grad, grad_stride);
+    if (st != DLM_OK) return st;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return token_run(a, dtype, stream);
+}
+
+size_t dlm_preference_workspace_size(int64_t n_rows, int64_t n_pairs) {
+    if (n_rows < 0 || n_pairs < 0) return 0;
+    return dlm::preference_workspace(n_rows, n_pairs);
+}
+
+static dlm_status preference_prepare(dlm::TokenArgs& a, const void* logits, dlm_dtype dtype, int64_t n_rows,
+                                     int64_t vocab, int64_t row_stride, const int32_t* tokens, double temperature,
+                                     const int32_t* offsets, int64_t n_pairs, const float* ref_logp,
+                                     const float* weights, const float* margins, const float* pair_weights,
+                                     const dlm_preference_params* params, float* loss, float* score, float* logp,
+                                     const void* scratch, size_t scratch_bytes, uint32_t* dev_status) {
+    if (!params || n_pairs < 0 || n_pairs > 0x3fffffffLL) return DLM_ERR_INVALID_ARG;
+    const dlm_preference_params& p = *params;
+    if (!(p.beta > 0.f && p.beta < INFINITY) || !(p.label_smoothing >= 0.f && p.label_smoothing <= 1.f) ||
+        p.kind < DLM_PREF_SIGMOID || p.kind > DLM_PREF_IPO || (p.kind != DLM_PREF_SIGMOID && p.label_smoothing != 0.f))
+        return DLM_ERR_INVALID_ARG;
+    const dlm_status st = token_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, dev_status);
+    if (st != DLM_OK) return st;
+    if (n_pairs > 0 && (!offsets || !loss)) return DLM_ERR_INVALID_ARG;
+    if (!aligned16(scratch)) return DLM_ERR_ALIGNMENT;
+    if (overlapping({{scratch, (int64_t)(scratch_bytes / 4)}, {loss, n_pairs}, {score, 2 * n_pairs}, {logp, n_rows}},
+                    {{tokens, n_rows}, {offsets, 2 * n_pairs + 1}, {ref_logp, n_rows}, {weights, n_rows},
+                     {margins, n_pairs}, {pair_weights, n_pairs}}))
+        return DLM_ERR_INVALID_ARG;
+    a.op = dlm::kTokenPreference;
+    a.sums = 1;
+    a.dev_status = dev_status;
+    a.offsets = offsets;
+    a.n_pairs = n_pairs;
+    a.ref_logp = ref_logp;
+    a.weights = weights;
+    a.margins = margins;
+    a.pair_weights = pair_weights;
+    a.preference = dlm::PreferenceRule{(double)p.beta, p.label_smoothing, p.kind};
+    a.loss = loss;
+    a.score = score;
+    a.logp = logp;
+    return DLM_OK;
+}
+
+dlm_status dlm_preference_loss(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                               const int32_t* tokens, double temperature, const int32_t* offsets, int64_t n_pairs,
+                               const float* ref_logp, const float* weights, const float* margins,
+                               const float* pair_weights, const dlm_preference_params* params, float* loss,
+                               float* score, float* logp, float* state, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::TokenArgs a;
+    if (n_rows > 0 && !state) return DLM_ERR_INVALID_ARG;
+    const dlm_status st = preference_prepare(
+        a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, offsets, n_pairs, ref_logp, weights, margins,
+        pair_weights, params, loss, score, logp, state, (size_t)(n_rows > 0 ? n_rows : 0) * DLM_TOKEN_STATE * 4, dev_status);
+    if (st != DLM_OK || (n_rows == 0 && n_pairs == 0)) return st;
+    a.state = state;
+    return token_run(a, dtype, stream);
+}
+
+dlm_status dlm_preference_grad(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                               const int32_t* tokens, double temperature, int64_t n_pairs, const float* state,
+                               const float* grad_loss, void* grad, int64_t grad_stride, uint32_t* dev_status,
+                               dlm_stream_t stream) {
+    if (n_pairs < 0) return DLM_ERR_INVALID_ARG;
+    return token_grad(dlm::kTokenPreference, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, n_pairs, state,
+                      grad_loss, grad, grad_stride, dev_status, stream);
+}
+
+dlm_status dlm_preference_step(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                               const int32_t* tokens, double temperature, const int32_t* offsets, int64_t n_pairs,
+                               const float* ref_logp, const float* weights, const float* margins,
+                               const float* pair_weights, const dlm_preference_params* params, float* loss,
+                               float* score, float* logp, void* grad, int64_t grad_stride, void* workspace,
+                               size_t ws_bytes, uint32_t* dev_status, dlm_stream_t stream) {
+    dlm::TokenArgs a;
+    const size_t need = dlm_preference_workspace_size(n_rows, n_pairs);
+    dlm_status st = preference_prepare(a, logits, dtype, n_rows, vocab, row_stride, tokens, temperature, offsets, n_pairs,
+                                       ref_logp, weights, margins, pair_weights, params, loss, score, logp, workspace, need,
+                                       dev_status);
+    if (st != DLM_OK || (n_rows == 0 && n_pairs == 0)) return st;
+    if (n_rows > 0) {
+        st = grad_rows_ok(logits, dtype, n_rows, vocab, row_stride, grad, grad_stride);
+        if (st != DLM_OK) return st;
+    }
+    if (!workspace || ws_bytes < need) return DLM_ERR_WORKSPACE;
+    a.workspace = workspace;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return token_run(a, dtype, stream);
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "dlm.h"
+#include "token_rules.h"
 
 namespace dlm {
 
@@ -269,6 +270,45 @@ struct DistillArgs {
 void distill_plan(DistillArgs& a, int dtype, int num_sms);  // split and slice_vecs
 cudaError_t launch_distill_loss(const DistillArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_distill_grad(const DistillArgs& a, int dtype, cudaStream_t s);
+
+// Log-probabilities of given tokens, the policy and the preference loss.
+enum { kTokenLogprob = 0, kTokenPolicy = 1, kTokenPreference = 2 };
+struct TokenArgs {
+    const void* logits;
+    int64_t n_rows, vocab, row_stride;
+    const int32_t* row_index; // nullable
+    int64_t n_src;            // rows the logits hold (0 = unchecked)
+    int gather;               // per-row arrays at r instead of q
+    const int32_t* tokens;
+    float scale, scale_lo;    // log2(e) / temperature in two floats
+    double inv_t;             // 1 / temperature
+    int op;                   // kToken*
+    int sums;                 // the rows' sums are taken (else the state has them)
+    const float* weights;     // [n_rows], nullable: 1
+    const float* advantages;  // policy
+    const float* old_logp;    // nullable: the ratio is 1
+    const float* ref_logp;    // nullable
+    PolicyRule policy;
+    const int32_t* offsets;   // preference: [2 n_pairs + 1]
+    int64_t n_pairs;
+    const float* margins;     // nullable
+    const float* pair_weights;
+    PreferenceRule preference;
+    float* loss;              // [n_rows], or [n_pairs]
+    float* score;             // [2 n_pairs], nullable
+    float* logp;              // nullable
+    float* lse;               // nullable
+    float* state;             // [n_rows][DLM_TOKEN_STATE], nullable
+    const float* grad_loss;   // nullable: 1
+    int64_t n_up;             // its entries
+    void* grad;               // nullable
+    int64_t grad_stride;
+    void* workspace;          // preference step
+    uint32_t* dev_status;
+    int num_sms;
+};
+size_t preference_workspace(int64_t n_rows, int64_t n_pairs);
+cudaError_t launch_token(const TokenArgs& a, int dtype, cudaStream_t s);
 
 // attention -> sums (every sequence) -> infl[b][j] = column sums over masked rows / (L H)
 cudaError_t launch_attention_influence(DapdArgs& a, int num_sms, float* infl, cudaStream_t s);

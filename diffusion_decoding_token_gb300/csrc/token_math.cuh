@@ -1,0 +1,194 @@
+// token_math.cuh -- what the losses over given tokens do with a row's sums (sm_103a;
+// the arithmetic also compiles for the host, where the tests compare it with long
+// double).
+//
+// One token a against all others: with m_o the others' largest logit and
+// s_o = sum_{v != a} exp((z_v - m_o) / T),
+//   ln p = -ln(1 + s_o)                              a at the row's maximum, s_o relative to it
+//   ln p = (z_a - m) / T - ln(s_o + e^((z_a - m) / T))   otherwise
+//   1 - p = s_o / (s_o + e_a)
+// The token's own weight never enters s_o, so ln p and 1 - p keep all their digits
+// when the row is sure of the token (as 1 - q from the whole sum 1 - p would be
+// rounded away from p = 1 - 2^-24 on, and the token's gradient with it).
+#pragma once
+
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "dlm.h"
+#include "token_rules.h"
+
+#ifndef DLM_HD
+#ifdef __CUDACC__
+#define DLM_HD __device__ __forceinline__
+#else
+#define DLM_HD inline
+#endif
+#endif
+
+namespace dlm {
+
+DLM_HD bool is_finite(float x) { return fabsf(x) < INFINITY; }
+DLM_HD float f32_nan() { return NAN; }
+
+// ln x for a normal x >= 1: the exponent's share in 64 bits, so that what is left to
+// the float logarithm is at most ln 2 / 2 (of x itself it is up to 14, and its last
+// place 2^-20).
+DLM_HD double ln_split(float x) {
+    uint32_t b;
+    memcpy(&b, &x, 4);
+    int e = (int)(b >> 23) - 127;
+    b = (b & 0x7fffffu) | 0x3f800000u;
+    float m;
+    memcpy(&m, &b, 4);
+    if (m > 1.41421354f) {
+        m *= 0.5f;
+        ++e;
+    }
+    return (double)e * 0.6931471805599453 + (double)logf(m);
+}
+
+// What follows from a row's sums: its maximum, 1 / sum, 1 - p of the token, and the
+// log-probabilities.  A row that holds NaN or +inf, or -inf only, has NaN in all but
+// m, and ok is 0.
+struct TokenRow {
+    float m, inv, away;
+    int ok;
+    double logp, lse;
+};
+
+// The others' sum s_o relative to m_o (-inf: there are none, or all are -inf), and the
+// token's logit.  exp of the two differences to the maximum m is the caller's: e_a of
+// (z_a - m) / T and e_o of (m_o - m) / T.
+DLM_HD TokenRow token_row(float m_o, float s_o, float z_a, float e_a, float e_o, double inv_t) {
+    TokenRow t;
+    t.m = z_a >= m_o ? z_a : m_o;
+    const float others = m_o > -INFINITY ? s_o * e_o : 0.f;
+    const float total = e_a + others;
+    // (total is 0 where nothing but -inf is)
+    t.ok = is_finite(t.m) && s_o >= 0.f && z_a < INFINITY && m_o < INFINITY && total > 0.f;
+    t.inv = 1.f / total;
+    t.away = others * t.inv;
+    // (where the token is at the maximum e_a is 1)
+    const double ln = z_a >= m_o && others < 0.5f ? (double)log1pf(others) : ln_split(total);
+    t.logp = ((double)z_a - (double)t.m) * inv_t - ln;
+    t.lse = (double)t.m * inv_t + ln;
+    if (!t.ok) {
+        t.inv = t.away = f32_nan();
+        t.logp = t.lse = (double)f32_nan();
+    }
+    return t;
+}
+
+// e^y - 1 - y without its cancellation near 0.
+DLM_HD float exp_past_line(float y) {
+    if (!(fabsf(y) < 1.f)) {
+        const float e = expm1f(y);
+        return e == INFINITY ? e : e - y;
+    }
+    // y^2 (1/2! + y/3! + y^2/4! + ...), up to y^11/13!: the next term is below 2^-36
+    float r = 1.f / 6227020800.f;
+    r = fmaf(y, r, 1.f / 479001600);
+    r = fmaf(y, r, 1.f / 39916800);
+    r = fmaf(y, r, 1.f / 3628800);
+    r = fmaf(y, r, 1.f / 362880);
+    r = fmaf(y, r, 1.f / 40320);
+    r = fmaf(y, r, 1.f / 5040);
+    r = fmaf(y, r, 1.f / 720);
+    r = fmaf(y, r, 1.f / 120);
+    r = fmaf(y, r, 1.f / 24);
+    r = fmaf(y, r, 1.f / 6);
+    r = fmaf(y, r, 0.5f);
+    return y * y * r;
+}
+
+// A loss and its derivative by the token's log-probability (or the score difference).
+struct LossSlope {
+    float loss, slope;
+};
+
+// A loss or a derivative that is not finite: the gradient is NaN.
+DLM_HD LossSlope flagged(LossSlope x) {
+    if (!is_finite(x.loss) || !is_finite(x.slope)) x.slope = f32_nan();
+    return x;
+}
+
+DLM_HD LossSlope policy_row(const PolicyRule& p, double logp, float weight, float advantage, bool has_old, float old_logp,
+                            float ref_logp) {
+    const float rho = has_old ? expf((float)(logp - (double)old_logp)) : 1.f;
+    const float a = advantage;
+    float gain = rho * a, slope = gain;
+    if (a > 0.f && rho > p.hi) {
+        gain = p.hi * a;
+        slope = 0.f;
+    } else if (a < 0.f && rho < p.lo) {
+        gain = p.lo * a;
+        slope = 0.f;
+    } else if (a < 0.f && p.dual > 0.f && rho > p.dual) {
+        gain = p.dual * a;
+        slope = 0.f;
+    } else if (a == 0.f && !(rho != rho)) {
+        gain = slope = 0.f;  // also of a ratio beyond a float's range
+    }
+    LossSlope r{-gain, -slope};
+    // (no ratio of its own: logp counts as old, and a row without one has no loss)
+    if (!has_old && !(logp > -INFINITY)) r.loss = r.slope = f32_nan();
+    if (p.kl_weight != 0.f) {
+        const float y = (float)((double)ref_logp - logp);
+        float kl, d;
+        if (p.kl == DLM_KL_K1) {
+            kl = -y;
+            d = 1.f;
+        } else if (p.kl == DLM_KL_K2) {
+            kl = 0.5f * y * y;
+            d = -y;
+        } else {
+            kl = exp_past_line(y);
+            d = -expm1f(y);
+        }
+        r.loss = fmaf(p.kl_weight, kl, r.loss);
+        r.slope = fmaf(p.kl_weight, d, r.slope);
+    }
+    r.loss *= weight;
+    r.slope *= weight;
+    return flagged(r);
+}
+
+// ln(1 + e^x)
+DLM_HD float softplus(float x) { return log1pf(expf(-fabsf(x))) + fmaxf(x, 0.f); }
+// 1 / (1 + e^-x)
+DLM_HD float sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    return (x >= 0.f ? 1.f : e) / (1.f + e);
+}
+
+// A pair's loss, and its derivative by the difference of the two scores.
+DLM_HD LossSlope preference_pair(const PreferenceRule& p, double chosen, double rejected, float margin, float weight) {
+    const double h64 = p.beta * (chosen - rejected) - (double)margin;
+    const float h = (float)h64;
+    LossSlope r;
+    if (p.kind == DLM_PREF_HINGE) {
+        const float short_of = (float)(1.0 - h64);
+        r.loss = short_of > 0.f ? short_of : (h != h ? h : 0.f);
+        r.slope = short_of > 0.f ? -(float)p.beta : (h != h ? h : 0.f);
+    } else if (p.kind == DLM_PREF_IPO) {
+        const double x = (h64 - 0.5) / p.beta;
+        r.loss = (float)(x * x);
+        r.slope = (float)(2.0 * x);
+    } else {
+        // (a smoothing of 0 leaves its side out: 0 times an infinite loss is NaN)
+        r.loss = p.smooth < 1.f ? (1.f - p.smooth) * softplus(-h) : 0.f;
+        r.slope = -(1.f - p.smooth) * sigmoid(-h);
+        if (p.smooth > 0.f) {
+            r.loss += p.smooth * softplus(h);
+            r.slope += p.smooth * sigmoid(h);
+        }
+        r.slope *= (float)p.beta;
+    }
+    r.loss *= weight;
+    r.slope *= weight;
+    return flagged(r);
+}
+
+}  // namespace dlm

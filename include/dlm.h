@@ -830,6 +830,192 @@ dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows
                             const float* teacher_lse, double temperature, const float* weights, float* loss,
                             void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
 
+/*
+ * dlm_row_logprob / dlm_row_logprob_grad / dlm_row_logprob_step -- the
+ * log-probability of one given token per row.
+ *
+ * Row q with token a, q_v = softmax(row / T):
+ *   logp = ln q_a,   lse = ln sum_v exp(z_v / T)
+ *   d logp / d z_v = ([v = a] - q_v) / T
+ * What a policy's or a reference's rollout needs stored for dlm_policy_loss and
+ * dlm_preference_loss, and, with weights, the likelihood bound that a masked
+ * diffusion model is trained on.
+ *
+ * The token is summed apart from all others: logp and 1 - q_a keep their digits
+ * where the row is sure of the token.  The others' sum of exponentials is held in
+ * 32 bits (within 2^-18 of itself, 2^-21 seen), which is what logp, lse, ratios and
+ * q are off by, beside their own rounding.  Equal inputs give equal bits on every
+ * launch of a call; two calls of different kind may sum in another order.
+ *
+ * dlm_row_logprob writes logp, lse and, if given, the state that
+ * dlm_row_logprob_grad takes to write grad[r] = grad_logp[r] * d logp[r] / d z.
+ * dlm_row_logprob_step writes logp and the gradient of sum_r weights[r] logp[r] in
+ * one launch.
+ *
+ * logits .. n_src_rows, flags : as in dlm_row_topk.  state needs row_index NULL.
+ * tokens      : int32 [.], row r's at o = q, or at o = r with DLM_ROWS_GATHER.  A
+ *               negative token is none (a position without a target): the row is
+ *               not read, logp and lse are 0, the gradient is 0.  One >= vocab is
+ *               treated as that and sets DLM_DEV_BAD_INDEX.
+ * temperature : DLM_MIN_TEMPERATURE <= T <= DLM_MAX_TEMPERATURE.
+ * weights     : nullable float [n_rows] (1).  A row of weight 0 is not read: logp 0,
+ *               gradient 0.  weights[r] / T has to be a finite float.
+ * logp, lse   : float outputs at o; lse nullable.
+ * state       : float [n_rows][DLM_TOKEN_STATE], opaque, 16-byte aligned; nullable.
+ *               The gradient call must get the logits, tokens and temperature of
+ *               the call that wrote it.
+ * grad_logp   : nullable float [n_rows] (1); 0 writes a zero row unread.
+ * grad        : [n_rows][grad_stride] in the logits' dtype, aligned like them; may
+ *               be the logits' memory itself (same base and stride), else it must
+ *               not overlap it.  Elements past vocab are left alone.
+ * dev_status  : DLM_DEV_NONFINITE for a row that holds NaN or +inf, or -inf only:
+ *               its logp, lse and gradient are NaN.  (The gradient calls write such
+ *               a row's NaN and set no status.)  A token at -inf has logp -inf,
+ *               which sets no status here.
+ * Outputs may overlap neither each other nor an input, but for grad as said
+ * (per-row arrays that do are DLM_ERR_INVALID_ARG).
+ */
+#define DLM_TOKEN_STATE 8
+
+dlm_status dlm_row_logprob(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* row_index, int64_t n_src_rows, const int32_t* tokens, double temperature,
+                           float* logp, float* lse, float* state, uint32_t* dev_status, uint32_t flags,
+                           dlm_stream_t stream);
+
+dlm_status dlm_row_logprob_grad(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                                const int32_t* tokens, double temperature, const float* state, const float* grad_logp,
+                                void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
+
+dlm_status dlm_row_logprob_step(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                                const int32_t* tokens, double temperature, const float* weights, float* logp, void* grad,
+                                int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
+
+/*
+ * dlm_policy_loss / dlm_policy_grad / dlm_policy_step -- the clipped policy loss
+ * with a KL term, per row.
+ *
+ * With logp as in dlm_row_logprob, rho = exp(logp - old_logp[r]), A = advantages[r],
+ * y = ref_logp[r] - logp:
+ *   gain = min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
+ *          (A < 0 and dual_clip c > 0: max(gain, c A))
+ *   kl   = -y (DLM_KL_K1),  y^2 / 2 (DLM_KL_K2)  or  e^y - 1 - y (DLM_KL_K3)
+ *   loss[r] = weights[r] (kl_weight kl - gain)
+ *   d loss / d logp = weights[r] (kl_weight d kl / d logp - [gain is rho A] rho A)
+ * The derivative of kl is 1, -y or 1 - e^y.  At a border of the clip gain is rho A.
+ *
+ * logits, tokens, temperature, weights, state, grad, dev_status : as in
+ *               dlm_row_logprob_step (a row without a token or of weight 0: loss 0,
+ *               logp 0, gradient 0).
+ * advantages  : float [n_rows].
+ * old_logp    : nullable float [n_rows], the rollout policy's log-probabilities.
+ *               Without it rho is 1 and its derivative A: the policy is the
+ *               rollout's own.
+ * ref_logp    : float [n_rows], the reference policy's; nullable (and not read)
+ *               where kl_weight is 0.
+ * params      : 0 <= clip_low <= 1, clip_high >= 0 (INFINITY: no clip), dual_clip 0
+ *               or >= 1, kl_weight >= 0 and finite, kl one of DLM_KL_*.
+ * loss, logp  : float [n_rows] outputs; logp nullable.
+ * grad_loss   : nullable float [n_rows] (1): grad[r] = grad_loss[r] * d loss[r] / d z.
+ * dev_status  : DLM_DEV_NONFINITE also for a row whose loss or its derivative by
+ *               logp is not finite (a token at -inf with a KL term, a ratio beyond a
+ *               float's range): the loss is what the formula gives, the gradient NaN.
+ */
+#define DLM_KL_K1 1
+#define DLM_KL_K2 2
+#define DLM_KL_K3 3
+
+typedef struct dlm_policy_params {
+    float clip_low;
+    float clip_high;
+    float dual_clip;
+    float kl_weight;
+    int32_t kl;
+} dlm_policy_params;
+
+dlm_status dlm_policy_loss(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* tokens, double temperature, const float* advantages, const float* old_logp,
+                           const float* ref_logp, const float* weights, const dlm_policy_params* params, float* loss,
+                           float* logp, float* state, uint32_t* dev_status, dlm_stream_t stream);
+
+dlm_status dlm_policy_grad(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* tokens, double temperature, const float* state, const float* grad_loss,
+                           void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
+
+dlm_status dlm_policy_step(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                           const int32_t* tokens, double temperature, const float* advantages, const float* old_logp,
+                           const float* ref_logp, const float* weights, const dlm_policy_params* params, float* loss,
+                           float* logp, void* grad, int64_t grad_stride, uint32_t* dev_status, dlm_stream_t stream);
+
+/*
+ * dlm_preference_loss / dlm_preference_grad / dlm_preference_step -- the
+ * preference loss of pairs of sequences, from the log-ratios of their tokens.
+ *
+ * Sequence s is rows [offsets[s], offsets[s + 1]); pair i is sequences 2i (chosen)
+ * and 2i + 1 (rejected).  With logp as in dlm_row_logprob:
+ *   score[s] = sum over its rows of weights[r] (logp - ref_logp[r])
+ *   h = beta (score[2i] - score[2i + 1]) - margins[i]
+ *   l = -(1 - label_smoothing) ln sigma(h) - label_smoothing ln sigma(-h)   DLM_PREF_SIGMOID
+ *     = max(0, 1 - h)                                                       DLM_PREF_HINGE
+ *     = ((h - 1/2) / beta)^2                                                DLM_PREF_IPO
+ *   loss[i] = pair_weights[i] l
+ *   d loss[i] / d logp[r] = +- pair_weights[i] l'(h) beta weights[r]
+ * (the hinge's derivative at h = 1 is 0).  Scores are summed in 64 bits in a fixed
+ * order.  A sequence may be empty: its score is 0.  Rows in no sequence have a logp
+ * and the gradient 0.
+ *
+ * logits, tokens, temperature, weights, grad : as in dlm_row_logprob_step (a row
+ *               without a token or of weight 0 adds nothing; logp 0, gradient 0).
+ * offsets     : int32 [2 n_pairs + 1], ascending, within [0, n_rows].  Others are
+ *               taken as the nearest that are (an offset below a predecessor as
+ *               that) and set DLM_DEV_BAD_INDEX.
+ * ref_logp    : nullable float [n_rows] (0: no reference; a sequence's score is then
+ *               the weighted sum of its log-probabilities).
+ * margins, pair_weights : nullable float [n_pairs] (0, 1).
+ * params      : beta > 0 and finite; 0 <= label_smoothing <= 1, 0 unless
+ *               DLM_PREF_SIGMOID; kind one of DLM_PREF_*.
+ * loss, score : float [n_pairs] / [2 n_pairs] outputs; score nullable.
+ * logp        : nullable float [n_rows] output.
+ * state       : float [n_rows][DLM_TOKEN_STATE], opaque, 16-byte aligned; required.
+ * grad_loss   : nullable float [n_pairs] (1).
+ * workspace   : dlm_preference_workspace_size(n_rows, n_pairs) bytes, 16-byte
+ *               aligned; calls sharing it must not overlap.  Nothing need be in it,
+ *               and nothing is kept in it.
+ * dev_status  : DLM_DEV_NONFINITE for a row as in dlm_row_logprob and for a pair whose
+ *               loss or its derivative is not finite: the loss is what the formula
+ *               gives, the gradient of all its rows NaN.  A row with NaN makes its
+ *               pair's loss NaN.  DLM_DEV_TIMEOUT if dlm_preference_step's wait for
+ *               a pair's other rows gave up: its outputs are then unspecified.
+ */
+#define DLM_PREF_SIGMOID 0
+#define DLM_PREF_HINGE 1
+#define DLM_PREF_IPO 2
+
+typedef struct dlm_preference_params {
+    float beta;
+    float label_smoothing;
+    int32_t kind;
+} dlm_preference_params;
+
+size_t dlm_preference_workspace_size(int64_t n_rows, int64_t n_pairs);
+
+dlm_status dlm_preference_loss(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                               const int32_t* tokens, double temperature, const int32_t* offsets, int64_t n_pairs,
+                               const float* ref_logp, const float* weights, const float* margins,
+                               const float* pair_weights, const dlm_preference_params* params, float* loss,
+                               float* score, float* logp, float* state, uint32_t* dev_status, dlm_stream_t stream);
+
+dlm_status dlm_preference_grad(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                               const int32_t* tokens, double temperature, int64_t n_pairs, const float* state,
+                               const float* grad_loss, void* grad, int64_t grad_stride, uint32_t* dev_status,
+                               dlm_stream_t stream);
+
+dlm_status dlm_preference_step(const void* logits, dlm_dtype dtype, int64_t n_rows, int64_t vocab, int64_t row_stride,
+                               const int32_t* tokens, double temperature, const int32_t* offsets, int64_t n_pairs,
+                               const float* ref_logp, const float* weights, const float* margins,
+                               const float* pair_weights, const dlm_preference_params* params, float* loss,
+                               float* score, float* logp, void* grad, int64_t grad_stride, void* workspace,
+                               size_t ws_bytes, uint32_t* dev_status, dlm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
