@@ -275,8 +275,8 @@ def test_the_same_row_picked_twice(dlm):
     token = tokens_of(z, 4)
     index = np.array([4, 4, 4, 8, 4], np.int32)
     out = dlm.row_logprob(on_gpu(z), cuda(token[index]), row_index=cuda(index), gather=True)
-    want = dlm.row_logprob(on_gpu(z[[4, 8]]), cuda(token[[4, 8]]))
-    near(float(out.logp[0]), float(want.logp[0]), 2.0 ** -17, 0)
+    want = dlm.row_logprob(on_gpu(z), cuda(token))
+    near(float(out.logp[0]), float(want.logp[4]), 2.0 ** -17, 0)
     assert (out.logp[[1, 2, 4]] == out.logp[0]).all() and (out.lse[[1, 2, 4]] == out.lse[0]).all()
 
 
@@ -660,8 +660,8 @@ def test_captured_steps_replay_on_new_inputs(dlm, n, vocab):
     adv, w = torch.randn(n, device="cuda"), torch.rand(n, device="cuda")
     offsets = torch.tensor([0, n // 3, n // 2, n - 5, n], dtype=torch.int32, device="cuda")
     f = lambda k: torch.empty(k, device="cuda")  # noqa: E731
-    one = dlm.PolicyStep(f(n), f(n), torch.empty_like(z))
-    two = dlm.PreferenceStep(f(2), f(4), f(n), torch.empty_like(z))
+    one = dlm.PolicyStep(f(n), f(n), on_gpu(z))
+    two = dlm.PreferenceStep(f(2), f(4), f(n), on_gpu(z))
     ws = dlm.preference_workspace(n, 2, "cuda")
     ws.fill_(255)                      # whatever a workspace holds before a call
     g = graph_of(lambda: dlm.policy_step(z, token, adv, weights=w, out=one))
