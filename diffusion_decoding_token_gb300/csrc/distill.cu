@@ -75,7 +75,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float or_zero(float ref) { return ref > -INFINITY ? ref : 0.f; }
 __device__ __forceinline__ bool is_twice(float listed) { return __float_as_uint(listed) >> 31; }
 
 // A sum that is relative to `ref` relative to `to` (-inf: nothing, and 0).
@@ -464,13 +463,6 @@ __device__ __forceinline__ void finish_loss(const DistillArgs& a, const List& l,
     if (!fine) raise_status(a.dev_status, DLM_DEV_NONFINITE);
 }
 
-// 2^((z - ref) c) with c in two floats (one float's rounding, the same for every
-// token, would show in the loss's seventh digit).
-__device__ __forceinline__ f2 weights_of(f2 z, f2 ref, f2 c, f2 c_lo) {
-    const f2 d = sub2(z, ref);
-    return ex2x2(fma2(d, c, mul2(d, c_lo)));  // the large product inside the fma: one rounding of it less
-}
-
 // Sums of vectors [v0, v1) of a row (kThreads threads; the whole CTA calls).  The
 // listed tokens are taken out of the vectors first, so that a batch's arithmetic
 // is straight code with one test for a new reference (with a branch on the mask
@@ -602,46 +594,6 @@ __device__ __forceinline__ void started(const Cluster& cl) {
 }
 __device__ __forceinline__ void all_started(const Cluster& cl) {
     if (cl.split > 1) cg::this_cluster().barrier_wait();
-}
-
-// One float to storage.
-template <int DT>
-__device__ __forceinline__ void store_elem(void* row, int64_t i, float x) {
-    if constexpr (DT == DLM_F32)
-        static_cast<float*>(row)[i] = x;
-    else if constexpr (DT == DLM_BF16)
-        static_cast<__nv_bfloat16*>(row)[i] = __float2bfloat16_rn(x);
-    else
-        static_cast<__half*>(row)[i] = __float2half_rn(x);
-}
-
-// scale * 2^((z - m) c) of a vector, in storage.
-struct Slope {
-    f2 m, c, scale;
-    __device__ Slope(float m1, float c1, float s1) : m(pack2(m1, m1)), c(pack2(c1, c1)), scale(pack2(s1, s1)) {}
-};
-template <int DT>
-__device__ __forceinline__ uint4 slope_of(uint4 w, const Slope& s) {
-    constexpr int EPV = Row<DT>::EPV;
-    float z[EPV];
-    Row<DT>::unpack(w, z);
-    uint32_t r[4];
-#pragma unroll
-    for (int p = 0; p < EPV / 2; ++p) {
-        float x, y;
-        unpack2(mul2(ex2x2(mul2(sub2(pack2(z[2 * p], z[2 * p + 1]), s.m), s.c)), s.scale), x, y);
-        if constexpr (DT == DLM_F32) {
-            r[2 * p] = __float_as_uint(x);
-            r[2 * p + 1] = __float_as_uint(y);
-        } else if constexpr (DT == DLM_BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-            r[p] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-            const __half2 h = __floats2half2_rn(x, y);
-            r[p] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    }
-    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // scale * 2^((z - m) c) for vectors [v0, v1) of the row; scale = 0 writes

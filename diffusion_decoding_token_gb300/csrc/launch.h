@@ -306,6 +306,9 @@ struct TokenArgs {
     void* workspace;          // preference step
     uint32_t* dev_status;
     int num_sms;
+    int split;                // CTAs per row (thread-block cluster size)
+    int ring;                 // chunks of a row that a CTA holds
+    int resident;             // a step's row stays there between its sums and its gradient
 };
 size_t preference_workspace(int64_t n_rows, int64_t n_pairs);
 cudaError_t launch_token(const TokenArgs& a, int dtype, cudaStream_t s);

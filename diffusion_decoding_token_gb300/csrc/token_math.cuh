@@ -58,20 +58,36 @@ struct TokenRow {
     double logp, lse;
 };
 
+// x 2^e to 2^-22 for e <= 0 of any size (as a float's product, e would be off by 2^-24 of
+// itself: 2^-17 at e = 115).
+DLM_HD float times_exp2(float x, double e) {
+    if (!(e >= -200.0)) return e != e ? f32_nan() : 0.f;
+    const double n = rint(e);
+    return ldexpf(x * exp2f((float)(e - n)), (int)n);
+}
+
+// The hardware's 2^x, which the weights are made with, is a little too small on average
+// (2^-25 over arguments in [-1, 0), 2^-22.7 at most): a row's sum of thousands of them by
+// 2^-24.3 (4.0e-8 to 5.8e-8 over rows of 32000 and 152064 N(0, 4) logits of each type;
+// its rounding scatters by as much).  A sequence's score is a sum of thousands of
+// log-sum-exps, all off to that side, so it is put right where the weights are summed.
+constexpr double kWeightsLow = 4.8e-8;
+
 // The others' sum s_o relative to m_o (-inf: there are none, or all are -inf), and the
-// token's logit.  exp of the two differences to the maximum m is the caller's: e_a of
-// (z_a - m) / T and e_o of (m_o - m) / T.
-DLM_HD TokenRow token_row(float m_o, float s_o, float z_a, float e_a, float e_o, double inv_t) {
+// token's logit.
+DLM_HD TokenRow token_row(float m_o, float s_o, float z_a, double inv_t) {
+    const double log2_t = 1.4426950408889634 * inv_t;
     TokenRow t;
     t.m = z_a >= m_o ? z_a : m_o;
-    const float others = m_o > -INFINITY ? s_o * e_o : 0.f;
+    const float e_a = times_exp2(1.f, ((double)z_a - (double)t.m) * log2_t);
+    const float others = m_o > -INFINITY ? times_exp2(s_o, ((double)m_o - (double)t.m) * log2_t) : 0.f;
     const float total = e_a + others;
     // (total is 0 where nothing but -inf is)
     t.ok = is_finite(t.m) && s_o >= 0.f && z_a < INFINITY && m_o < INFINITY && total > 0.f;
     t.inv = 1.f / total;
     t.away = others * t.inv;
     // (where the token is at the maximum e_a is 1)
-    const double ln = z_a >= m_o && others < 0.5f ? (double)log1pf(others) : ln_split(total);
+    const double ln = (z_a >= m_o && others < 0.5f ? (double)log1pf(others) : ln_split(total)) + kWeightsLow * (double)t.away;
     t.logp = ((double)z_a - (double)t.m) * inv_t - ln;
     t.lse = (double)t.m * inv_t + ln;
     if (!t.ok) {

@@ -28,10 +28,14 @@ int main() {
         // a token at the maximum and below it, the others' sum from 2^-60 to 2^20
         const float m_o = (float)(drand48() * 8), z = m_o + (float)((drand48() - 0.5) * (i % 2 ? 40 : 1));
         const float s_o = (float)exp((drand48() - 0.75) * 50) + (i % 2 ? 1.f : 0.f);
-        const float m = fmaxf(m_o, z), ea = exp2f((z - m) * 1.44269502f), eo = exp2f((m_o - m) * 1.44269502f);
-        const TokenRow t = token_row(m_o, s_o, z, ea, eo, 1.0);
-        const long double o = (long double)s_o * eo, a = ea;
-        const long double want = z >= m_o ? -log1pl(o) : (long double)z - m - logl(a + o);
+        const double inv_t = i % 7 ? 1.0 : 5.0;
+        const float m = fmaxf(m_o, z);
+        const TokenRow t = token_row(m_o, s_o, z, inv_t);
+        // (the weights that s_o is the sum of are taken for this much too small)
+        const long double a = expl(((long double)z - m) * inv_t),
+                          o = (long double)s_o * (1 + (long double)kWeightsLow) * expl(((long double)m_o - m) * inv_t);
+        const long double want = z >= m_o ? -log1pl(o) : ((long double)z - m) * inv_t - logl(a + o);
+        if (o < 1.2e-38L) continue;  // below a normal float
         logp = fmax(logp, (double)(fabsl(t.logp - want) / fmaxl(fabsl(want) * 4, z >= m_o && o < 0.5L ? 0.L : 1.L)));
         away = fmax(away, off(t.away, o / (a + o)));
         if (!t.ok) return 2;
@@ -75,8 +79,8 @@ int main() {
     printf("ln %.3g line %.3g logp %.3g away %.3g policy %.3g pair %.3g\n", ln, line, logp, away, pol, pair);
     const float u = 5.9604645e-8f;  // 2^-24
     // ln: half of the values' ulp (|.| <= 0.35: 2^-26) and logf's; line: series of 13 roundings or expm1f - y;
-    // logp: of o (1 rounding) and log1pf, or absolute; away: 4 roundings; policy: expf and 6; pair: 8 and e^h's
-    int bad = ln > u || line > 8 * u || logp > 4 * u || away > 6 * u || pol > 10 * u || pair > 12 * u;
+    // logp: of o (5 roundings: e^n and its product) and log1pf, a quarter of it, or absolute; away: 10 roundings; policy: expf and 6; pair: 8 and e^h's
+    int bad = ln > u || line > 8 * u || logp > 4 * u || away > 10 * u || pol > 10 * u || pair > 12 * u;
     // what is not finite
     const LossSlope n1 = policy_row(PolicyRule{0.8f, 1.2f, 0.f, 0.f, 1}, -INFINITY, 1.f, -2.f, true, -3.f, 0.f);
     bad |= n1.loss != 1.6f || n1.slope != 0.f;                                     // ratio 0, clipped from below
@@ -100,14 +104,16 @@ int main() {
     bad |= p4.loss != 0.f || p4.slope != 0.f;                                      // the hinge's corner
     const LossSlope p5 = preference_pair(PreferenceRule{1.0, 1.f, 0}, -INFINITY, 0.0, 0.f, 1.f);
     bad |= p5.loss != 0.f || p5.slope != 0.f;                                      // labels turned round
-    const TokenRow r1 = token_row(-INFINITY, 0.f, 3.f, 1.f, 0.f, 1.0);
+    const TokenRow r1 = token_row(-INFINITY, 0.f, 3.f, 1.0);
     bad |= !r1.ok || r1.logp != 0.0 || r1.away != 0.f || r1.lse != 3.0;            // the only token
-    const TokenRow r2 = token_row(-3.4028235e38f, 0.f, -INFINITY, 0.f, 1.f, 1.0);
+    const TokenRow r2 = token_row(-3.4028235e38f, 0.f, -INFINITY, 1.0);
     bad |= r2.ok || r2.logp == r2.logp || r2.inv == r2.inv;                        // nothing but -inf
-    const TokenRow r3 = token_row(1.f, 2.f, -INFINITY, 0.f, 1.f, 1.0);
+    const TokenRow r3 = token_row(1.f, 2.f, -INFINITY, 1.0);
     bad |= !r3.ok || r3.logp != -INFINITY || r3.away != 1.f;
-    const TokenRow r4 = token_row(1.f, NAN, 0.f, 1.f, 1.f, 1.0), r5 = token_row(1.f, 1.f, NAN, NAN, 1.f, 1.0),
-                   r6 = token_row(INFINITY, 1.f, 0.f, 0.f, NAN, 1.0), r7 = token_row(1.f, 1.f, INFINITY, NAN, 0.f, 1.0);
+    const TokenRow r4 = token_row(1.f, NAN, 0.f, 1.0), r5 = token_row(1.f, 1.f, NAN, 1.0),
+                   r6 = token_row(INFINITY, 1.f, 0.f, 1.0), r7 = token_row(1.f, 1.f, INFINITY, 1.0);
+    const TokenRow r8 = token_row(0.f, 1.f, 2000.f, 1.0), r9 = token_row(2000.f, 1.f, 0.f, 1.0);
+    bad |= r8.logp != 0.0 || r8.away != 0.f || r9.away != 1.f || r9.logp > -2000.0 || r9.logp < -2000.0001;
     bad |= r4.ok || r5.ok || r6.ok || r7.ok;
     return bad;
 }
