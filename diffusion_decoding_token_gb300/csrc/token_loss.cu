@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kThreads = kRowThreads;   // consumers: threads that do the arithmetic
 constexpr int kWarps = kRowWarps;
-constexpr int kBlock = kThreads + 32;   // and the warp that fetches
+constexpr int kBlock = kThreads + 64;   // and the warps that finish rows and that fetch them
 constexpr int kPerThread = 2;           // vectors of a chunk per thread
 constexpr int kChunkVecs = kPerThread * kThreads, kChunkBytes = kChunkVecs * 16;
 constexpr int kItems = 4;               // rows that the fetching warp may be ahead
@@ -299,87 +299,143 @@ __device__ __forceinline__ TokenRow merge_row(const TokenArgs& a, const Shared& 
         p.z = max_nan(p.z, b.z);
     }
     p = warp_part(p, c);
-    return token_row(p.ref, p.sum, p.z, a.inv_t);
+    return token_row(p.ref, p.sum, p.z, a.scale, a.scale_lo, a.inv_t);
 }
 
 // The fetching warp's thread: rows in the order in which the hardware gives them, their
-// settings, and their slices chunk by chunk into the ring.
+// settings, and their slices chunk by chunk into the ring.  What the next row needs is
+// asked for while this row's chunks are on their way: the row itself (about 1 us), then
+// its token and weight (another), which are not looked at before the row's turn.
 template <int DT, bool SUMS, bool GRAD>
-__device__ bool fetch_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, int rank, Cursor& cur, uint32_t& issued) {
-    const int64_t V = a.vocab;
-    const TokenSlice<DT> sl(V, a.split, rank);
-    int64_t r = blockIdx.x / a.split;
-    const int passes = SUMS && GRAD && !a.resident ? 2 : 1;
-    bool more = true;
-    for (uint32_t i = 0;; ++i) {
-        Item it{};
-        it.kind = kEnd;
-        if (more) {
-            it.kind = kRow;
-            it.q = r;
-            if (SUMS && a.row_index) {
-                it.q = a.row_index[r];
-                if (it.q < 0 || (a.n_src > 0 && it.q >= a.n_src)) {
-                    it.kind = kSkip;
-                    if (rank == 0) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
-                }
-            }
-            it.o = a.gather ? r : it.q;
-            if (it.kind == kRow) {
-                it.token = a.tokens[it.o];
-                bool none = it.token < 0 || it.token >= V;
-                if (SUMS) {
-                    it.weight = a.weights ? a.weights[it.o] : 1.f;
-                    none = none || it.weight == 0.f;
-                    if (it.token >= V && rank == 0) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
-                } else {
-                    const float4 s = *reinterpret_cast<const float4*>(a.state + r * DLM_TOKEN_STATE);
-                    it.m = s.x;
-                    it.inv = s.y;
-                    it.away = s.z;
-                    it.k = s.w * (float)a.inv_t;
-                    if (a.grad_loss) {
-                        const int64_t at = a.op == kTokenPreference ? (int64_t)__float_as_int(a.state[r * DLM_TOKEN_STATE + 6]) : r;
-                        it.k *= at >= 0 && at < a.n_up ? a.grad_loss[at] : 0.f;
-                    }
-                    none = none || it.k == 0.f || it.inv == 0.f;
-                }
-                if (none) it.kind = kNone;
+struct Fetcher {
+    const TokenArgs& a;
+    Shared& sh;
+    unsigned char* ring;
+    const int rank;
+    const TokenSlice<DT> sl;
+    Cursor cur;
+    uint32_t issued = 0;
+    Item next_item{};
+    uint32_t asked = 0, answers = 0;     // (asked: the first CTA's)
+    bool have_next = false;                      // next_item is being read
+
+    __device__ Fetcher(const TokenArgs& args, Shared& s, unsigned char* r, int k)
+        : a(args), sh(s), ring(r), rank(k), sl(args.vocab, args.split, k) {}
+
+    // Starts to read what belongs to row r.
+    __device__ __forceinline__ void read_row(int64_t r) {
+        Item& it = next_item;
+        it.kind = kRow;
+        it.q = r;
+        if (SUMS && a.row_index) {
+            it.q = a.row_index[r];
+            if (it.q < 0 || (a.n_src > 0 && it.q >= a.n_src)) {
+                it.kind = kSkip;
+                if (rank == 0) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
             }
         }
-        const int slot = i % kItems;
-        if (!wait_for(&sh.item_empty[slot], ((i / kItems) & 1u) ^ 1u)) return false;
-        sh.item[slot] = it;
-        arrive(&sh.item_full[slot]);
-        if (it.kind == kEnd) return true;
-        if (it.kind == kRow) {
-            const char* src = static_cast<const char*>(a.logits) + it.q * a.row_stride * Row<DT>::ESZ + (int64_t)sl.v0 * 16;
-            for (int pass = 0; pass < passes; ++pass)
-                for (int c = 0; c < sl.chunks; ++c) {
-                    if (!wait_for(&sh.empty[cur.at], cur.parity ^ 1u)) return false;
-                    const uint32_t bytes = (uint32_t)min(kChunkVecs, sl.whole - c * kChunkVecs) * 16;
-                    mbar_expect_tx(&sh.full[cur.at], bytes);
-                    fetch(ring + cur.at * kChunkBytes, src + (int64_t)c * kChunkBytes, bytes, &sh.full[cur.at]);
-                    cur.step(a.ring);
-                    ++issued;
-                }
-        }
-        // the next row: asked for when this one was begun
-        if (!wait_for(&sh.next, i & 1u)) return false;
-        uint32_t cta;
-        more = next_cta(sh.answer, cta);
-        r = cta / a.split;
-        if (more) {
-            mbar_expect_tx(&sh.next, 16);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the answer has been read before the next one is written
-            arrive_at(&sh.next_free, 0);
-            if (rank == 0) {
-                if (!wait_for(&sh.next_free, i & 1u)) return false;
-                ask_next(sh.answer, &sh.next, a.split > 1);
+        it.o = a.gather ? r : it.q;
+        if (it.kind != kRow) return;
+        it.token = a.tokens[it.o];
+        if (SUMS) {
+            it.weight = a.weights ? a.weights[it.o] : 1.f;
+        } else {
+            const float4 s = *reinterpret_cast<const float4*>(a.state + r * DLM_TOKEN_STATE);
+            it.m = s.x;
+            it.inv = s.y;
+            it.away = s.z;
+            it.k = s.w;
+            it.weight = 1.f;
+            if (a.grad_loss) {
+                const int64_t at = a.op == kTokenPreference ? (int64_t)__float_as_int(a.state[r * DLM_TOKEN_STATE + 6]) : r;
+                it.weight = at >= 0 && at < a.n_up ? a.grad_loss[at] : 0.f;
             }
         }
     }
-}
+    // The item that read_row() began.
+    __device__ __forceinline__ Item row_read() {
+        Item it = next_item;
+        if (it.kind == kRow) {
+            bool none = it.token < 0 || it.token >= a.vocab;
+            if (SUMS) {
+                none = none || it.weight == 0.f;
+                if (it.token >= a.vocab && rank == 0) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
+            } else {
+                it.k *= (float)a.inv_t * it.weight;
+                none = none || it.k == 0.f || it.inv == 0.f;
+            }
+            if (none) it.kind = kNone;
+        }
+        return it;
+    }
+    // The first CTA asks for a row once every CTA has read the last answer.
+    __device__ __forceinline__ bool ask(bool block) {
+        if (rank != 0 || asked > answers) return true;
+        if (asked > 0) {
+            const uint32_t parity = (asked - 1) & 1u;
+            if (block ? !wait_for(&sh.next_free, parity) : !mbar_test_wait(&sh.next_free, parity)) return !block;
+        }
+        ask_next(sh.answer, &sh.next, a.split > 1);
+        ++asked;
+        return true;
+    }
+    // Takes the answer if it is there (block: waits for it).
+    __device__ __forceinline__ bool look_ahead(bool block) {
+        if (have_next) return ask(false);
+        if (!ask(block)) return false;
+        if (block ? !wait_for(&sh.next, answers & 1u) : !mbar_test_wait(&sh.next, answers & 1u)) return !block;
+        uint32_t cta;
+        const bool more = next_cta(sh.answer, cta);
+        ++answers;
+        have_next = true;
+        next_item.kind = kEnd;
+        if (!more) {
+            asked = answers + 1;  // and nothing is asked for any more
+            return true;
+        }
+        mbar_expect_tx(&sh.next, 16);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the answer has been read before the next one is written
+        arrive_at(&sh.next_free, 0);
+        read_row(cta / a.split);
+        return ask(false);
+    }
+    __device__ bool run() {
+        const int passes = SUMS && GRAD && !a.resident ? 2 : 1;
+        read_row(blockIdx.x / a.split);
+        for (uint32_t i = 0;; ++i) {
+            const Item it = row_read();
+            have_next = false;
+            const int slot = i % kItems;
+            if (!wait_for(&sh.item_empty[slot], ((i / kItems) & 1u) ^ 1u)) return false;
+            sh.item[slot] = it;
+            arrive(&sh.item_full[slot]);
+            if (it.kind == kEnd) return true;
+            if (it.kind == kRow) {
+                const char* src = static_cast<const char*>(a.logits) + it.q * a.row_stride * Row<DT>::ESZ + (int64_t)sl.v0 * 16;
+                for (int pass = 0; pass < passes; ++pass)
+                    for (int c = 0; c < sl.chunks; ++c) {
+                        if (!wait_for(&sh.empty[cur.at], cur.parity ^ 1u)) return false;
+                        const uint32_t bytes = (uint32_t)min(kChunkVecs, sl.whole - c * kChunkVecs) * 16;
+                        mbar_expect_tx(&sh.full[cur.at], bytes);
+                        fetch(ring + cur.at * kChunkBytes, src + (int64_t)c * kChunkBytes, bytes, &sh.full[cur.at]);
+                        cur.step(a.ring);
+                        ++issued;
+                        look_ahead(false);
+                    }
+            }
+            if (!have_next && !look_ahead(true)) return false;
+        }
+    }
+    // Copies still in flight land before the CTA ends.
+    __device__ void drain() {
+        Cursor c;
+        for (uint32_t i = 0; i < issued; ++i) {
+            if (i + a.ring >= issued) wait_for(&sh.full[c.at], c.parity);
+            c.step(a.ring);
+        }
+        wait_for(&sh.next, answers & 1u);
+    }
+};
 
 // Zeros where a row has no gradient.
 template <int DT>
@@ -391,7 +447,42 @@ __device__ void write_zeros(char* out, int64_t V, const TokenSlice<DT>& sl) {
         for (int64_t e = (int64_t)(sl.v0 + sl.whole) * Row<DT>::EPV + t; e < V; e += kThreads) store_elem<DT>(out, e, 0.f);
 }
 
-// The other warps: sums of their slice, the loss, the gradient.
+// A warp of its own finishes the rows: it waits for all CTAs' shares, merges them and
+// works the loss out, while the others go on.  (One of them doing this too was what a
+// row took: about 2 us for each.)  With a gradient every CTA's does, to go on with the
+// slope; the first CTA's writes.
+template <int DT, bool GRAD>
+__device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
+    const int lane = threadIdx.x & 31, n_parts = a.split * kWarps;
+    uint32_t rows = 0;
+    for (uint32_t i = 0;; ++i) {
+        const int slot = i % kItems;
+        if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
+        const int kind = sh.item[slot].kind;
+        const int64_t o = sh.item[slot].o;
+        if (kind == kEnd) return true;
+        if (kind == kNone && rank == 0 && lane == 0) finish_none(a, o);
+        if (kind == kRow) {
+            if (GRAD || rank == 0) {
+                const RowInputs in = row_inputs(a, o, sh.item[slot].weight);
+                const int ps = rows % kSlots;
+                if (lane == 0) mbar_expect_tx(&sh.shares[ps], n_parts * (uint32_t)sizeof(Part));
+                if (!wait_warp(&sh.shares[ps], (rows / kSlots) & 1u)) return false;
+                const TokenRow x = merge_row(a, sh, ps, n_parts);
+                const float slope = finish_row(a, o, x, in, rank == 0 && lane == 0);
+                if (GRAD && lane == 0) {
+                    sh.row[rows & 1] = make_float4(x.m, x.inv, x.away, slope);
+                    arrive(&sh.row_ready[rows & 1]);
+                }
+            }
+            ++rows;
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&sh.item_empty[slot]);
+    }
+}
+
+// The arithmetic's warps: sums of their slice, the gradient.
 template <int DT, bool SUMS, bool GRAD>
 __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, int rank) {
     constexpr int EPV = Row<DT>::EPV;
@@ -400,19 +491,8 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
     const TokenSlice<DT> sl(V, a.split, rank);
     const float c = a.scale;
     const f2 c2 = pack2(c, c), lo2 = pack2(a.scale_lo, a.scale_lo);
-    const int n_parts = a.split * kWarps;
-    const bool finisher = warp == 0 && (GRAD || rank == 0);
     Cursor cur;
     uint32_t rows = 0;                // rows whose sums were taken so far
-    int64_t last_o = -1;              // sums alone: the row that is finished after the next one's sums
-    RowInputs last{};
-    auto finish_last = [&]() -> bool {
-        const uint32_t j = rows - 1;
-        if (lane == 0) mbar_expect_tx(&sh.shares[j % kSlots], n_parts * (uint32_t)sizeof(Part));
-        if (!wait_warp(&sh.shares[j % kSlots], (j / kSlots) & 1u)) return false;
-        finish_row(a, last_o, merge_row(a, sh, j % kSlots, n_parts), last, lane == 0);
-        return true;
-    };
     for (uint32_t i = 0;; ++i) {
         const int slot = i % kItems;
         if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
@@ -420,7 +500,6 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
         if (it.kind == kEnd) break;
         char* out = GRAD ? static_cast<char*>(a.grad) + it.q * a.grad_stride * Row<DT>::ESZ : nullptr;
         if (it.kind == kNone) {
-            if (SUMS && rank == 0 && t == 0) finish_none(a, it.o);
             if (GRAD) write_zeros<DT>(out, V, sl);
         }
         if (it.kind == kRow) {
@@ -430,8 +509,6 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
             float m = it.m, inv = it.inv, away = it.away, k = it.k;
             Cursor from = cur;
             if (SUMS) {
-                RowInputs in{};
-                if (finisher) in = row_inputs(a, it.o, it.weight);
                 Running s;
                 float z_token = -INFINITY;
                 for (int ch = 0; ch < sl.chunks; ++ch) {
@@ -473,29 +550,14 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
                 const int to = GRAD ? a.split : 1;  // every CTA, or the first
                 if (lane < to) send(&sh.part[ps][rank * kWarps + warp], &sh.shares[ps], lane, part);
                 if (GRAD) {
-                    if (warp == 0) {
-                        if (lane == 0) mbar_expect_tx(&sh.shares[ps], n_parts * (uint32_t)sizeof(Part));
-                        if (!wait_warp(&sh.shares[ps], (rows / kSlots) & 1u)) return false;
-                        const TokenRow x = merge_row(a, sh, ps, n_parts);
-                        const float slope = finish_row(a, it.o, x, in, rank == 0 && lane == 0);
-                        if (lane == 0) {
-                            sh.row[rows & 1] = make_float4(x.m, x.inv, x.away, slope);
-                            arrive(&sh.row_ready[rows & 1]);
-                        }
-                    }
                     if (!wait_warp(&sh.row_ready[rows & 1], (rows >> 1) & 1u)) return false;
                     const float4 x = sh.row[rows & 1];
                     m = x.x;
                     inv = x.y;
                     away = x.z;
                     k = x.w * (float)a.inv_t;
-                    ++rows;
-                } else {
-                    if (finisher && last_o >= 0 && !finish_last()) return false;
-                    ++rows;
-                    last_o = it.o;
-                    last = in;
                 }
+                ++rows;
             }
             if (GRAD) {
                 if (SUMS && !a.resident) from = cur;
@@ -526,7 +588,7 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
         __syncwarp();
         if (lane == 0) arrive(&sh.item_empty[slot]);
     }
-    return !(SUMS && !GRAD) || !finisher || last_o < 0 || finish_last();
+    return true;
 }
 
 template <int DT, bool SUMS, bool GRAD>
@@ -538,7 +600,7 @@ __global__ void __launch_bounds__(kBlock, 2) token_kernel(const TokenArgs a) {
     if (t == 0) {
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], kWarps);
+            mbar_init(&sh.item_empty[i], kWarps + (SUMS ? 1 : 0));
         }
         for (int i = 0; i < a.ring; ++i) {
             mbar_init(&sh.full[i], 1);
@@ -556,19 +618,12 @@ __global__ void __launch_bounds__(kBlock, 2) token_kernel(const TokenArgs a) {
     bool ok = true;
     if (t < kThreads) {
         ok = work_rows<DT, SUMS, GRAD>(a, sh, ring, rank);
-    } else if (t == kThreads) {
-        if (rank == 0) ask_next(sh.answer, &sh.next, a.split > 1);
-        Cursor cur;
-        uint32_t issued = 0;
-        ok = fetch_rows<DT, SUMS, GRAD>(a, sh, ring, rank, cur, issued);
-        if (!ok) {  // copies still in flight land before the CTA ends
-            Cursor c;
-            for (uint32_t i = 0; i < issued; ++i) {
-                if (i + a.ring >= issued) wait_for(&sh.full[c.at], c.parity);
-                c.step(a.ring);
-            }
-            wait_for(&sh.next, 0);
-        }
+    } else if (t < kThreads + 32) {
+        if (SUMS) ok = finish_rows<DT, GRAD>(a, sh, rank);
+    } else if (t == kThreads + 32) {
+        Fetcher<DT, SUMS, GRAD> f(a, sh, ring, rank);
+        ok = f.ask(true) && f.run();
+        if (!ok) f.drain();
     }
     if (!ok) raise_status(a.dev_status, DLM_DEV_TIMEOUT);
     __syncwarp();

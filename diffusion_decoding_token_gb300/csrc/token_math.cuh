@@ -58,12 +58,14 @@ struct TokenRow {
     double logp, lse;
 };
 
-// x 2^e to 2^-22 for e <= 0 of any size (as a float's product, e would be off by 2^-24 of
-// itself: 2^-17 at e = 115).
-DLM_HD float times_exp2(float x, double e) {
-    if (!(e >= -200.0)) return e != e ? f32_nan() : 0.f;
-    const double n = rint(e);
-    return ldexpf(x * exp2f((float)(e - n)), (int)n);
+// x 2^(-d (hi + lo)) to 2^-21 for d >= 0 of any size, err what d was rounded by.  (As one
+// float the exponent would be off by 2^-24 of itself: 2^-17 at 115.)
+DLM_HD float times_exp2(float x, float d, float err, float hi, float lo) {
+    const float e = d * hi;
+    if (!(e < 200.f)) return e != e ? f32_nan() : 0.f;
+    const float n = rintf(e);
+    const float f = (e - n) + fmaf(err, hi, fmaf(d, lo, fmaf(d, hi, -e)));
+    return ldexpf(x * exp2f(-f), -(int)n);
 }
 
 // The hardware's 2^x, which the weights are made with, is a little too small on average
@@ -74,20 +76,23 @@ DLM_HD float times_exp2(float x, double e) {
 constexpr double kWeightsLow = 4.8e-8;
 
 // The others' sum s_o relative to m_o (-inf: there are none, or all are -inf), and the
-// token's logit.
-DLM_HD TokenRow token_row(float m_o, float s_o, float z_a, double inv_t) {
-    const double log2_t = 1.4426950408889634 * inv_t;
+// token's logit; hi + lo = log2(e) / T.  (64-bit arithmetic has a 64th of the 32-bit rate
+// here: a dozen operations of it are left, for ln p's and the log-sum-exp's last digits.)
+DLM_HD TokenRow token_row(float m_o, float s_o, float z_a, float hi, float lo, double inv_t) {
     TokenRow t;
-    t.m = z_a >= m_o ? z_a : m_o;
-    const float e_a = times_exp2(1.f, ((double)z_a - (double)t.m) * log2_t);
-    const float others = m_o > -INFINITY ? times_exp2(s_o, ((double)m_o - (double)t.m) * log2_t) : 0.f;
-    const float total = e_a + others;
+    const bool top = z_a >= m_o;  // the token is at the maximum
+    t.m = top ? z_a : m_o;
+    // the distance to the other one, and what it is rounded by
+    const float low = top ? m_o : z_a, d = t.m - low, back = t.m - d;
+    const float err = d < INFINITY ? back - low : 0.f;
+    const float far = d < INFINITY || d != d ? times_exp2(top ? s_o : 1.f, d, err, hi, lo) : 0.f;
+    const float others = top ? far : s_o;
+    const float total = top ? 1.f + others : far + others;
     // (total is 0 where nothing but -inf is)
-    t.ok = is_finite(t.m) && s_o >= 0.f && z_a < INFINITY && m_o < INFINITY && total > 0.f;
+    t.ok = is_finite(t.m) && s_o >= 0.f && total > 0.f && total < INFINITY && low == low;
     t.inv = 1.f / total;
     t.away = others * t.inv;
-    // (where the token is at the maximum e_a is 1)
-    const double ln = (z_a >= m_o && others < 0.5f ? (double)log1pf(others) : ln_split(total)) + kWeightsLow * (double)t.away;
+    const double ln = (top && others < 0.5f ? (double)log1pf(others) : ln_split(total)) + kWeightsLow * (double)t.away;
     t.logp = ((double)z_a - (double)t.m) * inv_t - ln;
     t.lse = (double)t.m * inv_t + ln;
     if (!t.ok) {

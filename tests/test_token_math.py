@@ -30,7 +30,9 @@ int main() {
         const float s_o = (float)exp((drand48() - 0.75) * 50) + (i % 2 ? 1.f : 0.f);
         const double inv_t = i % 7 ? 1.0 : 5.0;
         const float m = fmaxf(m_o, z);
-        const TokenRow t = token_row(m_o, s_o, z, inv_t);
+        const double l2 = 1.4426950408889634 * inv_t;
+        const float hi = nextafterf((float)l2, 0.f), lo = (float)(l2 - hi);
+        const TokenRow t = token_row(m_o, s_o, z, hi, lo, inv_t);
         // (the weights that s_o is the sum of are taken for this much too small)
         const long double a = expl(((long double)z - m) * inv_t),
                           o = (long double)s_o * (1 + (long double)kWeightsLow) * expl(((long double)m_o - m) * inv_t);
@@ -104,15 +106,15 @@ int main() {
     bad |= p4.loss != 0.f || p4.slope != 0.f;                                      // the hinge's corner
     const LossSlope p5 = preference_pair(PreferenceRule{1.0, 1.f, 0}, -INFINITY, 0.0, 0.f, 1.f);
     bad |= p5.loss != 0.f || p5.slope != 0.f;                                      // labels turned round
-    const TokenRow r1 = token_row(-INFINITY, 0.f, 3.f, 1.0);
+    const TokenRow r1 = token_row(-INFINITY, 0.f, 3.f, 1.44269502f, 1.93e-8f, 1.0);
     bad |= !r1.ok || r1.logp != 0.0 || r1.away != 0.f || r1.lse != 3.0;            // the only token
-    const TokenRow r2 = token_row(-3.4028235e38f, 0.f, -INFINITY, 1.0);
+    const TokenRow r2 = token_row(-3.4028235e38f, 0.f, -INFINITY, 1.44269502f, 1.93e-8f, 1.0);
     bad |= r2.ok || r2.logp == r2.logp || r2.inv == r2.inv;                        // nothing but -inf
-    const TokenRow r3 = token_row(1.f, 2.f, -INFINITY, 1.0);
+    const TokenRow r3 = token_row(1.f, 2.f, -INFINITY, 1.44269502f, 1.93e-8f, 1.0);
     bad |= !r3.ok || r3.logp != -INFINITY || r3.away != 1.f;
-    const TokenRow r4 = token_row(1.f, NAN, 0.f, 1.0), r5 = token_row(1.f, 1.f, NAN, 1.0),
-                   r6 = token_row(INFINITY, 1.f, 0.f, 1.0), r7 = token_row(1.f, 1.f, INFINITY, 1.0);
-    const TokenRow r8 = token_row(0.f, 1.f, 2000.f, 1.0), r9 = token_row(2000.f, 1.f, 0.f, 1.0);
+    const TokenRow r4 = token_row(1.f, NAN, 0.f, 1.44269502f, 1.93e-8f, 1.0), r5 = token_row(1.f, 1.f, NAN, 1.44269502f, 1.93e-8f, 1.0),
+                   r6 = token_row(INFINITY, 1.f, 0.f, 1.44269502f, 1.93e-8f, 1.0), r7 = token_row(1.f, 1.f, INFINITY, 1.44269502f, 1.93e-8f, 1.0);
+    const TokenRow r8 = token_row(0.f, 1.f, 2000.f, 1.44269502f, 1.93e-8f, 1.0), r9 = token_row(2000.f, 1.f, 0.f, 1.44269502f, 1.93e-8f, 1.0);
     bad |= r8.logp != 0.0 || r8.away != 0.f || r9.away != 1.f || r9.logp > -2000.0 || r9.logp < -2000.0001;
     bad |= r4.ok || r5.ok || r6.ok || r7.ok;
     return bad;
