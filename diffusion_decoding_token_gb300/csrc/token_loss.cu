@@ -7,6 +7,8 @@
 // needs of a row: maximum, 1 / sum, 1 - q_a, slope.
 //
 // The sums and the gradient are bound by HBM: one read of the row, and one write.
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
@@ -19,12 +21,21 @@ namespace {
 constexpr int kThreads = kRowThreads;   // consumers: threads that do the arithmetic
 constexpr int kWarps = kRowWarps;
 constexpr int kBlock = kThreads + 64;   // and the warps that finish rows and that fetch them
-constexpr int kPerThread = 2;           // vectors of a chunk per thread
+constexpr int kPerThread = 4;           // vectors of a chunk per thread
 constexpr int kChunkVecs = kPerThread * kThreads, kChunkBytes = kChunkVecs * 16;
 constexpr int kItems = 4;               // rows that the fetching warp may be ahead
 constexpr int kSlots = 8;               // rows whose shares may be on their way (more than kItems + 2)
-constexpr int kMaxRing = 24;
+// CTAs per SM, and the chunks that each has room for: a step's two passes want more of a
+// row on its way, sums or a gradient alone more warps.
+template <bool SUMS, bool GRAD>
+struct Shape {
+    static constexpr int ctas = SUMS && GRAD ? 2 : 3, ring = SUMS && GRAD ? 6 : 4;
+};
+constexpr int kMaxRing = 6;
 constexpr float kRebase = 12.0f;        // powers of 2 of headroom before a thread's reference moves
+constexpr int64_t kInL2 = 48 << 20;     // rows in flight that the second pass still finds in L2
+constexpr int kPairSlice = 160 * 1024;  // preference step: the same, by a slice's size
+constexpr int kLeast = 8 * 1024;        // a slice is not cut below this to fill the GPU
 constexpr long long kWaitLimit = 4000000000LL;  // ~2 s
 
 // What a thread, a warp or a CTA knows of a row: the sum of its slice's weights
@@ -150,19 +161,15 @@ __device__ constexpr uint32_t neg_inf_bits() {
     else
         return Row<DT>::kNegInf;
 }
-// The row's last vector, which V cuts: nothing past the row is touched.
-template <int DT>
-__device__ __forceinline__ uint4 load_cut(const char* row, int64_t V, int v) {
-    return load_vec<DT>(row, V, v);
-}
-
 // ---- rows -----------------------------------------------------------------------
 
 // A row as the fetching warp hands it over.
-enum : int { kEnd = 0, kSkip = 1, kNone = 2, kRow = 3 };  // no more rows; not touched; without a loss; read
+// no more rows; not touched; without a loss (its sums', its gradient's turn); read for its sums; for its gradient
+enum : int { kEnd, kSkip, kNone, kNoGrad, kRow, kGrad };
 struct Item {
     int64_t q, o;     // its place in the logits, and in the per-row arrays
     int kind, token;
+    int pair;         // preference step: its segment, and in the lowest bit the side of the pair
     float weight;
     float m, inv, away, k;  // gradient from the state
 };
@@ -170,10 +177,10 @@ struct Item {
 struct Shared {
     Part part[kSlots][8 * kWarps];  // every warp's of every CTA of the cluster
     Item item[kItems];
-    float4 row[2];                  // maximum, 1 / sum, 1 - q of the token, slope
+    float4 row[kItems];             // maximum, 1 / sum, 1 - q of the token, slope
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t full[kMaxRing], empty[kMaxRing];
-    uint64_t shares[kSlots], row_ready[2];
+    uint64_t shares[kSlots], row_ready[kItems];
     uint64_t next, next_free;       // the answer to ask_next is there; every CTA has read it (in the first CTA)
     __align__(16) unsigned char answer[16];
 };
@@ -306,7 +313,9 @@ __device__ __forceinline__ TokenRow merge_row(const TokenArgs& a, const Shared& 
 // settings, and their slices chunk by chunk into the ring.  What the next row needs is
 // asked for while this row's chunks are on their way: the row itself (about 1 us), then
 // its token and weight (another), which are not looked at before the row's turn.
-template <int DT, bool SUMS, bool GRAD>
+// PAIRS: the rows come from give_tickets instead, each once for its sums and once for its
+// gradient.
+template <int DT, bool SUMS, bool GRAD, bool PAIRS>
 struct Fetcher {
     const TokenArgs& a;
     Shared& sh;
@@ -325,9 +334,9 @@ struct Fetcher {
     // Starts to read what belongs to row r.
     __device__ __forceinline__ void read_row(int64_t r) {
         Item& it = next_item;
-        it.kind = kRow;
+        if (!PAIRS) it.kind = kRow;
         it.q = r;
-        if (SUMS && a.row_index) {
+        if (SUMS && !PAIRS && a.row_index) {
             it.q = a.row_index[r];
             if (it.q < 0 || (a.n_src > 0 && it.q >= a.n_src)) {
                 it.kind = kSkip;
@@ -335,7 +344,7 @@ struct Fetcher {
             }
         }
         it.o = a.gather ? r : it.q;
-        if (it.kind != kRow) return;
+        if (it.kind == kSkip) return;
         it.token = a.tokens[it.o];
         if (SUMS) {
             it.weight = a.weights ? a.weights[it.o] : 1.f;
@@ -355,7 +364,7 @@ struct Fetcher {
     // The item that read_row() began.
     __device__ __forceinline__ Item row_read() {
         Item it = next_item;
-        if (it.kind == kRow) {
+        if (it.kind == kRow || it.kind == kGrad) {
             bool none = it.token < 0 || it.token >= a.vocab;
             if (SUMS) {
                 none = none || it.weight == 0.f;
@@ -364,13 +373,13 @@ struct Fetcher {
                 it.k *= (float)a.inv_t * it.weight;
                 none = none || it.k == 0.f || it.inv == 0.f;
             }
-            if (none) it.kind = kNone;
+            if (none) it.kind = it.kind == kRow && SUMS ? kNone : kNoGrad;
         }
         return it;
     }
     // The first CTA asks for a row once every CTA has read the last answer.
     __device__ __forceinline__ bool ask(bool block) {
-        if (rank != 0 || asked > answers) return true;
+        if (PAIRS || rank != 0 || asked > answers) return true;
         if (asked > 0) {
             const uint32_t parity = (asked - 1) & 1u;
             if (block ? !wait_for(&sh.next_free, parity) : !mbar_test_wait(&sh.next_free, parity)) return !block;
@@ -384,24 +393,36 @@ struct Fetcher {
         if (have_next) return ask(false);
         if (!ask(block)) return false;
         if (block ? !wait_for(&sh.next, answers & 1u) : !mbar_test_wait(&sh.next, answers & 1u)) return !block;
-        uint32_t cta;
-        const bool more = next_cta(sh.answer, cta);
+        uint32_t cta = 0;
+        bool more;
+        if (PAIRS) {
+            const int4 x = *reinterpret_cast<const int4*>(sh.answer);
+            cta = (uint32_t)x.x;
+            next_item.pair = x.z;
+            more = x.y != kEnd;
+            next_item.kind = x.y;
+        } else {
+            more = next_cta(sh.answer, cta);
+        }
         ++answers;
         have_next = true;
-        next_item.kind = kEnd;
         if (!more) {
+            next_item.kind = kEnd;
             asked = answers + 1;  // and nothing is asked for any more
             return true;
         }
         mbar_expect_tx(&sh.next, 16);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the answer has been read before the next one is written
         arrive_at(&sh.next_free, 0);
-        read_row(cta / a.split);
+        read_row(PAIRS ? cta : cta / a.split);
         return ask(false);
     }
     __device__ bool run() {
-        const int passes = SUMS && GRAD && !a.resident ? 2 : 1;
-        read_row(blockIdx.x / a.split);
+        const int passes = SUMS && GRAD && !PAIRS && !a.resident ? 2 : 1;
+        if (!PAIRS)
+            read_row(blockIdx.x / a.split);
+        else if (!look_ahead(true))
+            return false;
         for (uint32_t i = 0;; ++i) {
             const Item it = row_read();
             have_next = false;
@@ -410,7 +431,7 @@ struct Fetcher {
             sh.item[slot] = it;
             arrive(&sh.item_full[slot]);
             if (it.kind == kEnd) return true;
-            if (it.kind == kRow) {
+            if (it.kind == kRow || it.kind == kGrad) {
                 const char* src = static_cast<const char*>(a.logits) + it.q * a.row_stride * Row<DT>::ESZ + (int64_t)sl.v0 * 16;
                 for (int pass = 0; pass < passes; ++pass)
                     for (int c = 0; c < sl.chunks; ++c) {
@@ -451,7 +472,7 @@ __device__ void write_zeros(char* out, int64_t V, const TokenSlice<DT>& sl) {
 // works the loss out, while the others go on.  (One of them doing this too was what a
 // row took: about 2 us for each.)  With a gradient every CTA's does, to go on with the
 // slope; the first CTA's writes.
-template <int DT, bool GRAD>
+template <bool GRAD>
 __device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
     const int lane = threadIdx.x & 31, n_parts = a.split * kWarps;
     uint32_t rows = 0;
@@ -471,8 +492,8 @@ __device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
                 const TokenRow x = merge_row(a, sh, ps, n_parts);
                 const float slope = finish_row(a, o, x, in, rank == 0 && lane == 0);
                 if (GRAD && lane == 0) {
-                    sh.row[rows & 1] = make_float4(x.m, x.inv, x.away, slope);
-                    arrive(&sh.row_ready[rows & 1]);
+                    sh.row[rows % kItems] = make_float4(x.m, x.inv, x.away, slope);
+                    arrive(&sh.row_ready[rows % kItems]);
                 }
             }
             ++rows;
@@ -482,132 +503,165 @@ __device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
     }
 }
 
-// The arithmetic's warps: sums of their slice, the gradient.
-template <int DT, bool SUMS, bool GRAD>
-__device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, int rank) {
+// The sums of this CTA's slice of row q, the chunks freed as they are done with where they
+// are not used again; false if they do not come.
+template <int DT>
+__device__ __forceinline__ bool take_sums(const TokenArgs& a, Shared& sh, unsigned char* ring, const TokenSlice<DT>& sl,
+                                          int64_t q, int token, bool keep, Cursor& cur, Part& part) {
     constexpr int EPV = Row<DT>::EPV;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t V = a.vocab;
-    const TokenSlice<DT> sl(V, a.split, rank);
+    const int t = threadIdx.x, lane = t & 31;
     const float c = a.scale;
     const f2 c2 = pack2(c, c), lo2 = pack2(a.scale_lo, a.scale_lo);
+    const int tv = token / EPV - sl.v0;  // the token's vector in the slice
+    const bool mine = tv >= 0 && tv < sl.n && (tv & (kThreads - 1)) == t;
+    Running s;
+    float z_token = -INFINITY;
+    for (int ch = 0; ch < sl.chunks; ++ch) {
+        if (!wait_warp(&sh.full[cur.at], cur.parity)) return false;
+        uint4* data = reinterpret_cast<uint4*>(ring + cur.at * kChunkBytes);
+        const int base = ch * kChunkVecs, n = min(kChunkVecs, sl.whole - base);
+        if (mine && tv >= base && tv < base + n) {  // the token leaves the slice (its vector is this thread's)
+            z_token = Row<DT>::scalar(data + (tv - base), token % EPV);
+            data[tv - base] = with_elem<DT>(data[tv - base], token % EPV, neg_inf_bits<DT>());
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a copy writes here again
+        }
+        if (n == kChunkVecs) {
+            uint4 w[kPerThread];
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u) w[u] = data[t + u * kThreads];
+            add_vectors<DT>(s, w, c2, lo2, c);
+        } else {
+            for (int v = t; v < n; v += kThreads) {
+                const uint4 w[1] = {data[v]};
+                add_vectors<DT>(s, w, c2, lo2, c);
+            }
+        }
+        if (!keep) {
+            __syncwarp();
+            if (lane == 0) arrive(&sh.empty[cur.at]);
+        }
+        cur.step(a.ring);
+    }
+    if (sl.whole < sl.n && (sl.whole & (kThreads - 1)) == t) {  // the row's last, cut vector
+        const char* row = static_cast<const char*>(a.logits) + q * a.row_stride * Row<DT>::ESZ;
+        uint4 w[1] = {load_vec<DT>(row, a.vocab, sl.v0 + sl.whole)};
+        if (mine && tv == sl.whole) {
+            z_token = Row<DT>::scalar(row, token);
+            w[0] = with_elem<DT>(w[0], token % EPV, neg_inf_bits<DT>());
+        }
+        add_vectors<DT>(s, w, c2, lo2, c);
+    }
+    part = warp_part(Part{s.top, hsum2(s.sum) * ex2((s.ref - or_zero(s.top)) * c), z_token, 0.f}, c);
+    return true;
+}
+
+// k ([v = token] - q_v) over this CTA's slice of row q.
+struct RowSlope {
+    float m, inv, away, k;
+};
+template <int DT>
+__device__ __forceinline__ bool put_gradient(const TokenArgs& a, Shared& sh, unsigned char* ring, const TokenSlice<DT>& sl,
+                                             int64_t q, int token, RowSlope x, bool there, Cursor& from) {
+    constexpr int EPV = Row<DT>::EPV;
+    const int t = threadIdx.x, lane = t & 31;
+    const float c = a.scale;
+    char* out = static_cast<char*>(a.grad) + q * a.grad_stride * Row<DT>::ESZ;
+    if (x.k == 0.f) {  // a clipped row, or one of no pair: zeros, whatever the row holds
+        for (int ch = 0; ch < sl.chunks; ++ch) {
+            if (!there && !wait_warp(&sh.full[from.at], from.parity)) return false;
+            if (lane == 0) arrive(&sh.empty[from.at]);
+            from.step(a.ring);
+        }
+        write_zeros<DT>(out, a.vocab, sl);
+        return true;
+    }
+    const Slope slope(x.m, c, -x.k * x.inv);
+    uint4* dst = reinterpret_cast<uint4*>(out) + sl.v0;
+    for (int ch = 0; ch < sl.chunks; ++ch) {
+        if (!there && !wait_warp(&sh.full[from.at], from.parity)) return false;
+        const uint4* data = reinterpret_cast<const uint4*>(ring + from.at * kChunkBytes);
+        const int base = ch * kChunkVecs, n = min(kChunkVecs, sl.whole - base);
+        if (n == kChunkVecs) {
+#pragma unroll
+            for (int u = 0; u < kPerThread; ++u)
+                st_row(dst + base + t + u * kThreads, slope_of<DT>(data[t + u * kThreads], slope));
+        } else {
+            for (int v = t; v < n; v += kThreads) st_row(dst + base + v, slope_of<DT>(data[v], slope));
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&sh.empty[from.at]);
+        from.step(a.ring);
+    }
+    if (sl.whole < sl.n && (sl.whole & (kThreads - 1)) == t) {
+        const char* row = static_cast<const char*>(a.logits) + q * a.row_stride * Row<DT>::ESZ;
+        for (int64_t e = (int64_t)(sl.v0 + sl.whole) * EPV; e < a.vocab; ++e)
+            store_elem<DT>(out, e, -x.k * x.inv * ex2((Row<DT>::scalar(row, e) - x.m) * c));
+    }
+    const int tv = token / EPV - sl.v0;
+    if (tv >= 0 && tv < sl.n && (tv & (kThreads - 1)) == t) store_elem<DT>(out, token, x.k * x.away);  // (after this thread's own vector)
+    return true;
+}
+
+// The arithmetic's warps.  BOTH: a row's gradient follows its sums; else an item is one of
+// the two (PAIRS: the slope comes from finish_rows, else it is in the item).
+template <int DT, bool SUMS, bool GRAD, bool PAIRS>
+__device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, int rank) {
+    constexpr bool BOTH = SUMS && GRAD && !PAIRS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const TokenSlice<DT> sl(a.vocab, a.split, rank);
     Cursor cur;
-    uint32_t rows = 0;                // rows whose sums were taken so far
+    uint32_t rows = 0, slopes = 0;  // rows whose sums were taken; slopes that were waited for
     for (uint32_t i = 0;; ++i) {
         const int slot = i % kItems;
         if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
-        const Item it = sh.item[slot];
-        if (it.kind == kEnd) break;
-        char* out = GRAD ? static_cast<char*>(a.grad) + it.q * a.grad_stride * Row<DT>::ESZ : nullptr;
-        if (it.kind == kNone) {
-            if (GRAD) write_zeros<DT>(out, V, sl);
+        const Item& it = sh.item[slot];
+        const int kind = it.kind;
+        if (kind == kEnd) return true;
+        const int64_t q = it.q;
+        if (GRAD && (BOTH ? kind == kNone : kind == kNoGrad))
+            write_zeros<DT>(static_cast<char*>(a.grad) + q * a.grad_stride * Row<DT>::ESZ, a.vocab, sl);
+        const int token = it.token;
+        Cursor from = cur;
+        if (SUMS && kind == kRow) {
+            Part part;
+            if (!take_sums<DT>(a, sh, ring, sl, q, token, BOTH && a.resident, cur, part)) return false;
+            const int ps = rows % kSlots, to = BOTH ? a.split : 1;  // every CTA, or the first
+            if (lane < to) send(&sh.part[ps][rank * kWarps + warp], &sh.shares[ps], lane, part);
+            ++rows;
         }
-        if (it.kind == kRow) {
-            const char* row = static_cast<const char*>(a.logits) + it.q * a.row_stride * Row<DT>::ESZ;
-            const int tv = it.token / EPV - sl.v0;        // the token's vector in the slice
-            const bool mine = tv >= 0 && tv < sl.n && (tv & (kThreads - 1)) == t;
-            float m = it.m, inv = it.inv, away = it.away, k = it.k;
-            Cursor from = cur;
+        if (GRAD && (kind == kGrad || (kind == kRow && !PAIRS))) {
+            RowSlope x{it.m, it.inv, it.away, it.k};
             if (SUMS) {
-                Running s;
-                float z_token = -INFINITY;
-                for (int ch = 0; ch < sl.chunks; ++ch) {
-                    if (!wait_warp(&sh.full[cur.at], cur.parity)) return false;
-                    uint4* data = reinterpret_cast<uint4*>(ring + cur.at * kChunkBytes);
-                    const int base = ch * kChunkVecs, n = min(kChunkVecs, sl.whole - base);
-                    if (mine && tv >= base && tv < base + n) {  // the token leaves the slice (its vector is this thread's)
-                        z_token = Row<DT>::scalar(data + (tv - base), it.token % EPV);
-                        data[tv - base] = with_elem<DT>(data[tv - base], it.token % EPV, neg_inf_bits<DT>());
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before a copy writes here again
-                    }
-                    if (n == kChunkVecs) {
-                        uint4 w[kPerThread];
-#pragma unroll
-                        for (int u = 0; u < kPerThread; ++u) w[u] = data[t + u * kThreads];
-                        add_vectors<DT>(s, w, c2, lo2, c);
-                    } else {
-                        for (int v = t; v < n; v += kThreads) {
-                            const uint4 w[1] = {data[v]};
-                            add_vectors<DT>(s, w, c2, lo2, c);
-                        }
-                    }
-                    if (!(GRAD && a.resident)) {
-                        __syncwarp();
-                        if (lane == 0) arrive(&sh.empty[cur.at]);
-                    }
-                    cur.step(a.ring);
-                }
-                if (sl.whole < sl.n && (sl.whole & (kThreads - 1)) == t) {  // the row's last, cut vector
-                    uint4 w[1] = {load_cut<DT>(row, V, sl.v0 + sl.whole)};
-                    if (mine && tv == sl.whole) {
-                        z_token = Row<DT>::scalar(row, it.token);
-                        w[0] = with_elem<DT>(w[0], it.token % EPV, neg_inf_bits<DT>());
-                    }
-                    add_vectors<DT>(s, w, c2, lo2, c);
-                }
-                const Part part = warp_part(Part{s.top, hsum2(s.sum) * ex2((s.ref - or_zero(s.top)) * c), z_token, 0.f}, c);
-                const int ps = rows % kSlots;
-                const int to = GRAD ? a.split : 1;  // every CTA, or the first
-                if (lane < to) send(&sh.part[ps][rank * kWarps + warp], &sh.shares[ps], lane, part);
-                if (GRAD) {
-                    if (!wait_warp(&sh.row_ready[rows & 1], (rows >> 1) & 1u)) return false;
-                    const float4 x = sh.row[rows & 1];
-                    m = x.x;
-                    inv = x.y;
-                    away = x.z;
-                    k = x.w * (float)a.inv_t;
-                }
-                ++rows;
+                const int rs = slopes % kItems;
+                if (!wait_warp(&sh.row_ready[rs], (slopes / kItems) & 1u)) return false;
+                const float4 y = sh.row[rs];
+                x = RowSlope{y.x, y.y, y.z, y.w * (float)a.inv_t};
+                ++slopes;
             }
-            if (GRAD) {
-                if (SUMS && !a.resident) from = cur;
-                const Slope slope(m, c, -k * inv);
-                uint4* dst = reinterpret_cast<uint4*>(out) + sl.v0;
-                for (int ch = 0; ch < sl.chunks; ++ch) {
-                    if (!(SUMS && a.resident) && !wait_warp(&sh.full[from.at], from.parity)) return false;
-                    const uint4* data = reinterpret_cast<const uint4*>(ring + from.at * kChunkBytes);
-                    const int base = ch * kChunkVecs, n = min(kChunkVecs, sl.whole - base);
-                    if (n == kChunkVecs) {
-#pragma unroll
-                        for (int u = 0; u < kPerThread; ++u)
-                            st_row(dst + base + t + u * kThreads, slope_of<DT>(data[t + u * kThreads], slope));
-                    } else {
-                        for (int v = t; v < n; v += kThreads) st_row(dst + base + v, slope_of<DT>(data[v], slope));
-                    }
-                    __syncwarp();
-                    if (lane == 0) arrive(&sh.empty[from.at]);
-                    from.step(a.ring);
-                }
-                cur = from;
-                if (sl.whole < sl.n && (sl.whole & (kThreads - 1)) == t)
-                    for (int64_t e = (int64_t)(sl.v0 + sl.whole) * EPV; e < V; ++e)
-                        store_elem<DT>(out, e, -k * inv * ex2((Row<DT>::scalar(row, e) - m) * c));
-                if (mine) store_elem<DT>(out, it.token, k * away);  // (after this thread's own vector)
-            }
+            const bool there = BOTH && a.resident;
+            if (!there) from = cur;
+            if (!put_gradient<DT>(a, sh, ring, sl, q, token, x, there, from)) return false;
+            cur = from;
         }
         __syncwarp();
         if (lane == 0) arrive(&sh.item_empty[slot]);
     }
-    return true;
 }
 
-template <int DT, bool SUMS, bool GRAD>
-__global__ void __launch_bounds__(kBlock, 2) token_kernel(const TokenArgs a) {
-    extern __shared__ __align__(128) unsigned char s_raw[];
-    Shared& sh = *reinterpret_cast<Shared*>(s_raw);
-    unsigned char* ring = s_raw + ring_offset();
-    const int t = threadIdx.x, rank = (int)(blockIdx.x % a.split);
-    if (t == 0) {
+// What a CTA starts with: its barriers, and all CTAs of its cluster running.
+template <bool FINISH>
+__device__ __forceinline__ void set_up(const TokenArgs& a, Shared& sh) {
+    if (threadIdx.x == 0) {
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], kWarps + (SUMS ? 1 : 0));
+            mbar_init(&sh.item_empty[i], kWarps + (FINISH ? 1 : 0));
+            mbar_init(&sh.row_ready[i], 1);
         }
         for (int i = 0; i < a.ring; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], kWarps);
         }
         for (int i = 0; i < kSlots; ++i) mbar_init(&sh.shares[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&sh.row_ready[i], 1);
         mbar_init(&sh.next, 1);
         mbar_init(&sh.next_free, a.split);
         mbar_init_fence();
@@ -615,19 +669,291 @@ __global__ void __launch_bounds__(kBlock, 2) token_kernel(const TokenArgs a) {
     }
     __syncthreads();
     if (a.split > 1) cg::this_cluster().sync();
+}
+
+template <int DT, bool SUMS, bool GRAD>
+__global__ void __launch_bounds__(kBlock, Shape<SUMS, GRAD>::ctas) token_kernel(const TokenArgs a) {
+    extern __shared__ __align__(128) unsigned char s_raw[];
+    Shared& sh = *reinterpret_cast<Shared*>(s_raw);
+    unsigned char* ring = s_raw + ring_offset();
+    const int t = threadIdx.x, rank = (int)(blockIdx.x % a.split);
+    set_up<SUMS>(a, sh);
     bool ok = true;
     if (t < kThreads) {
-        ok = work_rows<DT, SUMS, GRAD>(a, sh, ring, rank);
+        ok = work_rows<DT, SUMS, GRAD, false>(a, sh, ring, rank);
     } else if (t < kThreads + 32) {
-        if (SUMS) ok = finish_rows<DT, GRAD>(a, sh, rank);
+        if (SUMS) ok = finish_rows<GRAD>(a, sh, rank);
     } else if (t == kThreads + 32) {
-        Fetcher<DT, SUMS, GRAD> f(a, sh, ring, rank);
+        Fetcher<DT, SUMS, GRAD, false> f(a, sh, ring, rank);
         ok = f.ask(true) && f.run();
         if (!ok) f.drain();
     }
     if (!ok) raise_status(a.dev_status, DLM_DEV_TIMEOUT);
     __syncwarp();
     if (a.split > 1) cg::this_cluster().sync();  // no CTA ends before what others send to it has come
+}
+
+// ---- the preference step in one pass over the rows -------------------------------
+//
+// A row's gradient needs the sums of all rows of its pair.  Rows are handed out by a
+// counter in one order: their sums in row order, and a pair's gradients once `lag` more
+// rows' sums have been given out after its last, so that the pair is settled when they
+// come and its rows are still in L2 (the latest first, for a pair that L2 does not
+// hold).  Whoever finishes a pair's last row settles it.  An item waits only for items
+// that were given out before it, to clusters that run, so the waits end.
+
+struct PairWork {
+    uint32_t* ticket;
+    float* state;            // [n_rows][DLM_TOKEN_STATE]
+    int32_t* at;             // [2 n_pairs + 1] offsets, put right
+    uint32_t* left;          // [n_pairs + 2] rows of a segment that are not finished
+    unsigned long long* slope;  // [n_pairs + 2] its slope, and 1 in the upper half once it is there
+};
+__host__ __device__ inline size_t pair_work_bytes(int64_t n_rows, int64_t n_pairs) {
+    return 256 + (size_t)n_rows * DLM_TOKEN_STATE * 4 + (((size_t)n_pairs * 3 + 3) * 4 + 15) / 16 * 16 + (size_t)(n_pairs + 2) * 8;
+}
+__host__ __device__ inline PairWork pair_work(void* workspace, int64_t n_rows, int64_t n_pairs) {
+    unsigned char* p = static_cast<unsigned char*>(workspace);
+    PairWork w;
+    w.ticket = reinterpret_cast<uint32_t*>(p);
+    p += 256;
+    w.state = reinterpret_cast<float*>(p);
+    p += (size_t)n_rows * DLM_TOKEN_STATE * 4;
+    w.at = reinterpret_cast<int32_t*>(p);
+    w.left = reinterpret_cast<uint32_t*>(w.at + 2 * n_pairs + 1);
+    p += (((size_t)n_pairs * 3 + 3) * 4 + 15) / 16 * 16;
+    w.slope = reinterpret_cast<unsigned long long*>(p);
+    return w;
+}
+
+// Segments: the rows before the first pair, the pairs, the rows behind the last.
+struct Segments {
+    const PairWork& w;
+    const int64_t rows, pairs;
+    __device__ __forceinline__ int64_t begin(int64_t j) const {  // of segment j; of pairs + 2: the end
+        return j <= 0 ? 0 : j <= pairs + 1 ? (int64_t)w.at[2 * (j - 1)] : rows;
+    }
+};
+
+// The loss of pair i from its scores, by one thread: its slope.
+__device__ float finish_pair(const TokenArgs& a, int64_t i, double chosen, double rejected) {
+    const LossSlope x = preference_pair(a.preference, chosen, rejected, a.margins ? a.margins[i] : 0.f,
+                                        a.pair_weights ? a.pair_weights[i] : 1.f);
+    a.loss[i] = x.loss;
+    if (a.score) {
+        a.score[2 * i] = (float)chosen;
+        a.score[2 * i + 1] = (float)rejected;
+    }
+    if (x.slope != x.slope) raise_status(a.dev_status, DLM_DEV_NONFINITE);
+    return x.slope;
+}
+
+// The workspace before a step: the offsets put right, counters, and the losses of pairs
+// without rows.  One CTA.
+constexpr int kStartThreads = 1024;
+__global__ void __launch_bounds__(kStartThreads) pair_start_kernel(const TokenArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ int32_t s_top[kStartThreads / 32];
+    const PairWork w = pair_work(a.workspace, a.n_rows, a.n_pairs);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int64_t n = 2 * a.n_pairs + 1;
+    if (t == 0) *w.ticket = 0;
+    int32_t before = 0;  // the largest so far
+    for (int64_t base = 0; base < n; base += kStartThreads) {
+        const int64_t i = base + t;
+        const int32_t given = i < n ? a.offsets[i] : 0;
+        int32_t x = (int32_t)min(max((int64_t)given, (int64_t)0), a.n_rows);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(DLM_FULL_MASK, x, o);
+            if (lane >= o) x = max(x, y);
+        }
+        if (lane == 31) s_top[warp] = x;
+        __syncthreads();
+        int32_t low = before;
+        for (int k = 0; k < kStartThreads / 32; ++k) {
+            if (k < warp) low = max(low, s_top[k]);
+            before = max(before, s_top[k]);
+        }
+        x = max(x, low);
+        if (i < n) {
+            w.at[i] = x;
+            if (x != given) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
+        }
+        __syncthreads();
+    }
+    const Segments seg{w, a.n_rows, a.n_pairs};
+    for (int64_t j = t; j < a.n_pairs + 2; j += kStartThreads) {
+        const uint32_t rows = (uint32_t)(seg.begin(j + 1) - seg.begin(j));
+        w.left[j] = rows;
+        w.slope[j] = 0;
+        if (rows == 0 && j >= 1 && j <= a.n_pairs) finish_pair(a, j - 1, 0.0, 0.0);
+    }
+}
+
+// One thread of the first CTA of a cluster: what the cluster does next, to all its CTAs.
+constexpr int kAtOnce = 8;
+__device__ bool give_tickets(const TokenArgs& a, Shared& sh, const PairWork& w) {
+    const Segments seg{w, a.n_rows, a.n_pairs};
+    const int64_t N = a.n_rows, last = a.n_pairs + 1;
+    // the last segment whose gradients have begun (-1: none), where they begin, its rows
+    int64_t j = -1, g_start = 0, g_from = 0, g_to = 0;
+    int64_t f = 0, f_to = seg.begin(1);  // the segment whose sums are given out, and its end
+    for (uint32_t n = 0;; ++n) {
+        const int64_t t = atomicAdd(w.ticket, 1u);
+        int row = 0, kind = kEnd, pair = 0;
+        if (t < 2 * N) {
+            for (;;) {  // some segments at a time: their bounds are read together
+                int32_t b[kAtOnce + 1];
+#pragma unroll
+                for (int k = 0; k <= kAtOnce; ++k) b[k] = (int32_t)seg.begin(min(j + 1 + k, last + 1));
+                int took = 0;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int64_t start = min(N, (int64_t)b[k + 1] + a.lag) + b[k];
+                    if (took == k && j + 1 + k <= last && start <= t) {
+                        ++took;
+                        g_start = start;
+                        g_from = b[k];
+                        g_to = b[k + 1];
+                    }
+                }
+                j += took;
+                if (took < kAtOnce) break;
+            }
+            if (j >= 0 && t - g_start < g_to - g_from) {
+                kind = kGrad;
+                row = (int)(g_to - 1 - (t - g_start));
+                pair = (int)(2 * j) + (j >= 1 && j < last && row >= w.at[2 * (j - 1) + 1]);
+            } else {
+                kind = kRow;
+                row = (int)(t - g_to);  // (as many gradients as rows of the segments begun)
+                while (row >= f_to && f < last) {
+                    int32_t b[kAtOnce];
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) b[k] = (int32_t)seg.begin(min(f + 2 + k, last + 1));
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k)
+                        if (row >= f_to && f < last) {
+                            ++f;
+                            f_to = b[k];
+                        }
+                }
+                pair = (int)(2 * f);
+            }
+        }
+        if (n > 0 && !wait_for(&sh.next_free, (n - 1) & 1u)) return false;
+        for (int r = 0; r < a.split; ++r)
+            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                             remote(sh.answer, r)),
+                         "r"(row), "r"(kind), "r"(pair), "r"(0), "r"(remote(&sh.next, r))
+                         : "memory");
+        if (kind == kEnd) return true;
+    }
+}
+
+// A segment all of whose rows are finished: the pair's scores, loss and slope, by a warp
+// (rows in no pair: 0).
+__device__ void settle_pair(const TokenArgs& a, const PairWork& w, int64_t segment) {
+    const int lane = threadIdx.x & 31;
+    const int64_t i = segment - 1;
+    const bool outside = i < 0 || i == a.n_pairs;
+    double score[2];
+    for (int side = 0; side < 2; ++side) {
+        const int64_t to = outside ? 0 : w.at[2 * i + side + 1];
+        double sum = 0.0;
+#pragma unroll 8
+        for (int64_t r = outside ? 0 : w.at[2 * i + side] + lane; r < to; r += 32)
+            sum += __ldcg(reinterpret_cast<const double*>(w.state + r * DLM_TOKEN_STATE + 4));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(DLM_FULL_MASK, sum, o);
+        score[side] = sum;
+    }
+    if (lane == 0) {
+        const float slope = outside ? 0.f : finish_pair(a, i, score[0], score[1]);
+        asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(w.slope + segment), "l"((1ull << 32) | __float_as_uint(slope))
+                     : "memory");
+    }
+}
+
+// The warp that finishes rows: a row's sums as in finish_rows, and a gradient's slope.
+__device__ bool finish_pair_rows(const TokenArgs& a, Shared& sh, const PairWork& w, int rank) {
+    const int lane = threadIdx.x & 31, n_parts = a.split * kWarps;
+    uint32_t rows = 0, slopes = 0;
+    for (uint32_t i = 0;; ++i) {
+        const int slot = i % kItems;
+        if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
+        const int kind = sh.item[slot].kind, pair = sh.item[slot].pair;
+        const int64_t r = sh.item[slot].o;
+        if (kind == kEnd) return true;
+        if (kind == kGrad) {
+            unsigned long long x = 0;
+            const long long t0 = clock64();
+            for (;;) {
+                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(w.slope + (pair >> 1)) : "memory");
+                const bool late = clock64() - t0 > kWaitLimit;
+                if (__any_sync(DLM_FULL_MASK, (x >> 32) != 0)) break;
+                if (__any_sync(DLM_FULL_MASK, late)) return false;
+                __nanosleep(200);
+            }
+            if (lane == 0) {
+                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(w.slope + (pair >> 1)) : "memory");
+                const float4 s = __ldcg(reinterpret_cast<const float4*>(w.state + r * DLM_TOKEN_STATE));
+                const float slope = __uint_as_float((uint32_t)x) * sh.item[slot].weight;
+                sh.row[slopes % kItems] = make_float4(s.x, s.y, s.z, pair & 1 ? -slope : slope);
+                arrive(&sh.row_ready[slopes % kItems]);
+            }
+            ++slopes;
+        }
+        if (rank == 0 && (kind == kRow || kind == kNone)) {
+            if (kind == kRow) {
+                const RowInputs in = row_inputs(a, r, sh.item[slot].weight);
+                const int ps = rows % kSlots;
+                if (lane == 0) mbar_expect_tx(&sh.shares[ps], n_parts * (uint32_t)sizeof(Part));
+                if (!wait_warp(&sh.shares[ps], (rows / kSlots) & 1u)) return false;
+                const TokenRow x = merge_row(a, sh, ps, n_parts);
+                finish_row(a, r, x, in, lane == 0);
+                ++rows;
+            } else if (lane == 0) {
+                finish_none(a, r);
+            }
+            uint32_t left = 0;
+            if (lane == 0) {
+                __threadfence();
+                left = atomicSub(w.left + (pair >> 1), 1u);
+                __threadfence();
+            }
+            if (__shfl_sync(DLM_FULL_MASK, left, 0) == 1u) settle_pair(a, w, pair >> 1);
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&sh.item_empty[slot]);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kBlock + 32, Shape<true, true>::ctas) pair_step_kernel(const TokenArgs a) {
+    extern __shared__ __align__(128) unsigned char s_raw[];
+    Shared& sh = *reinterpret_cast<Shared*>(s_raw);
+    unsigned char* ring = s_raw + ring_offset();
+    const int t = threadIdx.x, rank = (int)(blockIdx.x % a.split);
+    const PairWork w = pair_work(a.workspace, a.n_rows, a.n_pairs);
+    set_up<true>(a, sh);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the workspace is ready
+    bool ok = true;
+    if (t < kThreads) {
+        ok = work_rows<DT, true, true, true>(a, sh, ring, rank);
+    } else if (t < kThreads + 32) {
+        ok = finish_pair_rows(a, sh, w, rank);
+    } else if (t == kThreads + 32) {
+        Fetcher<DT, true, true, true> f(a, sh, ring, rank);
+        ok = f.run();
+        if (!ok) f.drain();
+    } else if (t == kBlock && rank == 0) {  // (a warp of its own: it and the fetching one wait for each other)
+        ok = give_tickets(a, sh, w);
+    }
+    if (!ok) raise_status(a.dev_status, DLM_DEV_TIMEOUT);
+    __syncwarp();
+    if (a.split > 1) cg::this_cluster().sync();
 }
 
 // The offsets' bounds [b, e) of sequence s as they should be: within the rows and in
@@ -660,17 +986,12 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const TokenArgs a) {
     }
     __syncthreads();
     if (t == 0) {
-        double score[2];
-        for (int side = 0; side < 2; ++side) {
-            score[side] = 0.0;
-            for (int w = 0; w < kWarps; ++w) score[side] += s_sum[side][w];
-            if (a.score) a.score[2 * i + side] = (float)score[side];
+        double score[2] = {0.0, 0.0};
+        for (int w = 0; w < kWarps; ++w) {
+            score[0] += s_sum[0][w];
+            score[1] += s_sum[1][w];
         }
-        const LossSlope x = preference_pair(a.preference, score[0], score[1], a.margins ? a.margins[i] : 0.f,
-                                            a.pair_weights ? a.pair_weights[i] : 1.f);
-        a.loss[i] = x.loss;
-        s_slope = x.slope;
-        if (x.slope != x.slope) raise_status(a.dev_status, DLM_DEV_NONFINITE);
+        s_slope = finish_pair(a, i, score[0], score[1]);
     }
     __syncthreads();
     for (int side = 0; side < 2; ++side)
@@ -684,69 +1005,86 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const TokenArgs a) {
 
 }  // namespace
 
-size_t preference_workspace(int64_t n_rows, int64_t n_pairs) {
-    (void)n_pairs;
-    return (size_t)(n_rows * DLM_TOKEN_STATE * 4 + 16);
-}
+size_t preference_workspace(int64_t n_rows, int64_t n_pairs) { return pair_work_bytes(n_rows, n_pairs); }
 
 namespace {
 
+// after: the launch may begin while the one before it on the stream ends.
 template <typename F>
-cudaError_t launch_rows(F kernel, const TokenArgs& a, cudaStream_t st) {
-    const size_t smem = ring_offset() + (size_t)a.ring * kChunkBytes;
+cudaError_t launch_clusters(F kernel, const TokenArgs& a, int64_t clusters, int block, bool after, cudaStream_t st) {
     // the same limit whatever the call's size: calls may run side by side
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.n_rows * a.split));
-    cfg.blockDim = dim3(kBlock);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)(clusters * a.split));
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = ring_offset() + (size_t)a.ring * kChunkBytes;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = a.split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = after ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 // CTAs per row, and whether a step's row stays in the ring between its sums and its
 // gradient.
-void token_plan(TokenArgs& a, int dtype) {
-    const int64_t epv = dtype == DLM_F32 ? 4 : 8, nv = (a.vocab + epv - 1) / epv;
-    auto chunks = [&](int n) { return (((nv + n - 1) / n + 7) / 8 * 8 + kChunkVecs - 1) / kChunkVecs; };
-    a.ring = 12;
+template <int DT, bool SUMS, bool GRAD>
+cudaError_t launch_token_kernel(TokenArgs a, cudaStream_t st) {
+    using S = Shape<SUMS, GRAD>;
+    constexpr int EPV = Row<DT>::EPV;
+    const int64_t nv = (a.vocab + EPV - 1) / EPV, slots = (int64_t)S::ctas * a.num_sms;
+    auto slice = [&](int n) { return ((nv + n - 1) / n + 7) / 8 * 8; };
+    auto chunks = [&](int n) { return (slice(n) + kChunkVecs - 1) / kChunkVecs; };
+    a.ring = S::ring;
     int split = 1;
-    a.resident = 0;
-    if (a.sums && a.grad) {
-        while (split < 8 && chunks(split) > 5) split *= 2;
-        a.resident = chunks(split) <= a.ring;
-    }
-    while (split < 8 && a.n_rows * split < 2LL * a.num_sms && chunks(split) > 1) split *= 2;
+    if (SUMS && GRAD)
+        while (split < 8 && chunks(split) > a.ring && slots / split * nv * 16 > kInL2) split *= 2;
+    while (split < 8 && a.n_rows * split < slots && slice(split) * 16 > kLeast) split *= 2;
     a.split = split;
+    a.resident = chunks(split) <= a.ring;
+    return launch_clusters(token_kernel<DT, SUMS, GRAD>, a, a.n_rows, kBlock, false, st);
+}
+
+template <int DT>
+cudaError_t launch_pair_step(TokenArgs a, cudaStream_t st) {
+    pair_start_kernel<<<1, kStartThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || a.n_rows == 0) return e;
+    using S = Shape<true, true>;
+    constexpr int EPV = Row<DT>::EPV;
+    const int64_t nv = (a.vocab + EPV - 1) / EPV, slots = (int64_t)S::ctas * a.num_sms;
+    auto slice = [&](int n) { return ((nv + n - 1) / n + 7) / 8 * 8; };
+    a.ring = S::ring;
+    int split = 1;
+    while (split < 8 && slice(split) * 16 > kPairSlice) split *= 2;
+    while (split < 8 && a.n_rows * split < slots && slice(split) * 16 > kLeast) split *= 2;
+    a.split = split;
+    const int64_t clusters = std::min(slots / split, 2 * a.n_rows);
+    a.lag = 2 * clusters;
+    a.state = pair_work(a.workspace, a.n_rows, a.n_pairs).state;
+    return launch_clusters(pair_step_kernel<DT>, a, clusters, kBlock + 32, true, st);
 }
 
 template <int DT>
 cudaError_t run_token(TokenArgs a, cudaStream_t st) {
-    if (a.workspace) a.state = static_cast<float*>(a.workspace);
-    if (a.op == kTokenPreference && a.sums) {  // sums, the pairs, and the gradient from the state
-        TokenArgs b = a;
-        b.grad = nullptr;
-        token_plan(b, DT);
-        cudaError_t e = a.n_rows ? launch_rows(token_kernel<DT, true, false>, b, st) : cudaSuccess;
+    if (a.workspace) return launch_pair_step<DT>(a, st);
+    if (a.op == kTokenPreference && a.sums) {  // sums, and the pairs
+        cudaError_t e = a.n_rows ? launch_token_kernel<DT, true, false>(a, st) : cudaSuccess;
         if (e == cudaSuccess && a.n_pairs > 0) {
             pair_kernel<<<(unsigned)a.n_pairs, kThreads, 0, st>>>(a);
             e = cudaGetLastError();
         }
-        if (e != cudaSuccess || !a.grad || !a.n_rows) return e;
-        a.sums = 0;
+        return e;
     }
-    token_plan(a, DT);
-    if (!a.sums) return launch_rows(token_kernel<DT, false, true>, a, st);
-    if (!a.grad) return launch_rows(token_kernel<DT, true, false>, a, st);
-    return launch_rows(token_kernel<DT, true, true>, a, st);
+    if (!a.sums) return launch_token_kernel<DT, false, true>(a, st);
+    if (!a.grad) return launch_token_kernel<DT, true, false>(a, st);
+    return launch_token_kernel<DT, true, true>(a, st);
 }
 
 }  // namespace
