@@ -308,7 +308,7 @@ struct TokenArgs {
     int num_sms;
     int split;                // CTAs per row (thread-block cluster size)
     int ring;                 // chunks of a row that a CTA holds
-    int64_t lag;              // preference step: rows whose sums come between a pair's and its gradients
+    int backwards;            // the last rows first
     int resident;             // a step's row stays there between its sums and its gradient
 };
 size_t preference_workspace(int64_t n_rows, int64_t n_pairs);

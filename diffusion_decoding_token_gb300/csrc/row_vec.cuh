@@ -157,21 +157,14 @@ __device__ __forceinline__ void store_elem(void* row, int64_t i, float x) {
         static_cast<__half*>(row)[i] = __float2half_rn(x);
 }
 
-// scale * 2^((z - m) c) of a vector, in storage.
-struct Slope {
-    f2 m, c, scale;
-    __device__ Slope(float m1, float c1, float s1) : m(pack2(m1, m1)), c(pack2(c1, c1)), scale(pack2(s1, s1)) {}
-};
+// A vector's floats to storage.
 template <int DT>
-__device__ __forceinline__ uint4 slope_of(uint4 w, const Slope& s) {
-    constexpr int EPV = Row<DT>::EPV;
-    float z[EPV];
-    Row<DT>::unpack(w, z);
+__device__ __forceinline__ uint4 packed(const f2 (&g)[Row<DT>::EPV / 2]) {
     uint32_t r[4];
 #pragma unroll
-    for (int p = 0; p < EPV / 2; ++p) {
+    for (int p = 0; p < Row<DT>::EPV / 2; ++p) {
         float x, y;
-        unpack2(mul2(ex2x2(mul2(sub2(pack2(z[2 * p], z[2 * p + 1]), s.m), s.c)), s.scale), x, y);
+        unpack2(g[p], x, y);
         if constexpr (DT == DLM_F32) {
             r[2 * p] = __float_as_uint(x);
             r[2 * p + 1] = __float_as_uint(y);
@@ -184,6 +177,22 @@ __device__ __forceinline__ uint4 slope_of(uint4 w, const Slope& s) {
         }
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// scale * 2^((z - m) c) of a vector, in storage.
+struct Slope {
+    f2 m, c, scale;
+    __device__ Slope(float m1, float c1, float s1) : m(pack2(m1, m1)), c(pack2(c1, c1)), scale(pack2(s1, s1)) {}
+};
+template <int DT>
+__device__ __forceinline__ uint4 slope_of(uint4 w, const Slope& s) {
+    constexpr int EPV = Row<DT>::EPV;
+    float z[EPV];
+    Row<DT>::unpack(w, z);
+    f2 g[EPV / 2];
+#pragma unroll
+    for (int p = 0; p < EPV / 2; ++p) g[p] = mul2(ex2x2(mul2(sub2(pack2(z[2 * p], z[2 * p + 1]), s.m), s.c)), s.scale);
+    return packed<DT>(g);
 }
 
 // ---- block-wide helpers (every thread of the CTA calls them) --------------

@@ -34,7 +34,6 @@ struct Shape {
 constexpr int kMaxRing = 6;
 constexpr float kRebase = 12.0f;        // powers of 2 of headroom before a thread's reference moves
 constexpr int64_t kInL2 = 48 << 20;     // rows in flight that the second pass still finds in L2
-constexpr int kPairSlice = 160 * 1024;  // preference step: the same, by a slice's size
 constexpr int kLeast = 8 * 1024;        // a slice is not cut below this to fill the GPU
 constexpr long long kWaitLimit = 4000000000LL;  // ~2 s
 
@@ -110,6 +109,9 @@ __device__ __forceinline__ void fetch(void* dst, const void* src, uint32_t bytes
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
+// Every launch here may begin while the one before it on the stream ends, and nothing of
+// it touches memory before that has ended.
+__device__ __forceinline__ void wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Asks for a cluster of the grid that has not started: its first CTA's index arrives
 // in all CTAs of this one, or that there is none.
 __device__ __forceinline__ void ask_next(void* answer, uint64_t* bar, bool cluster) {
@@ -164,12 +166,10 @@ __device__ constexpr uint32_t neg_inf_bits() {
 // ---- rows -----------------------------------------------------------------------
 
 // A row as the fetching warp hands it over.
-// no more rows; not touched; without a loss (its sums', its gradient's turn); read for its sums; for its gradient
-enum : int { kEnd, kSkip, kNone, kNoGrad, kRow, kGrad };
+enum : int { kEnd, kSkip, kNone, kRow };  // no more rows; not touched; without a loss or gradient; read
 struct Item {
     int64_t q, o;     // its place in the logits, and in the per-row arrays
     int kind, token;
-    int pair;         // preference step: its segment, and in the lowest bit the side of the pair
     float weight;
     float m, inv, away, k;  // gradient from the state
 };
@@ -313,9 +313,7 @@ __device__ __forceinline__ TokenRow merge_row(const TokenArgs& a, const Shared& 
 // settings, and their slices chunk by chunk into the ring.  What the next row needs is
 // asked for while this row's chunks are on their way: the row itself (about 1 us), then
 // its token and weight (another), which are not looked at before the row's turn.
-// PAIRS: the rows come from give_tickets instead, each once for its sums and once for its
-// gradient.
-template <int DT, bool SUMS, bool GRAD, bool PAIRS>
+template <int DT, bool SUMS, bool GRAD>
 struct Fetcher {
     const TokenArgs& a;
     Shared& sh;
@@ -331,12 +329,17 @@ struct Fetcher {
     __device__ Fetcher(const TokenArgs& args, Shared& s, unsigned char* r, int k)
         : a(args), sh(s), ring(r), rank(k), sl(args.vocab, args.split, k) {}
 
+    // (the last rows first where the call before on the stream has read them last: L2 has them)
+    __device__ __forceinline__ int64_t row_of(uint32_t cta) const {
+        const int64_t r = cta / a.split;
+        return a.backwards ? a.n_rows - 1 - r : r;
+    }
     // Starts to read what belongs to row r.
     __device__ __forceinline__ void read_row(int64_t r) {
         Item& it = next_item;
-        if (!PAIRS) it.kind = kRow;
+        it.kind = kRow;
         it.q = r;
-        if (SUMS && !PAIRS && a.row_index) {
+        if (SUMS && a.row_index) {
             it.q = a.row_index[r];
             if (it.q < 0 || (a.n_src > 0 && it.q >= a.n_src)) {
                 it.kind = kSkip;
@@ -364,7 +367,7 @@ struct Fetcher {
     // The item that read_row() began.
     __device__ __forceinline__ Item row_read() {
         Item it = next_item;
-        if (it.kind == kRow || it.kind == kGrad) {
+        if (it.kind == kRow) {
             bool none = it.token < 0 || it.token >= a.vocab;
             if (SUMS) {
                 none = none || it.weight == 0.f;
@@ -373,13 +376,13 @@ struct Fetcher {
                 it.k *= (float)a.inv_t * it.weight;
                 none = none || it.k == 0.f || it.inv == 0.f;
             }
-            if (none) it.kind = it.kind == kRow && SUMS ? kNone : kNoGrad;
+            if (none) it.kind = kNone;
         }
         return it;
     }
     // The first CTA asks for a row once every CTA has read the last answer.
     __device__ __forceinline__ bool ask(bool block) {
-        if (PAIRS || rank != 0 || asked > answers) return true;
+        if (rank != 0 || asked > answers) return true;
         if (asked > 0) {
             const uint32_t parity = (asked - 1) & 1u;
             if (block ? !wait_for(&sh.next_free, parity) : !mbar_test_wait(&sh.next_free, parity)) return !block;
@@ -393,17 +396,8 @@ struct Fetcher {
         if (have_next) return ask(false);
         if (!ask(block)) return false;
         if (block ? !wait_for(&sh.next, answers & 1u) : !mbar_test_wait(&sh.next, answers & 1u)) return !block;
-        uint32_t cta = 0;
-        bool more;
-        if (PAIRS) {
-            const int4 x = *reinterpret_cast<const int4*>(sh.answer);
-            cta = (uint32_t)x.x;
-            next_item.pair = x.z;
-            more = x.y != kEnd;
-            next_item.kind = x.y;
-        } else {
-            more = next_cta(sh.answer, cta);
-        }
+        uint32_t cta;
+        const bool more = next_cta(sh.answer, cta);
         ++answers;
         have_next = true;
         if (!more) {
@@ -414,15 +408,12 @@ struct Fetcher {
         mbar_expect_tx(&sh.next, 16);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the answer has been read before the next one is written
         arrive_at(&sh.next_free, 0);
-        read_row(PAIRS ? cta : cta / a.split);
+        read_row(row_of(cta));
         return ask(false);
     }
     __device__ bool run() {
-        const int passes = SUMS && GRAD && !PAIRS && !a.resident ? 2 : 1;
-        if (!PAIRS)
-            read_row(blockIdx.x / a.split);
-        else if (!look_ahead(true))
-            return false;
+        const int passes = SUMS && GRAD && !a.resident ? 2 : 1;
+        read_row(row_of(blockIdx.x));
         for (uint32_t i = 0;; ++i) {
             const Item it = row_read();
             have_next = false;
@@ -431,7 +422,7 @@ struct Fetcher {
             sh.item[slot] = it;
             arrive(&sh.item_full[slot]);
             if (it.kind == kEnd) return true;
-            if (it.kind == kRow || it.kind == kGrad) {
+            if (it.kind == kRow) {
                 const char* src = static_cast<const char*>(a.logits) + it.q * a.row_stride * Row<DT>::ESZ + (int64_t)sl.v0 * 16;
                 for (int pass = 0; pass < passes; ++pass)
                     for (int c = 0; c < sl.chunks; ++c) {
@@ -602,15 +593,13 @@ __device__ __forceinline__ bool put_gradient(const TokenArgs& a, Shared& sh, uns
     return true;
 }
 
-// The arithmetic's warps.  BOTH: a row's gradient follows its sums; else an item is one of
-// the two (PAIRS: the slope comes from finish_rows, else it is in the item).
-template <int DT, bool SUMS, bool GRAD, bool PAIRS>
+// The arithmetic's warps.
+template <int DT, bool SUMS, bool GRAD>
 __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, int rank) {
-    constexpr bool BOTH = SUMS && GRAD && !PAIRS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const TokenSlice<DT> sl(a.vocab, a.split, rank);
     Cursor cur;
-    uint32_t rows = 0, slopes = 0;  // rows whose sums were taken; slopes that were waited for
+    uint32_t rows = 0;  // rows whose sums were taken
     for (uint32_t i = 0;; ++i) {
         const int slot = i % kItems;
         if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
@@ -618,30 +607,31 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
         const int kind = it.kind;
         if (kind == kEnd) return true;
         const int64_t q = it.q;
-        if (GRAD && (BOTH ? kind == kNone : kind == kNoGrad))
+        if (GRAD && kind == kNone)
             write_zeros<DT>(static_cast<char*>(a.grad) + q * a.grad_stride * Row<DT>::ESZ, a.vocab, sl);
-        const int token = it.token;
-        Cursor from = cur;
-        if (SUMS && kind == kRow) {
-            Part part;
-            if (!take_sums<DT>(a, sh, ring, sl, q, token, BOTH && a.resident, cur, part)) return false;
-            const int ps = rows % kSlots, to = BOTH ? a.split : 1;  // every CTA, or the first
-            if (lane < to) send(&sh.part[ps][rank * kWarps + warp], &sh.shares[ps], lane, part);
-            ++rows;
-        }
-        if (GRAD && (kind == kGrad || (kind == kRow && !PAIRS))) {
-            RowSlope x{it.m, it.inv, it.away, it.k};
+        if (kind == kRow) {
+            const int token = it.token;
+            Cursor from = cur;
             if (SUMS) {
-                const int rs = slopes % kItems;
-                if (!wait_warp(&sh.row_ready[rs], (slopes / kItems) & 1u)) return false;
-                const float4 y = sh.row[rs];
-                x = RowSlope{y.x, y.y, y.z, y.w * (float)a.inv_t};
-                ++slopes;
+                Part part;
+                if (!take_sums<DT>(a, sh, ring, sl, q, token, GRAD && a.resident, cur, part)) return false;
+                const int ps = rows % kSlots, to = GRAD ? a.split : 1;  // every CTA, or the first
+                if (lane < to) send(&sh.part[ps][rank * kWarps + warp], &sh.shares[ps], lane, part);
             }
-            const bool there = BOTH && a.resident;
-            if (!there) from = cur;
-            if (!put_gradient<DT>(a, sh, ring, sl, q, token, x, there, from)) return false;
-            cur = from;
+            if (GRAD) {
+                RowSlope x{it.m, it.inv, it.away, it.k};
+                if (SUMS) {
+                    const int rs = rows % kItems;
+                    if (!wait_warp(&sh.row_ready[rs], (rows / kItems) & 1u)) return false;
+                    const float4 y = sh.row[rs];
+                    x = RowSlope{y.x, y.y, y.z, y.w * (float)a.inv_t};
+                }
+                const bool there = SUMS && a.resident;
+                if (!there) from = cur;
+                if (!put_gradient<DT>(a, sh, ring, sl, q, token, x, there, from)) return false;
+                cur = from;
+            }
+            ++rows;
         }
         __syncwarp();
         if (lane == 0) arrive(&sh.item_empty[slot]);
@@ -674,17 +664,19 @@ __device__ __forceinline__ void set_up(const TokenArgs& a, Shared& sh) {
 template <int DT, bool SUMS, bool GRAD>
 __global__ void __launch_bounds__(kBlock, Shape<SUMS, GRAD>::ctas) token_kernel(const TokenArgs a) {
     extern __shared__ __align__(128) unsigned char s_raw[];
+    asm volatile("griddepcontrol.launch_dependents;");
     Shared& sh = *reinterpret_cast<Shared*>(s_raw);
     unsigned char* ring = s_raw + ring_offset();
     const int t = threadIdx.x, rank = (int)(blockIdx.x % a.split);
     set_up<SUMS>(a, sh);
+    wait_prior();
     bool ok = true;
     if (t < kThreads) {
-        ok = work_rows<DT, SUMS, GRAD, false>(a, sh, ring, rank);
+        ok = work_rows<DT, SUMS, GRAD>(a, sh, ring, rank);
     } else if (t < kThreads + 32) {
         if (SUMS) ok = finish_rows<GRAD>(a, sh, rank);
     } else if (t == kThreads + 32) {
-        Fetcher<DT, SUMS, GRAD, false> f(a, sh, ring, rank);
+        Fetcher<DT, SUMS, GRAD> f(a, sh, ring, rank);
         ok = f.ask(true) && f.run();
         if (!ok) f.drain();
     }
@@ -692,48 +684,6 @@ __global__ void __launch_bounds__(kBlock, Shape<SUMS, GRAD>::ctas) token_kernel(
     __syncwarp();
     if (a.split > 1) cg::this_cluster().sync();  // no CTA ends before what others send to it has come
 }
-
-// ---- the preference step in one pass over the rows -------------------------------
-//
-// A row's gradient needs the sums of all rows of its pair.  Rows are handed out by a
-// counter in one order: their sums in row order, and a pair's gradients once `lag` more
-// rows' sums have been given out after its last, so that the pair is settled when they
-// come and its rows are still in L2 (the latest first, for a pair that L2 does not
-// hold).  Whoever finishes a pair's last row settles it.  An item waits only for items
-// that were given out before it, to clusters that run, so the waits end.
-
-struct PairWork {
-    uint32_t* ticket;
-    float* state;            // [n_rows][DLM_TOKEN_STATE]
-    int32_t* at;             // [2 n_pairs + 1] offsets, put right
-    uint32_t* left;          // [n_pairs + 2] rows of a segment that are not finished
-    unsigned long long* slope;  // [n_pairs + 2] its slope, and 1 in the upper half once it is there
-};
-__host__ __device__ inline size_t pair_work_bytes(int64_t n_rows, int64_t n_pairs) {
-    return 256 + (size_t)n_rows * DLM_TOKEN_STATE * 4 + (((size_t)n_pairs * 3 + 3) * 4 + 15) / 16 * 16 + (size_t)(n_pairs + 2) * 8;
-}
-__host__ __device__ inline PairWork pair_work(void* workspace, int64_t n_rows, int64_t n_pairs) {
-    unsigned char* p = static_cast<unsigned char*>(workspace);
-    PairWork w;
-    w.ticket = reinterpret_cast<uint32_t*>(p);
-    p += 256;
-    w.state = reinterpret_cast<float*>(p);
-    p += (size_t)n_rows * DLM_TOKEN_STATE * 4;
-    w.at = reinterpret_cast<int32_t*>(p);
-    w.left = reinterpret_cast<uint32_t*>(w.at + 2 * n_pairs + 1);
-    p += (((size_t)n_pairs * 3 + 3) * 4 + 15) / 16 * 16;
-    w.slope = reinterpret_cast<unsigned long long*>(p);
-    return w;
-}
-
-// Segments: the rows before the first pair, the pairs, the rows behind the last.
-struct Segments {
-    const PairWork& w;
-    const int64_t rows, pairs;
-    __device__ __forceinline__ int64_t begin(int64_t j) const {  // of segment j; of pairs + 2: the end
-        return j <= 0 ? 0 : j <= pairs + 1 ? (int64_t)w.at[2 * (j - 1)] : rows;
-    }
-};
 
 // The loss of pair i from its scores, by one thread: its slope.
 __device__ float finish_pair(const TokenArgs& a, int64_t i, double chosen, double rejected) {
@@ -748,245 +698,64 @@ __device__ float finish_pair(const TokenArgs& a, int64_t i, double chosen, doubl
     return x.slope;
 }
 
-// The workspace before a step: the offsets put right, counters, and the losses of pairs
-// without rows.  One CTA.
-constexpr int kStartThreads = 1024;
-__global__ void __launch_bounds__(kStartThreads) pair_start_kernel(const TokenArgs a) {
-    asm volatile("griddepcontrol.launch_dependents;");
-    __shared__ int32_t s_top[kStartThreads / 32];
-    const PairWork w = pair_work(a.workspace, a.n_rows, a.n_pairs);
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t n = 2 * a.n_pairs + 1;
-    if (t == 0) *w.ticket = 0;
-    int32_t before = 0;  // the largest so far
-    for (int64_t base = 0; base < n; base += kStartThreads) {
-        const int64_t i = base + t;
-        const int32_t given = i < n ? a.offsets[i] : 0;
-        int32_t x = (int32_t)min(max((int64_t)given, (int64_t)0), a.n_rows);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int32_t y = __shfl_up_sync(DLM_FULL_MASK, x, o);
-            if (lane >= o) x = max(x, y);
-        }
-        if (lane == 31) s_top[warp] = x;
-        __syncthreads();
-        int32_t low = before;
-        for (int k = 0; k < kStartThreads / 32; ++k) {
-            if (k < warp) low = max(low, s_top[k]);
-            before = max(before, s_top[k]);
-        }
-        x = max(x, low);
-        if (i < n) {
-            w.at[i] = x;
-            if (x != given) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
-        }
-        __syncthreads();
-    }
-    const Segments seg{w, a.n_rows, a.n_pairs};
-    for (int64_t j = t; j < a.n_pairs + 2; j += kStartThreads) {
-        const uint32_t rows = (uint32_t)(seg.begin(j + 1) - seg.begin(j));
-        w.left[j] = rows;
-        w.slope[j] = 0;
-        if (rows == 0 && j >= 1 && j <= a.n_pairs) finish_pair(a, j - 1, 0.0, 0.0);
-    }
-}
-
-// One thread of the first CTA of a cluster: what the cluster does next, to all its CTAs.
-constexpr int kAtOnce = 8;
-__device__ bool give_tickets(const TokenArgs& a, Shared& sh, const PairWork& w) {
-    const Segments seg{w, a.n_rows, a.n_pairs};
-    const int64_t N = a.n_rows, last = a.n_pairs + 1;
-    // the last segment whose gradients have begun (-1: none), where they begin, its rows
-    int64_t j = -1, g_start = 0, g_from = 0, g_to = 0;
-    int64_t f = 0, f_to = seg.begin(1);  // the segment whose sums are given out, and its end
-    for (uint32_t n = 0;; ++n) {
-        const int64_t t = atomicAdd(w.ticket, 1u);
-        int row = 0, kind = kEnd, pair = 0;
-        if (t < 2 * N) {
-            for (;;) {  // some segments at a time: their bounds are read together
-                int32_t b[kAtOnce + 1];
-#pragma unroll
-                for (int k = 0; k <= kAtOnce; ++k) b[k] = (int32_t)seg.begin(min(j + 1 + k, last + 1));
-                int took = 0;
-#pragma unroll
-                for (int k = 0; k < kAtOnce; ++k) {
-                    const int64_t start = min(N, (int64_t)b[k + 1] + a.lag) + b[k];
-                    if (took == k && j + 1 + k <= last && start <= t) {
-                        ++took;
-                        g_start = start;
-                        g_from = b[k];
-                        g_to = b[k + 1];
-                    }
-                }
-                j += took;
-                if (took < kAtOnce) break;
-            }
-            if (j >= 0 && t - g_start < g_to - g_from) {
-                kind = kGrad;
-                row = (int)(g_to - 1 - (t - g_start));
-                pair = (int)(2 * j) + (j >= 1 && j < last && row >= w.at[2 * (j - 1) + 1]);
-            } else {
-                kind = kRow;
-                row = (int)(t - g_to);  // (as many gradients as rows of the segments begun)
-                while (row >= f_to && f < last) {
-                    int32_t b[kAtOnce];
-#pragma unroll
-                    for (int k = 0; k < kAtOnce; ++k) b[k] = (int32_t)seg.begin(min(f + 2 + k, last + 1));
-#pragma unroll
-                    for (int k = 0; k < kAtOnce; ++k)
-                        if (row >= f_to && f < last) {
-                            ++f;
-                            f_to = b[k];
-                        }
-                }
-                pair = (int)(2 * f);
-            }
-        }
-        if (n > 0 && !wait_for(&sh.next_free, (n - 1) & 1u)) return false;
-        for (int r = 0; r < a.split; ++r)
-            asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                             remote(sh.answer, r)),
-                         "r"(row), "r"(kind), "r"(pair), "r"(0), "r"(remote(&sh.next, r))
-                         : "memory");
-        if (kind == kEnd) return true;
-    }
-}
-
-// A segment all of whose rows are finished: the pair's scores, loss and slope, by a warp
-// (rows in no pair: 0).
-__device__ void settle_pair(const TokenArgs& a, const PairWork& w, int64_t segment) {
-    const int lane = threadIdx.x & 31;
-    const int64_t i = segment - 1;
-    const bool outside = i < 0 || i == a.n_pairs;
-    double score[2];
-    for (int side = 0; side < 2; ++side) {
-        const int64_t to = outside ? 0 : w.at[2 * i + side + 1];
-        double sum = 0.0;
-#pragma unroll 8
-        for (int64_t r = outside ? 0 : w.at[2 * i + side] + lane; r < to; r += 32)
-            sum += __ldcg(reinterpret_cast<const double*>(w.state + r * DLM_TOKEN_STATE + 4));
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(DLM_FULL_MASK, sum, o);
-        score[side] = sum;
-    }
-    if (lane == 0) {
-        const float slope = outside ? 0.f : finish_pair(a, i, score[0], score[1]);
-        asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(w.slope + segment), "l"((1ull << 32) | __float_as_uint(slope))
-                     : "memory");
-    }
-}
-
-// The warp that finishes rows: a row's sums as in finish_rows, and a gradient's slope.
-__device__ bool finish_pair_rows(const TokenArgs& a, Shared& sh, const PairWork& w, int rank) {
-    const int lane = threadIdx.x & 31, n_parts = a.split * kWarps;
-    uint32_t rows = 0, slopes = 0;
-    for (uint32_t i = 0;; ++i) {
-        const int slot = i % kItems;
-        if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
-        const int kind = sh.item[slot].kind, pair = sh.item[slot].pair;
-        const int64_t r = sh.item[slot].o;
-        if (kind == kEnd) return true;
-        if (kind == kGrad) {
-            unsigned long long x = 0;
-            const long long t0 = clock64();
-            for (;;) {
-                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(w.slope + (pair >> 1)) : "memory");
-                const bool late = clock64() - t0 > kWaitLimit;
-                if (__any_sync(DLM_FULL_MASK, (x >> 32) != 0)) break;
-                if (__any_sync(DLM_FULL_MASK, late)) return false;
-                __nanosleep(200);
-            }
-            if (lane == 0) {
-                asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(w.slope + (pair >> 1)) : "memory");
-                const float4 s = __ldcg(reinterpret_cast<const float4*>(w.state + r * DLM_TOKEN_STATE));
-                const float slope = __uint_as_float((uint32_t)x) * sh.item[slot].weight;
-                sh.row[slopes % kItems] = make_float4(s.x, s.y, s.z, pair & 1 ? -slope : slope);
-                arrive(&sh.row_ready[slopes % kItems]);
-            }
-            ++slopes;
-        }
-        if (rank == 0 && (kind == kRow || kind == kNone)) {
-            if (kind == kRow) {
-                const RowInputs in = row_inputs(a, r, sh.item[slot].weight);
-                const int ps = rows % kSlots;
-                if (lane == 0) mbar_expect_tx(&sh.shares[ps], n_parts * (uint32_t)sizeof(Part));
-                if (!wait_warp(&sh.shares[ps], (rows / kSlots) & 1u)) return false;
-                const TokenRow x = merge_row(a, sh, ps, n_parts);
-                finish_row(a, r, x, in, lane == 0);
-                ++rows;
-            } else if (lane == 0) {
-                finish_none(a, r);
-            }
-            uint32_t left = 0;
-            if (lane == 0) {
-                __threadfence();
-                left = atomicSub(w.left + (pair >> 1), 1u);
-                __threadfence();
-            }
-            if (__shfl_sync(DLM_FULL_MASK, left, 0) == 1u) settle_pair(a, w, pair >> 1);
-        }
-        __syncwarp();
-        if (lane == 0) arrive(&sh.item_empty[slot]);
-    }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kBlock + 32, Shape<true, true>::ctas) pair_step_kernel(const TokenArgs a) {
-    extern __shared__ __align__(128) unsigned char s_raw[];
-    Shared& sh = *reinterpret_cast<Shared*>(s_raw);
-    unsigned char* ring = s_raw + ring_offset();
-    const int t = threadIdx.x, rank = (int)(blockIdx.x % a.split);
-    const PairWork w = pair_work(a.workspace, a.n_rows, a.n_pairs);
-    set_up<true>(a, sh);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the workspace is ready
-    bool ok = true;
-    if (t < kThreads) {
-        ok = work_rows<DT, true, true, true>(a, sh, ring, rank);
-    } else if (t < kThreads + 32) {
-        ok = finish_pair_rows(a, sh, w, rank);
-    } else if (t == kThreads + 32) {
-        Fetcher<DT, true, true, true> f(a, sh, ring, rank);
-        ok = f.run();
-        if (!ok) f.drain();
-    } else if (t == kBlock && rank == 0) {  // (a warp of its own: it and the fetching one wait for each other)
-        ok = give_tickets(a, sh, w);
-    }
-    if (!ok) raise_status(a.dev_status, DLM_DEV_TIMEOUT);
-    __syncwarp();
-    if (a.split > 1) cg::this_cluster().sync();
-}
-
-// The offsets' bounds [b, e) of sequence s as they should be: within the rows and in
-// order (each offset at least its predecessors).
-__device__ __forceinline__ int64_t clean_offset(const TokenArgs& a, int64_t s) {
-    int64_t most = 0;
-    for (int64_t i = threadIdx.x & 31; i <= s; i += 32) most = max(most, (int64_t)a.offsets[i]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(DLM_FULL_MASK, most, o));
-    return min(most, a.n_rows);
-}
-
-// One CTA per pair: the scores, the loss, and the slope of every row of the pair.
+// One CTA per pair: the scores, the loss, and the slope of every row of the pair.  Bound
+// by latency: three loads after each other, a sum over the CTA, the loss and a store; a
+// thread's first rows are read before the sum, so that only stores follow it.
+constexpr int kPairRows = 4;
 __global__ void __launch_bounds__(kThreads) pair_kernel(const TokenArgs a) {
     __shared__ double s_sum[2][kWarps];
+    __shared__ int32_t s_top[kWarps];
     __shared__ float s_slope;
-    const int t = threadIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t i = blockIdx.x;
+    wait_prior();
+    // the pair's offsets, and the largest of those before them: within the rows and in order
+    const int32_t given[3] = {a.offsets[2 * i], a.offsets[2 * i + 1], a.offsets[2 * i + 2]};
+    int32_t top = 0;
+    for (int64_t k = t; k < 2 * i; k += kThreads) top = max(top, a.offsets[k]);
+    top = __reduce_max_sync(DLM_FULL_MASK, top);
+    if (lane == 0) s_top[warp] = top;
+    __syncthreads();
     int64_t at[3];
-    for (int j = 0; j < 3; ++j) {
-        at[j] = clean_offset(a, 2 * i + j);
-        if (t == 0 && at[j] != a.offsets[2 * i + j]) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = max(top, s_top[w]);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        top = max(top, given[k]);
+        at[k] = min((int64_t)top, a.n_rows);
+        if (t == 0 && at[k] != given[k]) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
     }
-    for (int side = 0; side < 2; ++side) {
-        double sum = 0.0;
-        for (int64_t r = at[side] + t; r < at[side + 1]; r += kThreads)
-            sum += *reinterpret_cast<const double*>(a.state + r * DLM_TOKEN_STATE + 4);
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(DLM_FULL_MASK, sum, o);
-        if ((t & 31) == 0) s_sum[side][t >> 5] = sum;
+    double sum[2] = {0.0, 0.0};
+    float weight[kPairRows];
+    bool has[kPairRows];
+#pragma unroll
+    for (int k = 0; k < kPairRows; ++k) {
+        const int64_t r = at[0] + t + k * kThreads;
+        has[k] = false;
+        if (r < at[2]) {
+            const float* s = a.state + r * DLM_TOKEN_STATE;
+            weight[k] = a.weights ? a.weights[r] : 1.f;
+            has[k] = s[1] != 0.f;  // (0: no loss of its own)
+            const double term = *reinterpret_cast<const double*>(s + 4);
+            sum[r >= at[1]] += term;
+        }
+    }
+    for (int64_t r = at[0] + t + kPairRows * kThreads; r < at[2]; r += kThreads)
+        sum[r >= at[1]] += *reinterpret_cast<const double*>(a.state + r * DLM_TOKEN_STATE + 4);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        sum[0] += __shfl_xor_sync(DLM_FULL_MASK, sum[0], o);
+        sum[1] += __shfl_xor_sync(DLM_FULL_MASK, sum[1], o);
+    }
+    if (lane == 0) {
+        s_sum[0][warp] = sum[0];
+        s_sum[1][warp] = sum[1];
     }
     __syncthreads();
     if (t == 0) {
         double score[2] = {0.0, 0.0};
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             score[0] += s_sum[0][w];
             score[1] += s_sum[1][w];
@@ -994,41 +763,44 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const TokenArgs a) {
         s_slope = finish_pair(a, i, score[0], score[1]);
     }
     __syncthreads();
-    for (int side = 0; side < 2; ++side)
-        for (int64_t r = at[side] + t; r < at[side + 1]; r += kThreads) {
-            float* s = a.state + r * DLM_TOKEN_STATE;
-            if (s[1] == 0.f) continue;  // no loss of its own
-            s[3] = (side ? -s_slope : s_slope) * (a.weights ? a.weights[r] : 1.f);
-            s[6] = __int_as_float((int)i);
-        }
+    const float slope = s_slope;
+    auto put = [&](int64_t r, float w) {
+        float* s = a.state + r * DLM_TOKEN_STATE;
+        s[3] = (r >= at[1] ? -slope : slope) * w;
+        s[6] = __int_as_float((int)i);
+    };
+#pragma unroll
+    for (int k = 0; k < kPairRows; ++k)
+        if (has[k]) put(at[0] + t + k * kThreads, weight[k]);
+    for (int64_t r = at[0] + t + kPairRows * kThreads; r < at[2]; r += kThreads)
+        if (a.state[r * DLM_TOKEN_STATE + 1] != 0.f) put(r, a.weights ? a.weights[r] : 1.f);
 }
 
 }  // namespace
 
-size_t preference_workspace(int64_t n_rows, int64_t n_pairs) { return pair_work_bytes(n_rows, n_pairs); }
+size_t preference_workspace(int64_t n_rows, int64_t n_pairs) {
+    (void)n_pairs;
+    return (size_t)(n_rows * DLM_TOKEN_STATE * 4 + 16);
+}
 
 namespace {
 
-// after: the launch may begin while the one before it on the stream ends.
 template <typename F>
-cudaError_t launch_clusters(F kernel, const TokenArgs& a, int64_t clusters, int block, bool after, cudaStream_t st) {
-    // the same limit whatever the call's size: calls may run side by side
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    if (e != cudaSuccess) return e;
+cudaError_t launch_grid(F kernel, const TokenArgs& a, unsigned grid, int block, size_t smem, int cluster, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * a.split));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = ring_offset() + (size_t)a.ring * kChunkBytes;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = after ? 2 : 1;
+    cfg.numAttrs = cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -1043,44 +815,41 @@ cudaError_t launch_token_kernel(TokenArgs a, cudaStream_t st) {
     auto chunks = [&](int n) { return (slice(n) + kChunkVecs - 1) / kChunkVecs; };
     a.ring = S::ring;
     int split = 1;
-    if (SUMS && GRAD)
+    if (SUMS && GRAD) {
+        // the second reading is from the ring or from L2 (2048 rows of 152064 bf16: 187 us so
+        // with two CTAs per row, 232 with one, whose rows in flight L2 does not hold)
         while (split < 8 && chunks(split) > a.ring && slots / split * nv * 16 > kInL2) split *= 2;
-    while (split < 8 && a.n_rows * split < slots && slice(split) * 16 > kLeast) split *= 2;
+    } else if (GRAD) {
+        // slices that the ring holds (1024 rows of 126464 bf16: 76 us with four, 83 with one)
+        while (split < 8 && chunks(split) > a.ring) split *= 2;
+    } else if (a.n_rows > slots && a.n_rows < 7 * slots / 2) {
+        // whole rows would leave the last of two to four rounds to few CTAs (1024 rows of
+        // 126464 bf16: 50 us with two, 56 with one; 2048 of 152064: 99 and 96)
+        split = 2;
+    }
+    // rows too few for all SMs (76 rows of 126464 bf16: 12.4 us with two CTAs each, 14.8 with
+    // one, 13.1 with eight)
+    while (split < 8 && a.n_rows * split < a.num_sms && slice(split) * 16 > kLeast) split *= 2;
     a.split = split;
     a.resident = chunks(split) <= a.ring;
-    return launch_clusters(token_kernel<DT, SUMS, GRAD>, a, a.n_rows, kBlock, false, st);
-}
-
-template <int DT>
-cudaError_t launch_pair_step(TokenArgs a, cudaStream_t st) {
-    pair_start_kernel<<<1, kStartThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.n_rows == 0) return e;
-    using S = Shape<true, true>;
-    constexpr int EPV = Row<DT>::EPV;
-    const int64_t nv = (a.vocab + EPV - 1) / EPV, slots = (int64_t)S::ctas * a.num_sms;
-    auto slice = [&](int n) { return ((nv + n - 1) / n + 7) / 8 * 8; };
-    a.ring = S::ring;
-    int split = 1;
-    while (split < 8 && slice(split) * 16 > kPairSlice) split *= 2;
-    while (split < 8 && a.n_rows * split < slots && slice(split) * 16 > kLeast) split *= 2;
-    a.split = split;
-    const int64_t clusters = std::min(slots / split, 2 * a.n_rows);
-    a.lag = 2 * clusters;
-    a.state = pair_work(a.workspace, a.n_rows, a.n_pairs).state;
-    return launch_clusters(pair_step_kernel<DT>, a, clusters, kBlock + 32, true, st);
+    // the same limit whatever the call's size: calls may run side by side
+    const cudaError_t e =
+        cudaFuncSetAttribute(token_kernel<DT, SUMS, GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    return launch_grid(token_kernel<DT, SUMS, GRAD>, a, (unsigned)(a.n_rows * a.split), kBlock,
+                       ring_offset() + (size_t)a.ring * kChunkBytes, a.split, st);
 }
 
 template <int DT>
 cudaError_t run_token(TokenArgs a, cudaStream_t st) {
-    if (a.workspace) return launch_pair_step<DT>(a, st);
-    if (a.op == kTokenPreference && a.sums) {  // sums, and the pairs
-        cudaError_t e = a.n_rows ? launch_token_kernel<DT, true, false>(a, st) : cudaSuccess;
-        if (e == cudaSuccess && a.n_pairs > 0) {
-            pair_kernel<<<(unsigned)a.n_pairs, kThreads, 0, st>>>(a);
-            e = cudaGetLastError();
-        }
-        return e;
+    if (a.op == kTokenPreference && a.sums) {  // sums, the pairs, and the gradient from the state
+        if (a.workspace) a.state = static_cast<float*>(a.workspace);
+        cudaError_t e = cudaSuccess;
+        if (a.n_rows) e = launch_token_kernel<DT, true, false>(a, st);
+        if (e == cudaSuccess && a.n_pairs > 0) e = launch_grid(pair_kernel, a, (unsigned)a.n_pairs, kThreads, 0, 0, st);
+        if (e != cudaSuccess || !a.grad || !a.n_rows) return e;
+        a.backwards = 1;
+        return launch_token_kernel<DT, false, true>(a, st);
     }
     if (!a.sums) return launch_token_kernel<DT, false, true>(a, st);
     if (!a.grad) return launch_token_kernel<DT, true, false>(a, st);
