@@ -254,7 +254,7 @@ __device__ __forceinline__ void add_vectors(Running& a, const uint4 (&w)[N], f2 
     a.sum = add2(a.sum, sum[0]);
 }
 
-// What a row's loss is, by the warp that has its sums (lane 0 writes): its slope.
+// What a row's loss needs beside its sums.
 struct RowInputs {
     float weight, advantage, old_logp, ref_logp;
 };
@@ -262,24 +262,24 @@ __device__ __forceinline__ RowInputs row_inputs(const TokenArgs& a, int64_t o, f
     return RowInputs{weight, a.op == kTokenPolicy ? a.advantages[o] : 0.f, a.old_logp ? a.old_logp[o] : 0.f,
                      a.ref_logp ? a.ref_logp[o] : 0.f};
 }
-__device__ float finish_row(const TokenArgs& a, int64_t o, const TokenRow& t, const RowInputs& in, bool write) {
-    LossSlope x{0.f, in.weight};
-    double term = 0.0;
+// What a row's loss is.
+__device__ __forceinline__ LossSlope row_loss(const TokenArgs& a, const TokenRow& t, const RowInputs& in) {
     if (a.op == kTokenPolicy)
-        x = policy_row(a.policy, t.logp, in.weight, in.advantage, a.old_logp != nullptr, in.old_logp, in.ref_logp);
-    else if (a.op == kTokenPreference)
-        term = (double)in.weight * (t.logp - (double)in.ref_logp);
-    if (!write) return x.slope;
+        return policy_row(a.policy, t.logp, in.weight, in.advantage, a.old_logp != nullptr, in.old_logp, in.ref_logp);
+    return LossSlope{0.f, in.weight};
+}
+// Its outputs, by one thread.
+__device__ __forceinline__ void write_row(const TokenArgs& a, int64_t o, const TokenRow& t, const RowInputs& in, LossSlope x) {
     if (!t.ok || x.slope != x.slope) raise_status(a.dev_status, DLM_DEV_NONFINITE);
     if (a.op == kTokenPolicy) a.loss[o] = x.loss;
     if (a.logp) a.logp[o] = (float)t.logp;
     if (a.lse) a.lse[o] = (float)t.lse;
     if (a.state) {
+        const double term = a.op == kTokenPreference ? (double)in.weight * (t.logp - (double)in.ref_logp) : 0.0;
         float4* s = reinterpret_cast<float4*>(a.state + o * DLM_TOKEN_STATE);
         s[0] = make_float4(t.m, t.inv, t.away, a.op == kTokenPreference ? 0.f : x.slope);  // (a row in no pair: 0)
         s[1] = make_float4(__int_as_float(__double2loint(term)), __int_as_float(__double2hiint(term)), __int_as_float(-1), 0.f);
     }
-    return x.slope;
 }
 // A row without a loss.
 __device__ void finish_none(const TokenArgs& a, int64_t o) {
@@ -481,11 +481,12 @@ __device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
                 if (lane == 0) mbar_expect_tx(&sh.shares[ps], n_parts * (uint32_t)sizeof(Part));
                 if (!wait_warp(&sh.shares[ps], (rows / kSlots) & 1u)) return false;
                 const TokenRow x = merge_row(a, sh, ps, n_parts);
-                const float slope = finish_row(a, o, x, in, rank == 0 && lane == 0);
-                if (GRAD && lane == 0) {
-                    sh.row[rows % kItems] = make_float4(x.m, x.inv, x.away, slope);
+                const LossSlope y = row_loss(a, x, in);
+                if (GRAD && lane == 0) {  // first of all: the gradient waits for it
+                    sh.row[rows % kItems] = make_float4(x.m, x.inv, x.away, y.slope);
                     arrive(&sh.row_ready[rows % kItems]);
                 }
+                if (rank == 0 && lane == 0) write_row(a, o, x, in, y);
             }
             ++rows;
         }
