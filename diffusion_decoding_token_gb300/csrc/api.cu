@@ -850,8 +850,10 @@ static dlm_status token_prepare(dlm::TokenArgs& a, const void* logits, dlm_dtype
     a.vocab = vocab;
     a.row_stride = row_stride;
     a.tokens = tokens;
-    a.inv_t = 1.0 / temperature;
-    split_scale(a.inv_t, a.scale, a.scale_lo);
+    const double inv_t = 1.0 / temperature;
+    a.inv_t = (float)inv_t;
+    a.inv_t_lo = (float)(inv_t - (double)a.inv_t);
+    split_scale(inv_t, a.scale, a.scale_lo);
     a.dev_status = dev_status;
     a.num_sms = sm_count();
     return DLM_OK;

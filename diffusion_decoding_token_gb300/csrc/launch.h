@@ -281,7 +281,7 @@ struct TokenArgs {
     int gather;               // per-row arrays at r instead of q
     const int32_t* tokens;
     float scale, scale_lo;    // log2(e) / temperature in two floats
-    double inv_t;             // 1 / temperature
+    float inv_t, inv_t_lo;    // 1 / temperature, likewise
     int op;                   // kToken*
     int sums;                 // the rows' sums are taken (else the state has them)
     const float* weights;     // [n_rows], nullable: 1

@@ -254,6 +254,8 @@ __device__ __forceinline__ void add_vectors(Running& a, const uint4 (&w)[N], f2 
     a.sum = add2(a.sum, sum[0]);
 }
 
+__device__ __forceinline__ Temper temper(const TokenArgs& a) { return Temper{a.scale, a.scale_lo, Two{a.inv_t, a.inv_t_lo}}; }
+
 // What a row's loss needs beside its sums.
 struct RowInputs {
     float weight, advantage, old_logp, ref_logp;
@@ -272,10 +274,10 @@ __device__ __forceinline__ LossSlope row_loss(const TokenArgs& a, const TokenRow
 __device__ __forceinline__ void write_row(const TokenArgs& a, int64_t o, const TokenRow& t, const RowInputs& in, LossSlope x) {
     if (!t.ok || x.slope != x.slope) raise_status(a.dev_status, DLM_DEV_NONFINITE);
     if (a.op == kTokenPolicy) a.loss[o] = x.loss;
-    if (a.logp) a.logp[o] = (float)t.logp;
-    if (a.lse) a.lse[o] = (float)t.lse;
+    if (a.logp) a.logp[o] = rounded(t.logp);
+    if (a.lse) a.lse[o] = token_lse(t, temper(a));
     if (a.state) {
-        const double term = a.op == kTokenPreference ? (double)in.weight * (t.logp - (double)in.ref_logp) : 0.0;
+        const double term = a.op == kTokenPreference ? (double)in.weight * (((double)t.logp.hi - (double)in.ref_logp) + (double)t.logp.lo) : 0.0;
         float4* s = reinterpret_cast<float4*>(a.state + o * DLM_TOKEN_STATE);
         s[0] = make_float4(t.m, t.inv, t.away, a.op == kTokenPreference ? 0.f : x.slope);  // (a row in no pair: 0)
         s[1] = make_float4(__int_as_float(__double2loint(term)), __int_as_float(__double2hiint(term)), __int_as_float(-1), 0.f);
@@ -306,7 +308,7 @@ __device__ __forceinline__ TokenRow merge_row(const TokenArgs& a, const Shared& 
         p.z = max_nan(p.z, b.z);
     }
     p = warp_part(p, c);
-    return token_row(p.ref, p.sum, p.z, a.scale, a.scale_lo, a.inv_t);
+    return token_row(p.ref, p.sum, p.z, temper(a));
 }
 
 // The fetching warp's thread: rows in the order in which the hardware gives them, their
@@ -373,7 +375,7 @@ struct Fetcher {
                 none = none || it.weight == 0.f;
                 if (it.token >= a.vocab && rank == 0) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
             } else {
-                it.k *= (float)a.inv_t * it.weight;
+                it.k *= a.inv_t * it.weight;
                 none = none || it.k == 0.f || it.inv == 0.f;
             }
             if (none) it.kind = kNone;
@@ -625,7 +627,7 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
                     const int rs = rows % kItems;
                     if (!wait_warp(&sh.row_ready[rs], (rows / kItems) & 1u)) return false;
                     const float4 y = sh.row[rs];
-                    x = RowSlope{y.x, y.y, y.z, y.w * (float)a.inv_t};
+                    x = RowSlope{y.x, y.y, y.z, y.w * a.inv_t};
                 }
                 const bool there = SUMS && a.resident;
                 if (!there) from = cur;

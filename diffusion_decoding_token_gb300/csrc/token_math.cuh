@@ -32,10 +32,33 @@ namespace dlm {
 DLM_HD bool is_finite(float x) { return fabsf(x) < INFINITY; }
 DLM_HD float f32_nan() { return NAN; }
 
-// ln x for a normal x >= 1: the exponent's share in 64 bits, so that what is left to
-// the float logarithm is at most ln 2 / 2 (of x itself it is up to 14, and its last
-// place 2^-20).
-DLM_HD double ln_split(float x) {
+// A number as a sum of two floats, to about 2^-45.  (64-bit arithmetic has a 64th of the
+// 32-bit rate here: with a dozen operations of it a row's slope took 2300 cycles, and the
+// row's gradient waits for that.)
+struct Two {
+    float hi, lo;
+};
+DLM_HD Two two_sum(float a, float b) {
+    const float s = a + b, x = s - a;
+    const float e = (a - (s - x)) + (b - x);
+    return Two{s, is_finite(s) ? e : 0.f};
+}
+DLM_HD Two two_prod(float a, float b) {
+    const float p = a * b;
+    return Two{p, is_finite(p) ? fmaf(a, b, -p) : 0.f};
+}
+DLM_HD Two plus(Two a, Two b) {
+    Two s = two_sum(a.hi, b.hi);
+    if (!is_finite(s.hi)) return s;
+    return two_sum(s.hi, s.lo + (a.lo + b.lo));
+}
+DLM_HD Two minus(Two a) { return Two{-a.hi, -a.lo}; }
+DLM_HD float rounded(Two a) { return a.hi + a.lo; }
+
+// ln x for a normal x >= 1: the exponent's share exactly, so that what is left to the
+// float logarithm is at most ln 2 / 2 (of x itself it is up to 14, and its last place
+// 2^-20).
+DLM_HD Two ln_split(float x) {
     uint32_t b;
     memcpy(&b, &x, 4);
     int e = (int)(b >> 23) - 127;
@@ -46,7 +69,8 @@ DLM_HD double ln_split(float x) {
         m *= 0.5f;
         ++e;
     }
-    return (double)e * 0.6931471805599453 + (double)logf(m);
+    // ln 2 to 12 bits (2839 / 4096), so that times e it is exact, and the rest of it
+    return two_sum((float)e * (2839.f / 4096.f), fmaf((float)e, 3.1946184945e-5f, logf(m)));
 }
 
 // What follows from a row's sums: its maximum, 1 / sum, 1 - p of the token, and the
@@ -55,17 +79,24 @@ DLM_HD double ln_split(float x) {
 struct TokenRow {
     float m, inv, away;
     int ok;
-    double logp, lse;
+    Two logp, ln;  // ln: of the sum relative to m
 };
 
+// 2^-n, 0 <= n <= 126
+DLM_HD float pow2_neg(int n) {
+    const uint32_t b = (uint32_t)(127 - n) << 23;
+    float x;
+    memcpy(&x, &b, 4);
+    return x;
+}
 // x 2^(-d (hi + lo)) to 2^-21 for d >= 0 of any size, err what d was rounded by.  (As one
 // float the exponent would be off by 2^-24 of itself: 2^-17 at 115.)
 DLM_HD float times_exp2(float x, float d, float err, float hi, float lo) {
     const float e = d * hi;
     if (!(e < 200.f)) return e != e ? f32_nan() : 0.f;
-    const float n = rintf(e);
-    const float f = (e - n) + fmaf(err, hi, fmaf(d, lo, fmaf(d, hi, -e)));
-    return ldexpf(x * exp2f(-f), -(int)n);
+    const int n = (int)e, half = n >> 1;
+    const float f = (e - (float)n) + fmaf(err, hi, fmaf(d, lo, fmaf(d, hi, -e)));
+    return x * exp2f(-f) * pow2_neg(half) * pow2_neg(n - half);
 }
 
 // The hardware's 2^x, which the weights are made with, is a little too small on average
@@ -73,33 +104,49 @@ DLM_HD float times_exp2(float x, float d, float err, float hi, float lo) {
 // 2^-24.3 (4.0e-8 to 5.8e-8 over rows of 32000 and 152064 N(0, 4) logits of each type;
 // its rounding scatters by as much).  A sequence's score is a sum of thousands of
 // log-sum-exps, all off to that side, so it is put right where the weights are summed.
-constexpr double kWeightsLow = 4.8e-8;
+constexpr float kWeightsLow = 4.8e-8f;
+
+// log2(e) / T and 1 / T, each as two floats.
+struct Temper {
+    float hi, lo;
+    Two inv;
+};
 
 // The others' sum s_o relative to m_o (-inf: there are none, or all are -inf), and the
-// token's logit; hi + lo = log2(e) / T.  (64-bit arithmetic has a 64th of the 32-bit rate
-// here: a dozen operations of it are left, for ln p's and the log-sum-exp's last digits.)
-DLM_HD TokenRow token_row(float m_o, float s_o, float z_a, float hi, float lo, double inv_t) {
+// token's logit.
+DLM_HD TokenRow token_row(float m_o, float s_o, float z_a, const Temper& c) {
     TokenRow t;
     const bool top = z_a >= m_o;  // the token is at the maximum
     t.m = top ? z_a : m_o;
-    // the distance to the other one, and what it is rounded by
-    const float low = top ? m_o : z_a, d = t.m - low, back = t.m - d;
-    const float err = d < INFINITY ? back - low : 0.f;
-    const float far = d < INFINITY || d != d ? times_exp2(top ? s_o : 1.f, d, err, hi, lo) : 0.f;
+    const float low = top ? m_o : z_a;
+    const Two d = two_sum(t.m, -low);  // the distance to the other one
+    const float far = d.hi < INFINITY || d.hi != d.hi ? times_exp2(top ? s_o : 1.f, d.hi, d.lo, c.hi, c.lo) : 0.f;
     const float others = top ? far : s_o;
     const float total = top ? 1.f + others : far + others;
     // (total is 0 where nothing but -inf is)
     t.ok = is_finite(t.m) && s_o >= 0.f && total > 0.f && total < INFINITY && low == low;
     t.inv = 1.f / total;
     t.away = others * t.inv;
-    const double ln = (top && others < 0.5f ? (double)log1pf(others) : ln_split(total)) + kWeightsLow * (double)t.away;
-    t.logp = ((double)z_a - (double)t.m) * inv_t - ln;
-    t.lse = (double)t.m * inv_t + ln;
+    Two ln = top && others < 0.5f ? Two{log1pf(others), 0.f} : ln_split(total);
+    ln.lo = fmaf(kWeightsLow, t.away, ln.lo);
+    t.logp = minus(ln);
+    if (!top) {
+        Two y = two_prod(d.hi, c.inv.hi);
+        y.lo += is_finite(y.hi) ? fmaf(d.hi, c.inv.lo, d.lo * c.inv.hi) : 0.f;
+        t.logp = plus(minus(y), t.logp);
+    }
+    t.ln = ln;
     if (!t.ok) {
         t.inv = t.away = f32_nan();
-        t.logp = t.lse = (double)f32_nan();
+        t.logp = t.ln = Two{f32_nan(), 0.f};
     }
     return t;
+}
+// The row's log-sum-exp.
+DLM_HD float token_lse(const TokenRow& t, const Temper& c) {
+    Two y = two_prod(t.m, c.inv.hi);
+    y.lo += is_finite(y.hi) ? t.m * c.inv.lo : 0.f;
+    return rounded(plus(y, t.ln));
 }
 
 // e^y - 1 - y without its cancellation near 0.
@@ -135,9 +182,15 @@ DLM_HD LossSlope flagged(LossSlope x) {
     return x;
 }
 
-DLM_HD LossSlope policy_row(const PolicyRule& p, double logp, float weight, float advantage, bool has_old, float old_logp,
+// a - b and b - a of ln p and another log-probability.
+DLM_HD float less(Two a, float b) {
+    const Two s = two_sum(a.hi, -b);
+    return s.hi + (is_finite(s.hi) ? s.lo + a.lo : 0.f);
+}
+
+DLM_HD LossSlope policy_row(const PolicyRule& p, Two logp, float weight, float advantage, bool has_old, float old_logp,
                             float ref_logp) {
-    const float rho = has_old ? expf((float)(logp - (double)old_logp)) : 1.f;
+    const float rho = has_old ? expf(less(logp, old_logp)) : 1.f;
     const float a = advantage;
     float gain = rho * a, slope = gain;
     if (a > 0.f && rho > p.hi) {
@@ -154,9 +207,9 @@ DLM_HD LossSlope policy_row(const PolicyRule& p, double logp, float weight, floa
     }
     LossSlope r{-gain, -slope};
     // (no ratio of its own: logp counts as old, and a row without one has no loss)
-    if (!has_old && !(logp > -INFINITY)) r.loss = r.slope = f32_nan();
+    if (!has_old && !(logp.hi > -INFINITY)) r.loss = r.slope = f32_nan();
     if (p.kl_weight != 0.f) {
-        const float y = (float)((double)ref_logp - logp);
+        const float y = -less(logp, ref_logp);
         float kl, d;
         if (p.kl == DLM_KL_K1) {
             kl = -y;
