@@ -308,7 +308,8 @@ struct TokenArgs {
     int num_sms;
     int split;                // CTAs per row (thread-block cluster size)
     int ring;                 // chunks of a row that a CTA holds
-    int backwards;            // the last rows first
+    int paired;               // sums and gradient of a preference step, one launch each
+    int64_t stay_from;        // its rows from here on are to stay in L2
     int resident;             // a step's row stays there between its sums and its gradient
 };
 size_t preference_workspace(int64_t n_rows, int64_t n_pairs);

@@ -34,6 +34,9 @@ struct Shape {
 constexpr int kMaxRing = 6;
 constexpr float kRebase = 12.0f;        // powers of 2 of headroom before a thread's reference moves
 constexpr int64_t kInL2 = 48 << 20;     // rows in flight that the second pass still finds in L2
+// Rows' bytes that a preference step leaves in L2 for its gradient (1024 rows of 126464
+// bf16: 132 us with 60 to 80 MB, 134 with 40, 139 without, 143 with the first rows first).
+constexpr int64_t kStays = 70 << 20;
 constexpr int kLeast = 8 * 1024;        // a slice is not cut below this to fill the GPU
 constexpr long long kWaitLimit = 4000000000LL;  // ~2 s
 
@@ -103,10 +106,27 @@ __device__ __forceinline__ void send(Part* slot, uint64_t* bar, int rank, Part p
                  "r"(remote(bar, rank))
                  : "memory");
 }
+// How long L2 keeps what a copy reads.
+__device__ __forceinline__ uint64_t l2_normal() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t l2_stays() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t l2_goes() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
 // Untiled copy into this CTA's shared memory: both addresses and the size in whole 16 bytes.
-__device__ __forceinline__ void fetch(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+__device__ __forceinline__ void fetch(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
                  : "memory");
 }
 // Every launch here may begin while the one before it on the stream ends, and nothing of
@@ -331,10 +351,10 @@ struct Fetcher {
     __device__ Fetcher(const TokenArgs& args, Shared& s, unsigned char* r, int k)
         : a(args), sh(s), ring(r), rank(k), sl(args.vocab, args.split, k) {}
 
-    // (the last rows first where the call before on the stream has read them last: L2 has them)
+    // (a preference step's gradient: the last rows first, which L2 still has)
     __device__ __forceinline__ int64_t row_of(uint32_t cta) const {
         const int64_t r = cta / a.split;
-        return a.backwards ? a.n_rows - 1 - r : r;
+        return !SUMS && a.paired ? a.n_rows - 1 - r : r;
     }
     // Starts to read what belongs to row r.
     __device__ __forceinline__ void read_row(int64_t r) {
@@ -425,13 +445,15 @@ struct Fetcher {
             arrive(&sh.item_full[slot]);
             if (it.kind == kEnd) return true;
             if (it.kind == kRow) {
+                // a preference step's gradient begins with the rows whose sums came last
+                const uint64_t policy = !a.paired ? l2_normal() : SUMS && it.q >= a.stay_from ? l2_stays() : l2_goes();
                 const char* src = static_cast<const char*>(a.logits) + it.q * a.row_stride * Row<DT>::ESZ + (int64_t)sl.v0 * 16;
                 for (int pass = 0; pass < passes; ++pass)
                     for (int c = 0; c < sl.chunks; ++c) {
                         if (!wait_for(&sh.empty[cur.at], cur.parity ^ 1u)) return false;
                         const uint32_t bytes = (uint32_t)min(kChunkVecs, sl.whole - c * kChunkVecs) * 16;
                         mbar_expect_tx(&sh.full[cur.at], bytes);
-                        fetch(ring + cur.at * kChunkBytes, src + (int64_t)c * kChunkBytes, bytes, &sh.full[cur.at]);
+                        fetch(ring + cur.at * kChunkBytes, src + (int64_t)c * kChunkBytes, bytes, &sh.full[cur.at], policy);
                         cur.step(a.ring);
                         ++issued;
                         look_ahead(false);
@@ -848,10 +870,11 @@ cudaError_t run_token(TokenArgs a, cudaStream_t st) {
     if (a.op == kTokenPreference && a.sums) {  // sums, the pairs, and the gradient from the state
         if (a.workspace) a.state = static_cast<float*>(a.workspace);
         cudaError_t e = cudaSuccess;
+        a.paired = a.grad != nullptr;
+        a.stay_from = a.n_rows - kStays / (a.vocab * Row<DT>::ESZ);
         if (a.n_rows) e = launch_token_kernel<DT, true, false>(a, st);
         if (e == cudaSuccess && a.n_pairs > 0) e = launch_grid(pair_kernel, a, (unsigned)a.n_pairs, kThreads, 0, 0, st);
         if (e != cudaSuccess || !a.grad || !a.n_rows) return e;
-        a.backwards = 1;
         return launch_token_kernel<DT, false, true>(a, st);
     }
     if (!a.sums) return launch_token_kernel<DT, false, true>(a, st);
