@@ -6,9 +6,36 @@
 // derivative by ln q_a (token_math.cuh has both).  `state` holds what the gradient
 // needs of a row: maximum, 1 / sum, 1 - q_a, slope.
 //
-// The sums and the gradient are bound by HBM: one read of the row, and one write.
-#include <algorithm>
-
+// All of it is bound by HBM: the sums by one read of the row, the gradient by a read and
+// a write.  One kernel does sums, gradient or both:
+//  * A row is cut over a cluster of 1 to 8 CTAs.  Clusters stay and take the next row that
+//    has not begun from the hardware (a cluster launch cancelled in their favour), so rows
+//    that are not read cost nothing and no counter is needed.
+//  * In each CTA one thread fetches: 16 KB at a time into a ring with asynchronous bulk
+//    copies, across rows, so that HBM does not wait at a row's end.  Eight warps add up
+//    what is there.  A warp of its own merges the cluster's shares (sent into shared memory,
+//    counted by a barrier there) and works out the loss, while the others go on.
+//  * A step reads a row once: the slice stays in the ring (up to 96 KB) from its sums to
+//    its gradient.  Rows above 768 KB come twice.
+// Measured (GB300, a call among others; HBM copies 6.8 TB/s):
+//    2048 rows of 152064 bf16: log-probabilities 94 us (6.6 TB/s of 623 MB);
+//      policy step, a quarter of the rows without a loss, 184 us (5.9 TB/s of 1.09 GB);
+//      gradient alone 187 us (6.7 TB/s of 1.25 GB)
+//    512 rows of 126464 bf16: policy loss 32 us, step with a quarter unread 48 us: of
+//      either about 9 us are there whatever the size (the launch, the first copies, the
+//      last row's exchange; 32 rows of 1024 take 6 us)
+//    A step's row in the cluster, slices of 76 KB, in cycles: sums 5500 (the copies), shares
+//      1100, merge and loss 1800, gradient 4400.  With the loss in 64-bit arithmetic 2300, with
+//      one of the eight warps doing it too every row took 2 us more.
+// Without these: a CTA per row, loads to registers, step 837 us; chunks of 8 KB 109 us for
+// the log-probabilities, two CTAs per SM 101, four of half the threads 102; the next row's
+// sums taken before a row's gradient 197 us for the step; a maximum saved per vector (a
+// reference kept until a weight passes 2^90) 103 us for the log-probabilities.
+// The preference step is three launches, since a gradient needs its whole pair: sums, pairs
+// (pair_kernel), gradients.  1024 rows of 126464 bf16 in 8 pairs: 132 us, 50, 6 and 76 us of
+// it alone; floor 76 us with one read of the rows, 114 with two.  One launch, rows handed out
+// by a counter, each pair's gradients as soon as its sums were there: 140 us; the second
+// read came from HBM there too.
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
@@ -25,15 +52,15 @@ constexpr int kPerThread = 4;           // vectors of a chunk per thread
 constexpr int kChunkVecs = kPerThread * kThreads, kChunkBytes = kChunkVecs * 16;
 constexpr int kItems = 4;               // rows that the fetching warp may be ahead
 constexpr int kSlots = 8;               // rows whose shares may be on their way (more than kItems + 2)
-// CTAs per SM, and the chunks that each has room for: a step's two passes want more of a
-// row on its way, sums or a gradient alone more warps.
+// CTAs per SM, and the chunks that each has room for: a step's slices want room, sums or a
+// gradient alone more warps (2048 x 152064 bf16: log-probabilities 97 us with three, 101 with
+// two; policy step 191 with three, 184 with two).
 template <bool SUMS, bool GRAD>
 struct Shape {
     static constexpr int ctas = SUMS && GRAD ? 2 : 3, ring = SUMS && GRAD ? 6 : 4;
 };
 constexpr int kMaxRing = 6;
 constexpr float kRebase = 12.0f;        // powers of 2 of headroom before a thread's reference moves
-constexpr int64_t kInL2 = 48 << 20;     // rows in flight that the second pass still finds in L2
 // Rows' bytes that a preference step leaves in L2 for its gradient (1024 rows of 126464
 // bf16: 132 us with 60 to 80 MB, 134 with 40, 139 without, 143 with the first rows first).
 constexpr int64_t kStays = 70 << 20;
@@ -75,18 +102,23 @@ __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
 __device__ __forceinline__ void arrive_at(uint64_t* bar, int rank) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote(bar, rank)) : "memory");
 }
-// Waits for a phase that CTAs of the cluster complete; false if that takes too long.
+// Waits for a phase; false if that takes too long.  CLUSTER: other CTAs write what it
+// stands for.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
     long long t0 = 0;
     for (int n = 0;; ++n) {
         uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
+        if (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity)
+                : "memory");
+        else
+            ok = mbar_try_wait(bar, parity);
         if (ok) return true;
         if (n == 0)
             t0 = clock64();
@@ -95,8 +127,9 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
     }
 }
 // The same for a whole warp, whose lanes go on together or give up together.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
-    return __all_sync(DLM_FULL_MASK, wait_for(bar, parity));
+    return __all_sync(DLM_FULL_MASK, wait_for<CLUSTER>(bar, parity));
 }
 // A share into CTA `rank`'s slot, counted there by its barrier.
 __device__ __forceinline__ void send(Part* slot, uint64_t* bar, int rank, Part p) {
@@ -407,7 +440,7 @@ struct Fetcher {
         if (rank != 0 || asked > answers) return true;
         if (asked > 0) {
             const uint32_t parity = (asked - 1) & 1u;
-            if (block ? !wait_for(&sh.next_free, parity) : !mbar_test_wait(&sh.next_free, parity)) return !block;
+            if (block ? !wait_for<true>(&sh.next_free, parity) : !mbar_test_wait(&sh.next_free, parity)) return !block;
         }
         ask_next(sh.answer, &sh.next, a.split > 1);
         ++asked;
@@ -417,7 +450,7 @@ struct Fetcher {
     __device__ __forceinline__ bool look_ahead(bool block) {
         if (have_next) return ask(false);
         if (!ask(block)) return false;
-        if (block ? !wait_for(&sh.next, answers & 1u) : !mbar_test_wait(&sh.next, answers & 1u)) return !block;
+        if (block ? !wait_for<true>(&sh.next, answers & 1u) : !mbar_test_wait(&sh.next, answers & 1u)) return !block;
         uint32_t cta;
         const bool more = next_cta(sh.answer, cta);
         ++answers;
@@ -469,7 +502,7 @@ struct Fetcher {
             if (i + a.ring >= issued) wait_for(&sh.full[c.at], c.parity);
             c.step(a.ring);
         }
-        wait_for(&sh.next, answers & 1u);
+        wait_for<true>(&sh.next, answers & 1u);
     }
 };
 
@@ -484,9 +517,8 @@ __device__ void write_zeros(char* out, int64_t V, const TokenSlice<DT>& sl) {
 }
 
 // A warp of its own finishes the rows: it waits for all CTAs' shares, merges them and
-// works the loss out, while the others go on.  (One of them doing this too was what a
-// row took: about 2 us for each.)  With a gradient every CTA's does, to go on with the
-// slope; the first CTA's writes.
+// works the loss out, while the others go on.  With a gradient every CTA's does, to go on
+// with the slope; the first CTA's writes.
 template <bool GRAD>
 __device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
     const int lane = threadIdx.x & 31, n_parts = a.split * kWarps;
@@ -503,7 +535,7 @@ __device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
                 const RowInputs in = row_inputs(a, o, sh.item[slot].weight);
                 const int ps = rows % kSlots;
                 if (lane == 0) mbar_expect_tx(&sh.shares[ps], n_parts * (uint32_t)sizeof(Part));
-                if (!wait_warp(&sh.shares[ps], (rows / kSlots) & 1u)) return false;
+                if (!wait_warp<true>(&sh.shares[ps], (rows / kSlots) & 1u)) return false;
                 const TokenRow x = merge_row(a, sh, ps, n_parts);
                 const LossSlope y = row_loss(a, x, in);
                 if (GRAD && lane == 0) {  // first of all: the gradient waits for it
@@ -725,7 +757,9 @@ __device__ float finish_pair(const TokenArgs& a, int64_t i, double chosen, doubl
 
 // One CTA per pair: the scores, the loss, and the slope of every row of the pair.  Bound
 // by latency: three loads after each other, a sum over the CTA, the loss and a store; a
-// thread's first rows are read before the sum, so that only stores follow it.
+// thread's first rows are read before the sum, so that only stores follow it (8 pairs of 128
+// rows: 6 us, 8 with the loads one after the other).  Every CTA reads the offsets before
+// its pair's: meant for thousands of pairs, not millions.
 constexpr int kPairRows = 4;
 __global__ void __launch_bounds__(kThreads) pair_kernel(const TokenArgs a) {
     __shared__ double s_sum[2][kWarps];
@@ -840,12 +874,11 @@ cudaError_t launch_token_kernel(TokenArgs a, cudaStream_t st) {
     auto chunks = [&](int n) { return (slice(n) + kChunkVecs - 1) / kChunkVecs; };
     a.ring = S::ring;
     int split = 1;
-    if (SUMS && GRAD) {
-        // the second reading is from the ring or from L2 (2048 rows of 152064 bf16: 187 us so
-        // with two CTAs per row, 232 with one, whose rows in flight L2 does not hold)
-        while (split < 8 && chunks(split) > a.ring && slots / split * nv * 16 > kInL2) split *= 2;
-    } else if (GRAD) {
-        // slices that the ring holds (1024 rows of 126464 bf16: 76 us with four, 83 with one)
+    if (GRAD) {
+        // Slices that the ring holds.  A step then reads a row once (2048 rows of 152064 bf16
+        // with four CTAs per row 183 us; from L2 the second time, two, 184, and one, whose
+        // rows in flight L2 does not hold, 230; 512 of 126464 48, 49 and 53).  A gradient
+        // alone: 1024 rows of 126464 76 us with four, 83 with one.
         while (split < 8 && chunks(split) > a.ring) split *= 2;
     } else if (a.n_rows > slots && a.n_rows < 7 * slots / 2) {
         // whole rows would leave the last of two to four rounds to few CTAs (1024 rows of

@@ -871,7 +871,8 @@ dlm_status dlm_distill_step(const void* student, dlm_dtype dtype, int64_t n_rows
  * dev_status  : DLM_DEV_NONFINITE for a row that holds NaN or +inf, or -inf only:
  *               its logp, lse and gradient are NaN.  (The gradient calls write such
  *               a row's NaN and set no status.)  A token at -inf has logp -inf,
- *               which sets no status here.
+ *               which sets no status here.  DLM_DEV_TIMEOUT if a wait for copies or
+ *               for the cluster's other CTAs gave up (these calls, and those below).
  * Outputs may overlap neither each other nor an input, but for grad as said
  * (per-row arrays that do are DLM_ERR_INVALID_ARG).
  */
@@ -983,8 +984,7 @@ dlm_status dlm_policy_step(const void* logits, dlm_dtype dtype, int64_t n_rows, 
  * dev_status  : DLM_DEV_NONFINITE for a row as in dlm_row_logprob and for a pair whose
  *               loss or its derivative is not finite: the loss is what the formula
  *               gives, the gradient of all its rows NaN.  A row with NaN makes its
- *               pair's loss NaN.  DLM_DEV_TIMEOUT if dlm_preference_step's wait for
- *               a pair's other rows gave up: its outputs are then unspecified.
+ *               pair's loss NaN.
  */
 #define DLM_PREF_SIGMOID 0
 #define DLM_PREF_HINGE 1

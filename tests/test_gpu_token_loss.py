@@ -114,7 +114,7 @@ def check_logprob(dlm, z, token, temperature=1.0, weights=None, up=None, status_
                 check_grad(got[r], zz[r], token[r], slope, 2.0 ** -22 * abs(slope), temperature, z.dtype, r)
 
 
-SHAPES = [(1, 1), (2, 9), (3, 130), (4, 1025), (5, 5003), (2, 32003), (330, 2051), (700, 257), (2, 126464), (41, 16383)]
+SHAPES = [(1, 1), (2, 9), (3, 130), (4, 1025), (5, 5003), (2, 32003), (330, 2051), (700, 257), (2, 126464), (41, 16383), (3, 262147)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
@@ -698,6 +698,37 @@ def test_calls_on_two_streams_at_once(dlm):
     for i in range(2):
         assert all(same_bits(a, b) for r in got[i] for a, b in zip(r, want[i]))
         assert all(same_bits(a, b) for r in got_lp[i] for a, b in zip(r, want_lp[i]))
+
+
+@pytest.mark.parametrize("n,vocab", [(60, 5000), (500, 30011)])
+def test_a_call_sees_what_the_one_before_it_wrote(dlm, n, vocab):
+    # launches begin while the one before them ends: a chain of calls, each on the last one's
+    # outputs, and torch's kernels between them, with and without waiting in between
+    start = on_gpu(row_ref.rows(n, vocab, "bf16", 60))
+    token = cuda(tokens_of(start.cpu(), 1))
+    adv, offsets = torch.randn(n, device="cuda"), torch.tensor([0, n // 2, n], dtype=torch.int32, device="cuda")
+
+    def chain(wait):
+        z, out = on_gpu(start), []
+        f = lambda k: torch.empty(k, device="cuda")  # noqa: E731
+        grad = on_gpu(start)
+        for i in range(6):
+            lp = dlm.row_logprob(z, token)
+            wait()
+            r = dlm.policy_step(z, token, adv, old=lp.logp, ref=lp.lse, kl_weight=0.1, kl="k2",
+                                out=dlm.PolicyStep(f(n), f(n), grad))
+            wait()
+            p = dlm.preference_step(r.grad, token, offsets, ref=r.loss, weights=r.logp,
+                                    out=dlm.PreferenceStep(f(1), f(2), f(n), r.grad))
+            wait()
+            _, z = dlm.row_logprob_step(p.grad, token, p.logp, grad=z)
+            wait()
+            if i % 2:
+                z.add_(start)
+            out += [lp.logp, r.loss, p.loss, p.score, p.logp, z.clone()]
+        return out
+
+    assert all(same_bits(a, b) for a, b in zip(chain(lambda: None), chain(torch.cuda.synchronize)))
 
 
 def test_refusals(dlm):
