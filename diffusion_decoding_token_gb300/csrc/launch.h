@@ -303,7 +303,8 @@ struct TokenArgs {
     int64_t n_up;             // its entries
     void* grad;               // nullable
     int64_t grad_stride;
-    void* workspace;          // preference step
+    void* workspace;          // preference step: state, and then
+    int32_t* at;              // [2 n_pairs + 1] the offsets put right
     uint32_t* dev_status;
     int num_sms;
     int split;                // CTAs per row (thread-block cluster size)

@@ -332,7 +332,8 @@ __device__ __forceinline__ void write_row(const TokenArgs& a, int64_t o, const T
     if (a.state) {
         const double term = a.op == kTokenPreference ? (double)in.weight * (((double)t.logp.hi - (double)in.ref_logp) + (double)t.logp.lo) : 0.0;
         float4* s = reinterpret_cast<float4*>(a.state + o * DLM_TOKEN_STATE);
-        s[0] = make_float4(t.m, t.inv, t.away, a.op == kTokenPreference ? 0.f : x.slope);  // (a row in no pair: 0)
+        // (preference: the pair's slope is still to come; 0 stands for a row in no pair)
+        s[0] = make_float4(t.m, t.inv, t.away, a.op == kTokenPreference && !a.paired ? 0.f : x.slope);
         s[1] = make_float4(__int_as_float(__double2loint(term)), __int_as_float(__double2hiint(term)), __int_as_float(-1), 0.f);
     }
 }
@@ -516,6 +517,126 @@ __device__ void write_zeros(char* out, int64_t V, const TokenSlice<DT>& sl) {
         for (int64_t e = (int64_t)(sl.v0 + sl.whole) * Row<DT>::EPV + t; e < V; e += kThreads) store_elem<DT>(out, e, 0.f);
 }
 
+// ---- pairs --------------------------------------------------------------------------
+
+// The loss of pair i from its scores.
+__device__ __forceinline__ LossSlope pair_loss(const TokenArgs& a, int64_t i, double chosen, double rejected) {
+    return preference_pair(a.preference, chosen, rejected, a.margins ? a.margins[i] : 0.f,
+                           a.pair_weights ? a.pair_weights[i] : 1.f);
+}
+// Its outputs, by one thread: its slope.
+__device__ float finish_pair(const TokenArgs& a, int64_t i, double chosen, double rejected) {
+    const LossSlope x = pair_loss(a, i, chosen, rejected);
+    a.loss[i] = x.loss;
+    if (a.score) {
+        a.score[2 * i] = (float)chosen;
+        a.score[2 * i + 1] = (float)rejected;
+    }
+    if (x.slope != x.slope) raise_status(a.dev_status, DLM_DEV_NONFINITE);
+    return x.slope;
+}
+
+// The offsets put right (within the rows and in order) for a preference step's second
+// launch, by one warp of the first.
+__device__ void clean_offsets(const TokenArgs& a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t n = 2 * a.n_pairs + 1;
+    int32_t top = 0;
+    for (int64_t base = 0; base < n; base += 32) {
+        const int64_t i = base + lane;
+        const int32_t given = i < n ? a.offsets[i] : 0;
+        int32_t x = (int32_t)min((int64_t)max(given, 0), a.n_rows);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(DLM_FULL_MASK, x, o);
+            if (lane >= o) x = max(x, y);
+        }
+        x = max(x, top);
+        top = __shfl_sync(DLM_FULL_MASK, x, 31);
+        if (i < n) {
+            a.at[i] = x;
+            if (x != given) raise_status(a.dev_status, DLM_DEV_BAD_INDEX);
+        }
+    }
+}
+
+// The pair of a row, by a warp: its rows [from, to), those of the sequence that is not
+// preferred from `mid` on, and its slope.  Rows in no pair: pair -1, slope 0.
+struct PairOf {
+    int64_t pair = -1, from = 0, mid = 0, to = 0;
+    double score[2] = {0.0, 0.0};
+    float slope = 0.f;
+};
+__device__ __noinline__ PairOf pair_of(const TokenArgs& a, int64_t r) {
+    const int lane = threadIdx.x & 31;
+    const int64_t n = 2 * a.n_pairs;
+    PairOf p;
+    p.to = a.n_rows;
+    if (n == 0) return p;
+    const int64_t first = a.at[0], last = a.at[n];
+    if (r < first || r >= last) {
+        p.from = r < first ? 0 : last;
+        p.to = r < first ? first : a.n_rows;
+        return p;
+    }
+    int64_t lo = 0, hi = n;  // the last sequence that begins at or before r, 32 places at a time
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const uint32_t at_or_before = __ballot_sync(DLM_FULL_MASK, i < hi && a.at[i] <= r);
+        lo += (__popc(at_or_before) - 1) * step;
+        hi = min(hi, lo + step);
+    }
+    p.pair = lo >> 1;
+    p.from = a.at[2 * p.pair];
+    p.mid = a.at[2 * p.pair + 1];
+    p.to = a.at[2 * p.pair + 2];
+#pragma unroll 8
+    for (int64_t k = p.from + lane; k < p.to; k += 32) {
+        const double term = *reinterpret_cast<const double*>(a.state + k * DLM_TOKEN_STATE + 4);
+        p.score[0] += k < p.mid ? term : 0.0;
+        p.score[1] += k < p.mid ? 0.0 : term;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        p.score[0] += __shfl_xor_sync(DLM_FULL_MASK, p.score[0], o);
+        p.score[1] += __shfl_xor_sync(DLM_FULL_MASK, p.score[1], o);
+    }
+    p.slope = pair_loss(a, p.pair, p.score[0], p.score[1]).slope;
+    return p;
+}
+
+// A preference step's second launch: the warp that finishes sums in the first finds the
+// slope of each row's pair, ahead of the warps that write the gradient.  (A pair is added
+// up once by every CTA that has rows of it, in one order; the first row's cluster writes
+// its loss.)
+__device__ bool find_slopes(const TokenArgs& a, Shared& sh, int rank) {
+    const int lane = threadIdx.x & 31;
+    PairOf p;
+    uint32_t rows = 0;
+    for (uint32_t i = 0;; ++i) {
+        const int slot = i % kItems;
+        if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
+        const int kind = sh.item[slot].kind;
+        const int64_t r = sh.item[slot].o;
+        if (kind == kEnd) return true;
+        if (r < p.from || r >= p.to) p = pair_of(a, r);
+        if (kind == kRow) {
+            if (lane == 0) {
+                sh.row[rows % kItems].w = r >= p.mid ? -p.slope : p.slope;
+                arrive(&sh.row_ready[rows % kItems]);
+            }
+            ++rows;
+        }
+        if (rank == 0 && lane == 0) {
+            if (p.pair >= 0 && r == p.from) finish_pair(a, p.pair, p.score[0], p.score[1]);
+            for (int64_t k = r; k < a.n_pairs; k += a.n_rows)  // pairs without rows
+                if (a.at[2 * k] == a.at[2 * k + 2]) finish_pair(a, k, 0.0, 0.0);
+        }
+        __syncwarp();
+        if (lane == 0) arrive(&sh.item_empty[slot]);
+    }
+}
+
 // A warp of its own finishes the rows: it waits for all CTAs' shares, merges them and
 // works the loss out, while the others go on.  With a gradient every CTA's does, to go on
 // with the slope; the first CTA's writes.
@@ -546,6 +667,7 @@ __device__ bool finish_rows(const TokenArgs& a, Shared& sh, int rank) {
             }
             ++rows;
         }
+        if (!GRAD && a.paired && a.n_pairs > 0 && rank == 0 && o == 0) clean_offsets(a);
         __syncwarp();
         if (lane == 0) arrive(&sh.item_empty[slot]);
     }
@@ -677,11 +799,14 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
             }
             if (GRAD) {
                 RowSlope x{it.m, it.inv, it.away, it.k};
-                if (SUMS) {
+                if (SUMS || a.paired) {
                     const int rs = rows % kItems;
                     if (!wait_warp(&sh.row_ready[rs], (rows / kItems) & 1u)) return false;
                     const float4 y = sh.row[rs];
-                    x = RowSlope{y.x, y.y, y.z, y.w * a.inv_t};
+                    if (SUMS)
+                        x = RowSlope{y.x, y.y, y.z, y.w * a.inv_t};
+                    else
+                        x.k *= y.w;
                 }
                 const bool there = SUMS && a.resident;
                 if (!there) from = cur;
@@ -696,12 +821,11 @@ __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, i
 }
 
 // What a CTA starts with: its barriers, and all CTAs of its cluster running.
-template <bool FINISH>
-__device__ __forceinline__ void set_up(const TokenArgs& a, Shared& sh) {
+__device__ __forceinline__ void set_up(const TokenArgs& a, Shared& sh, bool finish) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], kWarps + (FINISH ? 1 : 0));
+            mbar_init(&sh.item_empty[i], kWarps + finish);
             mbar_init(&sh.row_ready[i], 1);
         }
         for (int i = 0; i < a.ring; ++i) {
@@ -725,13 +849,16 @@ __global__ void __launch_bounds__(kBlock, Shape<SUMS, GRAD>::ctas) token_kernel(
     Shared& sh = *reinterpret_cast<Shared*>(s_raw);
     unsigned char* ring = s_raw + ring_offset();
     const int t = threadIdx.x, rank = (int)(blockIdx.x % a.split);
-    set_up<SUMS>(a, sh);
+    set_up(a, sh, SUMS || a.paired);
     wait_prior();
     bool ok = true;
     if (t < kThreads) {
         ok = work_rows<DT, SUMS, GRAD>(a, sh, ring, rank);
     } else if (t < kThreads + 32) {
-        if (SUMS) ok = finish_rows<GRAD>(a, sh, rank);
+        if (SUMS)
+            ok = finish_rows<GRAD>(a, sh, rank);
+        else if (a.paired)
+            ok = find_slopes(a, sh, rank);
     } else if (t == kThreads + 32) {
         Fetcher<DT, SUMS, GRAD> f(a, sh, ring, rank);
         ok = f.ask(true) && f.run();
@@ -742,20 +869,8 @@ __global__ void __launch_bounds__(kBlock, Shape<SUMS, GRAD>::ctas) token_kernel(
     if (a.split > 1) cg::this_cluster().sync();  // no CTA ends before what others send to it has come
 }
 
-// The loss of pair i from its scores, by one thread: its slope.
-__device__ float finish_pair(const TokenArgs& a, int64_t i, double chosen, double rejected) {
-    const LossSlope x = preference_pair(a.preference, chosen, rejected, a.margins ? a.margins[i] : 0.f,
-                                        a.pair_weights ? a.pair_weights[i] : 1.f);
-    a.loss[i] = x.loss;
-    if (a.score) {
-        a.score[2 * i] = (float)chosen;
-        a.score[2 * i + 1] = (float)rejected;
-    }
-    if (x.slope != x.slope) raise_status(a.dev_status, DLM_DEV_NONFINITE);
-    return x.slope;
-}
-
-// One CTA per pair: the scores, the loss, and the slope of every row of the pair.  Bound
+// One CTA per pair, after the sums of dlm_preference_loss: the scores, the loss, and the slope
+// of every row of the pair in its state.  Bound
 // by latency: three loads after each other, a sum over the CTA, the loss and a store; a
 // thread's first rows are read before the sum, so that only stores follow it (8 pairs of 128
 // rows: 6 us, 8 with the loads one after the other).  Every CTA reads the offsets before
@@ -837,9 +952,9 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const TokenArgs a) {
 
 }  // namespace
 
+// A step's workspace: the rows' state and the offsets put right.
 size_t preference_workspace(int64_t n_rows, int64_t n_pairs) {
-    (void)n_pairs;
-    return (size_t)(n_rows * DLM_TOKEN_STATE * 4 + 16);
+    return (size_t)n_rows * DLM_TOKEN_STATE * 4 + ((size_t)n_pairs * 2 + 1 + 3) / 4 * 16;
 }
 
 namespace {
@@ -900,15 +1015,18 @@ cudaError_t launch_token_kernel(TokenArgs a, cudaStream_t st) {
 
 template <int DT>
 cudaError_t run_token(TokenArgs a, cudaStream_t st) {
-    if (a.op == kTokenPreference && a.sums) {  // sums, the pairs, and the gradient from the state
-        if (a.workspace) a.state = static_cast<float*>(a.workspace);
+    if (a.op == kTokenPreference && a.sums) {
         cudaError_t e = cudaSuccess;
-        a.paired = a.grad != nullptr;
+        if (a.workspace) {
+            a.state = static_cast<float*>(a.workspace);
+            a.at = reinterpret_cast<int32_t*>(a.state + a.n_rows * DLM_TOKEN_STATE);
+        }
+        a.paired = a.workspace && a.n_rows;  // a step: sums, then the gradient, which adds up the pairs
         a.stay_from = a.n_rows - kStays / (a.vocab * Row<DT>::ESZ);
         if (a.n_rows) e = launch_token_kernel<DT, true, false>(a, st);
-        if (e == cudaSuccess && a.n_pairs > 0) e = launch_grid(pair_kernel, a, (unsigned)a.n_pairs, kThreads, 0, 0, st);
-        if (e != cudaSuccess || !a.grad || !a.n_rows) return e;
-        return launch_token_kernel<DT, false, true>(a, st);
+        if (e != cudaSuccess) return e;
+        if (a.paired) return launch_token_kernel<DT, false, true>(a, st);
+        return a.n_pairs > 0 ? launch_grid(pair_kernel, a, (unsigned)a.n_pairs, kThreads, 0, 0, st) : cudaSuccess;
     }
     if (!a.sums) return launch_token_kernel<DT, false, true>(a, st);
     if (!a.grad) return launch_token_kernel<DT, true, false>(a, st);
