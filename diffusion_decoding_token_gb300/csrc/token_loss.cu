@@ -995,9 +995,10 @@ cudaError_t launch_token_kernel(TokenArgs a, cudaStream_t st) {
         // rows in flight L2 does not hold, 230; 512 of 126464 48, 49 and 53).  A gradient
         // alone: 1024 rows of 126464 76 us with four, 83 with one.
         while (split < 8 && chunks(split) > a.ring) split *= 2;
-    } else if (a.n_rows > slots && a.n_rows < 7 * slots / 2) {
-        // whole rows would leave the last of two to four rounds to few CTAs (1024 rows of
-        // 126464 bf16: 50 us with two, 56 with one; 2048 of 152064: 99 and 96)
+    } else if (a.n_rows > slots && a.n_rows < 4 * slots && a.n_rows % slots > slots / 6 && a.n_rows % slots < slots * 3 / 5) {
+        // whole rows would leave the last of two to four rounds to some of the CTAs (1024 rows
+        // of 126464 bf16: 50 us with two, 56 with one; 912, two rounds, 47 and 43).  A second
+        // launch of the rows left over, cut finer, began too late: 1024 rows took as long.
         split = 2;
     }
     // rows too few for all SMs (76 rows of 126464 bf16: 12.4 us with two CTAs each, 14.8 with
