@@ -255,7 +255,7 @@ template <int DT>
 struct TokenSlice {
     int v0, n;        // vectors of this CTA
     int whole;        // those that V does not cut
-    int chunks;
+    int chunks, most_chunks;  // its chunks; the most that a CTA of the cluster has
     __device__ TokenSlice(int64_t V, int split, int rank) {
         constexpr int EPV = Row<DT>::EPV;
         const int nv = (int)((V + EPV - 1) / EPV);
@@ -264,6 +264,7 @@ struct TokenSlice {
         n = min(nv, v0 + per) - v0;
         whole = max(0, min((int)(V / EPV), v0 + n) - v0);
         chunks = (whole + kChunkVecs - 1) / kChunkVecs;
+        most_chunks = (per + kChunkVecs - 1) / kChunkVecs;
     }
 };
 
@@ -772,49 +773,68 @@ __device__ __forceinline__ bool put_gradient(const TokenArgs& a, Shared& sh, uns
     return true;
 }
 
-// The arithmetic's warps.
+// The arithmetic's warps.  A row's slope is known about 2 us after its sums (to all CTAs and
+// back): where the ring holds two slices a step takes the next row's sums before a row's
+// gradient (2048 rows of 16000 bf16: 33 us without).
 template <int DT, bool SUMS, bool GRAD>
 __device__ bool work_rows(const TokenArgs& a, Shared& sh, unsigned char* ring, int rank) {
+    constexpr bool BOTH = SUMS && GRAD;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const TokenSlice<DT> sl(a.vocab, a.split, rank);
+    const bool there = BOTH && a.resident;
+    const bool ahead = there && 2 * sl.most_chunks <= a.ring;
     Cursor cur;
-    uint32_t rows = 0;  // rows whose sums were taken
+    uint32_t rows = 0;      // rows whose sums were taken
+    int64_t open_q = -1;    // a row before whose gradient is still to come, its token, its place in the ring
+    int open_token = 0;
+    Cursor open_from;
+    // the gradient of a row (its number) from the slope that the finishing warp leaves
+    auto gradient = [&](uint32_t row, int64_t q, int token, Cursor& from) -> bool {
+        const int rs = row % kItems;
+        if (!wait_warp(&sh.row_ready[rs], (row / kItems) & 1u)) return false;
+        const float4 y = sh.row[rs];
+        return put_gradient<DT>(a, sh, ring, sl, q, token, RowSlope{y.x, y.y, y.z, y.w * a.inv_t}, there, from);
+    };
     for (uint32_t i = 0;; ++i) {
         const int slot = i % kItems;
         if (!wait_warp(&sh.item_full[slot], (i / kItems) & 1u)) return false;
         const Item& it = sh.item[slot];
-        const int kind = it.kind;
-        if (kind == kEnd) return true;
+        const int kind = it.kind, token = it.token;
         const int64_t q = it.q;
         if (GRAD && kind == kNone)
             write_zeros<DT>(static_cast<char*>(a.grad) + q * a.grad_stride * Row<DT>::ESZ, a.vocab, sl);
-        if (kind == kRow) {
-            const int token = it.token;
-            Cursor from = cur;
-            if (SUMS) {
-                Part part;
-                if (!take_sums<DT>(a, sh, ring, sl, q, token, GRAD && a.resident, cur, part)) return false;
-                const int ps = rows % kSlots, to = GRAD ? a.split : 1;  // every CTA, or the first
-                if (lane < to) send(&sh.part[ps][rank * kWarps + warp], &sh.shares[ps], lane, part);
-            }
-            if (GRAD) {
-                RowSlope x{it.m, it.inv, it.away, it.k};
-                if (SUMS || a.paired) {
-                    const int rs = rows % kItems;
-                    if (!wait_warp(&sh.row_ready[rs], (rows / kItems) & 1u)) return false;
-                    const float4 y = sh.row[rs];
-                    if (SUMS)
-                        x = RowSlope{y.x, y.y, y.z, y.w * a.inv_t};
-                    else
-                        x.k *= y.w;
-                }
-                const bool there = SUMS && a.resident;
-                if (!there) from = cur;
-                if (!put_gradient<DT>(a, sh, ring, sl, q, token, x, there, from)) return false;
-                cur = from;
-            }
-            ++rows;
+        Cursor from = cur;
+        if (SUMS && kind == kRow) {
+            Part part;
+            if (!take_sums<DT>(a, sh, ring, sl, q, token, there, cur, part)) return false;
+            const int ps = rows % kSlots, to = GRAD ? a.split : 1;  // every CTA, or the first
+            if (lane < to) send(&sh.part[ps][rank * kWarps + warp], &sh.shares[ps], lane, part);
         }
+        if (BOTH) {
+            if (open_q >= 0 && (kind == kRow || kind == kEnd)) {
+                if (!gradient(rows - 1, open_q, open_token, open_from)) return false;
+                open_q = -1;
+            }
+            if (kind == kRow) {
+                if (ahead) {
+                    open_q = q;
+                    open_token = token;
+                    open_from = from;
+                } else if (!gradient(rows, q, token, there ? from : cur)) {
+                    return false;
+                }
+            }
+        } else if (GRAD && kind == kRow) {
+            RowSlope x{it.m, it.inv, it.away, it.k};
+            if (a.paired) {
+                const int rs = rows % kItems;
+                if (!wait_warp(&sh.row_ready[rs], (rows / kItems) & 1u)) return false;
+                x.k *= sh.row[rs].w;
+            }
+            if (!put_gradient<DT>(a, sh, ring, sl, q, token, x, false, cur)) return false;
+        }
+        if (kind == kEnd) return true;
+        if (kind == kRow) ++rows;
         __syncwarp();
         if (lane == 0) arrive(&sh.item_empty[slot]);
     }
