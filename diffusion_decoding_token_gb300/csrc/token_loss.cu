@@ -21,7 +21,7 @@
 //    2048 rows of 152064 bf16: log-probabilities 94 us (6.6 TB/s of 623 MB);
 //      policy step, a quarter of the rows without a loss, 184 us (5.9 TB/s of 1.09 GB);
 //      gradient alone 187 us (6.7 TB/s of 1.25 GB)
-//    512 rows of 126464 bf16: policy loss 32 us, step with a quarter unread 48 us: of
+//    512 rows of 126464 bf16: policy loss 30 us, step with a quarter unread 48 us: of
 //      either about 9 us are there whatever the size (the launch, the first copies, the
 //      last row's exchange; 32 rows of 1024 take 6 us)
 //    A step's row in the cluster, slices of 76 KB, in cycles: sums 5500 (the copies), shares
@@ -29,13 +29,14 @@
 //      one of the eight warps doing it too every row took 2 us more.
 // Without these: a CTA per row, loads to registers, step 837 us; chunks of 8 KB 109 us for
 // the log-probabilities, two CTAs per SM 101, four of half the threads 102; the next row's
-// sums taken before a row's gradient 197 us for the step; a maximum saved per vector (a
-// reference kept until a weight passes 2^90) 103 us for the log-probabilities.
-// The preference step is three launches, since a gradient needs its whole pair: sums, pairs
-// (pair_kernel), gradients.  1024 rows of 126464 bf16 in 8 pairs: 132 us, 50, 6 and 76 us of
-// it alone; floor 76 us with one read of the rows, 114 with two.  One launch, rows handed out
-// by a counter, each pair's gradients as soon as its sums were there: 140 us; the second
-// read came from HBM there too.
+// sums taken before a row's gradient where the row then comes twice, 197 us for the step; a
+// maximum saved per vector (a reference kept until a weight passes 2^90) 103 us for the
+// log-probabilities.
+// The preference step is two launches, since a gradient needs its whole pair: sums, and
+// gradients, whose launch adds up the pairs.  1024 rows of 126464 bf16 in 8 pairs: 128 us, 50
+// and 76 alone; floor 76 us with one read of the rows, 114 with two.  One launch, rows
+// handed out by a counter, each pair's gradients as soon as its sums were there: 140 us;
+// the second read came from HBM there too.
 #include "common.cuh"
 #include "launch.h"
 #include "row_vec.cuh"
