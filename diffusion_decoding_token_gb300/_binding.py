@@ -511,18 +511,27 @@ _KL = {"k1": 1, "k2": 2, "k3": 3}                      # DLM_KL_*
 _PREF = {"sigmoid": 0, "hinge": 1, "ipo": 2}           # DLM_PREF_*
 
 
+def _vector(t, n, index, name, dtype=torch.float32):
+    """The address of a per-row array that is used in place (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape ({n},) on cuda:{index}")
+    return t.data_ptr()
+
+
+def _vectors(index, *given):
+    for name, t, n in given:
+        _vector(t, n, index, name)
+
+
 def _token_rows(logits, tokens):
-    """The arguments that the calls over given tokens begin with, apart from the tokens."""
+    """(device, its index, the arguments that the calls over given tokens begin with)."""
     _rows_arg(logits, "logits")
-    rows = logits.shape[0]
-    _same(tokens, (rows,), torch.int32, logits.device, "tokens")
-    return _ptr(logits), _dt(logits), rows, logits.shape[1], _stride(logits)
-
-
-def _floats(n, device, *given):
-    """Per-row inputs: float32 tensors of ``n`` entries, or None."""
-    for name, t in given:
-        _same(t, (n,), torch.float32, device, name)
+    rows, vocab = logits.shape
+    index = logits.get_device()
+    return logits.device, index, rows, (logits.data_ptr(), _dt(logits), rows, vocab, _stride(logits),
+                                        _vector(tokens, rows, index, "tokens", torch.int32))
 
 
 def _new(shape, device):
@@ -539,26 +548,25 @@ def row_logprob(logits: torch.Tensor, tokens: torch.Tensor, *, temperature: floa
     ``row_index`` and ``gather`` as in :func:`row_stats`."""
     _rows_arg(logits, "logits")
     row_index, n, m = _gathered(logits, row_index, gather)
-    dev = logits.device
-    _same(tokens, (m,), torch.int32, dev, "tokens")
+    dev, index = logits.device, logits.get_device()
+    tokens_at = _vector(tokens, m, index, "tokens", torch.int32)
     if out is None:
         out = RowLogprob(_new(m, dev), _new(m, dev), _new((m, TOKEN_STATE), dev) if with_state else None)
     else:
-        _floats(m, dev, ("out.logp", out.logp), ("out.lse", out.lse))
+        _vectors(index, ("out.logp", out.logp, m), ("out.lse", out.lse, m))
         _same(out.state, (m, TOKEN_STATE), torch.float32, dev, "out.state")
-    _on(dev, lib().dlm_row_logprob, _ptr(logits), _dt(logits), n, logits.shape[1], _stride(logits), _ptr(row_index),
-        logits.shape[0], _ptr(tokens), float(temperature), _ptr(out.logp), _ptr(out.lse), _ptr(out.state),
+    _on(dev, lib().dlm_row_logprob, logits.data_ptr(), _dt(logits), n, logits.shape[1], _stride(logits), _ptr(row_index),
+        logits.shape[0], tokens_at, float(temperature), _ptr(out.logp), _ptr(out.lse), _ptr(out.state),
         _status_ptr(status, dev), ROWS_GATHER if gather else 0)
     return out
 
 
-def _token_grad(call, logits, tokens, state, up, up_shape, temperature, out, status, name, *pairs):
-    args = _token_rows(logits, tokens)
-    dev = logits.device
-    _same(state, (logits.shape[0], TOKEN_STATE), torch.float32, dev, "state")
-    _same(up, up_shape, torch.float32, dev, name)
+def _token_grad(call, logits, tokens, state, up, n_up, temperature, out, status, name, *pairs):
+    dev, index, rows, args = _token_rows(logits, tokens)
+    _same(state, (rows, TOKEN_STATE), torch.float32, dev, "state")
+    up_at = _vector(up, rows if n_up is None else n_up, index, name)
     out = _grad_out(logits, out)
-    _on(dev, call, *args, _ptr(tokens), float(temperature), *pairs, _ptr(state), _ptr(up), _ptr(out), _stride(out),
+    _on(dev, call, *args, float(temperature), *pairs, state.data_ptr(), up_at, out.data_ptr(), _stride(out),
         _status_ptr(status, dev))
     return out
 
@@ -569,8 +577,8 @@ def row_logprob_grad(logits: torch.Tensor, tokens: torch.Tensor, state: torch.Te
     """dlm_row_logprob_grad: the gradient of sum_r grad_logp[r] * logp[r] with
     respect to ``logits``, from the state of the :func:`row_logprob` call with the
     same arguments.  ``out`` may be ``logits`` itself."""
-    return _token_grad(lib().dlm_row_logprob_grad, logits, tokens, state, grad_logp, logits.shape[:1], temperature, out,
-                       status, "grad_logp")
+    return _token_grad(lib().dlm_row_logprob_grad, logits, tokens, state, grad_logp, None, temperature, out, status,
+                       "grad_logp")
 
 
 def row_logprob_step(logits: torch.Tensor, tokens: torch.Tensor, weights: torch.Tensor | None = None, *,
@@ -580,24 +588,26 @@ def row_logprob_step(logits: torch.Tensor, tokens: torch.Tensor, weights: torch.
     sum_r weights[r] * logp[r]) in one launch; ``grad`` may be ``logits`` itself.
     The loss of a likelihood bound has negative weights: ``-1 / t`` at masked
     positions, 0 elsewhere."""
-    args = _token_rows(logits, tokens)
-    rows, dev = logits.shape[0], logits.device
-    _floats(rows, dev, ("weights", weights), ("logp", logp))
+    dev, index, rows, args = _token_rows(logits, tokens)
+    weights_at = _vector(weights, rows, index, "weights")  # (the tensor lives until the launch)
     if logp is None:
         logp = _new(rows, dev)
+    else:
+        _vector(logp, rows, index, "logp")
     grad = _grad_out(logits, grad)
-    _on(dev, lib().dlm_row_logprob_step, *args, _ptr(tokens), float(temperature), _ptr(weights), _ptr(logp), _ptr(grad),
-        _stride(grad), _status_ptr(status, dev))
+    _on(dev, lib().dlm_row_logprob_step, *args, float(temperature), weights_at, logp.data_ptr(),
+        grad.data_ptr(), _stride(grad), _status_ptr(status, dev))
     return logp, grad
 
 
 def _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip, kl_weight, kl, temperature):
-    args = _token_rows(logits, tokens)
+    dev, index, rows, args = _token_rows(logits, tokens)
     if kl not in _KL:
         raise ValueError(f"kl must be one of {sorted(_KL)}")
-    _floats(logits.shape[0], logits.device, ("advantages", advantages), ("old", old), ("ref", ref), ("weights", weights))
-    return (*args, _ptr(tokens), float(temperature), _ptr(advantages), _ptr(old), _ptr(ref), _ptr(weights),
-            ctypes.byref(PolicyParams(clip_low, clip_high, dual_clip, kl_weight, _KL[kl])))
+    return dev, index, rows, (*args, float(temperature), _vector(advantages, rows, index, "advantages"),
+                              _vector(old, rows, index, "old"), _vector(ref, rows, index, "ref"),
+                              _vector(weights, rows, index, "weights"),
+                              ctypes.byref(PolicyParams(clip_low, clip_high, dual_clip, kl_weight, _KL[kl])))
 
 
 def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, advantages: torch.Tensor, *, old: torch.Tensor | None = None,
@@ -610,13 +620,12 @@ def policy_loss(logits: torch.Tensor, tokens: torch.Tensor, advantages: torch.Te
     holds the rollout policy's (None: the policy is the rollout's own).  Returns the
     losses, the log-probabilities and the state that :func:`policy_grad` takes.
     The result carries no autograd graph."""
-    args = _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip, kl_weight, kl,
-                        temperature)
-    rows, dev = logits.shape[0], logits.device
+    dev, index, rows, args = _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip,
+                                          kl_weight, kl, temperature)
     if out is None:
         out = PolicyLoss(_new(rows, dev), _new(rows, dev), _new((rows, TOKEN_STATE), dev))
     else:
-        _floats(rows, dev, ("out.loss", out.loss), ("out.logp", out.logp))
+        _vectors(index, ("out.loss", out.loss, rows), ("out.logp", out.logp, rows))
         _same(out.state, (rows, TOKEN_STATE), torch.float32, dev, "out.state")
     _on(dev, lib().dlm_policy_loss, *args, _ptr(out.loss), _ptr(out.logp), _ptr(out.state), _status_ptr(status, dev))
     return out
@@ -628,7 +637,7 @@ def policy_grad(logits: torch.Tensor, tokens: torch.Tensor, state: torch.Tensor,
     """dlm_policy_grad: the gradient of sum_r grad_loss[r] * loss[r] with respect to
     ``logits``, from the state of the :func:`policy_loss` call with the same
     arguments.  ``out`` may be ``logits`` itself."""
-    return _token_grad(lib().dlm_policy_grad, logits, tokens, state, grad_loss, logits.shape[:1], temperature, out, status,
+    return _token_grad(lib().dlm_policy_grad, logits, tokens, state, grad_loss, None, temperature, out, status,
                        "grad_loss")
 
 
@@ -639,32 +648,31 @@ def policy_step(logits: torch.Tensor, tokens: torch.Tensor, advantages: torch.Te
     """dlm_policy_step: :func:`policy_loss` and the gradient of the losses' sum in
     one launch; ``out.grad`` may be ``logits`` itself.  Feed a model's own graph with
     ``logits.backward(grad)``."""
-    args = _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip, kl_weight, kl,
-                        temperature)
-    rows, dev = logits.shape[0], logits.device
+    dev, index, rows, args = _policy_args(logits, tokens, advantages, old, ref, weights, clip_low, clip_high, dual_clip,
+                                          kl_weight, kl, temperature)
     if out is None:
         out = PolicyStep(_new(rows, dev), _new(rows, dev), _grad_out(logits, None))
     else:
-        _floats(rows, dev, ("out.loss", out.loss), ("out.logp", out.logp))
+        _vectors(index, ("out.loss", out.loss, rows), ("out.logp", out.logp, rows))
         _grad_out(logits, out.grad)
-    _on(dev, lib().dlm_policy_step, *args, _ptr(out.loss), _ptr(out.logp), _ptr(out.grad), _stride(out.grad),
+    _on(dev, lib().dlm_policy_step, *args, _ptr(out.loss), _ptr(out.logp), out.grad.data_ptr(), _stride(out.grad),
         _status_ptr(status, dev))
     return out
 
 
 def _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta, label_smoothing, kind, temperature):
-    args = _token_rows(logits, tokens)
-    dev = logits.device
+    dev, index, rows, args = _token_rows(logits, tokens)
     if kind not in _PREF:
         raise ValueError(f"kind must be one of {sorted(_PREF)}")
-    if offsets.dim() != 1 or offsets.shape[0] % 2 != 1:
+    n = offsets.numel()
+    if n % 2 != 1:
         raise ValueError("offsets must have 2 * pairs + 1 entries")
-    _same(offsets, offsets.shape, torch.int32, dev, "offsets")
-    pairs = offsets.shape[0] // 2
-    _floats(logits.shape[0], dev, ("ref", ref), ("weights", weights))
-    _floats(pairs, dev, ("margins", margins), ("pair_weights", pair_weights))
-    return pairs, (*args, _ptr(tokens), float(temperature), _ptr(offsets), pairs, _ptr(ref), _ptr(weights), _ptr(margins),
-                   _ptr(pair_weights), ctypes.byref(PreferenceParams(beta, label_smoothing, _PREF[kind])))
+    pairs = n // 2
+    return dev, index, rows, pairs, (*args, float(temperature), _vector(offsets, n, index, "offsets", torch.int32), pairs,
+                                     _vector(ref, rows, index, "ref"), _vector(weights, rows, index, "weights"),
+                                     _vector(margins, pairs, index, "margins"),
+                                     _vector(pair_weights, pairs, index, "pair_weights"),
+                                     ctypes.byref(PreferenceParams(beta, label_smoothing, _PREF[kind])))
 
 
 def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, offsets: torch.Tensor, *, ref: torch.Tensor | None = None,
@@ -679,15 +687,12 @@ def preference_loss(logits: torch.Tensor, tokens: torch.Tensor, offsets: torch.T
     the token's log-probability less the reference's ``ref`` (None: no reference).
     Returns the pairs' losses, the scores, the log-probabilities and the state that
     :func:`preference_grad` takes.  The result carries no autograd graph."""
-    pairs, args = _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta, label_smoothing, kind,
-                                   temperature)
-    rows, dev = logits.shape[0], logits.device
+    dev, index, rows, pairs, args = _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta,
+                                                     label_smoothing, kind, temperature)
     if out is None:
         out = PreferenceLoss(_new(pairs, dev), _new(2 * pairs, dev), _new(rows, dev), _new((rows, TOKEN_STATE), dev))
     else:
-        _floats(pairs, dev, ("out.loss", out.loss))
-        _floats(2 * pairs, dev, ("out.score", out.score))
-        _floats(rows, dev, ("out.logp", out.logp))
+        _vectors(index, ("out.loss", out.loss, pairs), ("out.score", out.score, 2 * pairs), ("out.logp", out.logp, rows))
         _same(out.state, (rows, TOKEN_STATE), torch.float32, dev, "out.state")
     _on(dev, lib().dlm_preference_loss, *args, _ptr(out.loss), _ptr(out.score), _ptr(out.logp), _ptr(out.state),
         _status_ptr(status, dev))
@@ -701,9 +706,9 @@ def preference_grad(logits: torch.Tensor, tokens: torch.Tensor, state: torch.Ten
     per pair) with respect to ``logits``, from the state of the
     :func:`preference_loss` call with the same arguments.  ``out`` may be ``logits``
     itself."""
-    shape = grad_loss.shape[:1] if grad_loss is not None else (0,)
-    return _token_grad(lib().dlm_preference_grad, logits, tokens, state, grad_loss, shape, temperature, out, status,
-                       "grad_loss", shape[0])
+    pairs = 0 if grad_loss is None else grad_loss.numel()
+    return _token_grad(lib().dlm_preference_grad, logits, tokens, state, grad_loss, pairs, temperature, out, status,
+                       "grad_loss", pairs)
 
 
 def preference_workspace(rows: int, pairs: int, device) -> torch.Tensor:
@@ -719,22 +724,21 @@ def preference_step(logits: torch.Tensor, tokens: torch.Tensor, offsets: torch.T
     """dlm_preference_step: :func:`preference_loss` and the gradient of the losses'
     sum; ``out.grad`` may be ``logits`` itself.  ``workspace``:
     :func:`preference_workspace` (None: a new one)."""
-    pairs, args = _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta, label_smoothing, kind,
-                                   temperature)
-    rows, dev = logits.shape[0], logits.device
-    if workspace is None:
-        workspace = preference_workspace(rows, pairs, dev)
+    dev, index, rows, pairs, args = _preference_args(logits, tokens, offsets, ref, weights, margins, pair_weights, beta,
+                                                     label_smoothing, kind, temperature)
+    nbytes = None
+    if workspace is None:  # (the rows' state and the offsets; the call checks that it is enough)
+        workspace = _new(rows * TOKEN_STATE + 2 * pairs + 4, dev)
+        nbytes = workspace.numel() * 4
     elif workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     if out is None:
         out = PreferenceStep(_new(pairs, dev), _new(2 * pairs, dev), _new(rows, dev), _grad_out(logits, None))
     else:
-        _floats(pairs, dev, ("out.loss", out.loss))
-        _floats(2 * pairs, dev, ("out.score", out.score))
-        _floats(rows, dev, ("out.logp", out.logp))
+        _vectors(index, ("out.loss", out.loss, pairs), ("out.score", out.score, 2 * pairs), ("out.logp", out.logp, rows))
         _grad_out(logits, out.grad)
-    _on(dev, lib().dlm_preference_step, *args, _ptr(out.loss), _ptr(out.score), _ptr(out.logp), _ptr(out.grad),
-        _stride(out.grad), _ptr(workspace), workspace.numel(), _status_ptr(status, dev))
+    _on(dev, lib().dlm_preference_step, *args, _ptr(out.loss), _ptr(out.score), _ptr(out.logp), out.grad.data_ptr(),
+        _stride(out.grad), workspace.data_ptr(), nbytes or workspace.numel(), _status_ptr(status, dev))
     return out
 
 
